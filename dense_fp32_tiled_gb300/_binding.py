@@ -14,7 +14,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm_f32.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_f32.h")
 HEADER_PATHS = [HEADER_PATH, os.path.join(os.path.dirname(_PKG), "include", "transpose_f32.h"),
-                os.path.join(os.path.dirname(_PKG), "include", "smem_bank_probe.h")]
+                os.path.join(os.path.dirname(_PKG), "include", "smem_bank_probe.h"),
+                os.path.join(os.path.dirname(_PKG), "include", "linear.h"),
+                os.path.join(os.path.dirname(_PKG), "include", "experts.h")]
 
 SGEMM_OK = 0
 _lib = None
@@ -86,6 +88,32 @@ def load_library():
     lib.smem_bank_pattern_probe.argtypes = [i32, ctypes.POINTER(ctypes.c_int), i32, i32,
                                             ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]
     lib.smem_bank_pattern_probe.restype = i32
+    i64, size = ctypes.c_int64, ctypes.c_size_t
+    # type, sizes; x; w; bias; residual; activation; preact; y; workspace; stream
+    lib.linear_forward.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32, p, p, i64, i32, p, i64, p, i64, p, size, p]
+    lib.linear_forward_workspace_size.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32]
+    lib.expert_linear_forward.argtypes = [i32, i32, i32, i32, i32, p, p, i64, p, i64, i64, i32, p, p, i64, i32, p, i64,
+                                          p, i64, p, size, p]
+    lib.expert_linear_forward_workspace_size.argtypes = [i32, i32, i32, i32, i32, p, i64, p, i64, i64, i32]
+    # type, sizes; dy; x; w; preact; activation; dx; dw; dbias; workspace; stream
+    lib.linear_backward.argtypes = [i32, i32, i32, i32, p, i64, p, i64, p, i64, i32, p, i64, i32, p, i64, p, i64, p, p,
+                                    size, p]
+    lib.linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, p, i64, p, i64, p, i64, i32, i32, i32, i32, i32]
+    lib.expert_linear_backward.argtypes = [i32, i32, i32, i32, i32, p, p, i64, p, i64, p, i64, i64, i32, p, i64, i32, p,
+                                           i64, p, i64, i64, p, p, size, p]
+    lib.expert_linear_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, p, i64, p, i64, p, i64, i64, i32, i32,
+                                                          i32, i32, i32]
+    lib.linear_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
+    lib.expert_sort.argtypes = [i32, i32, i32, p, i32, p, p, p, size, p]
+    lib.expert_sort_workspace_size.argtypes = [i32, i32, i32]
+    lib.expert_gather.argtypes = [i32, i32, i32, i32, i32, p, p, p, i64, p, i64, p]
+    lib.expert_combine.argtypes = [i32, i32, i32, i32, p, p, p, i64, p, i64, p, i64, p]
+    lib.expert_combine_backward.argtypes = [i32, i32, i32, i32, i32, p, p, p, p, i64, p, i64, p, i64, p, p]
+    for name in ("linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward",
+                 "linear_timeouts", "expert_sort", "expert_gather", "expert_combine", "expert_combine_backward"):
+        getattr(lib, name).restype = i32
+    for name in ("linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward", "expert_sort"):
+        getattr(lib, name + "_workspace_size").restype = size
     _lib = lib
     return lib
 
@@ -96,7 +124,7 @@ def declared_functions() -> list[str]:
     for path in HEADER_PATHS:
         with open(path) as f:
             text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
-        names |= set(re.findall(r"\b((?:sgemm|transpose)_f32\w*|smem_bank_\w+)\s*\(", text))
+        names |= set(re.findall(r"\b((?:sgemm|transpose)_f32\w*|smem_bank_\w+|linear_\w+|expert_\w+)\s*\(", text))
     return sorted(names)
 
 

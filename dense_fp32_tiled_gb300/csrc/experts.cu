@@ -1,0 +1,482 @@
+// experts.cu -- the tokens' way to their experts and back (C ABI:
+// include/experts.h).  Everything here moves bytes: a stable counting sort of
+// the choices, and copies and sums of whole rows in 16-byte accesses where
+// the rows allow it, one 16-byte column per thread so that each row of x, y
+// and dy is read or written once.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+#include <type_traits>
+
+#include "experts.h"
+#include "linear_types.cuh"
+#include "nvtx_range.cuh"
+
+namespace {
+
+using lt::from_f;
+using lt::to_f;
+
+// ---- sort ------------------------------------------------------------------------
+// Choices are cut into `blocks` equal ranges.  With more than one, a first
+// kernel counts each range's choices by expert; the second adds up what lies
+// before its range, counts its own range warp by warp and gives each choice
+// its place: places before the expert + before the range + before the warp +
+// in the warp.  No atomics, so the order is that of the choices.
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_RANGE = 8192;   // choices a block sorts, at least
+constexpr int SORT_BLOCKS = 512;   // ranges, at most
+constexpr int SORT_SMEM = 200 * 1024;
+
+struct SortPlan {
+    int blocks, range, warps;
+    size_t smem;
+};
+SortPlan sort_plan(long long R, int E) {
+    SortPlan s;
+    long long blocks = (R + SORT_RANGE - 1) / SORT_RANGE;
+    if (blocks < 1) blocks = 1;
+    if (blocks > SORT_BLOCKS) blocks = SORT_BLOCKS;
+    s.range = static_cast<int>(((R + blocks - 1) / blocks + 31) / 32 * 32);
+    if (s.range < 32) s.range = 32;
+    s.blocks = static_cast<int>((R + s.range - 1) / s.range);
+    if (s.blocks < 1) s.blocks = 1;
+    const int most = SORT_SMEM / 4 / E - 1;  // tables of E counts that fit
+    s.warps = most < SORT_THREADS / 32 ? most : SORT_THREADS / 32;
+    s.smem = static_cast<size_t>(s.warps + 1) * E * 4;
+    return s;
+}
+
+template <typename I>
+__device__ __forceinline__ int choice_at(const I *choices, long long i, long long end, int E) {
+    if (i >= end) return -1;
+    const I c = choices[i];
+    return c >= 0 && c < E ? static_cast<int>(c) : -1;
+}
+// Adds 32 choices (one per lane, -1: none) to a warp's counts; returns each
+// one's place among its expert's (before: what the counts held).
+__device__ __forceinline__ int count32(int key, int *counts, int lane) {
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    int before = 0;
+    if (key >= 0) before = counts[key];
+    __syncwarp();
+    if (key >= 0 && lane == __ffs(same) - 1) counts[key] = before + __popc(same);
+    __syncwarp();
+    return before + __popc(same & ((1u << lane) - 1u));
+}
+
+template <typename I>
+__global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const I *__restrict__ choices, long long R, int E,
+                                                                  int range, int warps, int *__restrict__ counts) {
+    extern __shared__ int shared[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < warps * E; i += SORT_THREADS) shared[i] = 0;
+    __syncthreads();
+    const long long begin = static_cast<long long>(blockIdx.x) * range;
+    const long long end = begin + range < R ? begin + range : R;
+    const int per = ((range + warps - 1) / warps + 31) / 32 * 32;
+    if (warp < warps) {
+        const long long b = begin + static_cast<long long>(warp) * per, e = b + per < end ? b + per : end;
+        for (long long i = b; i < e; i += 32) count32(choice_at(choices, i + lane, e, E), shared + warp * E, lane);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+        int n = 0;
+        for (int w = 0; w < warps; ++w) n += shared[w * E + e];
+        counts[static_cast<long long>(blockIdx.x) * E + e] = n;
+    }
+}
+
+template <typename I>
+__global__ void __launch_bounds__(SORT_THREADS)
+sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, int warps, int blocks,
+                  const int *__restrict__ counts, int *__restrict__ rows, int *__restrict__ offsets) {
+    extern __shared__ int shared[];
+    __shared__ int sums[32];
+    int *base = shared;                  // E: the expert's first place in this range
+    int *mine = shared + E;              // warps x E
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < warps * E; i += SORT_THREADS) mine[i] = 0;
+    __syncthreads();
+    const long long begin = static_cast<long long>(blockIdx.x) * range;
+    const long long end = begin + range < R ? begin + range : R;
+    const int per = ((range + warps - 1) / warps + 31) / 32 * 32;
+    const long long b = begin + static_cast<long long>(warp) * per, e1 = b + per < end ? b + per : end;
+    if (warp < warps)
+        for (long long i = b; i < e1; i += 32) count32(choice_at(choices, i + lane, e1, E), mine + warp * E, lane);
+    __syncthreads();
+    // per expert: all its choices, those before this range, and the warps' first places;
+    // the running sum over the experts carries from one group of 1024 to the next
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += SORT_THREADS) {
+        const int e = e0 + threadIdx.x;
+        int total = 0, before = 0;
+        if (e < E) {
+            int own = 0;
+            for (int w = 0; w < warps; ++w) {
+                const int n = mine[w * E + e];
+                mine[w * E + e] = own;
+                own += n;
+            }
+            if (blocks == 1) {
+                total = own;
+            } else {
+                for (int k = 0; k < blocks; ++k) {
+                    const int n = counts[static_cast<long long>(k) * E + e];
+                    total += n;
+                    if (k < static_cast<int>(blockIdx.x)) before += n;
+                }
+            }
+        }
+        int scan = total;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += o;
+        }
+        if (lane == 31) sums[warp] = scan;
+        __syncthreads();
+        int ahead = 0, all = 0;
+        for (int w = 0; w < SORT_THREADS / 32; ++w) {
+            if (w < warp) ahead += sums[w];
+            all += sums[w];
+        }
+        const int first = carry + ahead + scan - total;
+        if (e < E) {
+            base[e] = first + before;
+            if (blockIdx.x == 0) {
+                offsets[e] = first;
+                if (e == E - 1) offsets[E] = first + total;
+            }
+        }
+        carry += all;
+        __syncthreads();
+    }
+    if (warp < warps)
+        for (long long i = b; i < e1; i += 32) {
+            const int key = choice_at(choices, i + lane, e1, E);
+            const int at = count32(key, mine + warp * E, lane);
+            if (i + lane < e1) rows[i + lane] = key >= 0 ? base[key] + at : -1;
+        }
+}
+
+// ---- rows --------------------------------------------------------------------------
+// V values (16 bytes, or one) of a row.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+    T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load(const T *p) {
+    return *reinterpret_cast<const Pack<T, V> *>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const Pack<T, V> &v) {
+    *reinterpret_cast<Pack<T, V> *>(p) = v;
+}
+
+constexpr int ROW_THREADS = 256;
+constexpr int ZERO_BLOCKS = 64;  // blocks that clear the places in no use
+
+// The places from `used` on, by the last ZERO_BLOCKS blocks of a grid.
+template <typename T, int V>
+__device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long long R, int packs, int block) {
+    const long long first = static_cast<long long>(min(max(used, 0), static_cast<int>(R))) * packs;
+    Pack<T, V> zero;
+#pragma unroll
+    for (int i = 0; i < V; ++i) zero.v[i] = from_f<T>(0.0f);
+    for (long long u = first + static_cast<long long>(block) * ROW_THREADS + threadIdx.x; u < R * packs;
+         u += static_cast<long long>(ZERO_BLOCKS) * ROW_THREADS) {
+        const long long r = u / packs;
+        store<T, V>(out + r * ld + (u - r * packs) * V, zero);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(ROW_THREADS)
+gather_kernel(int T_, int J, int packs, int E, const int *__restrict__ rows, const int *__restrict__ offsets,
+              const T *__restrict__ x, long long ldx, T *__restrict__ xs, long long ldxs, int blocks) {
+    const long long R = static_cast<long long>(T_) * J;
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        clear_rest<T, V>(xs, ldxs, offsets[E], R, packs, blockIdx.x - blocks);
+        return;
+    }
+    const long long u = static_cast<long long>(blockIdx.x) * ROW_THREADS + threadIdx.x;
+    const long long t = u / packs;
+    if (t >= T_) return;
+    const long long c = (u - t * packs) * V;
+    const Pack<T, V> v = load<T, V>(x + t * ldx + c);
+    for (int j = 0; j < J; ++j) {
+        const int r = rows[t * J + j];
+        if (r >= 0 && r < R) store<T, V>(xs + r * ldxs + c, v);
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(ROW_THREADS)
+combine_kernel(int T_, int J, int packs, const int *__restrict__ rows, const float *__restrict__ weights,
+               const T *__restrict__ ys, long long ldys, const T *residual, long long ldr, T *y, long long ldy) {
+    const long long R = static_cast<long long>(T_) * J;
+    const long long u = static_cast<long long>(blockIdx.x) * ROW_THREADS + threadIdx.x;
+    const long long t = u / packs;
+    if (t >= T_) return;
+    const long long c = (u - t * packs) * V;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+    constexpr int U = 4;  // rows in flight
+    for (int j0 = 0; j0 < J; j0 += U) {
+        Pack<T, V> v[U];
+        float w[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            w[k] = 0.0f;
+            const int r = j0 + k < J ? rows[t * J + j0 + k] : -1;
+            const bool in = r >= 0 && r < R;
+            if (in) {
+                v[k] = load<T, V>(ys + r * ldys + c);
+                w[k] = weights != nullptr ? weights[t * J + j0 + k] : 1.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[k].v[i] = from_f<T>(0.0f);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = fmaf(w[k], to_f(v[k].v[i]), sum[i]);
+    }
+    if (residual != nullptr) {
+        const Pack<T, V> r = load<T, V>(residual + t * ldr + c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += to_f(r.v[i]);
+    }
+    Pack<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(sum[i]);
+    store<T, V>(y + t * ldy + c, o);
+}
+
+// A warp per choice; the other choices of the token find dy in the L1 or L2.
+template <typename T, int V>
+__global__ void __launch_bounds__(ROW_THREADS)
+combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__ rows, const int *__restrict__ offsets,
+                        const float *__restrict__ weights, const T *__restrict__ dy, long long lddy,
+                        const T *__restrict__ ys, long long ldys, T *__restrict__ dys, long long lddys,
+                        float *__restrict__ dweights, int blocks) {
+    const long long R = static_cast<long long>(T_) * J;
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        clear_rest<T, V>(dys, lddys, offsets[E], R, packs, blockIdx.x - blocks);
+        return;
+    }
+    const long long i = static_cast<long long>(blockIdx.x) * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (i >= R) return;
+    const int r = rows[i];
+    if (r < 0 || r >= R) {
+        if (dweights != nullptr && lane == 0) dweights[i] = 0.0f;
+        return;
+    }
+    const float w = weights != nullptr ? weights[i] : 1.0f;
+    const T *d = dy + i / J * lddy, *s = ys + r * ldys;
+    T *o = dys + r * lddys;
+    float dot = 0.0f;
+#pragma unroll 4
+    for (int p = lane; p < packs; p += 32) {
+        const Pack<T, V> g = load<T, V>(d + static_cast<long long>(p) * V);
+        if (dweights != nullptr) {
+            const Pack<T, V> v = load<T, V>(s + static_cast<long long>(p) * V);
+#pragma unroll
+            for (int k = 0; k < V; ++k) dot = fmaf(to_f(g.v[k]), to_f(v.v[k]), dot);
+        }
+        Pack<T, V> q;
+#pragma unroll
+        for (int k = 0; k < V; ++k) q.v[k] = from_f<T>(w * to_f(g.v[k]));
+        store<T, V>(o + static_cast<long long>(p) * V, q);
+    }
+    if (dweights != nullptr) {
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
+        if (lane == 0) dweights[i] = dot;
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------
+struct Span {
+    uintptr_t lo = 0, hi = 0;
+};
+Span span(const void *p, long long rows, long long width, long long ld, long long bytes) {
+    Span s;
+    if (p == nullptr || rows <= 0 || width <= 0) return s;
+    s.lo = reinterpret_cast<uintptr_t>(p);
+    s.hi = s.lo + static_cast<uintptr_t>(((rows - 1) * ld + width) * bytes);
+    return s;
+}
+bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
+bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+int check_sizes(int type, int T, int J, int H, long long E) {
+    if (type < LINEAR_F32 || type > LINEAR_F16) return SGEMM_ERR_INVALID_ARG;
+    if (T < 0 || J < 0 || H < 0 || E < 0 || E > LINEAR_MAX_EXPERTS || J > EXPERTS_MAX_CHOICES ||
+        static_cast<long long>(T) * J > INT_MAX)
+        return SGEMM_ERR_INVALID_DIM;
+    return SGEMM_OK;
+}
+bool wide(const void *p, long long ld, int type) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * lt::type_bytes(type) % 16 == 0);
+}
+int launched() {
+    if (cudaPeekAtLastError() == cudaSuccess) return SGEMM_OK;
+    (void)cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+}
+// f(element, values per access) for the type and whether rows allow 16 bytes.
+template <typename F>
+int with_rows(int type, bool vec, F &&f) {
+    if (type == LINEAR_F32) return vec ? f(float(), lt::Int<4>{}) : f(float(), lt::Int<1>{});
+    if (type == LINEAR_BF16) return vec ? f(__nv_bfloat16(), lt::Int<8>{}) : f(__nv_bfloat16(), lt::Int<1>{});
+    return vec ? f(__half(), lt::Int<8>{}) : f(__half(), lt::Int<1>{});
+}
+long long blocks_for(long long units) { return (units + ROW_THREADS - 1) / ROW_THREADS; }
+
+template <typename I>
+int sort(long long R, int E, const I *choices, int *rows, int *offsets, int *counts, cudaStream_t stream) {
+    const SortPlan s = sort_plan(R, E);
+    if (s.smem > 48 * 1024 &&
+        (cudaFuncSetAttribute(sort_count_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, SORT_SMEM) != cudaSuccess ||
+         cudaFuncSetAttribute(sort_place_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize, SORT_SMEM) != cudaSuccess)) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_DEVICE;
+    }
+    sg_nvtx::Range r("experts: sort");
+    if (s.blocks > 1)
+        sort_count_kernel<I><<<s.blocks, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, counts);
+    sort_place_kernel<I><<<s.blocks, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, s.blocks, counts,
+                                                                     rows, offsets);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" size_t expert_sort_workspace_size(int T, int J, int E) {
+    if (T <= 0 || J <= 0 || E <= 0 || E > LINEAR_MAX_EXPERTS || static_cast<long long>(T) * J > INT_MAX) return 0;
+    const SortPlan s = sort_plan(static_cast<long long>(T) * J, E);
+    return s.blocks > 1 ? static_cast<size_t>(s.blocks) * E * sizeof(int) : 0;
+}
+
+extern "C" int expert_sort(int T, int J, int E, const void *choices, int choice_bytes, int *rows, int *offsets,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (choice_bytes != 4 && choice_bytes != 8) return SGEMM_ERR_INVALID_ARG;
+    const int st = check_sizes(LINEAR_F32, T, J, 0, E);
+    if (st != SGEMM_OK) return st;
+    if (E < 1) return SGEMM_ERR_INVALID_DIM;
+    const long long R = static_cast<long long>(T) * J;
+    const size_t need = expert_sort_workspace_size(T, J, E);
+    if (offsets == nullptr || (R > 0 && (choices == nullptr || rows == nullptr)) || (need > 0 && workspace == nullptr))
+        return SGEMM_ERR_NULL_PTR;
+    if (misaligned(choices, choice_bytes) || misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(workspace, 16) ||
+        workspace_bytes < need)
+        return SGEMM_ERR_INVALID_ARG;
+    const Span sc = span(choices, 1, R, R, choice_bytes), sr = span(rows, 1, R, R, 4), so = span(offsets, 1, E + 1, 1, 4),
+               sw = span(workspace, 1, static_cast<long long>(need), 1, 1);
+    if (overlap(sr, sc) || overlap(so, sc) || overlap(sw, sc) || overlap(sr, so) || overlap(sr, sw) || overlap(so, sw))
+        return SGEMM_ERR_ALIAS;
+    int *counts = static_cast<int *>(workspace);
+    return choice_bytes == 4 ? sort(R, E, static_cast<const int *>(choices), rows, offsets, counts, stream)
+                             : sort(R, E, static_cast<const long long *>(choices), rows, offsets, counts, stream);
+}
+
+extern "C" int expert_gather(int type, int T, int J, int H, int E, const int *rows, const int *offsets, const void *x,
+                             int64_t ldx, void *xs, int64_t ldxs, cudaStream_t stream) {
+    const int st = check_sizes(type, T, J, H, E);
+    if (st != SGEMM_OK) return st;
+    const int least = H > 1 ? H : 1, b = lt::type_bytes(type);
+    if (ldx < least || ldxs < least) return SGEMM_ERR_INVALID_LD;
+    const long long R = static_cast<long long>(T) * J;
+    if (R == 0 || H == 0) return SGEMM_OK;
+    if (rows == nullptr || offsets == nullptr || x == nullptr || xs == nullptr) return SGEMM_ERR_NULL_PTR;
+    if (misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(x, b) || misaligned(xs, b)) return SGEMM_ERR_INVALID_ARG;
+    const Span so = span(xs, R, H, ldxs, b);
+    if (overlap(so, span(x, T, H, ldx, b)) || overlap(so, span(rows, 1, R, R, 4)) || overlap(so, span(offsets, 1, E + 1, 1, 4)))
+        return SGEMM_ERR_ALIAS;
+    const int n = 16 / b;
+    const bool vec = H % n == 0 && wide(x, ldx, type) && wide(xs, ldxs, type);
+    const int packs = vec ? H / n : H;
+    const long long blocks = blocks_for(static_cast<long long>(T) * packs);
+    if (blocks + ZERO_BLOCKS > INT_MAX) return SGEMM_ERR_INVALID_DIM;
+    sg_nvtx::Range r("experts: gather");
+    return with_rows(type, vec, [&](auto el, auto v) {
+        using El = decltype(el);
+        gather_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
+            T, J, packs, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks));
+        return launched();
+    });
+}
+
+extern "C" int expert_combine(int type, int T, int J, int H, const int *rows, const float *weights, const void *ys,
+                              int64_t ldys, const void *residual, int64_t ldr, void *y, int64_t ldy, cudaStream_t stream) {
+    const int st = check_sizes(type, T, J, H, 0);
+    if (st != SGEMM_OK) return st;
+    const int least = H > 1 ? H : 1, b = lt::type_bytes(type);
+    if (ldys < least || ldy < least || (residual != nullptr && ldr < least)) return SGEMM_ERR_INVALID_LD;
+    if (T == 0 || H == 0) return SGEMM_OK;
+    const long long R = static_cast<long long>(T) * J;
+    if (y == nullptr || (J > 0 && (rows == nullptr || ys == nullptr))) return SGEMM_ERR_NULL_PTR;
+    if (misaligned(rows, 4) || misaligned(weights, 4) || misaligned(ys, b) || misaligned(residual, b) || misaligned(y, b))
+        return SGEMM_ERR_INVALID_ARG;
+    const Span so = span(y, T, H, ldy, b);
+    const bool in_place = residual == y && ldr == ldy;
+    if (overlap(so, span(ys, R, H, ldys, b)) || overlap(so, span(rows, 1, R, R, 4)) || overlap(so, span(weights, 1, R, R, 4)) ||
+        (!in_place && overlap(so, span(residual, T, H, ldr, b))))
+        return SGEMM_ERR_ALIAS;
+    const int n = 16 / b;
+    const bool vec = H % n == 0 && wide(ys, ldys, type) && wide(y, ldy, type) && wide(residual, ldr, type);
+    const int packs = vec ? H / n : H;
+    const long long blocks = blocks_for(static_cast<long long>(T) * packs);
+    if (blocks > INT_MAX) return SGEMM_ERR_INVALID_DIM;
+    sg_nvtx::Range r("experts: combine");
+    return with_rows(type, vec, [&](auto el, auto v) {
+        using El = decltype(el);
+        combine_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks), ROW_THREADS, 0, stream>>>(
+            T, J, packs, rows, weights, static_cast<const El *>(ys), ldys, static_cast<const El *>(residual), ldr,
+            static_cast<El *>(y), ldy);
+        return launched();
+    });
+}
+
+extern "C" int expert_combine_backward(int type, int T, int J, int H, int E, const int *rows, const int *offsets,
+                                       const float *weights, const void *dy, int64_t lddy, const void *ys, int64_t ldys,
+                                       void *dys, int64_t lddys, float *dweights, cudaStream_t stream) {
+    const int st = check_sizes(type, T, J, H, E);
+    if (st != SGEMM_OK) return st;
+    const int least = H > 1 ? H : 1, b = lt::type_bytes(type);
+    if (lddy < least || lddys < least || (dweights != nullptr && ldys < least)) return SGEMM_ERR_INVALID_LD;
+    const long long R = static_cast<long long>(T) * J;
+    if (R == 0) return SGEMM_OK;
+    if (rows == nullptr || offsets == nullptr || (H > 0 && (dy == nullptr || dys == nullptr || (dweights != nullptr && ys == nullptr))))
+        return SGEMM_ERR_NULL_PTR;
+    if (misaligned(rows, 4) || misaligned(offsets, 4) || misaligned(weights, 4) || misaligned(dy, b) || misaligned(ys, b) ||
+        misaligned(dys, b) || misaligned(dweights, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    const Span out[2] = {span(dys, R, H, lddys, b), span(dweights, 1, R, R, 4)};
+    const Span in[5] = {span(dy, T, H, lddy, b), dweights != nullptr ? span(ys, R, H, ldys, b) : Span(),
+                        span(rows, 1, R, R, 4), span(offsets, 1, E + 1, 1, 4), span(weights, 1, R, R, 4)};
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (overlap(o, i)) return SGEMM_ERR_ALIAS;
+    if (overlap(out[0], out[1])) return SGEMM_ERR_ALIAS;
+    const int n = 16 / b;
+    const bool vec = H % n == 0 && wide(dy, lddy, type) && (dweights == nullptr || wide(ys, ldys, type)) && wide(dys, lddys, type);
+    const int packs = vec ? H / n : H;
+    const long long blocks = (R + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+    if (blocks + ZERO_BLOCKS > INT_MAX) return SGEMM_ERR_INVALID_DIM;
+    sg_nvtx::Range r("experts: combine backward");
+    return with_rows(type, vec, [&](auto el, auto v) {
+        using El = decltype(el);
+        combine_backward_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
+            T, J, packs, E, rows, offsets, weights, static_cast<const El *>(dy), lddy, static_cast<const El *>(ys), ldys,
+            static_cast<El *>(dys), lddys, dweights, static_cast<int>(blocks));
+        return launched();
+    });
+}

@@ -1,0 +1,1226 @@
+// linear.cu -- the layer products of GB300 (sm_103a): y = act(x.w + bias) +
+// residual, the same over rows grouped by expert, and the products of their
+// gradients, all on one tensor-core kernel (C ABI: include/linear.h).
+//
+// The kernel computes out[t][f] = sum_k Q[t][k] P[f][k] for "tokens" t (rows
+// of out) and "features" f (its columns), with P, the weight or the operand
+// that owns the columns, on the 128 rows of the tensor core and Q on its
+// columns.  The features lie on the lanes of tensor memory then: an epilogue
+// thread owns one feature (its bias is one register), a warp stores 32
+// neighbouring features of one token, and the tile can be as narrow in tokens
+// as a decoding step needs (16) without idle rows.
+//   forward   P = w (N features),  Q = x          reduction over K
+//   dx        P = w (K features),  Q = dz         reduction over N
+//   dw        P, Q = x, dz transposed              reduction over the rows
+// Each operand is read in the order it is held in: K-major or MN-major (the
+// transposed one) is a matter of box shape and descriptor, so no operand is
+// ever transposed in memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+#include <utility>
+
+#include "ctx_key.cuh"
+#include "linear.h"
+#include "linear_prep.cuh"
+#include "linear_types.cuh"
+#include "nvtx_range.cuh"
+#include "tensor_core.cuh"
+
+namespace {
+
+using lt::from_f;
+using lt::to_f;
+
+constexpr int BK = 64;                       // K of a tile: one 128-byte swizzle row of 16-bit values
+constexpr int PROWS = 128;                   // features per CTA
+constexpr int P_BYTES = PROWS * BK * 2;      // 16 KiB
+constexpr int MN_BOX_BYTES = 64 * BK * 2;    // an MN-major box: 64 operand rows x 64 K
+constexpr int MAX_STAGES = 12;
+constexpr int TMEM_COLS = 512;
+constexpr int EPI_WARPS = 8;                 // warp w: tensor-memory lanes 32 (w % 4).., column half w / 4
+constexpr int COPY_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
+constexpr int THREADS = (EPI_WARPS + 2) * 32;
+constexpr int EPI_THREADS = EPI_WARPS * 32;
+constexpr int SMEM_MAX = 227 * 1024;
+// FP32: the six products of the pieces, small ones first, so that the last
+// and largest partial sums see the fewest further additions.  A block of
+// KBLK tiles of K runs through all six in tensor memory and is then added in
+// FP32 registers with round-to-nearest: the tensor core's accumulation
+// truncates, and its error grows with the number of additions.
+constexpr int PAIRS = 6;
+constexpr int KBLK = 2;
+
+enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
+
+struct Product {
+    int T, F, K;              // K_BY_EXPERT: K = all rows, shared out by offsets
+    int mode, E;
+    const int *offsets;
+    int bt;                   // tokens per tile (multiple of 16 * CG)
+    int nt, nf;               // tiles in tokens (DENSE, K_BY_EXPERT) and in features
+    int splits;               // CTAs of a cluster that share the K of a tile (CG = 1)
+    int stages, stage_bytes, q_bytes;
+    int p_mn, q_mn;
+    const void *bias, *residual;
+    void *z, *out;
+    long long ldr, ldz, ldo, out_expert;
+    int act;
+    unsigned *timeout_flag;
+};
+struct Maps {
+    CUtensorMap p, q;
+};
+
+// One output tile: expert e, tokens [t0, t_end), features from f0 (of this
+// CTA), K tiles [k0, k1) of this CTA, the first at element kbase.
+struct Tile {
+    int e, t0, t_end, ft, k0, k1, kbase, k_rows;
+    bool none;  // rows of no expert: zeros
+};
+
+// Experts' tables in shared memory: clamped first rows and, for
+// ROWS_BY_EXPERT, the first tile of each (group E: the rows of no expert).
+struct Tables {
+    const int *begin;  // E + 2
+    const int *first;  // E + 2
+};
+
+__device__ __forceinline__ void raster(int idx, int nt, int nf, int &tt, int &ft) {
+    // 8 token tiles at a time: the tiles in flight share few panels of both operands
+    const int per_group = 8 * nf;
+    const int g = idx / per_group, r = idx - g * per_group;
+    const int rows = min(8, nt - 8 * g);
+    tt = 8 * g + r % rows;
+    ft = r / rows;
+}
+
+template <int CG>
+__device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &tb, int rank) {
+    Tile w;
+    int tt, ft, ktiles = (p.K + BK - 1) / BK;
+    w.none = false;
+    w.e = 0;
+    w.kbase = 0;
+    w.k_rows = p.K;
+    if (p.mode == DENSE) {
+        raster(idx, p.nt, p.nf, tt, ft);
+        w.t0 = tt * p.bt;
+        w.t_end = p.T;
+    } else if (p.mode == ROWS_BY_EXPERT) {
+        int lo = 0, hi = p.E + 1;  // the last group whose first tile is <= idx
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tb.first[mid] <= idx)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        w.e = lo;
+        const int b = tb.begin[lo], n = tb.begin[lo + 1] - b;
+        raster(idx - tb.first[lo], (n + p.bt - 1) / p.bt, p.nf, tt, ft);
+        w.t0 = b + tt * p.bt;
+        w.t_end = b + n;
+        if (lo == p.E) {
+            w.none = true;
+            ktiles = 0;
+        }
+    } else {
+        const int per = p.nt * p.nf;
+        w.e = idx / per;
+        raster(idx - w.e * per, p.nt, p.nf, tt, ft);
+        w.t0 = tt * p.bt;
+        w.t_end = p.T;
+        w.kbase = tb.begin[w.e];
+        w.k_rows = tb.begin[w.e + 1] - w.kbase;
+        ktiles = (w.k_rows + BK - 1) / BK;
+    }
+    w.ft = ft;
+    if (CG == 1 && p.splits > 1) {
+        w.k0 = static_cast<int>(static_cast<long long>(ktiles) * rank / p.splits);
+        w.k1 = static_cast<int>(static_cast<long long>(ktiles) * (rank + 1) / p.splits);
+    } else {
+        w.k0 = 0;
+        w.k1 = ktiles;
+    }
+    return w;
+}
+
+// Piece of P and of Q of FP32 product i: (3,1) (1,3) (2,2) (2,1) (1,2) (1,1), from 0.
+__device__ __forceinline__ int p_piece(int i) { return (0x001102 >> (4 * i)) & 15; }
+__device__ __forceinline__ int q_piece(int i) { return (0x010120 >> (4 * i)) & 15; }
+
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;\n" ::"n"(EPI_THREADS) : "memory"); }
+
+// Bias, activation, residual and the stores for 16 tokens (rows row0 .. of
+// out, n of them valid) of one feature.
+template <typename T>
+__device__ __forceinline__ void finish16(const float (&acc)[16], const Product &p, float bias, int f, long long row0,
+                                         int n, T *out, bool none) {
+    constexpr bool EXACT = std::is_same<T, float>::value;
+    if (n <= 0) return;
+    T *o = out + row0 * p.ldo + f;
+    if (none) {
+        T *z = p.z != nullptr ? static_cast<T *>(p.z) + row0 * p.ldz + f : nullptr;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < n) {
+                o[c * p.ldo] = from_f<T>(0.0f);
+                if (z != nullptr) z[c * p.ldz] = from_f<T>(0.0f);
+            }
+        return;
+    }
+    T r[16];
+    const bool res = p.residual != nullptr;
+    if (res) {
+        const T *rp = static_cast<const T *>(p.residual) + row0 * p.ldr + f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < n) r[c] = rp[c * p.ldr];
+    }
+    float v[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = acc[c] + bias;
+    if (p.z != nullptr) {
+        T *z = static_cast<T *>(p.z) + row0 * p.ldz + f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < n) z[c * p.ldz] = from_f<T>(v[c]);
+    }
+    lt::with_activation(p.act, [&](auto a) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] = lt::activate<decltype(a)::value, EXACT>(v[c]);
+    });
+    if (res) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < n) v[c] += to_f(r[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+        if (c < n) o[c * p.ldo] = from_f<T>(v[c]);
+}
+
+// A persistent grid of CTA pairs (CG = 2, tiles of 256 features) or of
+// clusters of `splits` CTAs (CG = 1, 128 features, the K of a tile shared
+// out).  Per CTA, warp 8 issues the tensor copies into a ring of stages, one
+// K tile of P and Q each, warp 9 issues the products (in a pair, CTA 0's for
+// both), warps 0-7 drain the accumulators, of which tensor memory holds two
+// sets, while the next tile (FP32: the next block of K) is multiplied.
+//
+// Barriers: full[s] (of CTA 0 in a pair) completes when the copies of stage s
+// have landed; empty[s] when the products reading it are done; acc_full[b]
+// when accumulator set b is complete; acc_empty[b] (CTA 0) when all warps
+// have read it; tail: see below; part_ready, part_read: the splits' hand-over.
+//
+// K_BY_EXPERT: the last K tile of an expert also holds rows of the next one.
+// It is copied on a barrier of its own, the copying warp clears those rows in
+// both operands (a NaN times 0 would be one) and then reports the stage full.
+template <int CG, typename T>
+__global__ void __launch_bounds__(THREADS, 1)
+product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
+    constexpr bool F32 = std::is_same<T, float>::value;
+    constexpr bool BF16 = !std::is_same<T, __half>::value;  // FP32's pieces are bf16
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t tail_bar, part_ready, part_read;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t sbase = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *sgen = smem_raw + (sbase - tc::smem_u32(smem_raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int S = CG == 1 ? p.splits : 1;
+    const int cluster = CG == 2 ? 2 : S;
+    const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
+    const uint32_t lead = CG == 2 ? 0 : rank;
+    float *partial = reinterpret_cast<float *>(sgen + static_cast<size_t>(p.stages) * p.stage_bytes);
+    int *tables = reinterpret_cast<int *>(partial + (S > 1 ? p.bt * PROWS : 0));
+    const Tables tb{tables, tables + p.E + 2};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            tc::mbar_init(tc::smem_u32(&full_bar[s]), CG);
+            tc::mbar_init(tc::smem_u32(&empty_bar[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(tc::smem_u32(&acc_full[b]), 1);
+            tc::mbar_init(tc::smem_u32(&acc_empty[b]), CG * EPI_WARPS);
+        }
+        tc::mbar_init(tc::smem_u32(&tail_bar), 1);
+        tc::mbar_init(tc::smem_u32(&part_ready), S);
+        tc::mbar_init(tc::smem_u32(&part_read), S);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        tc::tma_prefetch(&maps.p);
+        tc::tma_prefetch(&maps.q);
+    }
+    if (warp == MMA_WARP) tc::tmem_alloc<CG, TMEM_COLS>(tc::smem_u32(&tmem_slot));
+    tc::grid_wait();  // nothing of global memory is touched before the earlier kernels are done
+    int tiles = p.nt * p.nf;
+    if (p.mode != DENSE) {
+        // clamp: non-decreasing and inside the rows, whatever the offsets hold
+        const int rows = p.mode == ROWS_BY_EXPERT ? p.T : p.K;
+        if (warp == 0) {
+            int high = 0, tile0 = 0;
+            for (int e0 = 0; e0 < p.E + 2; e0 += 32) {
+                const int e = e0 + lane;
+                int b = e <= p.E ? min(max(p.offsets[e], 0), rows) : rows;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, b, d);
+                    if (lane >= d) b = max(b, o);
+                }
+                b = max(b, high);
+                if (e < p.E + 2) tables[e] = b;
+                high = __shfl_sync(0xffffffffu, b, 31);
+            }
+            __syncwarp();
+            if (p.mode == ROWS_BY_EXPERT)
+                for (int e0 = 0; e0 < p.E + 2; e0 += 32) {
+                    const int e = e0 + lane;
+                    const int n = e <= p.E ? (tables[e + 1] - tables[e] + p.bt - 1) / p.bt * p.nf : 0;
+                    int sum = n;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, sum, d);
+                        if (lane >= d) sum += o;
+                    }
+                    if (e < p.E + 2) tables[p.E + 2 + e] = tile0 + sum - n;
+                    tile0 += __shfl_sync(0xffffffffu, sum, 31);
+                }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // the barriers of all CTAs exist before any remote arrive or copy
+    tc::fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (p.mode == ROWS_BY_EXPERT)
+        tiles = tb.first[p.E + 1];
+    else if (p.mode == K_BY_EXPERT)
+        tiles *= p.E;
+    tc::Waiter waiter(p.timeout_flag);
+
+    // Stages of a tile: (piece pair, K tile) in order.  FP32 runs each block of
+    // KBLK tiles through the six pairs.
+    const int q_rows = p.bt / CG;
+    if (warp == COPY_WARP) {
+        const uint32_t full0 = tc::peer_addr(tc::smem_u32(&full_bar[0]), lead);
+        const uint32_t my_tail = tc::peer_addr(tc::smem_u32(&tail_bar), rank);
+        uint32_t it = 0, tails = 0;
+        for (int idx = unit; idx < tiles; idx += units) {
+            const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+            const int f0 = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS;
+            const int tq = w.t0 + static_cast<int>(CG == 2 ? rank : 0) * q_rows;
+            const int z_p = p.mode == ROWS_BY_EXPERT ? w.e : 0;
+            const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
+            for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0) {
+                const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
+                for (int pair = 0; pair < (F32 ? PAIRS : 1); ++pair) {
+                    const int zp = z_p + (F32 ? p_piece(pair) * z_planes : 0), zq = F32 ? q_piece(pair) : 0;
+                    for (int kt = kb; kt < ke; ++kt, ++it) {
+                        const uint32_t s = it % p.stages;
+                        const uint32_t st = sbase + s * p.stage_bytes;
+                        const int k_left = w.k_rows - kt * BK;  // of this expert
+                        const bool tail = p.mode == K_BY_EXPERT && k_left < BK;
+                        if (lane == 0) {
+                            if (it >= static_cast<uint32_t>(p.stages))
+                                waiter.wait(tc::smem_u32(&empty_bar[s]), ((it / p.stages) - 1) & 1);
+                            const uint32_t bar = tail ? my_tail : full0 + 8u * s;
+                            tc::mbar_arrive_expect(bar, P_BYTES + p.q_bytes);
+                            const int k = w.kbase + kt * BK;
+                            if (p.p_mn) {
+                                tc::tma_load_3d<CG>(st, &maps.p, f0, k, zp, bar);
+                                tc::tma_load_3d<CG>(st + MN_BOX_BYTES, &maps.p, f0 + 64, k, zp, bar);
+                            } else {
+                                tc::tma_load_3d<CG>(st, &maps.p, k, f0, zp, bar);
+                            }
+                            if (p.q_mn) {
+                                for (int i = 0; i < q_rows; i += 64)
+                                    tc::tma_load_3d<CG>(st + P_BYTES + i / 64 * MN_BOX_BYTES, &maps.q, tq + i, k, zq, bar);
+                            } else {
+                                tc::tma_load_3d<CG>(st + P_BYTES, &maps.q, k, tq, zq, bar);
+                            }
+                        }
+                        if (tail) {  // all lanes: both operands are MN-major, a box row is one K
+                            __syncwarp();
+                            waiter.wait(tc::smem_u32(&tail_bar), tails & 1);
+                            ++tails;
+                            const int boxes = (P_BYTES + p.q_bytes) / MN_BOX_BYTES;
+                            const int chunks = (BK - k_left) * 8;  // 16-byte chunks to clear in each box
+                            uint8_t *sg = sgen + static_cast<size_t>(s) * p.stage_bytes + k_left * 128;
+                            for (int b = 0; b < boxes; ++b)
+                                for (int i = lane; i < chunks; i += 32)
+                                    *reinterpret_cast<uint4 *>(sg + b * MN_BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(full0 + 8u * s);
+                        }
+                    }
+                }
+            }
+        }
+        // this CTA's last copies are read before it can exit
+        if (lane == 0)
+            for (uint32_t j = it > static_cast<uint32_t>(p.stages) ? it - p.stages : 0; j < it; ++j)
+                waiter.wait(tc::smem_u32(&empty_bar[j % p.stages]), (j / p.stages) & 1);
+    } else if (warp == MMA_WARP) {
+        if (rank == lead && lane == 0) {
+            const uint32_t idesc = tc::instr_desc_f16(BF16, p.p_mn != 0, p.q_mn != 0, PROWS * CG, p.bt);
+            const uint32_t p_step = p.p_mn ? 2048u : 32u, q_step = p.q_mn ? 2048u : 32u;  // bytes per 16 K
+            uint32_t it = 0, g = 0;
+            for (int idx = unit; idx < tiles; idx += units) {
+                const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+                for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0, ++g) {
+                    const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
+                    const uint32_t set = g & 1;
+                    if (g >= 2) waiter.wait(tc::smem_u32(&acc_empty[set]), ((g / 2) - 1) & 1);
+                    tc::fence_after();
+                    const uint32_t d = tmem + set * (TMEM_COLS / 2);
+                    uint32_t more = 0;
+                    const int steps = (F32 ? PAIRS : 1) * (ke - kb);
+                    for (int i = 0; i < steps; ++i, ++it) {
+                        const uint32_t s = it % p.stages;
+                        waiter.wait(tc::smem_u32(&full_bar[s]), (it / p.stages) & 1);
+                        tc::fence_after();
+                        const uint32_t st = sbase + s * p.stage_bytes;
+                        const uint64_t ad = tc::smem_desc(st, p.p_mn ? MN_BOX_BYTES : 16);
+                        const uint64_t bd = tc::smem_desc(st + P_BYTES, p.q_mn ? MN_BOX_BYTES : 16);
+#pragma unroll
+                        for (int j = 0; j < BK / 16; ++j) {
+                            tc::umma_f16<CG>(d, ad + ((j * p_step) >> 4), bd + ((j * q_step) >> 4), idesc, more);
+                            more = 1;
+                        }
+                        tc::umma_commit<CG>(tc::smem_u32(&empty_bar[s]));
+                    }
+                    tc::umma_commit<CG>(tc::smem_u32(&acc_full[set]));
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3, h = warp >> 2;
+        const int half = p.bt >= 32 ? p.bt / 2 : 16;
+        const int col0 = h * half;                  // this warp's columns: [col0, col0 + cols)
+        const int cols = min(half, p.bt - col0);
+        const uint32_t t_off = (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(col0);
+        const uint32_t acc_empty0 = tc::peer_addr(tc::smem_u32(&acc_empty[0]), lead);
+        uint32_t g = 0, handed = 0;
+        for (int idx = unit; idx < tiles; idx += units) {
+            const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+            const int fl = 32 * q + lane;           // feature within the CTA's 128
+            const int f = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS + fl;
+            T *out = static_cast<T *>(p.out) + (p.mode == K_BY_EXPERT ? w.e * p.out_expert : 0);
+            const int n_tile = min(p.bt, w.t_end - w.t0);
+            const bool f_ok = f < p.F;
+            float bias = 0.0f;
+            if (p.bias != nullptr && f_ok && !w.none)
+                bias = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + f]);
+            const bool any = w.k1 > w.k0;
+            float total[F32 ? 128 : 1];
+            if constexpr (F32) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) total[c] = 0.0f;
+                for (int kb = w.k0; kb < w.k1; kb += KBLK, ++g) {
+                    const uint32_t set = g & 1;
+                    waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                    __syncwarp();
+                    tc::fence_after();
+                    const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 16)
+                        if (c < cols) {
+                            float v[16];
+                            tc::tmem_ld16(t_set + c, v);
+                            tc::tmem_ld_wait(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) total[c + i] += v[i];
+                        }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(acc_empty0 + 8u * set);
+                }
+            }
+            const uint32_t set = g & 1;
+            if (!F32 && any) {
+                waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                __syncwarp();
+                tc::fence_after();
+            }
+            const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
+            if (S > 1 && !w.none) {
+                // hand this CTA's part over: wait until the last one is read, store, tell all
+                if (handed > 0) waiter.wait(tc::smem_u32(&part_read), (handed - 1) & 1);
+#pragma unroll
+                for (int c = 0; c < 128; c += 16)
+                    if (c < cols) {
+                        float v[16];
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = total[c + i];
+                        } else if (any) {
+                            tc::tmem_ld16(t_set + c, v);
+                            tc::tmem_ld_wait(v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) partial[(col0 + c + i) * PROWS + fl] = v[i];
+                    }
+                asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; c += 16)
+                    if (c < cols) {
+                        float v[16];
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = total[c + i];
+                        } else if (any) {
+                            tc::tmem_ld16(t_set + c, v);
+                            tc::tmem_ld_wait(v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        }
+                        if (f_ok && (S == 1 || rank == 0))
+                            finish16<T>(v, p, bias, f, static_cast<long long>(w.t0) + col0 + c,
+                                        n_tile - (col0 + c), out, w.none);
+                    }
+            }
+            if (!F32 && any) {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(acc_empty0 + 8u * set);
+                ++g;
+            }
+            if (S > 1 && !w.none) {
+                epi_bar();
+                if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_ready), threadIdx.x));
+                waiter.wait(tc::smem_u32(&part_ready), handed & 1);
+                // the parts' sum in rank order, 32 features of a token per warp, shared out over all CTAs
+                const uint32_t mine = tc::smem_u32(partial);
+                const int fb = w.ft * PROWS;
+                for (int i = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i < n_tile * PROWS; i += S * EPI_THREADS) {
+                    float sum = 0.0f;
+                    for (int s = 0; s < S; ++s) sum += tc::ld_cluster_f32(tc::peer_addr(mine + 4u * i, s));
+                    const int fi = fb + (i & (PROWS - 1));
+                    if (fi < p.F) {
+                        float b = 0.0f;
+                        if (p.bias != nullptr)
+                            b = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + fi]);
+                        const long long row = static_cast<long long>(w.t0) + i / PROWS;
+                        float v = sum + b;
+                        if (p.z != nullptr) static_cast<T *>(p.z)[row * p.ldz + fi] = from_f<T>(v);
+                        lt::with_activation(p.act, [&](auto a) { v = lt::activate<decltype(a)::value, F32>(v); });
+                        if (p.residual != nullptr) v += to_f(static_cast<const T *>(p.residual)[row * p.ldr + fi]);
+                        out[row * p.ldo + fi] = from_f<T>(v);
+                    }
+                }
+                epi_bar();
+                if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_read), threadIdx.x));
+                ++handed;
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();  // no remote arrive and no read of this CTA's memory is still pending
+    if (warp == MMA_WARP) tc::tmem_free<CG, TMEM_COLS>(tmem);
+}
+
+__device__ unsigned g_linear_timeout;
+
+// ---- host: set-up ----------------------------------------------------------------
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn found = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            found = reinterpret_cast<EncodeTiledFn>(fn);
+        else
+            (void)cudaGetLastError();
+    });
+    return found;
+}
+
+struct Device {
+    int state = 0;  // 0 not set up, 1 ready, < 0 a status
+    unsigned long long ctx = 0;
+    int sms = 0, pairs = 0;
+    unsigned *timeout_flag = nullptr;
+};
+std::mutex g_mutex;
+Device g_devices[64];
+
+template <int CG, typename T>
+bool opt_in() {
+    return cudaFuncSetAttribute(product_kernel<CG, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) ==
+           cudaSuccess;
+}
+
+int set_up(Device *out) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_DEVICE;
+    }
+    if (dev < 0 || dev >= 64) return SGEMM_ERR_DEVICE;
+    unsigned long long ctx = 0;
+    const bool known = sg_ctx::current_id(dev, &ctx);
+    std::lock_guard<std::mutex> lock(g_mutex);
+    Device &d = g_devices[dev];
+    if (known && d.state != 0 && d.ctx != ctx) d.state = 0;  // a new context
+    if (d.state == 0) {
+        d.ctx = ctx;
+        int major = 0, minor = 0;
+        int st = SGEMM_OK;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10 ||
+            minor != 3 || d.sms < 2 || encode_fn() == nullptr || !opt_in<1, float>() || !opt_in<2, float>() ||
+            !opt_in<1, __nv_bfloat16>() || !opt_in<2, __nv_bfloat16>() || !opt_in<1, __half>() ||
+            !opt_in<2, __half>() ||
+            cudaGetSymbolAddress(reinterpret_cast<void **>(&d.timeout_flag), g_linear_timeout) != cudaSuccess)
+            st = SGEMM_ERR_DEVICE;
+        d.pairs = d.sms / 2;
+        if (st == SGEMM_OK) {
+            cudaLaunchConfig_t cfg;
+            memset(&cfg, 0, sizeof cfg);
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(2 * d.pairs));
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = SMEM_MAX - 1024;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, product_kernel<2, __nv_bfloat16>, &cfg) == cudaSuccess && n > 0)
+                d.pairs = n < d.pairs ? n : d.pairs;
+        }
+        (void)cudaGetLastError();
+        d.state = st == SGEMM_OK ? 1 : st;
+    }
+    *out = d;
+    return d.state > 0 ? SGEMM_OK : d.state;
+}
+
+// ---- host: one product --------------------------------------------------------------
+// An operand as the tensor copies see it: `outer` rows of `inner` 16-bit
+// values, `planes` of them.
+struct Operand {
+    const void *base = nullptr;
+    long long inner = 0, outer = 0, planes = 1;
+    long long ld = 0, plane = 0;  // elements
+    bool mn = false;              // inner runs along the operand's rows (else along K)
+};
+
+bool encode(CUtensorMap &map, const Operand &o, bool f16, int box_outer) {
+    const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.outer),
+                               static_cast<cuuint64_t>(o.planes)};
+    const long long plane = o.planes > 1 ? o.plane : o.ld * o.outer;
+    const cuuint64_t stride[2] = {static_cast<cuuint64_t>(o.ld) * 2, static_cast<cuuint64_t>(plane) * 2};
+    const cuuint32_t box[3] = {BK, static_cast<cuuint32_t>(box_outer), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encode_fn()(&map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                       const_cast<void *>(o.base), dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int cg = 2, bt = 256, splits = 1, units = 1;
+    double cost = 1e300;
+};
+
+// LINEAR_TUNE="cg=1|2,bt=16..256,splits=1..8", read once at the first call,
+// limits the plans of every product to those values, for sweeps without a
+// rebuild (a limit that leaves no plan is not applied).  It changes how the
+// work is split, not what is computed.
+struct Tune {
+    int cg = 0, bt = 0, splits = 0;
+};
+const Tune &tune() {
+    static const Tune t = [] {
+        Tune r;
+        const char *env = std::getenv("LINEAR_TUNE");
+        while (env != nullptr && *env != 0) {
+            if (strncmp(env, "cg=", 3) == 0) r.cg = std::atoi(env + 3);
+            if (strncmp(env, "bt=", 3) == 0) r.bt = std::atoi(env + 3);
+            if (strncmp(env, "splits=", 7) == 0) r.splits = std::atoi(env + 7);
+            const char *next = strchr(env, ',');
+            env = next != nullptr ? next + 1 : nullptr;
+        }
+        return r;
+    }();
+    return t;
+}
+
+// Time of a plan in SM clocks, by what bounds a K tile of a CTA: the tensor
+// cores (128 x bt/CG x 16 in bt/2/CG... clocks, four per tile) or the bytes
+// it copies.  Only the order of the results matters.
+Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
+    const double copy_rate = 40.0;  // bytes per clock and SM from L2 with all SMs copying
+    const int passes = type == LINEAR_F32 ? PAIRS : 1;
+    Plan best;
+    const int bts[] = {256, 224, 192, 160, 128, 96, 64, 32, 16};
+    for (int cg = 2; cg >= 1; --cg)
+        for (int bt : bts) {
+            if (cg == 2 && (bt < 64 || bt % 32 != 0)) continue;
+            if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
+            if (p.q_mn && bt / cg % 64 != 0) continue;
+            const int smem_q = bt / cg * 128;
+            double nt, ktiles = (p.K + BK - 1) / BK;
+            if (p.mode == ROWS_BY_EXPERT) {
+                // the host does not know the counts: as if the rows were spread evenly
+                const double met = p.E < p.T ? p.E : p.T;
+                const double each = met > 0 ? p.T / met : 0;
+                nt = met * (each <= bt ? 1.0 : each / bt + 0.5);
+            } else {
+                nt = (p.T + bt - 1) / bt;
+                if (p.mode == K_BY_EXPERT) {
+                    nt *= p.E;
+                    ktiles = (p.K / (p.E > 0 ? p.E : 1) + BK - 1) / BK + 0.5;
+                }
+            }
+            const double tiles = nt * ((p.F + PROWS * cg - 1) / (PROWS * cg));
+            const double mma = 4.0 * (bt / 2 > 32 ? bt / 2 : 32);  // 128 (256 as a pair) x bt x 64
+            const double copy = (P_BYTES + smem_q) / copy_rate;
+            const double per = passes * (mma > copy ? mma : copy);
+            const double drain = 1000.0 + 10.0 * bt;
+            const int most = cg == 2 || bt > 128 ? 1 : 8;
+            for (int s = 1; s <= most; ++s) {
+                if (s > 1 && s * 2 > ktiles) break;
+                if (only.splits != 0 && only.splits != s) continue;
+                const int units = cg == 2 ? d.pairs : d.sms / s;
+                const double waves = static_cast<double>(static_cast<long long>(tiles + units - 1) / units);
+                const double body = ktiles / s * per + 200.0;
+                const double cost = (waves < 1 ? 1 : waves) * (body > drain ? body : drain) + drain + (s > 1 ? 1500.0 : 0.0) + 1500.0;
+                if (cost < best.cost * 0.98) {
+                    best.cost = cost;
+                    best.cg = cg;
+                    best.bt = bt;
+                    best.splits = s;
+                    best.units = units;
+                }
+            }
+        }
+    return best;
+}
+
+template <int CG, typename T>
+cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG == 2 ? 2 : static_cast<unsigned>(p.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, product_kernel<CG, T>, maps, p);
+}
+
+// Enqueue one product: P and Q as 16-bit operands (FP32: three planes each).
+int run_product(int type, Product p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream) {
+    if (p.T == 0 || p.F == 0 || (p.mode == K_BY_EXPERT && p.E == 0)) return SGEMM_OK;
+    p.p_mn = P.mn;
+    p.q_mn = Q.mn;
+    p.timeout_flag = d.timeout_flag;
+    Plan pl = choose(p, d, type, tune());
+    if (pl.cost > 1e299) pl = choose(p, d, type, Tune());
+    p.bt = pl.bt;
+    p.splits = pl.splits;
+    p.q_bytes = p.bt / pl.cg * 128;
+    p.stage_bytes = P_BYTES + p.q_bytes;
+    const int per_unit = PROWS * pl.cg;
+    p.nf = (p.F + per_unit - 1) / per_unit;
+    p.nt = (p.T + p.bt - 1) / p.bt;
+    long long tiles = static_cast<long long>(p.nt) * p.nf;
+    if (p.mode == ROWS_BY_EXPERT) tiles = (static_cast<long long>(p.nt) + p.E + 1) * p.nf;  // at most
+    if (p.mode == K_BY_EXPERT) tiles *= p.E;
+    if (tiles > INT_MAX / 2) return SGEMM_ERR_INVALID_DIM;
+    const int tables = p.mode == DENSE ? 0 : 2 * (p.E + 2) * 4;
+    const int part = p.splits > 1 ? p.bt * PROWS * 4 : 0;
+    p.stages = (SMEM_MAX - 2048 - tables - part) / p.stage_bytes;
+    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
+    Maps maps;
+    memset(&maps, 0, sizeof maps);
+    const bool f16 = type == LINEAR_F16;
+    if (p.K > 0 && (!encode(maps.p, P, f16, P.mn ? BK : PROWS) || !encode(maps.q, Q, f16, Q.mn ? BK : p.bt / pl.cg)))
+        return SGEMM_ERR_DEVICE;
+    const int units = static_cast<int>(tiles < pl.units ? tiles : pl.units);
+    const int grid = units * (pl.cg == 2 ? 2 : p.splits);
+    sg_nvtx::Range r("linear: product");
+    cudaError_t err;
+    if (pl.cg == 2)
+        err = type == LINEAR_F32    ? launch<2, float>(maps, p, grid, smem, stream)
+              : type == LINEAR_BF16 ? launch<2, __nv_bfloat16>(maps, p, grid, smem, stream)
+                                    : launch<2, __half>(maps, p, grid, smem, stream);
+    else
+        err = type == LINEAR_F32    ? launch<1, float>(maps, p, grid, smem, stream)
+              : type == LINEAR_BF16 ? launch<1, __nv_bfloat16>(maps, p, grid, smem, stream)
+                                    : launch<1, __half>(maps, p, grid, smem, stream);
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    return SGEMM_OK;
+}
+
+// ---- host: operands -------------------------------------------------------------------
+size_t up256(long long bytes) { return (static_cast<size_t>(bytes) + 255) / 256 * 256; }
+long long up8(long long n) { return (n + 7) / 8 * 8; }
+
+// A matrix (or E of them) of the call: `outer` rows of `inner` values.
+struct Matrix {
+    const void *base = nullptr;
+    long long inner = 0, outer = 0, planes = 1;
+    long long ld = 0, plane = 0;
+};
+
+// Whether the tensor copies can read it as it is: 16-bit values, 16-byte
+// aligned rows.
+bool direct(int type, const Matrix &m) {
+    return type != LINEAR_F32 && reinterpret_cast<uintptr_t>(m.base) % 16 == 0 && m.ld % 8 == 0 &&
+           (m.planes <= 1 || m.plane % 8 == 0);
+}
+long long copy_elements(const Matrix &m) { return m.planes * m.outer * up8(m.inner); }
+// Workspace of the operand: nothing, an aligned copy, or the three FP32 pieces.
+size_t operand_bytes(int type, const Matrix &m) {
+    if (m.inner <= 0 || m.outer <= 0 || m.planes <= 0 || direct(type, m)) return 0;
+    return up256(copy_elements(m) * 2 * (type == LINEAR_F32 ? 3 : 1));
+}
+// The operand, copied or split into `ws` (moved past what it takes) where needed.
+int make_operand(int type, const Matrix &m, bool mn, char *&ws, Operand *o, cudaStream_t stream) {
+    o->mn = mn;
+    o->inner = m.inner;
+    o->outer = m.outer;
+    o->planes = m.planes;
+    if (m.inner <= 0 || m.outer <= 0 || m.planes <= 0) return SGEMM_OK;
+    if (direct(type, m)) {
+        o->base = m.base;
+        o->ld = m.ld;
+        o->plane = m.plane;
+        return SGEMM_OK;
+    }
+    o->base = ws;
+    o->ld = up8(m.inner);
+    o->plane = m.outer * o->ld;
+    if (type == LINEAR_F32) o->planes *= 3;
+    const cudaError_t err = linear_prep::copy_operand(type, m.base, m.ld, m.plane, static_cast<int>(m.inner),
+                                                      static_cast<int>(m.outer), static_cast<int>(m.planes), ws, stream);
+    ws += operand_bytes(type, m);
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
+    return SGEMM_OK;
+}
+
+// ---- host: argument checks ---------------------------------------------------------------
+struct Span {
+    uintptr_t lo = 0, hi = 0;
+};
+Span span(const void *p, long long rows, long long width, long long ld, int bytes) {
+    Span s;
+    if (p == nullptr || rows <= 0 || width <= 0) return s;
+    s.lo = reinterpret_cast<uintptr_t>(p);
+    s.hi = s.lo + static_cast<uintptr_t>(((rows - 1) * ld + width) * bytes);
+    return s;
+}
+bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
+bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+long long at_least_1(long long v) { return v > 1 ? v : 1; }
+
+// Everything of a call, dense (E < 0) or by expert.
+struct Call {
+    int type, M, N, K, E;
+    const int *offsets;
+    const void *x, *w, *bias, *residual, *dy, *preact_in;
+    void *preact, *y, *dx, *dw, *dbias;
+    long long ldx, ldw, w_expert, ldr, ldz, ldy, lddy, lddx, lddw, dw_expert;
+    int w_order, act;
+    void *ws;
+    size_t ws_bytes;
+    cudaStream_t stream;
+};
+Call new_call(int type, int M, int N, int K, int E, const int *offsets) {
+    Call c;
+    memset(&c, 0, sizeof c);
+    c.type = type;
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    c.E = E;
+    c.offsets = offsets;
+    return c;
+}
+int experts(const Call &c) { return c.E < 0 ? 1 : c.E; }
+
+int check_sizes(const Call &c) {
+    if (c.type < LINEAR_F32 || c.type > LINEAR_F16 || c.act < LINEAR_ACT_NONE || c.act > LINEAR_ACT_GELU_TANH ||
+        (c.w_order != 0 && c.w_order != 1))
+        return SGEMM_ERR_INVALID_ARG;
+    if (c.M < 0 || c.N < 0 || c.K < 0 || c.E < -1 || c.E > LINEAR_MAX_EXPERTS) return SGEMM_ERR_INVALID_DIM;
+    // one coordinate past the last tile has to fit 32 bits
+    if (c.M > INT_MAX - 1024 || c.N > INT_MAX - 1024 || c.K > INT_MAX - 1024) return SGEMM_ERR_INVALID_DIM;
+    return SGEMM_OK;
+}
+bool weight_strides_bad(const Call &c, long long ld, long long expert) {
+    const long long inner = c.w_order ? c.K : c.N, outer = c.w_order ? c.N : c.K;
+    if (ld < at_least_1(inner)) return true;
+    return c.E > 1 && expert < (outer - 1) * ld + inner;
+}
+Matrix weight_matrix(const Call &c) {
+    Matrix m;
+    m.base = c.w;
+    m.inner = c.w_order ? c.K : c.N;
+    m.outer = c.w_order ? c.N : c.K;
+    m.planes = experts(c);
+    m.ld = c.ldw;
+    m.plane = c.E > 1 ? c.w_expert : m.outer * c.ldw;
+    return m;
+}
+Span weight_span(const Call &c, const void *p, long long ld, long long expert) {
+    const long long inner = c.w_order ? c.K : c.N, outer = c.w_order ? c.N : c.K;
+    Span s = span(p, outer, inner, ld, lt::type_bytes(c.type));
+    if (s.hi != 0 && c.E > 1) s.hi += static_cast<uintptr_t>((c.E - 1) * expert * lt::type_bytes(c.type));
+    if (c.E == 0) s = Span();
+    return s;
+}
+Matrix row_matrix(const void *p, int rows, int width, long long ld) {
+    Matrix m;
+    m.base = p;
+    m.inner = width;
+    m.outer = rows;
+    m.ld = ld;
+    m.plane = rows * ld;
+    return m;
+}
+
+size_t forward_bytes(const Call &c) {
+    if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.K == 0 || c.E == 0) return 0;
+    return operand_bytes(c.type, row_matrix(c.x, c.M, c.K, c.ldx)) + operand_bytes(c.type, weight_matrix(c));
+}
+
+int forward(const Call &c) {
+    int st = check_sizes(c);
+    if (st != SGEMM_OK) return st;
+    const int b = lt::type_bytes(c.type);
+    if (c.ldx < at_least_1(c.K) || weight_strides_bad(c, c.ldw, c.w_expert) || c.ldy < at_least_1(c.N) ||
+        (c.residual != nullptr && c.ldr < at_least_1(c.N)) || (c.preact != nullptr && c.ldz < at_least_1(c.N)))
+        return SGEMM_ERR_INVALID_LD;
+    if (c.M == 0 || c.N == 0) return SGEMM_OK;
+    if (c.y == nullptr || (c.E >= 0 && c.offsets == nullptr) ||
+        (c.K > 0 && c.E != 0 && (c.x == nullptr || c.w == nullptr)))
+        return SGEMM_ERR_NULL_PTR;
+    const size_t need = forward_bytes(c);
+    if (need > 0 && c.ws == nullptr) return SGEMM_ERR_NULL_PTR;
+    if (misaligned(c.x, b) || misaligned(c.w, b) || misaligned(c.bias, b) || misaligned(c.residual, b) ||
+        misaligned(c.preact, b) || misaligned(c.y, b) || misaligned(c.offsets, 4) || misaligned(c.ws, 256) ||
+        c.ws_bytes < need)
+        return SGEMM_ERR_INVALID_ARG;
+    const Span sy = span(c.y, c.M, c.N, c.ldy, b), sz = span(c.preact, c.M, c.N, c.ldz, b),
+               sr = span(c.residual, c.M, c.N, c.ldr, b), sws{reinterpret_cast<uintptr_t>(c.ws),
+                                                              reinterpret_cast<uintptr_t>(c.ws) + need};
+    const bool in_place = c.residual == c.y && c.ldr == c.ldy;
+    const Span in[4] = {span(c.x, c.M, c.K, c.ldx, b), weight_span(c, c.w, c.ldw, c.w_expert),
+                        span(c.bias, experts(c), c.N, c.N, b), span(c.offsets, 1, c.E + 1, 1, 4)};
+    for (const Span &s : in)
+        if (overlap(sy, s) || overlap(sz, s) || overlap(sws, s)) return SGEMM_ERR_ALIAS;
+    if ((!in_place && overlap(sy, sr)) || overlap(sz, sr) || overlap(sws, sr) || overlap(sy, sz) || overlap(sws, sy) ||
+        overlap(sws, sz))
+        return SGEMM_ERR_ALIAS;
+    Device d;
+    st = set_up(&d);
+    if (st != SGEMM_OK) return st;
+    char *ws = static_cast<char *>(c.ws);
+    Operand P, Q;
+    if (c.K > 0 && c.E != 0) {
+        st = make_operand(c.type, weight_matrix(c), c.w_order == 0, ws, &P, c.stream);
+        if (st == SGEMM_OK) st = make_operand(c.type, row_matrix(c.x, c.M, c.K, c.ldx), false, ws, &Q, c.stream);
+        if (st != SGEMM_OK) return st;
+    }
+    Product p;
+    memset(&p, 0, sizeof p);
+    p.T = c.M;
+    p.F = c.N;
+    p.K = c.E == 0 ? 0 : c.K;
+    p.mode = c.E >= 0 ? ROWS_BY_EXPERT : DENSE;
+    p.E = c.E > 0 ? c.E : 0;
+    p.offsets = c.offsets;
+    p.bias = c.bias;
+    p.residual = c.residual;
+    p.z = c.preact;
+    p.out = c.y;
+    p.ldr = c.ldr;
+    p.ldz = c.ldz;
+    p.ldo = c.ldy;
+    p.act = c.act;
+    return run_product(c.type, p, P, Q, d, c.stream);
+}
+
+struct Wanted {
+    bool dx, dw, dbias;
+};
+// dz is a matrix of its own unless it is dy and the tensor copies can read that.
+bool dz_is_dy(const Call &c) {
+    return c.act == LINEAR_ACT_NONE && direct(c.type, row_matrix(c.dy, c.M, c.N, c.lddy));
+}
+struct BackwardBytes {
+    size_t dz, x, w, sums, total;
+};
+BackwardBytes backward_bytes(const Call &c, const Wanted &want) {
+    BackwardBytes r;
+    memset(&r, 0, sizeof r);
+    if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.E == 0) return r;
+    if ((want.dx || want.dw) && c.K > 0) {
+        if (!dz_is_dy(c)) r.dz = up256(c.M * up8(c.N) * 2 * (c.type == LINEAR_F32 ? 3 : 1));
+        if (want.dw) r.x = operand_bytes(c.type, row_matrix(c.x, c.M, c.K, c.ldx));
+        if (want.dx) r.w = operand_bytes(c.type, weight_matrix(c));
+    }
+    if (want.dbias) r.sums = up256(linear_prep::sums_bytes(c.M, c.N, experts(c)));
+    r.total = r.dz + r.x + r.w + r.sums;
+    return r;
+}
+
+int backward(const Call &c) {
+    int st = check_sizes(c);
+    if (st != SGEMM_OK) return st;
+    const int b = lt::type_bytes(c.type);
+    const Wanted want{c.dx != nullptr, c.dw != nullptr, c.dbias != nullptr};
+    if (c.lddy < at_least_1(c.N) || (want.dw && c.ldx < at_least_1(c.K)) ||
+        (want.dx && (weight_strides_bad(c, c.ldw, c.w_expert) || c.lddx < at_least_1(c.K))) ||
+        (want.dw && weight_strides_bad(c, c.lddw, c.dw_expert)) ||
+        (c.act != LINEAR_ACT_NONE && c.ldz < at_least_1(c.N)))
+        return SGEMM_ERR_INVALID_LD;
+    if ((c.preact_in != nullptr) != (c.act != LINEAR_ACT_NONE) && c.M > 0 && c.N > 0) return SGEMM_ERR_INVALID_ARG;
+    if (!want.dx && !want.dw && !want.dbias) return SGEMM_OK;
+    if (c.M > 0 && c.N > 0) {
+        if (c.dy == nullptr || (c.E >= 0 && c.offsets == nullptr) ||
+            (c.K > 0 && c.E != 0 && ((want.dw && c.x == nullptr) || (want.dx && c.w == nullptr))))
+            return SGEMM_ERR_NULL_PTR;
+    }
+    const BackwardBytes need = backward_bytes(c, want);
+    if (need.total > 0 && c.ws == nullptr) return SGEMM_ERR_NULL_PTR;
+    if (misaligned(c.dy, b) || misaligned(c.x, b) || misaligned(c.w, b) || misaligned(c.preact_in, b) ||
+        misaligned(c.dx, b) || misaligned(c.dw, b) || misaligned(c.dbias, b) || misaligned(c.offsets, 4) ||
+        misaligned(c.ws, 256) || c.ws_bytes < need.total)
+        return SGEMM_ERR_INVALID_ARG;
+    const Span in[5] = {span(c.dy, c.M, c.N, c.lddy, b),
+                        want.dw ? span(c.x, c.M, c.K, c.ldx, b) : Span(),
+                        want.dx ? weight_span(c, c.w, c.ldw, c.w_expert) : Span(),
+                        span(c.preact_in, c.M, c.N, c.ldz, b), span(c.offsets, 1, c.E + 1, 1, 4)};
+    const Span out[4] = {span(c.dx, c.M, c.K, c.lddx, b), weight_span(c, c.dw, c.lddw, c.dw_expert),
+                         span(c.dbias, experts(c), c.N, c.N, b),
+                         {reinterpret_cast<uintptr_t>(c.ws), reinterpret_cast<uintptr_t>(c.ws) + need.total}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span &s : in)
+            if (overlap(out[i], s)) return SGEMM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return SGEMM_ERR_ALIAS;
+    }
+    Device d;
+    st = set_up(&d);
+    if (st != SGEMM_OK) return st;
+    char *ws = static_cast<char *>(c.ws);
+    const bool products = (want.dx || want.dw) && c.K > 0;
+    const bool empty = c.M == 0 || c.N == 0 || c.E == 0;
+    // dz and the column sums
+    Operand dz;  // M rows of N
+    dz.inner = c.N;
+    dz.outer = c.M;
+    if (!empty) {
+        const bool make = products && !dz_is_dy(c);
+        if (dz_is_dy(c)) {
+            dz.base = c.dy;
+            dz.ld = c.lddy;
+        } else {
+            dz.base = ws;
+            dz.ld = up8(c.N);
+            dz.plane = c.M * dz.ld;
+            if (c.type == LINEAR_F32) dz.planes = 3;
+        }
+        void *sums = ws + need.dz;
+        const cudaError_t err = linear_prep::activation_gradient(
+            c.type, c.act, c.M, c.N, c.E, c.offsets, c.dy, c.lddy, c.preact_in, c.ldz, make ? ws : nullptr, dz.ld,
+            want.dbias ? sums : nullptr, c.dbias, c.stream);
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SGEMM_ERR_LAUNCH;
+        }
+        ws += need.dz + need.sums;
+    } else if (want.dbias && c.N > 0) {
+        if (cudaMemsetAsync(c.dbias, 0, static_cast<size_t>(experts(c)) * c.N * b, c.stream) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SGEMM_ERR_LAUNCH;
+        }
+    }
+    if (!products) return SGEMM_OK;
+    Product p;
+    memset(&p, 0, sizeof p);
+    p.offsets = c.offsets;
+    p.E = c.E > 0 ? c.E : 0;
+    if (want.dx && c.M > 0) {
+        Operand P, Q = dz;
+        if (!empty) {
+            st = make_operand(c.type, weight_matrix(c), c.w_order == 1, ws, &P, c.stream);
+            if (st != SGEMM_OK) return st;
+        }
+        Q.mn = false;
+        p.T = c.M;
+        p.F = c.K;
+        p.K = empty ? 0 : c.N;
+        p.mode = c.E >= 0 && !empty ? ROWS_BY_EXPERT : DENSE;
+        p.out = c.dx;
+        p.ldo = c.lddx;
+        st = run_product(c.type, p, P, Q, d, c.stream);
+        if (st != SGEMM_OK) return st;
+    }
+    if (want.dw && c.N > 0 && c.E != 0) {
+        Operand X, Z = dz;
+        if (!empty) {
+            st = make_operand(c.type, row_matrix(c.x, c.M, c.K, c.ldx), true, ws, &X, c.stream);
+            if (st != SGEMM_OK) return st;
+        }
+        X.mn = Z.mn = true;
+        // rows of dw in memory: K of N (order 0) or N of K (order 1)
+        p.T = c.w_order ? c.N : c.K;
+        p.F = c.w_order ? c.K : c.N;
+        p.K = empty ? 0 : c.M;
+        p.mode = c.E >= 0 && !empty ? K_BY_EXPERT : DENSE;
+        p.out = c.dw;
+        p.ldo = c.lddw;
+        p.out_expert = c.E > 1 ? c.dw_expert : 0;
+        if (empty && c.E > 1) {  // no rows: every expert's is zero
+            for (int e = 0; e < c.E; ++e) {
+                Product q = p;
+                q.out = static_cast<char *>(c.dw) + static_cast<long long>(e) * c.dw_expert * b;
+                st = run_product(c.type, q, X, Z, d, c.stream);
+                if (st != SGEMM_OK) return st;
+            }
+            return SGEMM_OK;
+        }
+        st = run_product(c.type, p, c.w_order ? X : Z, c.w_order ? Z : X, d, c.stream);
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" int linear_forward(int type, int M, int N, int K, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                              int w_order, const void *bias, const void *residual, int64_t ldr, int activation,
+                              void *preact, int64_t ldz, void *y, int64_t ldy, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    Call c = new_call(type, M, N, K, -1, nullptr);
+    c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_order = w_order, c.bias = bias, c.residual = residual, c.ldr = ldr;
+    c.act = activation, c.preact = preact, c.ldz = ldz, c.y = y, c.ldy = ldy;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.stream = stream;
+    return forward(c);
+}
+
+extern "C" size_t linear_forward_workspace_size(int type, int M, int N, int K, const void *x, int64_t ldx,
+                                                const void *w, int64_t ldw, int w_order) {
+    Call c = new_call(type, M, N, K, -1, nullptr);
+    c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_order = w_order;
+    return forward_bytes(c);
+}
+
+extern "C" int expert_linear_forward(int type, int R, int N, int K, int E, const int *offsets, const void *x,
+                                     int64_t ldx, const void *w, int64_t ldw, int64_t w_expert, int w_order,
+                                     const void *bias, const void *residual, int64_t ldr, int activation,
+                                     void *preact, int64_t ldz, void *y, int64_t ldy, void *workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+    if (E < 0) return SGEMM_ERR_INVALID_DIM;
+    Call c = new_call(type, R, N, K, E, offsets);
+    c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_expert = w_expert, c.w_order = w_order, c.bias = bias;
+    c.residual = residual, c.ldr = ldr, c.act = activation, c.preact = preact, c.ldz = ldz, c.y = y, c.ldy = ldy;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.stream = stream;
+    return forward(c);
+}
+
+extern "C" size_t expert_linear_forward_workspace_size(int type, int R, int N, int K, int E, const void *x,
+                                                       int64_t ldx, const void *w, int64_t ldw, int64_t w_expert,
+                                                       int w_order) {
+    if (E < 0) return 0;
+    Call c = new_call(type, R, N, K, E, nullptr);
+    c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_expert = w_expert, c.w_order = w_order;
+    return forward_bytes(c);
+}
+
+extern "C" int linear_backward(int type, int M, int N, int K, const void *dy, int64_t lddy, const void *x,
+                               int64_t ldx, const void *w, int64_t ldw, int w_order, const void *preact, int64_t ldz,
+                               int activation, void *dx, int64_t lddx, void *dw, int64_t lddw, void *dbias,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    Call c = new_call(type, M, N, K, -1, nullptr);
+    c.dy = dy, c.lddy = lddy, c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_order = w_order;
+    c.preact_in = preact, c.ldz = ldz, c.act = activation, c.dx = dx, c.lddx = lddx, c.dw = dw, c.lddw = lddw;
+    c.dbias = dbias, c.ws = workspace, c.ws_bytes = workspace_bytes, c.stream = stream;
+    return backward(c);
+}
+
+extern "C" size_t linear_backward_workspace_size(int type, int M, int N, int K, const void *dy, int64_t lddy,
+                                                 const void *x, int64_t ldx, const void *w, int64_t ldw, int w_order,
+                                                 int activation, int want_dx, int want_dw, int want_dbias) {
+    Call c = new_call(type, M, N, K, -1, nullptr);
+    c.dy = dy, c.lddy = lddy, c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_order = w_order, c.act = activation;
+    return backward_bytes(c, Wanted{want_dx != 0, want_dw != 0, want_dbias != 0}).total;
+}
+
+extern "C" int expert_linear_backward(int type, int R, int N, int K, int E, const int *offsets, const void *dy,
+                                      int64_t lddy, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                                      int64_t w_expert, int w_order, const void *preact, int64_t ldz, int activation,
+                                      void *dx, int64_t lddx, void *dw, int64_t lddw, int64_t dw_expert, void *dbias,
+                                      void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (E < 0) return SGEMM_ERR_INVALID_DIM;
+    Call c = new_call(type, R, N, K, E, offsets);
+    c.dy = dy, c.lddy = lddy, c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_expert = w_expert, c.w_order = w_order;
+    c.preact_in = preact, c.ldz = ldz, c.act = activation, c.dx = dx, c.lddx = lddx, c.dw = dw, c.lddw = lddw;
+    c.dw_expert = dw_expert, c.dbias = dbias, c.ws = workspace, c.ws_bytes = workspace_bytes, c.stream = stream;
+    return backward(c);
+}
+
+extern "C" size_t expert_linear_backward_workspace_size(int type, int R, int N, int K, int E, const void *dy,
+                                                        int64_t lddy, const void *x, int64_t ldx, const void *w,
+                                                        int64_t ldw, int64_t w_expert, int w_order, int activation,
+                                                        int want_dx, int want_dw, int want_dbias) {
+    if (E < 0) return 0;
+    Call c = new_call(type, R, N, K, E, nullptr);
+    c.dy = dy, c.lddy = lddy, c.x = x, c.ldx = ldx, c.w = w, c.ldw = ldw, c.w_expert = w_expert, c.w_order = w_order;
+    c.act = activation;
+    return backward_bytes(c, Wanted{want_dx != 0, want_dw != 0, want_dbias != 0}).total;
+}
+
+extern "C" int linear_timeouts(unsigned *count) {
+    if (count == nullptr) return SGEMM_ERR_NULL_PTR;
+    if (cudaMemcpyFromSymbol(count, g_linear_timeout, sizeof(unsigned)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_DEVICE;
+    }
+    return SGEMM_OK;
+}

@@ -1,0 +1,289 @@
+// linear_prep.cu -- see linear_prep.cuh.
+#include "linear_prep.cuh"
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "linear_types.cuh"
+#include "nvtx_range.cuh"
+#include "tensor_core.cuh"
+
+namespace {
+
+using lt::from_f;
+using lt::to_f;
+
+template <typename T>
+struct alignas(sizeof(T) * 8) Vec8 {
+    T v[8];
+};
+template <typename T>
+struct alignas(16) Chunk {  // 16 bytes
+    T v[16 / sizeof(T)];
+};
+
+// x = a + b + c to 2^-27 |x|, a and b rounded to nearest; a is cut instead
+// where rounding would overflow, and carries an infinity or NaN alone.
+__device__ __forceinline__ void pieces(float x, __nv_bfloat16 &a, __nv_bfloat16 &b, __nv_bfloat16 &c) {
+    a = __float2bfloat16_rn(x);
+    const bool finite = fabsf(x) <= 3.402823466e38f;
+    if (finite && fabsf(__bfloat162float(a)) > 3.402823466e38f) a = __float2bfloat16_rz(x);
+    const float r = finite ? x - __bfloat162float(a) : 0.0f;
+    b = __float2bfloat16_rn(r);
+    c = __float2bfloat16_rn(r - __bfloat162float(b));
+}
+
+// 8 consecutive values per thread; VEC: aligned 16-byte loads.  Bound by HBM:
+// 4 bytes read and 6 written per FP32 value.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) copy_operand_kernel(const T *__restrict__ src, long long ld, long long plane,
+                                                           int inner, int outer, int planes, void *__restrict__ dst) {
+    tc::grid_trigger();  // a product may set itself up meanwhile; it waits for this grid before it reads
+    const int per_row = (inner + 7) / 8;
+    const long long units = static_cast<long long>(planes) * outer * per_row;
+    const long long piece = static_cast<long long>(planes) * outer * per_row;  // in groups of 8
+    for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < units;
+         u += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long row = u / per_row;
+        const int j = static_cast<int>(u - row * per_row) * 8;
+        const long long e = row / outer;
+        const T *s = src + e * plane + (row - e * outer) * ld + j;
+        T v[8];
+        if (VEC && j + 8 <= inner) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 16 / static_cast<int>(sizeof(T))) {
+                const Chunk<T> c = *reinterpret_cast<const Chunk<T> *>(s + i);
+#pragma unroll
+                for (int k = 0; k < 16 / static_cast<int>(sizeof(T)); ++k) v[i + k] = c.v[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = j + i < inner ? s[i] : from_f<T>(0.0f);
+        }
+        if constexpr (std::is_same<T, float>::value) {
+            Vec8<__nv_bfloat16> a, b, c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pieces(v[i], a.v[i], b.v[i], c.v[i]);
+            auto *d = static_cast<Vec8<__nv_bfloat16> *>(dst);
+            d[u] = a;
+            d[piece + u] = b;
+            d[2 * piece + u] = c;
+        } else {
+            Vec8<T> o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.v[i] = v[i];
+            static_cast<Vec8<T> *>(dst)[u] = o;
+        }
+    }
+}
+
+template <typename T>
+void copy_operand_t(const void *src, long long ld, long long plane, int inner, int outer, int planes, void *dst,
+                    cudaStream_t stream) {
+    const int n = 16 / static_cast<int>(sizeof(T));
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % n == 0 && (planes <= 1 || plane % n == 0);
+    const long long units = static_cast<long long>(planes) * outer * ((inner + 7) / 8);
+    long long blocks = (units + 255) / 256;
+    if (blocks > 152 * 64) blocks = 152 * 64;
+    const T *s = static_cast<const T *>(src);
+    if (vec)
+        copy_operand_kernel<T, true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(s, ld, plane, inner, outer, planes, dst);
+    else
+        copy_operand_kernel<T, false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(s, ld, plane, inner, outer, planes, dst);
+}
+
+// ---- dz = dy * act'(z), and its column sums -------------------------------------------
+// A block takes CHUNK rows of 32 * V columns; warp w its rows w, w + 8, ...
+// Rows of different experts are summed apart: the rows of expert e in chunk c
+// go to partial sum c + e, which no other pair of the two shares, as both only
+// grow along the rows.  A second kernel adds each expert's partial sums in
+// chunk order, so the sums do not depend on timing.
+constexpr int CHUNK = 64;
+constexpr int GWARPS = 8;
+
+// The expert of `row`: the last e with offsets[e] <= row (E: none).
+__device__ __forceinline__ int expert_of(const int *offsets, int E, int row) {
+    int lo = 0, hi = E + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (offsets[mid] <= row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(GWARPS * 32)
+activation_gradient_kernel(int M, int N, int E, const int *__restrict__ offsets, const T *__restrict__ dy,
+                           long long lddy, const T *__restrict__ z, long long ldz, void *__restrict__ dz,
+                           long long lddz, float *__restrict__ sums, int strips) {
+    constexpr bool F32 = std::is_same<T, float>::value;
+    __shared__ float part[GWARPS][32 * V];
+    tc::grid_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunk = blockIdx.x / strips, strip = blockIdx.x - chunk * strips;
+    const int col = strip * 32 * V + lane * V;
+    const int r1 = min(M, (chunk + 1) * CHUNK);
+    int row = chunk * CHUNK;
+    while (row < r1) {
+        int e = 0, end = r1;
+        if (E >= 0) {
+            e = expert_of(offsets, E, row);
+            if (e < E) end = min(r1, max(offsets[e + 1], row + 1));
+        }
+        const bool counted = E < 0 || e < E;
+        float sum[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+        if (counted && col < N)
+            for (int r = row + warp; r < end; r += GWARPS) {
+                T d[V], zz[V];
+                if constexpr (V > 1) {
+                    *reinterpret_cast<Chunk<T> *>(d) = *reinterpret_cast<const Chunk<T> *>(dy + r * lddy + col);
+                    if constexpr (ACT != LINEAR_ACT_NONE)
+                        *reinterpret_cast<Chunk<T> *>(zz) = *reinterpret_cast<const Chunk<T> *>(z + r * ldz + col);
+                } else {
+                    d[0] = dy[r * lddy + col];
+                    if constexpr (ACT != LINEAR_ACT_NONE) zz[0] = z[r * ldz + col];
+                }
+                float g[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    g[i] = to_f(d[i]);
+                    if constexpr (ACT != LINEAR_ACT_NONE) g[i] *= lt::slope<ACT, F32>(to_f(zz[i]));
+                    sum[i] += g[i];
+                }
+                if (dz != nullptr) {
+                    if constexpr (F32) {
+                        auto *o = static_cast<__nv_bfloat16 *>(dz) + r * lddz + col;
+                        const long long piece = static_cast<long long>(M) * lddz;
+                        struct alignas(2 * V) Out {
+                            __nv_bfloat16 v[V];
+                        } a, b, c;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) pieces(g[i], a.v[i], b.v[i], c.v[i]);
+                        *reinterpret_cast<Out *>(o) = a;
+                        *reinterpret_cast<Out *>(o + piece) = b;
+                        *reinterpret_cast<Out *>(o + 2 * piece) = c;
+                    } else {
+                        struct alignas(sizeof(T) * V) Out {
+                            T v[V];
+                        } a;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) a.v[i] = from_f<T>(g[i]);
+                        *reinterpret_cast<Out *>(static_cast<T *>(dz) + r * lddz + col) = a;
+                    }
+                }
+            }
+        if (sums != nullptr && counted) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) part[warp][i * 32 + lane] = sum[i];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 32 * V; i += GWARPS * 32) {
+                const int c = strip * 32 * V + (i & 31) * V + (i >> 5);
+                float t = 0.0f;
+#pragma unroll
+                for (int w = 0; w < GWARPS; ++w) t += part[w][i];
+                if (c < N) sums[static_cast<long long>(chunk + (E < 0 ? 0 : e)) * N + c] = t;
+            }
+            __syncthreads();
+        }
+        row = end;
+    }
+}
+
+// Block (32, 8) per 32 columns of an expert: warp y adds chunks y, y + 8, ...
+template <typename T>
+__global__ void __launch_bounds__(256) column_sums_kernel(int M, int N, int E, const int *__restrict__ offsets,
+                                                          const float *__restrict__ sums, T *__restrict__ dbias) {
+    __shared__ float part[8][32];
+    tc::grid_trigger();
+    const int e = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
+    int b = 0, end = M;
+    if (E >= 0) {
+        b = min(max(offsets[e], 0), M);
+        end = min(max(offsets[e + 1], b), M);
+    }
+    float t = 0.0f;
+    if (col < N && end > b)
+        for (int c = b / CHUNK + threadIdx.y; c <= (end - 1) / CHUNK; c += 8)
+            t += sums[static_cast<long long>(c + e) * N + col];
+    part[threadIdx.y][threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.y == 0 && col < N) {
+        t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += part[i][threadIdx.x];
+        dbias[static_cast<long long>(e) * N + col] = from_f<T>(t);
+    }
+}
+
+template <typename T>
+cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offsets, const void *dy, long long lddy,
+                                  const void *z, long long ldz, void *dz, long long lddz, float *sums, void *dbias,
+                                  cudaStream_t stream) {
+    if (dz == nullptr && sums == nullptr) return cudaSuccess;
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const bool vec = N % V == 0 && lddy % V == 0 && reinterpret_cast<uintptr_t>(dy) % 16 == 0 &&
+                     (act == LINEAR_ACT_NONE || (ldz % V == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0));
+    const int strip = 32 * (vec ? V : 1);
+    const int strips = (N + strip - 1) / strip;
+    const long long blocks = (static_cast<long long>(M) + CHUNK - 1) / CHUNK * strips;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    lt::with_activation(act, [&](auto a) {
+        constexpr int ACT = decltype(a)::value;
+        if (vec)
+            activation_gradient_kernel<T, V, ACT><<<grid, GWARPS * 32, 0, stream>>>(
+                M, N, E, offsets, static_cast<const T *>(dy), lddy, static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
+        else
+            activation_gradient_kernel<T, 1, ACT><<<grid, GWARPS * 32, 0, stream>>>(
+                M, N, E, offsets, static_cast<const T *>(dy), lddy, static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
+    });
+    cudaError_t err = cudaPeekAtLastError();
+    if (err == cudaSuccess && sums != nullptr) {
+        const dim3 g2(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(E < 0 ? 1 : E));
+        column_sums_kernel<T><<<g2, dim3(32, 8), 0, stream>>>(M, N, E, offsets, sums, static_cast<T *>(dbias));
+        err = cudaPeekAtLastError();
+    }
+    return err;
+}
+
+}  // namespace
+
+namespace linear_prep {
+
+cudaError_t copy_operand(int type, const void *src, long long ld, long long plane, int inner, int outer, int planes,
+                         void *dst, cudaStream_t stream) {
+    sg_nvtx::Range r("linear: operand copy");
+    if (type == LINEAR_F32)
+        copy_operand_t<float>(src, ld, plane, inner, outer, planes, dst, stream);
+    else if (type == LINEAR_BF16)
+        copy_operand_t<__nv_bfloat16>(src, ld, plane, inner, outer, planes, dst, stream);
+    else
+        copy_operand_t<__half>(src, ld, plane, inner, outer, planes, dst, stream);
+    return cudaPeekAtLastError();
+}
+
+size_t sums_bytes(int M, int N, int E) {
+    return (static_cast<size_t>((static_cast<long long>(M) + CHUNK - 1) / CHUNK) + static_cast<size_t>(E)) *
+           static_cast<size_t>(N) * sizeof(float);
+}
+
+cudaError_t activation_gradient(int type, int act, int M, int N, int E, const int *offsets, const void *dy,
+                                long long lddy, const void *z, long long ldz, void *dz, long long lddz, void *sums,
+                                void *dbias, cudaStream_t stream) {
+    sg_nvtx::Range r("linear: activation gradient");
+    float *s = static_cast<float *>(sums);
+    if (type == LINEAR_F32)
+        return activation_gradient_t<float>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
+    if (type == LINEAR_BF16)
+        return activation_gradient_t<__nv_bfloat16>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
+    return activation_gradient_t<__half>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
+}
+
+}  // namespace linear_prep

@@ -1,0 +1,95 @@
+// linear_types.cuh -- element types and activations of the layer operators.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "linear.h"
+
+namespace lt {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) {
+    return __float2half_rn(v);
+}
+
+inline int type_bytes(int type) { return type == LINEAR_F32 ? 4 : 2; }
+
+// EXACT (FP32 tensors): the library's accurate exponential and division; the
+// 16-bit types round to 8 or 11 bits afterwards, so there the fast forms (a
+// few units in the last place of FP32) change nothing that is kept.
+template <bool EXACT>
+__device__ __forceinline__ float exp_of(float x) {
+    return EXACT ? expf(x) : __expf(x);
+}
+template <bool EXACT>
+__device__ __forceinline__ float quotient(float a, float b) {
+    return EXACT ? a / b : __fdividef(a, b);
+}
+template <bool EXACT>
+__device__ __forceinline__ float logistic(float x) {
+    return quotient<EXACT>(1.0f, 1.0f + exp_of<EXACT>(-x));
+}
+constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi): (1 + tanh u) / 2 = logistic(2 u)
+constexpr float kGeluB = 0.044715f;
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == LINEAR_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+    if constexpr (ACT == LINEAR_ACT_SILU) return z * logistic<EXACT>(z);
+    if constexpr (ACT == LINEAR_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if constexpr (ACT == LINEAR_ACT_GELU_TANH) return z * logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
+    return z;
+}
+// act'(z)
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float slope(float z) {
+    if constexpr (ACT == LINEAR_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == LINEAR_ACT_SILU) {
+        const float p = logistic<EXACT>(z);
+        return p * (1.0f + z * (1.0f - p));
+    }
+    if constexpr (ACT == LINEAR_ACT_GELU)
+        return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * exp_of<EXACT>(-0.5f * z * z);
+    if constexpr (ACT == LINEAR_ACT_GELU_TANH) {
+        const float p = logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
+        return p + z * p * (1.0f - p) * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+    }
+    return 1.0f;
+}
+
+// f(std::integral_constant-like tag) for the activation `act`.
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+template <typename F>
+__host__ __device__ __forceinline__ void with_activation(int act, F &&f) {
+    switch (act) {
+        case LINEAR_ACT_RELU: f(Int<LINEAR_ACT_RELU>{}); break;
+        case LINEAR_ACT_SILU: f(Int<LINEAR_ACT_SILU>{}); break;
+        case LINEAR_ACT_GELU: f(Int<LINEAR_ACT_GELU>{}); break;
+        case LINEAR_ACT_GELU_TANH: f(Int<LINEAR_ACT_GELU_TANH>{}); break;
+        default: f(Int<LINEAR_ACT_NONE>{}); break;
+    }
+}
+
+}  // namespace lt

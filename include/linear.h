@@ -1,0 +1,187 @@
+/*
+ * linear.h -- C ABI of the layer products (libsgemm_f32.so): a matrix product
+ * with bias, activation and residual in its epilogue, the same product over
+ * rows grouped by expert, and the gradients of both, on the tensor cores of
+ * GB300 (sm_103a).
+ *
+ *     z[i][j] = sum_k x[i][k] w[k][j] + bias[j]
+ *     y[i][j] = act(z[i][j]) + residual[i][j]
+ *
+ * x is M x K, w is K x N, y is M x N; the gradients of y = act(x.w + bias) are
+ *     dz = dy * act'(z),  dx = dz.w^T,  dw = x^T.dz,  dbias[j] = sum_i dz[i][j]
+ * (the residual's gradient is dy itself).  x, y, residual, preact, dy and dx
+ * are row-major with any row stride; w (and dw, in the same order) may be
+ * held either way: w_order 0, element (k, j) at w + k*ldw + j, or w_order 1,
+ * at w + j*ldw + k (a weight held as outputs x inputs).
+ *
+ * Types: all tensors of a call have one type.  LINEAR_BF16 and LINEAR_F16
+ * multiply exactly and add in FP32; everything up to the one rounding of y
+ * (and of preact, where it is saved) is in FP32.  dz is rounded to the
+ * tensors' type before the products that use it; dbias is summed in FP32
+ * from the unrounded values.  LINEAR_F32 splits each operand into three bf16
+ * pieces (x = x1 + x2 + x3 to 2^-27) and adds the six products that matter;
+ * the tensor cores sum blocks of 128 K, which are added in FP32 with
+ * round-to-nearest: the error is that of an FP32 product.  An infinity or a
+ * NaN in an FP32 operand makes every element of the result that it enters
+ * NaN or infinite.
+ *
+ * All sums have a fixed order: a call gives the same bits every time.
+ *
+ * Conventions are those of sgemm_f32.h: arguments are checked on the host
+ * before anything is launched, work is only enqueued on `stream`, nothing is
+ * allocated, status codes are sgemm_status.  Every wait in the kernels is
+ * bounded; one that runs out leaves the result wrong and sets the flag that
+ * linear_timeouts reports.
+ */
+#ifndef LINEAR_H
+#define LINEAR_H
+
+#include <stddef.h>
+#include <stdint.h>
+#include <cuda_runtime_api.h>
+
+#include "sgemm_f32.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { LINEAR_F32 = 0, LINEAR_BF16 = 1, LINEAR_F16 = 2 } linear_type;
+
+typedef enum {
+    LINEAR_ACT_NONE = 0,
+    LINEAR_ACT_RELU = 1,
+    LINEAR_ACT_SILU = 2,      /* z / (1 + exp(-z)) */
+    LINEAR_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+    LINEAR_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} linear_activation;
+
+/* Most experts of one call. */
+#define LINEAR_MAX_EXPERTS 4096
+
+/*
+ * linear_forward -- enqueue y = act(x.w + bias) + residual.
+ *   type       : linear_type of every tensor.
+ *   M, N, K    : sizes, each >= 0.  M == 0 or N == 0 is a no-op; K == 0 gives
+ *                act(bias) + residual.
+ *   x, ldx     : M x K, ldx >= max(1, K) elements between rows.
+ *   w, ldw     : K x N by w_order; ldw >= max(1, N) (order 0) or max(1, K).
+ *   bias       : N values, or NULL.
+ *   residual   : M x N, ldr >= max(1, N), or NULL.  It may be y itself (the
+ *                same pointer and stride), not overlap it otherwise.
+ *   preact, ldz: M x N, receives z (for the backward pass), or NULL.
+ *   y, ldy     : M x N.
+ *   workspace  : DEVICE memory, 256-byte aligned, of at least
+ *                linear_forward_workspace_size bytes for the same arguments
+ *                (NULL where that is 0).  It holds 16-byte aligned copies of
+ *                operands whose rows are not, and the pieces of FP32
+ *                operands.  Calls that share one must not overlap in time.
+ * Every tensor is aligned to its element.  Nothing written may overlap
+ * anything else of the call (SGEMM_ERR_ALIAS).
+ */
+int linear_forward(int type, int M, int N, int K,
+                   const void *x, int64_t ldx,
+                   const void *w, int64_t ldw, int w_order,
+                   const void *bias,
+                   const void *residual, int64_t ldr,
+                   int activation,
+                   void *preact, int64_t ldz,
+                   void *y, int64_t ldy,
+                   void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Workspace bytes of linear_forward (the pointers are only inspected for
+ * alignment).  Host-only. */
+size_t linear_forward_workspace_size(int type, int M, int N, int K,
+                                     const void *x, int64_t ldx,
+                                     const void *w, int64_t ldw, int w_order);
+
+/*
+ * linear_backward -- enqueue the gradients of y = act(x.w + bias) + residual.
+ *   dy, lddy     : M x N, the gradient of y.
+ *   preact, ldz  : z as linear_forward saved it; NULL if and only if the
+ *                  activation is LINEAR_ACT_NONE.
+ *   dx, lddx     : M x K, or NULL (not wanted).
+ *   dw, lddw     : K x N in the order of w_order, or NULL.
+ *   dbias        : N values, or NULL.
+ * x may be NULL when dw is, w when dx is.  Sizes of zero give the empty sums
+ * (zeros).  The rest is as for linear_forward.
+ */
+int linear_backward(int type, int M, int N, int K,
+                    const void *dy, int64_t lddy,
+                    const void *x, int64_t ldx,
+                    const void *w, int64_t ldw, int w_order,
+                    const void *preact, int64_t ldz, int activation,
+                    void *dx, int64_t lddx,
+                    void *dw, int64_t lddw,
+                    void *dbias,
+                    void *workspace, size_t workspace_bytes,
+                    cudaStream_t stream);
+
+size_t linear_backward_workspace_size(int type, int M, int N, int K,
+                                      const void *dy, int64_t lddy,
+                                      const void *x, int64_t ldx,
+                                      const void *w, int64_t ldw, int w_order,
+                                      int activation, int want_dx, int want_dw, int want_dbias);
+
+/*
+ * expert_linear_forward -- the same product over rows sorted by expert:
+ * rows offsets[e] .. offsets[e+1]-1 of x meet weight and bias e.
+ *   E            : experts, 0 .. LINEAR_MAX_EXPERTS.
+ *   offsets      : E + 1 non-decreasing row numbers in DEVICE memory,
+ *                  offsets[0] = 0, offsets[E] <= R (expert_sort makes them).
+ *                  They are read on the device and clamped to 0 .. R there, so
+ *                  wrong ones give wrong rows, not wrong addresses.
+ *   R            : rows of x, residual, preact and y.  Rows offsets[E] .. R-1
+ *                  belong to no expert: their y and preact are 0.
+ *   w, ldw, w_expert : expert e's K x N weight at w + e*w_expert, by w_order.
+ *   bias         : E x N, or NULL.
+ */
+int expert_linear_forward(int type, int R, int N, int K, int E,
+                          const int *offsets,
+                          const void *x, int64_t ldx,
+                          const void *w, int64_t ldw, int64_t w_expert, int w_order,
+                          const void *bias,
+                          const void *residual, int64_t ldr,
+                          int activation,
+                          void *preact, int64_t ldz,
+                          void *y, int64_t ldy,
+                          void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+size_t expert_linear_forward_workspace_size(int type, int R, int N, int K, int E,
+                                            const void *x, int64_t ldx,
+                                            const void *w, int64_t ldw, int64_t w_expert, int w_order);
+
+/*
+ * expert_linear_backward -- its gradients: dx (R x K, 0 in the rows of no
+ * expert), dw (like w: expert e's at dw + e*dw_expert, 0 for an expert without
+ * rows) and dbias (E x N).
+ */
+int expert_linear_backward(int type, int R, int N, int K, int E,
+                           const int *offsets,
+                           const void *dy, int64_t lddy,
+                           const void *x, int64_t ldx,
+                           const void *w, int64_t ldw, int64_t w_expert, int w_order,
+                           const void *preact, int64_t ldz, int activation,
+                           void *dx, int64_t lddx,
+                           void *dw, int64_t lddw, int64_t dw_expert,
+                           void *dbias,
+                           void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+size_t expert_linear_backward_workspace_size(int type, int R, int N, int K, int E,
+                                             const void *dy, int64_t lddy,
+                                             const void *x, int64_t ldx,
+                                             const void *w, int64_t ldw, int64_t w_expert, int w_order,
+                                             int activation, int want_dx, int want_dw, int want_dbias);
+
+/* Copies into *count whether any kernel of this header on the current device
+ * gave up a wait since the library was loaded (0 = never).  Synchronous. */
+int linear_timeouts(unsigned *count);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LINEAR_H */
