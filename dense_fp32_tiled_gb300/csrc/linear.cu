@@ -307,53 +307,62 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     tc::Waiter waiter(p.timeout_flag);
 
     // Stages of a tile: (piece pair, K tile) in order.  FP32 runs each block of
-    // KBLK tiles through the six pairs.
+    // KBLK tiles through the six pairs.  One thread issues the copies and one
+    // the products, so what they run per stage is kept to the least: no
+    // divisions, the stage and its phase counted along.
     const int q_rows = p.bt / CG;
+    const uint32_t stage_bytes = p.stage_bytes;
+    const int stages = p.stages;
     if (warp == COPY_WARP) {
         const uint32_t full0 = tc::peer_addr(tc::smem_u32(&full_bar[0]), lead);
+        const uint32_t empty0 = tc::smem_u32(&empty_bar[0]);
         const uint32_t my_tail = tc::peer_addr(tc::smem_u32(&tail_bar), rank);
-        uint32_t it = 0, tails = 0;
+        const uint32_t bytes = P_BYTES + p.q_bytes;
+        const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
+        const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
+        uint32_t tails = 0, ph = 1;
+        int s = 0, issued = 0;  // stage; how many of the ring are in use, at most
         for (int idx = unit; idx < tiles; idx += units) {
             const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
             const int f0 = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS;
             const int tq = w.t0 + static_cast<int>(CG == 2 ? rank : 0) * q_rows;
             const int z_p = p.mode == ROWS_BY_EXPERT ? w.e : 0;
-            const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
+            // of K_BY_EXPERT: the K tile that also holds the next expert's rows
+            const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
             for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0) {
                 const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
                 for (int pair = 0; pair < (F32 ? PAIRS : 1); ++pair) {
                     const int zp = z_p + (F32 ? p_piece(pair) * z_planes : 0), zq = F32 ? q_piece(pair) : 0;
-                    for (int kt = kb; kt < ke; ++kt, ++it) {
-                        const uint32_t s = it % p.stages;
-                        const uint32_t st = sbase + s * p.stage_bytes;
-                        const int k_left = w.k_rows - kt * BK;  // of this expert
-                        const bool tail = p.mode == K_BY_EXPERT && k_left < BK;
-                        if (lane == 0) {
-                            if (it >= static_cast<uint32_t>(p.stages))
-                                waiter.wait(tc::smem_u32(&empty_bar[s]), ((it / p.stages) - 1) & 1);
+                    int k = w.kbase + kb * BK;
+                    for (int kt = kb; kt < ke; ++kt, k += BK) {
+                        const uint32_t st = sbase + s * stage_bytes;
+                        const bool tail = kt == tail_kt;
+                        waiter.wait(empty0 + 8u * s, ph);  // passes at once on a ring not yet used
+                        __syncwarp();
+                        if (tc::elect()) {
                             const uint32_t bar = tail ? my_tail : full0 + 8u * s;
-                            tc::mbar_arrive_expect(bar, P_BYTES + p.q_bytes);
-                            const int k = w.kbase + kt * BK;
-                            if (p.p_mn) {
+                            tc::mbar_arrive_expect(bar, bytes);
+                            if (p_mn) {
                                 tc::tma_load_3d<CG>(st, &maps.p, f0, k, zp, bar);
                                 tc::tma_load_3d<CG>(st + MN_BOX_BYTES, &maps.p, f0 + 64, k, zp, bar);
                             } else {
                                 tc::tma_load_3d<CG>(st, &maps.p, k, f0, zp, bar);
                             }
-                            if (p.q_mn) {
+                            if (q_mn) {
                                 for (int i = 0; i < q_rows; i += 64)
-                                    tc::tma_load_3d<CG>(st + P_BYTES + i / 64 * MN_BOX_BYTES, &maps.q, tq + i, k, zq, bar);
+                                    tc::tma_load_3d<CG>(st + P_BYTES + i * (MN_BOX_BYTES / 64), &maps.q, tq + i, k, zq, bar);
                             } else {
                                 tc::tma_load_3d<CG>(st + P_BYTES, &maps.q, k, tq, zq, bar);
                             }
                         }
                         if (tail) {  // all lanes: both operands are MN-major, a box row is one K
+                            const int k_left = w.k_rows - kt * BK;
                             __syncwarp();
                             waiter.wait(tc::smem_u32(&tail_bar), tails & 1);
                             ++tails;
-                            const int boxes = (P_BYTES + p.q_bytes) / MN_BOX_BYTES;
+                            const int boxes = static_cast<int>(bytes) / MN_BOX_BYTES;
                             const int chunks = (BK - k_left) * 8;  // 16-byte chunks to clear in each box
-                            uint8_t *sg = sgen + static_cast<size_t>(s) * p.stage_bytes + k_left * 128;
+                            uint8_t *sg = sgen + static_cast<size_t>(s) * stage_bytes + k_left * 128;
                             for (int b = 0; b < boxes; ++b)
                                 for (int i = lane; i < chunks; i += 32)
                                     *reinterpret_cast<uint4 *>(sg + b * MN_BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
@@ -361,44 +370,66 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             __syncwarp();
                             if (lane == 0) tc::mbar_arrive(full0 + 8u * s);
                         }
+                        __syncwarp();
+                        issued = min(issued + 1, stages);
+                        if (++s == stages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
                 }
             }
         }
         // this CTA's last copies are read before it can exit
-        if (lane == 0)
-            for (uint32_t j = it > static_cast<uint32_t>(p.stages) ? it - p.stages : 0; j < it; ++j)
-                waiter.wait(tc::smem_u32(&empty_bar[j % p.stages]), (j / p.stages) & 1);
+        for (; issued > 0; --issued) {
+            if (s == 0) {
+                s = stages;
+                ph ^= 1;
+            }
+            --s;
+            waiter.wait(empty0 + 8u * s, ph ^ 1);
+        }
     } else if (warp == MMA_WARP) {
-        if (rank == lead && lane == 0) {
+        if (rank == lead) {
             const uint32_t idesc = tc::instr_desc_f16(BF16, p.p_mn != 0, p.q_mn != 0, PROWS * CG, p.bt);
-            const uint32_t p_step = p.p_mn ? 2048u : 32u, q_step = p.q_mn ? 2048u : 32u;  // bytes per 16 K
-            uint32_t it = 0, g = 0;
+            const uint32_t p_step = (p.p_mn ? 2048u : 32u) >> 4, q_step = (p.q_mn ? 2048u : 32u) >> 4;  // per 16 K
+            const uint64_t ad0 = tc::smem_desc(sbase, p.p_mn ? MN_BOX_BYTES : 16);
+            const uint64_t bd0 = tc::smem_desc(sbase + P_BYTES, p.q_mn ? MN_BOX_BYTES : 16);
+            const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
+            uint32_t ph = 0, g = 0;
+            int s = 0;
             for (int idx = unit; idx < tiles; idx += units) {
                 const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
                 for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0, ++g) {
                     const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
                     const uint32_t set = g & 1;
-                    if (g >= 2) waiter.wait(tc::smem_u32(&acc_empty[set]), ((g / 2) - 1) & 1);
+                    waiter.wait(tc::smem_u32(&acc_empty[set]), ((g >> 1) & 1) ^ 1);
                     tc::fence_after();
                     const uint32_t d = tmem + set * (TMEM_COLS / 2);
                     uint32_t more = 0;
                     const int steps = (F32 ? PAIRS : 1) * (ke - kb);
-                    for (int i = 0; i < steps; ++i, ++it) {
-                        const uint32_t s = it % p.stages;
-                        waiter.wait(tc::smem_u32(&full_bar[s]), (it / p.stages) & 1);
+                    for (int i = 0; i < steps; ++i) {
+                        waiter.wait(full0 + 8u * s, ph);
+                        if (p.mode == K_BY_EXPERT && ke == w.k1 && (F32 || i + 1 == steps))  // rows a copying warp cleared
+                            asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
                         tc::fence_after();
-                        const uint32_t st = sbase + s * p.stage_bytes;
-                        const uint64_t ad = tc::smem_desc(st, p.p_mn ? MN_BOX_BYTES : 16);
-                        const uint64_t bd = tc::smem_desc(st + P_BYTES, p.q_mn ? MN_BOX_BYTES : 16);
+                        const uint32_t off = (s * stage_bytes) >> 4;
+                        const uint64_t ad = ad0 + off, bd = bd0 + off;
+                        __syncwarp();
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int j = 0; j < BK / 16; ++j) {
-                            tc::umma_f16<CG>(d, ad + ((j * p_step) >> 4), bd + ((j * q_step) >> 4), idesc, more);
-                            more = 1;
+                            for (int j = 0; j < BK / 16; ++j)
+                                tc::umma_f16<CG>(d, ad + j * p_step, bd + j * q_step, idesc, j > 0 ? 1u : more);
+                            tc::umma_commit<CG>(empty0 + 8u * s);
                         }
-                        tc::umma_commit<CG>(tc::smem_u32(&empty_bar[s]));
+                        more = 1;
+                        if (++s == stages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    tc::umma_commit<CG>(tc::smem_u32(&acc_full[set]));
+                    __syncwarp();
+                    if (tc::elect()) tc::umma_commit<CG>(tc::smem_u32(&acc_full[set]));
                 }
             }
         }
@@ -454,7 +485,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
             if (S > 1 && !w.none) {
                 // hand this CTA's part over: wait until the last one is read, store, tell all
-                if (handed > 0) waiter.wait(tc::smem_u32(&part_read), (handed - 1) & 1);
+                if (handed > 0) waiter.wait<true>(tc::smem_u32(&part_read), (handed - 1) & 1);
 #pragma unroll
                 for (int c = 0; c < 128; c += 16)
                     if (c < cols) {
@@ -502,7 +533,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             if (S > 1 && !w.none) {
                 epi_bar();
                 if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_ready), threadIdx.x));
-                waiter.wait(tc::smem_u32(&part_ready), handed & 1);
+                waiter.wait<true>(tc::smem_u32(&part_ready), handed & 1);
                 // the parts' sum in rank order, 32 features of a token per warp, shared out over all CTAs
                 const uint32_t mine = tc::smem_u32(partial);
                 const int fb = w.ft * PROWS;

@@ -18,6 +18,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
     return r;
 }
+// True in one thread of a converged warp, the same one each time.  A warp that
+// runs its loop whole and elects only for the issuing instructions keeps its
+// addresses and descriptors in uniform registers, which those instructions
+// want; inside a branch of one lane each has to be moved there first.
+__device__ __forceinline__ bool elect() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e != 0;
+}
 // Address of the same shared-memory variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t smem_addr, uint32_t rank) {
     uint32_t r;
@@ -37,23 +46,38 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
 }
-// Arrive (and announce `bytes` of copies) on a barrier of any CTA of the cluster.
+// Arrive (and announce `bytes` of copies) on a barrier of any CTA of the
+// cluster.  Relaxed: the waiting thread is to see what the copies wrote, and
+// they order that themselves; a release here waits out the thread's earlier
+// copies' issue, about 0.9 us a stage.
 __device__ __forceinline__ void mbar_arrive_expect(uint32_t cluster_bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_bar),
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_bar),
                  "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
+// CLUSTER: what the arriving threads of other CTAs wrote themselves is to be
+// seen.  What copies and products wrote needs no more than the CTA's scope,
+// and the wider one costs each wait some hundred nanoseconds.
+template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return done != 0;
 }
 // A wait gives up after about a second and sets the flag; the thread's later
@@ -63,10 +87,11 @@ struct Waiter {
     unsigned *timeout_flag;
     bool gave_up = false;
     __device__ explicit Waiter(unsigned *flag) : timeout_flag(flag) {}
+    template <bool CLUSTER = false>
     __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
         if (gave_up) return;
         uint32_t polls = 0;
-        while (!mbar_try_wait(bar, parity)) {
+        while (!mbar_try_wait<CLUSTER>(bar, parity)) {
             if (++polls > kWaitPolls) {
                 *timeout_flag = 1u;
                 gave_up = true;
