@@ -67,13 +67,16 @@ struct Product {
     int nt, nf;               // tiles in tokens (DENSE, K_BY_EXPERT) and in features
     int splits;               // CTAs of a cluster that share the K of a tile (CG = 1)
     int stages, stage_bytes, q_bytes;
+    int epi_offset;           // of the epilogue's buffers in dynamic shared memory
     int p_mn, q_mn;
     const void *bias, *residual;
     void *z, *out;
     long long ldr, ldz, ldo, out_expert;
     int act;
+    int vec;                  // VEC_* of what has 16-byte aligned rows
     unsigned *timeout_flag;
 };
+constexpr int VEC_OUT = 1, VEC_Z = 2, VEC_RESIDUAL = 4;
 struct Maps {
     CUtensorMap p, q;
 };
@@ -207,6 +210,81 @@ __device__ __forceinline__ void finish16(const float (&acc)[16], const Product &
         if (c < n) o[c * p.ldo] = from_f<T>(v[c]);
 }
 
+// ---- the 16-bit types' epilogue ------------------------------------------------
+// A warp takes 32 features (the lanes of tensor memory that it may read) and 16
+// tokens at a time, as 8 x 8 fragments.  A token's 32 features are 64
+// contiguous bytes of out, so the fragments go through shared memory,
+// transposed on the way by stmatrix, and leave in 16-byte stores, 8 tokens an
+// instruction; the residual comes in the same way, copied ahead by cp.async
+// while the tile is still being multiplied.  A row of the buffer is 64 bytes,
+// its four 16-byte chunks XORed with half the row number, so that the eight
+// rows of a matrix fall on different banks.
+constexpr int STAGE16 = 16 * 64;               // bytes of 16 tokens x 32 features
+constexpr int EPI_BYTES = 3 * STAGE16;         // per warp: two residual buffers, one for z and out
+
+__device__ __forceinline__ uint32_t stage16(uint32_t buf, int row, int chunk) {
+    return buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+}
+// Residual rows row0 .. row0 + n of features f0 .. f0 + 31 into a buffer.
+template <typename T>
+__device__ __forceinline__ void fetch16(const Product &p, uint32_t buf, long long row0, int n, int f0, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
+        if (row < n && f < p.F) {
+            const T *src = static_cast<const T *>(p.residual) + (row0 + row) * p.ldr + f;
+            const uint32_t dst = stage16(buf, row, chunk);
+            if ((p.vec & VEC_RESIDUAL) && f + 8 <= p.F) {
+                tc::cp_async16(dst, src);
+            } else {
+                for (int k = 0; k < 8 && f + k < p.F; ++k)
+                    asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + 2 * k),
+                                 "h"(*reinterpret_cast<const unsigned short *>(src + k))
+                                 : "memory");
+            }
+        }
+    }
+    tc::cp_async_commit();
+}
+// 16 tokens x 32 features (fragments, rounded) to rows row0 .. row0 + n of dst.
+template <typename T>
+__device__ __forceinline__ void put16(const float (&v)[16], uint32_t buf, T *dst, long long ld, bool vec, long long row0,
+                                      int n, int f0, int F, int lane) {
+    __syncwarp();  // the buffer's last contents have been read
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t r[4];
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+            const int i = 8 * (o >> 1) + 4 * j + 2 * (o & 1);
+            r[o] = lt::pack2<T>(v[i], v[i + 1]);
+        }
+        tc::stmatrix_t(stage16(buf, 8 * j + (lane & 7), lane >> 3), r);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
+        if (row < n && f < F) {
+            uint32_t a, b, c, d;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                         : "r"(stage16(buf, row, chunk))
+                         : "memory");
+            T *o = dst + (row0 + row) * ld + f;
+            if (vec && f + 8 <= F) {
+                *reinterpret_cast<uint4 *>(o) = make_uint4(a, b, c, d);
+            } else {
+                const uint32_t w[4] = {a, b, c, d};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (f + k < F)
+                        reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[k >> 1] >> (16 * (k & 1)));
+            }
+        }
+    }
+}
+
 // A persistent grid of CTA pairs (CG = 2, tiles of 256 features) or of
 // clusters of `splits` CTAs (CG = 1, 128 features, the K of a tile shared
 // out).  Per CTA, warp 8 issues the tensor copies into a ring of stages, one
@@ -242,6 +320,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     float *partial = reinterpret_cast<float *>(sgen + static_cast<size_t>(p.stages) * p.stage_bytes);
     int *tables = reinterpret_cast<int *>(partial + (S > 1 ? p.bt * PROWS : 0));
     const Tables tb{tables, tables + p.E + 2};
+    const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset + (warp < EPI_WARPS ? warp : 0) * EPI_BYTES;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -477,15 +556,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 }
             }
             const uint32_t set = g & 1;
-            if (!F32 && any) {
-                waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
-                __syncwarp();
-                tc::fence_after();
-            }
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
             if (S > 1 && !w.none) {
                 // hand this CTA's part over: wait until the last one is read, store, tell all
                 if (handed > 0) waiter.wait<true>(tc::smem_u32(&part_read), (handed - 1) & 1);
+                if (!F32 && any) {
+                    waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                    __syncwarp();
+                    tc::fence_after();
+                }
 #pragma unroll
                 for (int c = 0; c < 128; c += 16)
                     if (c < cols) {
@@ -504,25 +583,74 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         for (int i = 0; i < 16; ++i) partial[(col0 + c + i) * PROWS + fl] = v[i];
                     }
                 asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
-            } else {
+            } else if constexpr (F32) {
 #pragma unroll
                 for (int c = 0; c < 128; c += 16)
-                    if (c < cols) {
+                    if (c < cols && f_ok && (S == 1 || rank == 0)) {
                         float v[16];
-                        if constexpr (F32) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = total[c + i];
-                        } else if (any) {
-                            tc::tmem_ld16(t_set + c, v);
-                            tc::tmem_ld_wait(v);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                        }
-                        if (f_ok && (S == 1 || rank == 0))
-                            finish16<T>(v, p, bias, f, static_cast<long long>(w.t0) + col0 + c,
-                                        n_tile - (col0 + c), out, w.none);
+                        for (int i = 0; i < 16; ++i) v[i] = total[c + i];
+                        finish16<T>(v, p, bias, f, static_cast<long long>(w.t0) + col0 + c, n_tile - (col0 + c), out, w.none);
                     }
+            } else if (S == 1 || rank == 0) {
+                const int f0 = f - lane;
+                const int n_warp = f0 < p.F ? min(cols, n_tile - col0) : 0;  // this warp's tokens
+                const long long row0 = static_cast<long long>(w.t0) + col0;
+                float b[4];
+#pragma unroll
+                for (int o = 0; o < 4; ++o) b[o] = __shfl_sync(0xffffffffu, bias, 8 * o + (lane >> 2));
+                const bool res = p.residual != nullptr && !w.none;
+                if (res && n_warp > 0) fetch16<T>(p, epi, row0, n_warp, f0, lane);
+                if (any) {
+                    waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                    __syncwarp();
+                    tc::fence_after();
+                }
+                for (int c = 0; c < n_warp; c += 16) {
+                    const uint32_t rbuf = epi + (c >> 4 & 1) * STAGE16, obuf = epi + 2 * STAGE16;
+                    if (res) {  // the next 16 tokens' residual, into the buffer read last time
+                        __syncwarp();
+                        if (c + 16 < n_warp)
+                            fetch16<T>(p, epi + ((c >> 4 & 1) ^ 1) * STAGE16, row0 + c + 16, n_warp - c - 16, f0, lane);
+                    }
+                    float v[16];
+                    if (any) {
+                        tc::tmem_ld_frag(t_set + c, v);
+                        tc::tmem_ld_wait(v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += b[2 * (i >> 3) + (i >> 1 & 1)];
+                    if (p.z != nullptr)
+                        put16<T>(v, obuf, static_cast<T *>(p.z), p.ldz, (p.vec & VEC_Z) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                    if (!w.none)
+                        lt::with_activation(p.act, [&](auto a) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = lt::activate<decltype(a)::value, F32>(v[i]);
+                        });
+                    if (res) {
+                        if (c + 16 < n_warp)
+                            tc::cp_async_wait<1>();
+                        else
+                            tc::cp_async_wait<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t r[4];
+                            tc::ldmatrix_t(stage16(rbuf, 8 * j + (lane & 7), lane >> 3), r);
+#pragma unroll
+                            for (int o = 0; o < 4; ++o) {
+                                const int i = 8 * (o >> 1) + 4 * j + 2 * (o & 1);
+                                const float2 x = lt::unpack2<T>(r[o]);
+                                v[i] += x.x;
+                                v[i + 1] += x.y;
+                            }
+                        }
+                    }
+                    put16<T>(v, obuf, out, p.ldo, (p.vec & VEC_OUT) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                }
             }
             if (!F32 && any) {
                 tc::fence_before();
@@ -795,9 +923,15 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     if (tiles > INT_MAX / 2) return SGEMM_ERR_INVALID_DIM;
     const int tables = p.mode == DENSE ? 0 : 2 * (p.E + 2) * 4;
     const int part = p.splits > 1 ? p.bt * PROWS * 4 : 0;
-    p.stages = (SMEM_MAX - 2048 - tables - part) / p.stage_bytes;
+    const int epi = type == LINEAR_F32 ? 0 : EPI_WARPS * EPI_BYTES + 128;
+    p.stages = (SMEM_MAX - 2048 - tables - part - epi) / p.stage_bytes;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-    const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
+    const size_t used = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
+    p.epi_offset = static_cast<int>((used + 127) / 128 * 128);
+    const size_t smem = used + epi;
+    auto rows16 = [&](const void *base, long long ld) { return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld % 8 == 0; };
+    p.vec = (rows16(p.out, p.ldo) && p.out_expert % 8 == 0 ? VEC_OUT : 0) | (rows16(p.z, p.ldz) ? VEC_Z : 0) |
+            (rows16(p.residual, p.ldr) ? VEC_RESIDUAL : 0);
     Maps maps;
     memset(&maps, 0, sizeof maps);
     const bool f16 = type == LINEAR_F16;
