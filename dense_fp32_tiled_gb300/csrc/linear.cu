@@ -104,6 +104,10 @@ __device__ __forceinline__ void raster(int idx, int nt, int nf, int &tt, int &ft
     ft = r / rows;
 }
 
+// The same value, known to the compiler as one for the whole warp: what the
+// issue loops derive from it stays in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int CG>
 __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &tb, int rank) {
     Tile w;
@@ -143,6 +147,15 @@ __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &
         w.kbase = tb.begin[w.e];
         w.k_rows = tb.begin[w.e + 1] - w.kbase;
         ktiles = (w.k_rows + BK - 1) / BK;
+    }
+    if (p.mode != DENSE) {
+        w.e = uniform(w.e);
+        w.t0 = uniform(w.t0);
+        w.t_end = uniform(w.t_end);
+        ft = uniform(ft);
+        w.kbase = uniform(w.kbase);
+        w.k_rows = uniform(w.k_rows);
+        ktiles = uniform(ktiles);
     }
     w.ft = ft;
     if (CG == 1 && p.splits > 1) {
@@ -220,7 +233,7 @@ __device__ __forceinline__ void finish16(const float (&acc)[16], const Product &
 // its four 16-byte chunks XORed with half the row number, so that the eight
 // rows of a matrix fall on different banks.
 constexpr int STAGE16 = 16 * 64;               // bytes of 16 tokens x 32 features
-constexpr int EPI_BYTES = 3 * STAGE16;         // per warp: two residual buffers, one for z and out
+constexpr int EPI_BYTES = STAGE16, EPI_BYTES_RESIDUAL = 3 * STAGE16;  // per warp: z and out; two residual buffers
 
 __device__ __forceinline__ uint32_t stage16(uint32_t buf, int row, int chunk) {
     return buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
@@ -245,6 +258,14 @@ __device__ __forceinline__ void fetch16(const Product &p, uint32_t buf, long lon
         }
     }
     tc::cp_async_commit();
+}
+// Asks for all the residual of a warp's n tokens in L2, when its tile begins:
+// from HBM it would arrive long after the two buffers' 32 tokens are done.
+template <typename T>
+__device__ __forceinline__ void prefetch_residual(const Product &p, long long row0, int n, int f0, int lane) {
+    const char *base = reinterpret_cast<const char *>(static_cast<const T *>(p.residual) + row0 * p.ldr + f0);
+    for (int r = lane; r < n; r += 32)
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(base + r * p.ldr * static_cast<long long>(sizeof(T))) : "memory");
 }
 // 16 tokens x 32 features (fragments, rounded) to rows row0 .. row0 + n of dst.
 template <typename T>
@@ -311,7 +332,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     __shared__ uint32_t tmem_slot;
     const uint32_t sbase = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *sgen = smem_raw + (sbase - tc::smem_u32(smem_raw));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const int S = CG == 1 ? p.splits : 1;
     const int cluster = CG == 2 ? 2 : S;
@@ -320,7 +341,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     float *partial = reinterpret_cast<float *>(sgen + static_cast<size_t>(p.stages) * p.stage_bytes);
     int *tables = reinterpret_cast<int *>(partial + (S > 1 ? p.bt * PROWS : 0));
     const Tables tb{tables, tables + p.E + 2};
-    const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset + (warp < EPI_WARPS ? warp : 0) * EPI_BYTES;
+    const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset +
+                         (warp < EPI_WARPS ? warp : 0) * (p.residual != nullptr ? EPI_BYTES_RESIDUAL : EPI_BYTES);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -378,7 +400,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     __syncthreads();
     tc::cluster_sync();  // the barriers of all CTAs exist before any remote arrive or copy
     tc::fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(static_cast<int>(tmem_slot));
     if (p.mode == ROWS_BY_EXPERT)
         tiles = tb.first[p.E + 1];
     else if (p.mode == K_BY_EXPERT)
@@ -600,27 +622,34 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 #pragma unroll
                 for (int o = 0; o < 4; ++o) b[o] = __shfl_sync(0xffffffffu, bias, 8 * o + (lane >> 2));
                 const bool res = p.residual != nullptr && !w.none;
-                if (res && n_warp > 0) fetch16<T>(p, epi, row0, n_warp, f0, lane);
+                if (res && n_warp > 0) {
+                    fetch16<T>(p, epi + STAGE16, row0, n_warp, f0, lane);
+                    if (n_warp > 16) prefetch_residual<T>(p, row0 + 16, n_warp - 16, f0, lane);
+                }
                 if (any) {
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
                     __syncwarp();
                     tc::fence_after();
                 }
+                float next[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) next[i] = 0.0f;
+                if (any && n_warp > 0) {
+                    tc::tmem_ld_frag(t_set, next);
+                    tc::tmem_ld_wait(next);
+                }
                 for (int c = 0; c < n_warp; c += 16) {
-                    const uint32_t rbuf = epi + (c >> 4 & 1) * STAGE16, obuf = epi + 2 * STAGE16;
+                    const uint32_t obuf = epi, rbuf = epi + (1 + (c >> 4 & 1)) * STAGE16;
                     if (res) {  // the next 16 tokens' residual, into the buffer read last time
                         __syncwarp();
                         if (c + 16 < n_warp)
-                            fetch16<T>(p, epi + ((c >> 4 & 1) ^ 1) * STAGE16, row0 + c + 16, n_warp - c - 16, f0, lane);
+                            fetch16<T>(p, epi + (2 - (c >> 4 & 1)) * STAGE16, row0 + c + 16, n_warp - c - 16, f0, lane);
                     }
                     float v[16];
-                    if (any) {
-                        tc::tmem_ld_frag(t_set + c, v);
-                        tc::tmem_ld_wait(v);
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                    }
+                    for (int i = 0; i < 16; ++i) v[i] = next[i];
+                    const bool more = any && c + 16 < n_warp;
+                    if (more) tc::tmem_ld_frag(t_set + c + 16, next);  // arrives while these are finished
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] += b[2 * (i >> 3) + (i >> 1 & 1)];
                     if (p.z != nullptr)
@@ -650,6 +679,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         }
                     }
                     put16<T>(v, obuf, out, p.ldo, (p.vec & VEC_OUT) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                    if (more) tc::tmem_ld_wait(next);
                 }
             }
             if (!F32 && any) {
@@ -830,20 +860,23 @@ const Tune &tune() {
     return t;
 }
 
-// Time of a plan in SM clocks, by what bounds a K tile of a CTA: the tensor
-// cores (128 x bt/CG x 16 in bt/2/CG... clocks, four per tile) or the bytes
-// it copies.  Only the order of the results matters.
+// Time of a plan in SM clocks.  A K tile of a CTA (128 features, bt tokens, 64
+// K) takes the longest of three: the tensor cores' bt/2 clocks per 16 K (2.2 bt
+// measured for the four with bt = 256), the bytes that it copies at what L2
+// gives an SM when all copy (62 a clock measured), and the issue of a stage
+// (370 clocks measured with narrow tiles).  Whole waves of tiles count, and
+// between filling the pipeline and draining the last accumulator about 6000
+// clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 78, 256 wide 86,
+// 128 wide 97; single CTAs 256 wide 102, 128 wide 135.
 Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
-    const double copy_rate = 40.0;  // bytes per clock and SM from L2 with all SMs copying
     const int passes = type == LINEAR_F32 ? PAIRS : 1;
     Plan best;
     const int bts[] = {256, 224, 192, 160, 128, 96, 64, 32, 16};
     for (int cg = 2; cg >= 1; --cg)
         for (int bt : bts) {
             if (cg == 2 && (bt < 64 || bt % 32 != 0)) continue;
-            if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
             if (p.q_mn && bt / cg % 64 != 0) continue;
-            const int smem_q = bt / cg * 128;
+            if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
             double nt, ktiles = (p.K + BK - 1) / BK;
             if (p.mode == ROWS_BY_EXPERT) {
                 // the host does not know the counts: as if the rows were spread evenly
@@ -858,19 +891,22 @@ Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
                 }
             }
             const double tiles = nt * ((p.F + PROWS * cg - 1) / (PROWS * cg));
-            const double mma = 4.0 * (bt / 2 > 32 ? bt / 2 : 32);  // 128 (256 as a pair) x bt x 64
-            const double copy = (P_BYTES + smem_q) / copy_rate;
-            const double per = passes * (mma > copy ? mma : copy);
-            const double drain = 1000.0 + 10.0 * bt;
+            double per = 370.0;
+            if (2.2 * bt > per) per = 2.2 * bt;
+            const double copy = (P_BYTES + bt / cg * 128) / 62.0;
+            if (copy > per) per = copy;
+            per *= passes;
+            const double drain = 1000.0 + 12.0 * bt;
             const int most = cg == 2 || bt > 128 ? 1 : 8;
             for (int s = 1; s <= most; ++s) {
                 if (s > 1 && s * 2 > ktiles) break;
                 if (only.splits != 0 && only.splits != s) continue;
                 const int units = cg == 2 ? d.pairs : d.sms / s;
-                const double waves = static_cast<double>(static_cast<long long>(tiles + units - 1) / units);
+                double waves = static_cast<double>(static_cast<long long>((tiles + units - 1) / units));
+                if (waves < 1) waves = 1;
                 const double body = ktiles / s * per + 200.0;
-                const double cost = (waves < 1 ? 1 : waves) * (body > drain ? body : drain) + drain + (s > 1 ? 1500.0 : 0.0) + 1500.0;
-                if (cost < best.cost * 0.98) {
+                const double cost = waves * (body > drain ? body : drain) + drain + (s > 1 ? 2500.0 : 0.0) + 2000.0;
+                if (cost < best.cost * 0.99) {
                     best.cost = cost;
                     best.cg = cg;
                     best.bt = bt;
@@ -923,7 +959,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     if (tiles > INT_MAX / 2) return SGEMM_ERR_INVALID_DIM;
     const int tables = p.mode == DENSE ? 0 : 2 * (p.E + 2) * 4;
     const int part = p.splits > 1 ? p.bt * PROWS * 4 : 0;
-    const int epi = type == LINEAR_F32 ? 0 : EPI_WARPS * EPI_BYTES + 128;
+    const int epi = type == LINEAR_F32 ? 0 : EPI_WARPS * (p.residual != nullptr ? EPI_BYTES_RESIDUAL : EPI_BYTES) + 128;
     p.stages = (SMEM_MAX - 2048 - tables - part - epi) / p.stage_bytes;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     const size_t used = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
