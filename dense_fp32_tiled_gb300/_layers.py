@@ -10,113 +10,131 @@ status of the library raises SgemmError.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
+from contextlib import nullcontext
 
-from ._binding import SGEMM_OK, SgemmError, _workspace, load_library
+from ._binding import SGEMM_OK, SgemmError, load_library
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+# The calls are short next to what they launch (a decoding step's product takes
+# a few microseconds), so the checks below run in as few Python steps as they
+# can: torch and the library are looked up once, a call on the current stream
+# enters no context, and 16-bit operands whose rows are 16-byte aligned, which
+# need no workspace, do not ask for its size.
+torch = None
+_lib = None
 _types = {}
+_raw_stream = None
+
+
+def _load():
+    global torch, _lib, _raw_stream
+    if _lib is None:
+        import torch as _torch
+        torch = _torch
+        _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _lib = load_library()
+    return _lib
 
 
 def _type_of(t, name):
-    import torch
-    if not _types:
-        _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _types:
+    kind = _types.get(getattr(t, "dtype", None))
+    if kind is None or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of float32, bfloat16 or float16")
-    return _types[t.dtype]
+    return kind
 
 
-def _like(t, ref, name):
-    if getattr(t, "dtype", None) != ref.dtype or t.device != ref.device:
-        raise TypeError(f"{name} must be a {ref.dtype} tensor on {ref.device}")
+def _alike(t, dtype, device, name):
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{device}")
 
 
-def _rows(t, rows, cols, name, ref=None):
+def _rows(t, rows, cols, dtype, device, name):
     """(address, row stride) of a row-major rows x cols tensor."""
-    if ref is not None:
-        _like(t, ref, name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != device:
+        _alike(t, dtype, device, name)
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    if rows <= 1:
-        ld = max(ld, cols, 1)
-    elif ld < cols:
-        raise ValueError(f"{name} has overlapping rows")
-    return t.data_ptr(), max(ld, 1)
+    if ld < cols or ld < 1:
+        if rows > 1:
+            raise ValueError(f"{name} has overlapping rows")
+        ld = max(cols, 1)
+    return t.data_ptr(), ld
 
 
-def _vector(t, shape, name, ref):
+def _vector(t, shape, dtype, device, name):
     if t is None:
         return None
-    _like(t, ref, name)
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    _alike(t, dtype, device, name)
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _weight(w, K, N, name, ref=None):
+def _weight(w, K, dtype, device, name):
     """(address, stride, order, expert stride) of (..., K, N) with either of the last two contiguous."""
-    if ref is not None:
-        _like(w, ref, name)
-    if w.shape[-2] != K or w.shape[-1] != N:
-        raise ValueError(f"{name} must end in ({K}, {N}), got {tuple(w.shape)}")
-    sk, sn = w.stride()[-2:]
-    expert = w.stride(0) if w.dim() == 3 and w.shape[0] > 1 else 0
-    if (sn == 1 or N == 1) and (K <= 1 or sk >= N):
-        return w.data_ptr(), (max(sk, N, 1) if K <= 1 else sk), 0, expert
-    if (sk == 1 or K == 1) and (N <= 1 or sn >= K):
-        return w.data_ptr(), (max(sn, K, 1) if N <= 1 else sn), 1, expert
+    _alike(w, dtype, device, name)
+    if w.shape[-2] != K:
+        raise ValueError(f"{name} must have {K} inputs in its last but one dimension, got {tuple(w.shape)}")
+    N = w.shape[-1]
+    strides = w.stride()
+    sk, sn = strides[-2:]
+    expert = strides[0] if len(strides) == 3 and w.shape[0] > 1 else 0
+    if (sn == 1 or N == 1) and (sk >= N or K <= 1):
+        return w.data_ptr(), (sk if K > 1 else max(sk, N, 1)), 0, expert
+    if (sk == 1 or K == 1) and (sn >= K or N <= 1):
+        return w.data_ptr(), (sn if N > 1 else max(sn, K, 1)), 1, expert
     raise ValueError(f"{name} must have one of its last two dimensions contiguous, its rows apart")
 
 
-def _int32(t, shape, name, ref):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != ref.device:
-        raise TypeError(f"{name} must be an int32 tensor on {ref.device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+def _int32(t, shape, device, name):
+    if getattr(t, "dtype", None) is not torch.int32 or t.get_device() != device:
+        raise TypeError(f"{name} must be an int32 tensor on cuda:{device}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-class _On:
-    """The device and stream of a call; what is allocated inside belongs to that stream."""
+_NOWHERE = nullcontext()
 
-    __slots__ = ("stream", "_stack")
 
-    def __init__(self, device, stream):
-        import torch
-        self._stack = None
-        here = torch.cuda.current_device() == device.index
-        if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-            if not here:
-                self._stack = contextlib.ExitStack()
-                self._stack.enter_context(torch.cuda.device(device))
-        else:
-            self.stream = stream
-            self._stack = contextlib.ExitStack()
-            self._stack.enter_context(torch.cuda.stream(stream))
+def _on(device, stream):
+    """The context in which a call allocates and launches: the device and stream it is for."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device:
+        return torch.cuda.device(device)
+    return _NOWHERE
 
-    def __enter__(self):
-        return self
 
-    def __exit__(self, *exc):
-        if self._stack is not None:
-            self._stack.__exit__(*exc)
-        return False
+_workspaces = {}
 
-    def workspace(self, device, nbytes):
-        return _workspace("layer", device, self.stream, nbytes).data_ptr() if nbytes else None
+
+def _workspace(device, stream, nbytes):
+    """Address of scratch for the calls of one stream, which are ordered and so
+    can share it.  It is allocated with that stream current, so it belongs to
+    it.  One that has become too small is kept, as a captured graph may hold
+    its address; each is at least twice the one before, so all of them
+    together take no more than the last one does."""
+    if not nbytes:
+        return None
+    held = _workspaces.setdefault((device, stream), [])
+    if not held or held[-1].numel() < nbytes:
+        size = max(nbytes, 2 * held[-1].numel() if held else 1 << 16)
+        held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{device}"))
+    return held[-1].data_ptr()
 
 
 def _act(name):
-    try:
-        return ACTIVATIONS[name]
-    except KeyError:
-        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
+    act = ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return act
 
 
 def _check(st, what):
@@ -145,36 +163,41 @@ def expert_linear(x, w, offsets, bias=None, residual=None, activation="none", pr
 
 
 def _forward(x, w, offsets, bias, residual, activation, preact, out, stream):
-    import torch
+    lib = _lib or _load()
     kind, act = _type_of(x, "x"), _act(activation)
     grouped = offsets is not None
     if x.dim() != 2 or w.dim() != 2 + grouped:
         raise ValueError(f"x must be 2-D and w {2 + grouped}-D, got {tuple(x.shape)} and {tuple(w.shape)}")
-    M, K = x.shape
+    (M, K), dtype, dev = x.shape, x.dtype, x.get_device()
+    xp, ldx = _rows(x, M, K, dtype, dev, "x")
+    wp, ldw, order, step = _weight(w, K, dtype, dev, "w")
     N = w.shape[-1]
-    xp, ldx = _rows(x, M, K, "x")
-    wp, ldw, order, step = _weight(w, K, N, "w", x)
-    rp, ldr = _rows(residual, M, N, "residual", x) if residual is not None else (None, 0)
-    zp, ldz = _rows(preact, M, N, "preact", x) if preact is not None else (None, 0)
-    lib = load_library()
-    with _On(x.device, stream) as on:
+    rp, ldr = _rows(residual, M, N, dtype, dev, "residual") if residual is not None else (None, 0)
+    zp, ldz = _rows(preact, M, N, dtype, dev, "preact") if preact is not None else (None, 0)
+    if grouped:
+        E = w.shape[0]
+        op = _int32(offsets, (E + 1,), dev, "offsets")
+    bp = _vector(bias, (E, N) if grouped else (N,), dtype, dev, "bias")
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-        yp, ldy = _rows(out, M, N, "out", x)
-        if grouped:
-            E = w.shape[0]
-            op = _int32(offsets, (E + 1,), "offsets", x)
-            bp = _vector(bias, (E, N), "bias", x)
-            nbytes = lib.expert_linear_forward_workspace_size(kind, M, N, K, E, xp, ldx, wp, ldw, step, order)
-            _check(lib.expert_linear_forward(kind, M, N, K, E, op, xp, ldx, wp, ldw, step, order, bp, rp, ldr, act, zp,
-                                             ldz, yp, ldy, on.workspace(x.device, nbytes), nbytes,
-                                             on.stream.cuda_stream), "expert_linear_forward")
+            out = torch.empty((M, N), dtype=dtype, device=x.device)
+            yp, ldy = out.data_ptr(), N or 1
         else:
-            bp = _vector(bias, (N,), "bias", x)
-            nbytes = lib.linear_forward_workspace_size(kind, M, N, K, xp, ldx, wp, ldw, order)
-            _check(lib.linear_forward(kind, M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, act, zp, ldz, yp, ldy,
-                                      on.workspace(x.device, nbytes), nbytes, on.stream.cuda_stream),
-                   "linear_forward")
+            yp, ldy = _rows(out, M, N, dtype, dev, "out")
+        raw = _raw_stream(dev)
+        nbytes, ws = 0, None
+        if kind == 0 or (xp | wp) & 15 or (ldx | ldw | step) & 7:
+            nbytes = (lib.expert_linear_forward_workspace_size(kind, M, N, K, E, xp, ldx, wp, ldw, step, order) if grouped
+                      else lib.linear_forward_workspace_size(kind, M, N, K, xp, ldx, wp, ldw, order))
+            ws = _workspace(dev, raw, nbytes)
+        if grouped:
+            st = lib.expert_linear_forward(kind, M, N, K, E, op, xp, ldx, wp, ldw, step, order, bp, rp, ldr, act, zp, ldz,
+                                           yp, ldy, ws, nbytes, raw)
+        else:
+            st = lib.linear_forward(kind, M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, act, zp, ldz, yp, ldy, ws, nbytes,
+                                    raw)
+    if st:
+        _check(st, "expert_linear_forward" if grouped else "linear_forward")
     return out
 
 
@@ -192,57 +215,56 @@ def expert_linear_backward(dy, x, w, offsets, preact=None, activation="none", ne
 
 
 def _backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbias, stream):
-    import torch
+    lib = _lib or _load()
     kind, act = _type_of(x, "x"), _act(activation)
     grouped = offsets is not None
     if x.dim() != 2 or w.dim() != 2 + grouped:
         raise ValueError(f"x must be 2-D and w {2 + grouped}-D, got {tuple(x.shape)} and {tuple(w.shape)}")
     if (preact is None) != (act == 0):
         raise ValueError("preact is needed with an activation, and only then")
-    M, K = x.shape
+    (M, K), dtype, dev = x.shape, x.dtype, x.get_device()
     N = w.shape[-1]
-    gp, lddy = _rows(dy, M, N, "dy", x)
-    xp, ldx = _rows(x, M, K, "x")
-    wp, ldw, order, step = _weight(w, K, N, "w", x)
-    zp, ldz = _rows(preact, M, N, "preact", x) if preact is not None else (None, 0)
-    lead = (w.shape[0],) if grouped else ()
-    lib = load_library()
-    with _On(x.device, stream) as on:
-        dx = dw = dbias = None
-        hp = ldh = vp = ldv = stepv = bp = None
+    gp, lddy = _rows(dy, M, N, dtype, dev, "dy")
+    xp, ldx = _rows(x, M, K, dtype, dev, "x")
+    wp, ldw, order, step = _weight(w, K, dtype, dev, "w")
+    zp, ldz = _rows(preact, M, N, dtype, dev, "preact") if preact is not None else (None, 0)
+    lead = ()
+    if grouped:
+        E = w.shape[0]
+        lead = (E,)
+        op = _int32(offsets, (E + 1,), dev, "offsets")
+    dx = dw = dbias = hp = vp = bp = None
+    ldh, ldv, stepv = K or 1, (K if order else N) or 1, K * N
+    with _on(dev, stream):
         if need_dx:
-            dx = torch.empty((M, K), dtype=x.dtype, device=x.device)
+            dx = torch.empty((M, K), dtype=dtype, device=x.device)
             hp = dx.data_ptr()
         if need_dw:
-            if order == 0:
-                dw = torch.empty(lead + (K, N), dtype=x.dtype, device=x.device)
-            else:
-                dw = torch.empty(lead + (N, K), dtype=x.dtype, device=x.device).transpose(-1, -2)
+            dw = torch.empty(lead + ((N, K) if order else (K, N)), dtype=dtype, device=x.device)
             vp = dw.data_ptr()
+            if order:
+                dw = dw.transpose(-1, -2)
         if need_dbias:
-            dbias = torch.empty(lead + (N,), dtype=x.dtype, device=x.device)
+            dbias = torch.empty(lead + (N,), dtype=dtype, device=x.device)
             bp = dbias.data_ptr()
-        ldh, ldv, stepv = max(K, 1), max(K if order else N, 1), K * N
+        raw = _raw_stream(dev)
         if grouped:
-            E = w.shape[0]
-            op = _int32(offsets, (E + 1,), "offsets", x)
             nbytes = lib.expert_linear_backward_workspace_size(kind, M, N, K, E, gp, lddy, xp, ldx, wp, ldw, step, order,
                                                                act, need_dx, need_dw, need_dbias)
-            _check(lib.expert_linear_backward(kind, M, N, K, E, op, gp, lddy, xp, ldx, wp, ldw, step, order, zp, ldz,
-                                              act, hp, ldh, vp, ldv, stepv, bp, on.workspace(x.device, nbytes), nbytes,
-                                              on.stream.cuda_stream), "expert_linear_backward")
+            st = lib.expert_linear_backward(kind, M, N, K, E, op, gp, lddy, xp, ldx, wp, ldw, step, order, zp, ldz, act, hp,
+                                            ldh, vp, ldv, stepv, bp, _workspace(dev, raw, nbytes), nbytes, raw)
         else:
             nbytes = lib.linear_backward_workspace_size(kind, M, N, K, gp, lddy, xp, ldx, wp, ldw, order, act, need_dx,
                                                         need_dw, need_dbias)
-            _check(lib.linear_backward(kind, M, N, K, gp, lddy, xp, ldx, wp, ldw, order, zp, ldz, act, hp, ldh, vp, ldv,
-                                       bp, on.workspace(x.device, nbytes), nbytes, on.stream.cuda_stream),
-                   "linear_backward")
+            st = lib.linear_backward(kind, M, N, K, gp, lddy, xp, ldx, wp, ldw, order, zp, ldz, act, hp, ldh, vp, ldv, bp,
+                                     _workspace(dev, raw, nbytes), nbytes, raw)
+    if st:
+        _check(st, "expert_linear_backward" if grouped else "linear_backward")
     return dx, dw, dbias
 
 
 def linear_timeouts() -> int:
     """1 if a kernel of the layer products gave up a wait since the library was loaded, else 0."""
-    import ctypes
     n = ctypes.c_uint()
     _check(load_library().linear_timeouts(ctypes.byref(n)), "linear_timeouts")
     return n.value
@@ -254,80 +276,81 @@ def expert_sort(choices, experts, stream=None):
     token (one outside 0 .. experts - 1 is dropped).  rows, int32 (T, J), is
     each choice's place among all T*J sorted by expert, then token and choice,
     or -1; places offsets[e] to offsets[e + 1] belong to expert e."""
-    import torch
-    if not isinstance(choices, torch.Tensor) or not choices.is_cuda or choices.dtype not in (torch.int32, torch.int64):
+    lib = _lib or _load()
+    dtype = getattr(choices, "dtype", None)
+    if dtype is torch.int32:
+        width = 4
+    elif dtype is torch.int64:
+        width = 8
+    else:
+        raise TypeError("choices must be a CUDA tensor of int32 or int64")
+    if not choices.is_cuda:
         raise TypeError("choices must be a CUDA tensor of int32 or int64")
     if choices.dim() != 2 or not choices.is_contiguous():
         raise ValueError(f"choices must be contiguous with shape (tokens, choices), got {tuple(choices.shape)}")
-    T, J = choices.shape
-    E = int(experts)
-    lib = load_library()
-    with _On(choices.device, stream) as on:
+    (T, J), E, dev = choices.shape, int(experts), choices.get_device()
+    with _on(dev, stream):
         rows = torch.empty((T, J), dtype=torch.int32, device=choices.device)
         offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=choices.device)
+        raw = _raw_stream(dev)
         nbytes = lib.expert_sort_workspace_size(T, J, E)
-        _check(lib.expert_sort(T, J, E, choices.data_ptr(), choices.element_size(), rows.data_ptr(), offsets.data_ptr(),
-                               on.workspace(choices.device, nbytes), nbytes, on.stream.cuda_stream), "expert_sort")
+        st = lib.expert_sort(T, J, E, choices.data_ptr(), width, rows.data_ptr(), offsets.data_ptr(),
+                             _workspace(dev, raw, nbytes), nbytes, raw)
+    if st:
+        _check(st, "expert_sort")
     return rows, offsets
 
 
-def _order(rows, offsets, T, ref):
-    if rows.dim() != 2 or rows.shape[0] != T:
-        raise ValueError(f"rows must have shape ({T}, choices), got {tuple(rows.shape)}")
-    if offsets is not None and offsets.dim() != 1:
-        raise ValueError("offsets must be 1-D")
-    J = rows.shape[1]
-    E = offsets.shape[0] - 1 if offsets is not None else 0
-    return J, E, _int32(rows, (T, J), "rows", ref), _int32(offsets, (E + 1,), "offsets", ref) if offsets is not None else None
-
-
-def _weights(weights, T, J, ref):
-    import torch
-    if weights is None:
-        return None
-    if not isinstance(weights, torch.Tensor) or weights.dtype != torch.float32 or weights.device != ref.device:
-        raise TypeError(f"weights must be a float32 tensor on {ref.device}")
-    if tuple(weights.shape) != (T, J) or not weights.is_contiguous():
-        raise ValueError(f"weights must be contiguous with shape ({T}, {J}), got {tuple(weights.shape)}")
-    return weights.data_ptr()
+def _order(rows, offsets, T, dev):
+    """(choices, experts, address of rows, address of offsets)."""
+    if rows.dim() != 2 or offsets is not None and offsets.dim() != 1:
+        raise ValueError("rows must be 2-D and offsets 1-D")
+    J, E = rows.shape[1], 0
+    op = None
+    if offsets is not None:
+        E = offsets.shape[0] - 1
+        op = _int32(offsets, (E + 1,), dev, "offsets")
+    return J, E, _int32(rows, (T, J), dev, "rows"), op
 
 
 def expert_gather(x, rows, offsets, out=None, stream=None):
     """The token rows in expert order: out[rows[t, j]] = x[t], (T*J, H); places in no use are 0."""
-    import torch
+    lib = _lib or _load()
     kind = _type_of(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
-    T, H = x.shape
-    xp, ldx = _rows(x, T, H, "x")
-    J, E, rp, op = _order(rows, offsets, T, x)
-    with _On(x.device, stream) as on:
+    (T, H), dtype, dev = x.shape, x.dtype, x.get_device()
+    xp, ldx = _rows(x, T, H, dtype, dev, "x")
+    J, E, rp, op = _order(rows, offsets, T, dev)
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((T * J, H), dtype=x.dtype, device=x.device)
-        sp, lds = _rows(out, T * J, H, "out", x)
-        _check(load_library().expert_gather(kind, T, J, H, E, rp, op, xp, ldx, sp, lds, on.stream.cuda_stream),
-               "expert_gather")
+            out = torch.empty((T * J, H), dtype=dtype, device=x.device)
+        sp, lds = _rows(out, T * J, H, dtype, dev, "out")
+        st = lib.expert_gather(kind, T, J, H, E, rp, op, xp, ldx, sp, lds, _raw_stream(dev))
+    if st:
+        _check(st, "expert_gather")
     return out
 
 
 def expert_combine(ys, rows, weights=None, residual=None, out=None, stream=None):
     """Each token's sum over its choices: residual[t] + sum_j weights[t, j] * ys[rows[t, j]].
     weights is float32 (T, J); None weighs all by 1.  Dropped choices add nothing."""
-    import torch
+    lib = _lib or _load()
     kind = _type_of(ys, "ys")
     if ys.dim() != 2 or rows.dim() != 2:
         raise ValueError(f"ys and rows must be 2-D, got {tuple(ys.shape)} and {tuple(rows.shape)}")
-    T, H = rows.shape[0], ys.shape[1]
-    J, _, rp, _ = _order(rows, None, T, ys)
-    sp, lds = _rows(ys, T * J, H, "ys")
-    wp = _weights(weights, T, J, ys)
-    dp, ldr = _rows(residual, T, H, "residual", ys) if residual is not None else (None, 0)
-    with _On(ys.device, stream) as on:
+    T, H, dtype, dev = rows.shape[0], ys.shape[1], ys.dtype, ys.get_device()
+    J, _, rp, _ = _order(rows, None, T, dev)
+    sp, lds = _rows(ys, T * J, H, dtype, dev, "ys")
+    wp = _vector(weights, (T, J), torch.float32, dev, "weights")
+    dp, ldr = _rows(residual, T, H, dtype, dev, "residual") if residual is not None else (None, 0)
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
-        yp, ldy = _rows(out, T, H, "out", ys)
-        _check(load_library().expert_combine(kind, T, J, H, rp, wp, sp, lds, dp, ldr, yp, ldy, on.stream.cuda_stream),
-               "expert_combine")
+            out = torch.empty((T, H), dtype=dtype, device=ys.device)
+        yp, ldy = _rows(out, T, H, dtype, dev, "out")
+        st = lib.expert_combine(kind, T, J, H, rp, wp, sp, lds, dp, ldr, yp, ldy, _raw_stream(dev))
+    if st:
+        _check(st, "expert_combine")
     return out
 
 
@@ -340,19 +363,22 @@ def expert_combine_backward(dy, ys, rows, weights, offsets, need_dweights=True, 
     """(dys, dweights) of expert_combine (the residual's gradient is dy itself):
     dys[rows[t, j]] = weights[t, j] * dy[t], 0 in the places in no use, and
     dweights[t, j] = dy[t] . ys[rows[t, j]], float32, 0 for a dropped choice."""
-    import torch
+    lib = _lib or _load()
     kind = _type_of(dy, "dy")
     if dy.dim() != 2:
         raise ValueError(f"dy must be 2-D, got {tuple(dy.shape)}")
-    T, H = dy.shape
-    gp, lddy = _rows(dy, T, H, "dy")
-    J, E, rp, op = _order(rows, offsets, T, dy)
-    wp = _weights(weights, T, J, dy)
-    sp, lds = _rows(ys, T * J, H, "ys", dy) if need_dweights else (None, 0)
-    with _On(dy.device, stream) as on:
-        dys = torch.empty((T * J, H), dtype=dy.dtype, device=dy.device)
-        dweights = torch.empty((T, J), dtype=torch.float32, device=dy.device) if need_dweights else None
-        _check(load_library().expert_combine_backward(kind, T, J, H, E, rp, op, wp, gp, lddy, sp, lds, dys.data_ptr(),
-                                                      max(H, 1), dweights.data_ptr() if need_dweights else None,
-                                                      on.stream.cuda_stream), "expert_combine_backward")
+    (T, H), dtype, dev = dy.shape, dy.dtype, dy.get_device()
+    gp, lddy = _rows(dy, T, H, dtype, dev, "dy")
+    J, E, rp, op = _order(rows, offsets, T, dev)
+    wp = _vector(weights, (T, J), torch.float32, dev, "weights")
+    sp, lds = _rows(ys, T * J, H, dtype, dev, "ys") if need_dweights else (None, 0)
+    dweights = None
+    with _on(dev, stream):
+        dys = torch.empty((T * J, H), dtype=dtype, device=dy.device)
+        if need_dweights:
+            dweights = torch.empty((T, J), dtype=torch.float32, device=dy.device)
+        st = lib.expert_combine_backward(kind, T, J, H, E, rp, op, wp, gp, lddy, sp, lds, dys.data_ptr(), H or 1,
+                                         dweights.data_ptr() if need_dweights else None, _raw_stream(dev))
+    if st:
+        _check(st, "expert_combine_backward")
     return dys, dweights

@@ -12,6 +12,7 @@
 #include "experts.h"
 #include "linear_types.cuh"
 #include "nvtx_range.cuh"
+#include "tensor_core.cuh"
 
 namespace {
 
@@ -25,8 +26,9 @@ using lt::to_f;
 // its place: places before the expert + before the range + before the warp +
 // in the warp.  No atomics, so the order is that of the choices.
 constexpr int SORT_THREADS = 1024;
-constexpr int SORT_RANGE = 8192;   // choices a block sorts, at least
-constexpr int SORT_BLOCKS = 512;   // ranges, at most
+constexpr int SORT_ALONE = 4096;   // choices that one block sorts in one launch
+constexpr int SORT_RANGE = 1024;   // choices of a block, with more: one step of its 32 warps
+constexpr int SORT_BLOCKS = 256;   // ranges, at most: each block reads all their counts
 constexpr int SORT_SMEM = 200 * 1024;
 
 struct SortPlan {
@@ -35,8 +37,7 @@ struct SortPlan {
 };
 SortPlan sort_plan(long long R, int E) {
     SortPlan s;
-    long long blocks = (R + SORT_RANGE - 1) / SORT_RANGE;
-    if (blocks < 1) blocks = 1;
+    long long blocks = R <= SORT_ALONE ? 1 : (R + SORT_RANGE - 1) / SORT_RANGE;
     if (blocks > SORT_BLOCKS) blocks = SORT_BLOCKS;
     s.range = static_cast<int>(((R + blocks - 1) / blocks + 31) / 32 * 32);
     if (s.range < 32) s.range = 32;
@@ -70,6 +71,7 @@ template <typename I>
 __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const I *__restrict__ choices, long long R, int E,
                                                                   int range, int warps, int *__restrict__ counts) {
     extern __shared__ int shared[];
+    tc::grid_trigger();  // the second kernel counts its ranges meanwhile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < warps * E; i += SORT_THREADS) shared[i] = 0;
     __syncthreads();
@@ -106,6 +108,7 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
     if (warp < warps)
         for (long long i = b; i < e1; i += 32) count32(choice_at(choices, i + lane, e1, E), mine + warp * E, lane);
     __syncthreads();
+    tc::grid_wait();  // the counts are there, and rows and offsets no longer in use
     // per expert: all its choices, those before this range, and the warps' first places;
     // the running sum over the experts carries from one group of 1024 to the next
     int carry = 0;
@@ -193,69 +196,97 @@ __device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long 
     }
 }
 
+// A warp takes a segment of one token's row: SEG accesses per lane, all in
+// flight together, with the token's places read once for them.
+__host__ __device__ constexpr int seg_of(int V) { return V > 1 ? 4 : 8; }
+
 template <typename T, int V>
 __global__ void __launch_bounds__(ROW_THREADS)
-gather_kernel(int T_, int J, int packs, int E, const int *__restrict__ rows, const int *__restrict__ offsets,
-              const T *__restrict__ x, long long ldx, T *__restrict__ xs, long long ldxs, int blocks) {
+gather_kernel(int T_, int J, int packs, int segments, int E, const int *__restrict__ rows,
+              const int *__restrict__ offsets, const T *__restrict__ x, long long ldx, T *__restrict__ xs,
+              long long ldxs, int blocks) {
+    constexpr int SEG = seg_of(V);
     const long long R = static_cast<long long>(T_) * J;
     if (static_cast<int>(blockIdx.x) >= blocks) {
         clear_rest<T, V>(xs, ldxs, offsets[E], R, packs, blockIdx.x - blocks);
         return;
     }
-    const long long u = static_cast<long long>(blockIdx.x) * ROW_THREADS + threadIdx.x;
-    const long long t = u / packs;
+    const int unit = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    const int t = unit / segments;
     if (t >= T_) return;
-    const long long c = (u - t * packs) * V;
-    const Pack<T, V> v = load<T, V>(x + t * ldx + c);
+    const int c0 = (unit - t * segments) * SEG * 32 + (threadIdx.x & 31);
+    Pack<T, V> v[SEG];
+#pragma unroll
+    for (int i = 0; i < SEG; ++i)
+        if (c0 + 32 * i < packs) v[i] = load<T, V>(x + t * ldx + static_cast<long long>(c0 + 32 * i) * V);
+    const int *at = rows + static_cast<long long>(t) * J;
     for (int j = 0; j < J; ++j) {
-        const int r = rows[t * J + j];
-        if (r >= 0 && r < R) store<T, V>(xs + r * ldxs + c, v);
+        const int r = at[j];
+        if (r >= 0 && r < R)
+#pragma unroll
+            for (int i = 0; i < SEG; ++i)
+                if (c0 + 32 * i < packs) store<T, V>(xs + r * ldxs + static_cast<long long>(c0 + 32 * i) * V, v[i]);
     }
 }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(ROW_THREADS)
-combine_kernel(int T_, int J, int packs, const int *__restrict__ rows, const float *__restrict__ weights,
+combine_kernel(int T_, int J, int packs, int segments, const int *__restrict__ rows, const float *__restrict__ weights,
                const T *__restrict__ ys, long long ldys, const T *residual, long long ldr, T *y, long long ldy) {
+    constexpr int SEG = seg_of(V);
+    constexpr int U = 2;  // rows in flight
     const long long R = static_cast<long long>(T_) * J;
-    const long long u = static_cast<long long>(blockIdx.x) * ROW_THREADS + threadIdx.x;
-    const long long t = u / packs;
+    const int unit = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    const int t = unit / segments;
     if (t >= T_) return;
-    const long long c = (u - t * packs) * V;
-    float sum[V];
+    const int c0 = (unit - t * segments) * SEG * 32 + (threadIdx.x & 31);
+    const int *at = rows + static_cast<long long>(t) * J;
+    const float *wt = weights + static_cast<long long>(t) * J;
+    float sum[SEG][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    constexpr int U = 4;  // rows in flight
+    for (int i = 0; i < SEG; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum[i][k] = 0.0f;
     for (int j0 = 0; j0 < J; j0 += U) {
-        Pack<T, V> v[U];
+        Pack<T, V> v[U][SEG];
         float w[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            w[k] = 0.0f;
-            const int r = j0 + k < J ? rows[t * J + j0 + k] : -1;
+        for (int u = 0; u < U; ++u) {
+            w[u] = 0.0f;
+            const int r = j0 + u < J ? at[j0 + u] : -1;
             const bool in = r >= 0 && r < R;
-            if (in) {
-                v[k] = load<T, V>(ys + r * ldys + c);
-                w[k] = weights != nullptr ? weights[t * J + j0 + k] : 1.0f;
-            } else {
+            if (in) w[u] = weights != nullptr ? wt[j0 + u] : 1.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[k].v[i] = from_f<T>(0.0f);
+            for (int i = 0; i < SEG; ++i) {
+                if (in && c0 + 32 * i < packs) {
+                    v[u][i] = load<T, V>(ys + r * ldys + static_cast<long long>(c0 + 32 * i) * V);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) v[u][i].v[k] = from_f<T>(0.0f);
+                }
             }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = fmaf(w[k], to_f(v[k].v[i]), sum[i]);
+            for (int i = 0; i < SEG; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) sum[i][k] = fmaf(w[u], to_f(v[u][i].v[k]), sum[i][k]);
     }
-    if (residual != nullptr) {
-        const Pack<T, V> r = load<T, V>(residual + t * ldr + c);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += to_f(r.v[i]);
+    for (int i = 0; i < SEG; ++i) {
+        const long long c = static_cast<long long>(c0 + 32 * i) * V;
+        if (c0 + 32 * i >= packs) continue;
+        if (residual != nullptr) {
+            const Pack<T, V> r = load<T, V>(residual + t * ldr + c);
+#pragma unroll
+            for (int k = 0; k < V; ++k) sum[i][k] += to_f(r.v[k]);
+        }
+        Pack<T, V> o;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o.v[k] = from_f<T>(sum[i][k]);
+        store<T, V>(y + t * ldy + c, o);
     }
-    Pack<T, V> o;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = from_f<T>(sum[i]);
-    store<T, V>(y + t * ldy + c, o);
 }
 
 // A warp per choice; the other choices of the token find dy in the L1 or L2.
@@ -282,7 +313,7 @@ combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__
     const T *d = dy + i / J * lddy, *s = ys + r * ldys;
     T *o = dys + r * lddys;
     float dot = 0.0f;
-#pragma unroll 4
+#pragma unroll seg_of(V)
     for (int p = lane; p < packs; p += 32) {
         const Pack<T, V> g = load<T, V>(d + static_cast<long long>(p) * V);
         if (dweights != nullptr) {
@@ -338,7 +369,11 @@ int with_rows(int type, bool vec, F &&f) {
     if (type == LINEAR_BF16) return vec ? f(__nv_bfloat16(), lt::Int<8>{}) : f(__nv_bfloat16(), lt::Int<1>{});
     return vec ? f(__half(), lt::Int<8>{}) : f(__half(), lt::Int<1>{});
 }
-long long blocks_for(long long units) { return (units + ROW_THREADS - 1) / ROW_THREADS; }
+int segments_of(int packs, bool vec) {
+    const int seg = 32 * seg_of(vec ? 4 : 1);
+    return packs / seg + (packs % seg != 0);
+}
+long long blocks_for(long long warps) { return (warps + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32); }
 
 template <typename I>
 int sort(long long R, int E, const I *choices, int *rows, int *offsets, int *counts, cudaStream_t stream) {
@@ -352,9 +387,25 @@ int sort(long long R, int E, const I *choices, int *rows, int *offsets, int *cou
     sg_nvtx::Range r("experts: sort");
     if (s.blocks > 1)
         sort_count_kernel<I><<<s.blocks, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, counts);
-    sort_place_kernel<I><<<s.blocks, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, s.blocks, counts,
-                                                                     rows, offsets);
-    return launched();
+    if (s.blocks == 1) {
+        sort_place_kernel<I><<<1, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, 1, counts, rows, offsets);
+        return launched();
+    }
+    // the choices are those the first kernel has waited for, so the second may start beside it
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(s.blocks));
+    cfg.blockDim = dim3(SORT_THREADS);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, sort_place_kernel<I>, choices, R, E, s.range, s.warps, s.blocks,
+                                               static_cast<const int *>(counts), rows, offsets);
+    const int st = launched();
+    return st == SGEMM_OK && err != cudaSuccess ? SGEMM_ERR_LAUNCH : st;
 }
 
 }  // namespace
@@ -403,13 +454,14 @@ extern "C" int expert_gather(int type, int T, int J, int H, int E, const int *ro
     const int n = 16 / b;
     const bool vec = H % n == 0 && wide(x, ldx, type) && wide(xs, ldxs, type);
     const int packs = vec ? H / n : H;
-    const long long blocks = blocks_for(static_cast<long long>(T) * packs);
-    if (blocks + ZERO_BLOCKS > INT_MAX) return SGEMM_ERR_INVALID_DIM;
+    const int segments = segments_of(packs, vec);
+    const long long blocks = blocks_for(static_cast<long long>(T) * segments);
+    if (static_cast<long long>(T) * segments > INT_MAX - ROW_THREADS) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: gather");
     return with_rows(type, vec, [&](auto el, auto v) {
         using El = decltype(el);
         gather_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
-            T, J, packs, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks));
+            T, J, packs, segments, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks));
         return launched();
     });
 }
@@ -433,13 +485,14 @@ extern "C" int expert_combine(int type, int T, int J, int H, const int *rows, co
     const int n = 16 / b;
     const bool vec = H % n == 0 && wide(ys, ldys, type) && wide(y, ldy, type) && wide(residual, ldr, type);
     const int packs = vec ? H / n : H;
-    const long long blocks = blocks_for(static_cast<long long>(T) * packs);
-    if (blocks > INT_MAX) return SGEMM_ERR_INVALID_DIM;
+    const int segments = segments_of(packs, vec);
+    const long long blocks = blocks_for(static_cast<long long>(T) * segments);
+    if (static_cast<long long>(T) * segments > INT_MAX - ROW_THREADS) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: combine");
     return with_rows(type, vec, [&](auto el, auto v) {
         using El = decltype(el);
         combine_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks), ROW_THREADS, 0, stream>>>(
-            T, J, packs, rows, weights, static_cast<const El *>(ys), ldys, static_cast<const El *>(residual), ldr,
+            T, J, packs, segments, rows, weights, static_cast<const El *>(ys), ldys, static_cast<const El *>(residual), ldr,
             static_cast<El *>(y), ldy);
         return launched();
     });
@@ -469,7 +522,7 @@ extern "C" int expert_combine_backward(int type, int T, int J, int H, int E, con
     const int n = 16 / b;
     const bool vec = H % n == 0 && wide(dy, lddy, type) && (dweights == nullptr || wide(ys, ldys, type)) && wide(dys, lddys, type);
     const int packs = vec ? H / n : H;
-    const long long blocks = (R + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+    const long long blocks = blocks_for(R);
     if (blocks + ZERO_BLOCKS > INT_MAX) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: combine backward");
     return with_rows(type, vec, [&](auto el, auto v) {

@@ -28,6 +28,7 @@
 
 #include "ctx_key.cuh"
 #include "linear.h"
+#include "linear_few.cuh"
 #include "linear_prep.cuh"
 #include "linear_types.cuh"
 #include "nvtx_range.cuh"
@@ -44,18 +45,23 @@ constexpr int P_BYTES = PROWS * BK * 2;      // 16 KiB
 constexpr int MN_BOX_BYTES = 64 * BK * 2;    // an MN-major box: 64 operand rows x 64 K
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
+constexpr int MAX_SPLITS = 8;                // the portable cluster size
 constexpr int EPI_WARPS = 8;                 // warp w: tensor-memory lanes 32 (w % 4).., column half w / 4
 constexpr int COPY_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
 constexpr int THREADS = (EPI_WARPS + 2) * 32;
 constexpr int EPI_THREADS = EPI_WARPS * 32;
 constexpr int SMEM_MAX = 227 * 1024;
-// FP32: the six products of the pieces, small ones first, so that the last
-// and largest partial sums see the fewest further additions.  A block of
-// KBLK tiles of K runs through all six in tensor memory and is then added in
-// FP32 registers with round-to-nearest: the tensor core's accumulation
-// truncates, and its error grows with the number of additions.
-constexpr int PAIRS = 6;
+// FP32: a stage holds one piece of both operands, and a K tile is the stages
+// of the third, second and first pieces in a row.  Their six products that
+// matter run small ones first, (3,1) (1,3) (2,2) (2,1) (1,2) (1,1), each piece
+// copied once for all of its products and its stage free after the last of
+// them.  The tensor core's accumulation truncates, with an error that grows
+// with the number of additions, so after KBLK tiles of K the accumulator is
+// added in FP32 registers with round-to-nearest and starts again from zero.
+constexpr int PIECES = 3;
+constexpr int PRODUCTS = 6;
 constexpr int KBLK = 2;
+constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles up to 224 tokens
 
 enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
 
@@ -167,10 +173,6 @@ __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &
     }
     return w;
 }
-
-// Piece of P and of Q of FP32 product i: (3,1) (1,3) (2,2) (2,1) (1,2) (1,1), from 0.
-__device__ __forceinline__ int p_piece(int i) { return (0x001102 >> (4 * i)) & 15; }
-__device__ __forceinline__ int q_piece(int i) { return (0x010120 >> (4 * i)) & 15; }
 
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;\n" ::"n"(EPI_THREADS) : "memory"); }
 
@@ -407,17 +409,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         tiles *= p.E;
     tc::Waiter waiter(p.timeout_flag);
 
-    // Stages of a tile: (piece pair, K tile) in order.  FP32 runs each block of
-    // KBLK tiles through the six pairs.  One thread issues the copies and one
-    // the products, so what they run per stage is kept to the least: no
-    // divisions, the stage and its phase counted along.
+    // One thread issues the copies and one the products, so what they run per
+    // stage is kept to the least: no divisions, the stage and its phase counted along.
     const int q_rows = p.bt / CG;
     const uint32_t stage_bytes = p.stage_bytes;
     const int stages = p.stages;
     if (warp == COPY_WARP) {
-        const uint32_t full0 = tc::peer_addr(tc::smem_u32(&full_bar[0]), lead);
+        const uint32_t full0 = CG == 2 ? tc::peer_addr(tc::smem_u32(&full_bar[0]), 0) : tc::smem_u32(&full_bar[0]);
         const uint32_t empty0 = tc::smem_u32(&empty_bar[0]);
-        const uint32_t my_tail = tc::peer_addr(tc::smem_u32(&tail_bar), rank);
+        const uint32_t my_tail = CG == 2 ? tc::peer_addr(tc::smem_u32(&tail_bar), rank) : tc::smem_u32(&tail_bar);
         const uint32_t bytes = P_BYTES + p.q_bytes;
         const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
         const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
@@ -430,53 +430,51 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const int z_p = p.mode == ROWS_BY_EXPERT ? w.e : 0;
             // of K_BY_EXPERT: the K tile that also holds the next expert's rows
             const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
-            for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0) {
-                const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
-                for (int pair = 0; pair < (F32 ? PAIRS : 1); ++pair) {
-                    const int zp = z_p + (F32 ? p_piece(pair) * z_planes : 0), zq = F32 ? q_piece(pair) : 0;
-                    int k = w.kbase + kb * BK;
-                    for (int kt = kb; kt < ke; ++kt, k += BK) {
-                        const uint32_t st = sbase + s * stage_bytes;
-                        const bool tail = kt == tail_kt;
-                        waiter.wait(empty0 + 8u * s, ph);  // passes at once on a ring not yet used
+            int k = w.kbase + w.k0 * BK;
+            for (int kt = w.k0; kt < w.k1; ++kt, k += BK) {
+                const bool tail = kt == tail_kt;
+#pragma unroll
+                for (int piece = F32 ? PIECES - 1 : 0; piece >= 0; --piece) {
+                    const int zp = z_p + piece * z_planes, zq = piece;
+                    const uint32_t st = sbase + s * stage_bytes;
+                    waiter.wait(empty0 + 8u * s, ph);  // passes at once on a ring not yet used
+                    __syncwarp();
+                    if (tc::elect()) {
+                        const uint32_t bar = tail ? my_tail : full0 + 8u * s;
+                        tc::mbar_arrive_expect<CG>(bar, bytes);
+                        if (p_mn) {
+                            tc::tma_load_3d<CG>(st, &maps.p, f0, k, zp, bar);
+                            tc::tma_load_3d<CG>(st + MN_BOX_BYTES, &maps.p, f0 + 64, k, zp, bar);
+                        } else {
+                            tc::tma_load_3d<CG>(st, &maps.p, k, f0, zp, bar);
+                        }
+                        if (q_mn) {
+                            for (int i = 0; i < q_rows; i += 64)
+                                tc::tma_load_3d<CG>(st + P_BYTES + i * (MN_BOX_BYTES / 64), &maps.q, tq + i, k, zq, bar);
+                        } else {
+                            tc::tma_load_3d<CG>(st + P_BYTES, &maps.q, k, tq, zq, bar);
+                        }
+                    }
+                    if (tail) {  // all lanes: both operands are MN-major, a box row is one K
+                        const int k_left = w.k_rows - kt * BK;
                         __syncwarp();
-                        if (tc::elect()) {
-                            const uint32_t bar = tail ? my_tail : full0 + 8u * s;
-                            tc::mbar_arrive_expect(bar, bytes);
-                            if (p_mn) {
-                                tc::tma_load_3d<CG>(st, &maps.p, f0, k, zp, bar);
-                                tc::tma_load_3d<CG>(st + MN_BOX_BYTES, &maps.p, f0 + 64, k, zp, bar);
-                            } else {
-                                tc::tma_load_3d<CG>(st, &maps.p, k, f0, zp, bar);
-                            }
-                            if (q_mn) {
-                                for (int i = 0; i < q_rows; i += 64)
-                                    tc::tma_load_3d<CG>(st + P_BYTES + i * (MN_BOX_BYTES / 64), &maps.q, tq + i, k, zq, bar);
-                            } else {
-                                tc::tma_load_3d<CG>(st + P_BYTES, &maps.q, k, tq, zq, bar);
-                            }
-                        }
-                        if (tail) {  // all lanes: both operands are MN-major, a box row is one K
-                            const int k_left = w.k_rows - kt * BK;
-                            __syncwarp();
-                            waiter.wait(tc::smem_u32(&tail_bar), tails & 1);
-                            ++tails;
-                            const int boxes = static_cast<int>(bytes) / MN_BOX_BYTES;
-                            const int chunks = (BK - k_left) * 8;  // 16-byte chunks to clear in each box
-                            uint8_t *sg = sgen + static_cast<size_t>(s) * stage_bytes + k_left * 128;
-                            for (int b = 0; b < boxes; ++b)
-                                for (int i = lane; i < chunks; i += 32)
-                                    *reinterpret_cast<uint4 *>(sg + b * MN_BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
-                            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0) tc::mbar_arrive(full0 + 8u * s);
-                        }
+                        waiter.wait(tc::smem_u32(&tail_bar), tails & 1);
+                        ++tails;
+                        const int boxes = static_cast<int>(bytes) / MN_BOX_BYTES;
+                        const int chunks = (BK - k_left) * 8;  // 16-byte chunks to clear in each box
+                        uint8_t *sg = sgen + static_cast<size_t>(s) * stage_bytes + k_left * 128;
+                        for (int b = 0; b < boxes; ++b)
+                            for (int i = lane; i < chunks; i += 32)
+                                *reinterpret_cast<uint4 *>(sg + b * MN_BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                         __syncwarp();
-                        issued = min(issued + 1, stages);
-                        if (++s == stages) {
-                            s = 0;
-                            ph ^= 1;
-                        }
+                        if (lane == 0) tc::mbar_arrive(CG == 2 ? full0 + 8u * s : tc::peer_addr(full0 + 8u * s, rank));
+                    }
+                    __syncwarp();
+                    issued = min(issued + 1, stages);
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
             }
@@ -508,26 +506,50 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     tc::fence_after();
                     const uint32_t d = tmem + set * (TMEM_COLS / 2);
                     uint32_t more = 0;
-                    const int steps = (F32 ? PAIRS : 1) * (ke - kb);
-                    for (int i = 0; i < steps; ++i) {
-                        waiter.wait(full0 + 8u * s, ph);
-                        if (p.mode == K_BY_EXPERT && ke == w.k1 && (F32 || i + 1 == steps))  // rows a copying warp cleared
-                            asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
-                        tc::fence_after();
-                        const uint32_t off = (s * stage_bytes) >> 4;
-                        const uint64_t ad = ad0 + off, bd = bd0 + off;
-                        __syncwarp();
-                        if (tc::elect()) {
+                    // 64 K of the operands in two stages (P's and Q's), as four instructions
+                    auto multiply = [&](int sp, int sq) {
+                        const uint64_t ad = ad0 + ((sp * stage_bytes) >> 4), bd = bd0 + ((sq * stage_bytes) >> 4);
 #pragma unroll
-                            for (int j = 0; j < BK / 16; ++j)
-                                tc::umma_f16<CG>(d, ad + j * p_step, bd + j * q_step, idesc, j > 0 ? 1u : more);
-                            tc::umma_commit<CG>(empty0 + 8u * s);
-                        }
+                        for (int j = 0; j < BK / 16; ++j)
+                            tc::umma_f16<CG>(d, ad + j * p_step, bd + j * q_step, idesc, j > 0 ? 1u : more);
                         more = 1;
+                    };
+                    auto advance = [&] {
                         if (++s == stages) {
                             s = 0;
                             ph ^= 1;
                         }
+                    };
+                    for (int kt = kb; kt < ke; ++kt) {
+                        int third = 0, second = 0;
+                        if constexpr (F32) {
+                            waiter.wait(full0 + 8u * s, ph);
+                            third = s;
+                            advance();
+                            waiter.wait(full0 + 8u * s, ph);
+                            second = s;
+                            advance();
+                        }
+                        waiter.wait(full0 + 8u * s, ph);
+                        if (p.mode == K_BY_EXPERT && kt + 1 == w.k1)  // rows that a copying warp cleared
+                            asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+                        tc::fence_after();
+                        __syncwarp();
+                        if (tc::elect()) {
+                            if constexpr (F32) {
+                                multiply(third, s);
+                                multiply(s, third);
+                                tc::umma_commit<CG>(empty0 + 8u * third);
+                                multiply(second, second);
+                                multiply(second, s);
+                                multiply(s, second);
+                                tc::umma_commit<CG>(empty0 + 8u * second);
+                            }
+                            multiply(s, s);
+                            tc::umma_commit<CG>(empty0 + 8u * s);
+                        }
+                        more = 1;
+                        advance();
                     }
                     __syncwarp();
                     if (tc::elect()) tc::umma_commit<CG>(tc::smem_u32(&acc_full[set]));
@@ -553,10 +575,12 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             if (p.bias != nullptr && f_ok && !w.none)
                 bias = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + f]);
             const bool any = w.k1 > w.k0;
-            float total[F32 ? 128 : 1];
+            float total[F32 ? F32_COLS : 1];
             if constexpr (F32) {
+                if (p.residual != nullptr && !w.none && S == 1 && f - lane < p.F)
+                    prefetch_residual<T>(p, static_cast<long long>(w.t0) + col0, min(cols, n_tile - col0), f - lane, lane);
 #pragma unroll
-                for (int c = 0; c < 128; ++c) total[c] = 0.0f;
+                for (int c = 0; c < F32_COLS; ++c) total[c] = 0.0f;
                 for (int kb = w.k0; kb < w.k1; kb += KBLK, ++g) {
                     const uint32_t set = g & 1;
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
@@ -564,7 +588,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     tc::fence_after();
                     const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 16)
+                    for (int c = 0; c < F32_COLS; c += 16)
                         if (c < cols) {
                             float v[16];
                             tc::tmem_ld16(t_set + c, v);
@@ -588,7 +612,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     tc::fence_after();
                 }
 #pragma unroll
-                for (int c = 0; c < 128; c += 16)
+                for (int c = 0; c < 64; c += 16)  // split tiles have at most 128 tokens
                     if (c < cols) {
                         float v[16];
                         if constexpr (F32) {
@@ -607,7 +631,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
             } else if constexpr (F32) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 16)
+                for (int c = 0; c < F32_COLS; c += 16)
                     if (c < cols && f_ok && (S == 1 || rank == 0)) {
                         float v[16];
 #pragma unroll
@@ -692,24 +716,50 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 epi_bar();
                 if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_ready), threadIdx.x));
                 waiter.wait<true>(tc::smem_u32(&part_ready), handed & 1);
-                // the parts' sum in rank order, 32 features of a token per warp, shared out over all CTAs
+                // the parts' sum in rank order, four features of a token per thread, shared out over
+                // all CTAs; the parts' loads are in flight together
                 const uint32_t mine = tc::smem_u32(partial);
                 const int fb = w.ft * PROWS;
-                for (int i = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i < n_tile * PROWS; i += S * EPI_THREADS) {
-                    float sum = 0.0f;
-                    for (int s = 0; s < S; ++s) sum += tc::ld_cluster_f32(tc::peer_addr(mine + 4u * i, s));
-                    const int fi = fb + (i & (PROWS - 1));
-                    if (fi < p.F) {
-                        float b = 0.0f;
-                        if (p.bias != nullptr)
-                            b = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + fi]);
-                        const long long row = static_cast<long long>(w.t0) + i / PROWS;
-                        float v = sum + b;
-                        if (p.z != nullptr) static_cast<T *>(p.z)[row * p.ldz + fi] = from_f<T>(v);
-                        lt::with_activation(p.act, [&](auto a) { v = lt::activate<decltype(a)::value, F32>(v); });
-                        if (p.residual != nullptr) v += to_f(static_cast<const T *>(p.residual)[row * p.ldr + fi]);
-                        out[row * p.ldo + fi] = from_f<T>(v);
+                for (int i = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i < n_tile * (PROWS / 4);
+                     i += S * EPI_THREADS) {
+                    const int fi = fb + 4 * (i & (PROWS / 4 - 1));
+                    if (fi >= p.F) continue;
+                    float4 part[MAX_SPLITS];
+#pragma unroll
+                    for (int s = 0; s < MAX_SPLITS; ++s)
+                        part[s] = s < S ? tc::ld_cluster_f32x4(tc::peer_addr(mine + 16u * i, s)) : make_float4(0, 0, 0, 0);
+                    const long long row = static_cast<long long>(w.t0) + i / (PROWS / 4);
+                    const T *bp = p.bias == nullptr ? nullptr
+                                                    : static_cast<const T *>(p.bias) +
+                                                          (p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + fi;
+                    const T *rp = p.residual == nullptr ? nullptr : static_cast<const T *>(p.residual) + row * p.ldr + fi;
+                    float v[4], b[4] = {0, 0, 0, 0}, r[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (fi + k < p.F) {
+                            if (bp != nullptr) b[k] = to_f(bp[k]);
+                            if (rp != nullptr) r[k] = to_f(rp[k]);
+                        }
+                    v[0] = part[0].x, v[1] = part[0].y, v[2] = part[0].z, v[3] = part[0].w;
+#pragma unroll
+                    for (int s = 1; s < MAX_SPLITS; ++s)
+                        v[0] += part[s].x, v[1] += part[s].y, v[2] += part[s].z, v[3] += part[s].w;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] += b[k];
+                    if (p.z != nullptr) {
+                        T *z = static_cast<T *>(p.z) + row * p.ldz + fi;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (fi + k < p.F) z[k] = from_f<T>(v[k]);
                     }
+                    lt::with_activation(p.act, [&](auto a) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = lt::activate<decltype(a)::value, F32>(v[k]);
+                    });
+                    T *o = out + row * p.ldo + fi;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (fi + k < p.F) o[k] = from_f<T>(rp != nullptr ? v[k] + r[k] : v[k]);
                 }
                 epi_bar();
                 if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_read), threadIdx.x));
@@ -861,7 +911,7 @@ const Tune &tune() {
 }
 
 // Time of a plan in SM clocks.  A K tile of a CTA (128 features, bt tokens, 64
-// K) takes the longest of three: the tensor cores' bt/2 clocks per 16 K (2.2 bt
+// K; FP32: three stages of pieces) takes the longest of three: the tensor cores' bt/2 clocks per 16 K (2.2 bt
 // measured for the four with bt = 256), the bytes that it copies at what L2
 // gives an SM when all copy (62 a clock measured), and the issue of a stage
 // (370 clocks measured with narrow tiles).  Whole waves of tiles count, and
@@ -869,13 +919,13 @@ const Tune &tune() {
 // clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 78, 256 wide 86,
 // 128 wide 97; single CTAs 256 wide 102, 128 wide 135.
 Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
-    const int passes = type == LINEAR_F32 ? PAIRS : 1;
+    const bool f32 = type == LINEAR_F32;
     Plan best;
     const int bts[] = {256, 224, 192, 160, 128, 96, 64, 32, 16};
     for (int cg = 2; cg >= 1; --cg)
         for (int bt : bts) {
             if (cg == 2 && (bt < 64 || bt % 32 != 0)) continue;
-            if (p.q_mn && bt / cg % 64 != 0) continue;
+            if ((p.q_mn && bt / cg % 64 != 0) || (f32 && bt > 2 * F32_COLS)) continue;
             if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
             double nt, ktiles = (p.K + BK - 1) / BK;
             if (p.mode == ROWS_BY_EXPERT) {
@@ -892,20 +942,22 @@ Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
             }
             const double tiles = nt * ((p.F + PROWS * cg - 1) / (PROWS * cg));
             double per = 370.0;
-            if (2.2 * bt > per) per = 2.2 * bt;
             const double copy = (P_BYTES + bt / cg * 128) / 62.0;
             if (copy > per) per = copy;
-            per *= passes;
+            if (f32) per *= PIECES;
+            const double mma = (f32 ? PRODUCTS : 1) * 2.2 * bt;
+            if (mma > per) per = mma;
             const double drain = 1000.0 + 12.0 * bt;
-            const int most = cg == 2 || bt > 128 ? 1 : 8;
+            const int most = cg == 2 || bt > 128 ? 1 : MAX_SPLITS;
             for (int s = 1; s <= most; ++s) {
                 if (s > 1 && s * 2 > ktiles) break;
                 if (only.splits != 0 && only.splits != s) continue;
                 const int units = cg == 2 ? d.pairs : d.sms / s;
                 double waves = static_cast<double>(static_cast<long long>((tiles + units - 1) / units));
                 if (waves < 1) waves = 1;
+                if (s > 1 && waves > 1 && only.splits == 0) break;  // a split is for fewer tiles than SMs
                 const double body = ktiles / s * per + 200.0;
-                const double cost = waves * (body > drain ? body : drain) + drain + (s > 1 ? 2500.0 : 0.0) + 2000.0;
+                const double cost = waves * (body > drain ? body : drain) + drain + (s > 1 ? 1500.0 + 45.0 * bt : 0.0) + 2000.0;
                 if (cost < best.cost * 0.99) {
                     best.cost = cost;
                     best.cg = cg;
@@ -1123,8 +1175,10 @@ Matrix row_matrix(const void *p, int rows, int width, long long ld) {
     return m;
 }
 
+bool few_tokens(const Call &c) { return c.E < 0 && c.M <= linear_few::MAX_TOKENS && c.K > 0; }
+
 size_t forward_bytes(const Call &c) {
-    if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.K == 0 || c.E == 0) return 0;
+    if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.K == 0 || c.E == 0 || few_tokens(c)) return 0;
     return operand_bytes(c.type, row_matrix(c.x, c.M, c.K, c.ldx)) + operand_bytes(c.type, weight_matrix(c));
 }
 
@@ -1159,6 +1213,15 @@ int forward(const Call &c) {
     Device d;
     st = set_up(&d);
     if (st != SGEMM_OK) return st;
+    if (few_tokens(c)) {
+        linear_few::Few p;
+        p.T = c.M, p.F = c.N, p.K = c.K, p.x = c.x, p.w = c.w, p.bias = c.bias, p.residual = c.residual;
+        p.z = c.preact, p.out = c.y, p.ldx = c.ldx, p.ldw = c.ldw, p.ldr = c.ldr, p.ldz = c.ldz, p.ldo = c.ldy;
+        p.order = c.w_order, p.act = c.act;
+        if (linear_few::run(c.type, p, c.stream) == cudaSuccess) return SGEMM_OK;
+        (void)cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    }
     char *ws = static_cast<char *>(c.ws);
     Operand P, Q;
     if (c.K > 0 && c.E != 0) {

@@ -13,6 +13,7 @@
 namespace {
 
 using lt::from_f;
+using lt::pieces;
 using lt::to_f;
 
 template <typename T>
@@ -23,17 +24,6 @@ template <typename T>
 struct alignas(16) Chunk {  // 16 bytes
     T v[16 / sizeof(T)];
 };
-
-// x = a + b + c to 2^-27 |x|, a and b rounded to nearest; a is cut instead
-// where rounding would overflow, and carries an infinity or NaN alone.
-__device__ __forceinline__ void pieces(float x, __nv_bfloat16 &a, __nv_bfloat16 &b, __nv_bfloat16 &c) {
-    a = __float2bfloat16_rn(x);
-    const bool finite = fabsf(x) <= 3.402823466e38f;
-    if (finite && fabsf(__bfloat162float(a)) > 3.402823466e38f) a = __float2bfloat16_rz(x);
-    const float r = finite ? x - __bfloat162float(a) : 0.0f;
-    b = __float2bfloat16_rn(r);
-    c = __float2bfloat16_rn(r - __bfloat162float(b));
-}
 
 // 8 consecutive values per thread; VEC: aligned 16-byte loads.  Bound by HBM:
 // 4 bytes read and 6 written per FP32 value.

@@ -53,6 +53,17 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
+// x = a + b + c to 2^-27 |x|, a and b rounded to nearest; a is cut instead
+// where rounding would overflow, and carries an infinity or NaN alone.
+__device__ __forceinline__ void pieces(float x, __nv_bfloat16 &a, __nv_bfloat16 &b, __nv_bfloat16 &c) {
+    a = __float2bfloat16_rn(x);
+    const bool finite = fabsf(x) <= 3.402823466e38f;
+    if (finite && fabsf(__bfloat162float(a)) > 3.402823466e38f) a = __float2bfloat16_rz(x);
+    const float r = finite ? x - __bfloat162float(a) : 0.0f;
+    b = __float2bfloat16_rn(r);
+    c = __float2bfloat16_rn(r - __bfloat162float(b));
+}
+
 inline int type_bytes(int type) { return type == LINEAR_F32 ? 4 : 2; }
 
 // EXACT (FP32 tensors): the library's accurate exponential and division; the

@@ -36,9 +36,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t smem_addr, uint32_t rank)
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 
@@ -46,14 +49,18 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
 }
-// Arrive (and announce `bytes` of copies) on a barrier of any CTA of the
-// cluster.  Relaxed: the waiting thread is to see what the copies wrote, and
+// Arrive and announce `bytes` of copies on a barrier of this CTA, or (CG = 2)
+// of either CTA of the pair.  Relaxed: the waiting thread is to see what the copies wrote, and
 // they order that themselves; a release here waits out the thread's earlier
 // copies' issue, about 0.9 us a stage.
-__device__ __forceinline__ void mbar_arrive_expect(uint32_t cluster_bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_bar),
-                 "r"(bytes)
-                 : "memory");
+template <int CG>
+__device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
+    if constexpr (CG == 2)
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
+                     : "memory");
+    else
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
+                     : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
