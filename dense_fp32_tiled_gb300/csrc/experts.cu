@@ -43,9 +43,9 @@ SortPlan sort_plan(long long R, int E) {
     if (s.range < 32) s.range = 32;
     s.blocks = static_cast<int>((R + s.range - 1) / s.range);
     if (s.blocks < 1) s.blocks = 1;
-    const int most = SORT_SMEM / 4 / E - 1;  // tables of E counts that fit
+    const int most = SORT_SMEM / 4 / E - 3;  // tables of E counts that fit, beside three for all warps
     s.warps = most < SORT_THREADS / 32 ? most : SORT_THREADS / 32;
-    s.smem = static_cast<size_t>(s.warps + 1) * E * 4;
+    s.smem = static_cast<size_t>(s.warps + 3) * E * 4;
     return s;
 }
 
@@ -97,9 +97,11 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
     extern __shared__ int shared[];
     __shared__ int sums[32];
     int *base = shared;                  // E: the expert's first place in this range
-    int *mine = shared + E;              // warps x E
+    int *totals = shared + E;            // E: all its choices
+    int *earlier = totals + E;           // E: those in the ranges before this one
+    int *mine = earlier + E;             // warps x E
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < warps * E; i += SORT_THREADS) mine[i] = 0;
+    for (int i = threadIdx.x; i < (warps + 2) * E; i += SORT_THREADS) totals[i] = 0;
     __syncthreads();
     const long long begin = static_cast<long long>(blockIdx.x) * range;
     const long long end = begin + range < R ? begin + range : R;
@@ -109,6 +111,16 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
         for (long long i = b; i < e1; i += 32) count32(choice_at(choices, i + lane, e1, E), mine + warp * E, lane);
     __syncthreads();
     tc::grid_wait();  // the counts are there, and rows and offsets no longer in use
+    if (blocks > 1) {
+        for (int i = threadIdx.x; i < blocks * E; i += SORT_THREADS) {
+            const int k = i / E, e = i - k * E, n = counts[i];
+            if (n != 0) {  // whole numbers: any order gives the same sums
+                atomicAdd(totals + e, n);
+                if (k < static_cast<int>(blockIdx.x)) atomicAdd(earlier + e, n);
+            }
+        }
+        __syncthreads();
+    }
     // per expert: all its choices, those before this range, and the warps' first places;
     // the running sum over the experts carries from one group of 1024 to the next
     int carry = 0;
@@ -122,15 +134,8 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
                 mine[w * E + e] = own;
                 own += n;
             }
-            if (blocks == 1) {
-                total = own;
-            } else {
-                for (int k = 0; k < blocks; ++k) {
-                    const int n = counts[static_cast<long long>(k) * E + e];
-                    total += n;
-                    if (k < static_cast<int>(blockIdx.x)) before += n;
-                }
-            }
+            total = blocks == 1 ? own : totals[e];
+            before = earlier[e];
         }
         int scan = total;
 #pragma unroll
@@ -165,18 +170,65 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
 }
 
 // ---- rows --------------------------------------------------------------------------
-// V values (16 bytes, or one) of a row.
+// V values (16 bytes, or one) of a row, as the words they travel in: a load
+// that may not happen is then one predicated instruction, and the next ones
+// follow it at once.
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
+struct Pack {
+    using Raw = typename std::conditional<V != 1, uint4, typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type>::type;
+    Raw raw;
+    __device__ __forceinline__ void clear() {
+        if constexpr (V != 1)
+            raw = make_uint4(0u, 0u, 0u, 0u);
+        else
+            raw = 0;
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+        if constexpr (V == 1) {
+            f[0] = to_f(*reinterpret_cast<const T *>(&raw));
+        } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = lt::unpack2<T>(w[i]);
+                    f[2 * i] = v.x;
+                    f[2 * i + 1] = v.y;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+        if constexpr (V == 1) {
+            const T v = from_f<T>(f[0]);
+            raw = *reinterpret_cast<const Raw *>(&v);
+        } else if constexpr (sizeof(T) == 4) {
+            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        } else {
+            raw = make_uint4(lt::pack2<T>(f[0], f[1]), lt::pack2<T>(f[2], f[3]), lt::pack2<T>(f[4], f[5]), lt::pack2<T>(f[6], f[7]));
+        }
+    }
 };
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load(const T *p) {
-    return *reinterpret_cast<const Pack<T, V> *>(p);
+    Pack<T, V> v;
+    v.raw = *reinterpret_cast<const typename Pack<T, V>::Raw *>(p);
+    return v;
+}
+// The values at p, or zeros.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_if(bool in, const T *p) {
+    Pack<T, V> v;
+    v.clear();
+    if (in) v.raw = *reinterpret_cast<const typename Pack<T, V>::Raw *>(p);
+    return v;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const Pack<T, V> &v) {
-    *reinterpret_cast<Pack<T, V> *>(p) = v;
+    *reinterpret_cast<typename Pack<T, V>::Raw *>(p) = v.raw;
 }
 
 constexpr int ROW_THREADS = 256;
@@ -187,8 +239,7 @@ template <typename T, int V>
 __device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long long R, int packs, int block) {
     const long long first = static_cast<long long>(min(max(used, 0), static_cast<int>(R))) * packs;
     Pack<T, V> zero;
-#pragma unroll
-    for (int i = 0; i < V; ++i) zero.v[i] = from_f<T>(0.0f);
+    zero.clear();
     for (long long u = first + static_cast<long long>(block) * ROW_THREADS + threadIdx.x; u < R * packs;
          u += static_cast<long long>(ZERO_BLOCKS) * ROW_THREADS) {
         const long long r = u / packs;
@@ -196,9 +247,12 @@ __device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long 
     }
 }
 
-// A warp takes a segment of one token's row: SEG accesses per lane, all in
-// flight together, with the token's places read once for them.
-__host__ __device__ constexpr int seg_of(int V) { return V > 1 ? 4 : 8; }
+// A warp takes a segment of one token's row: SEG accesses per lane.  With 16-byte
+// ones a single access per lane and four of the token's rows in flight serve the
+// sum best (16384 tokens, 4 choices, 4096 wide in bf16: 134 us; two accesses and
+// two rows 137, four and two 183: fewer registers, more warps); single values
+// want eight (5000 tokens, 6 choices, 1001 wide in FP32: 27 us, one 48).
+__host__ __device__ constexpr int seg_of(int V) { return V > 1 ? 1 : 8; }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(ROW_THREADS)
@@ -218,7 +272,7 @@ gather_kernel(int T_, int J, int packs, int segments, int E, const int *__restri
     Pack<T, V> v[SEG];
 #pragma unroll
     for (int i = 0; i < SEG; ++i)
-        if (c0 + 32 * i < packs) v[i] = load<T, V>(x + t * ldx + static_cast<long long>(c0 + 32 * i) * V);
+        v[i] = load_if<T, V>(c0 + 32 * i < packs, x + t * ldx + static_cast<long long>(c0 + 32 * i) * V);
     const int *at = rows + static_cast<long long>(t) * J;
     for (int j = 0; j < J; ++j) {
         const int r = at[j];
@@ -234,7 +288,7 @@ __global__ void __launch_bounds__(ROW_THREADS)
 combine_kernel(int T_, int J, int packs, int segments, const int *__restrict__ rows, const float *__restrict__ weights,
                const T *__restrict__ ys, long long ldys, const T *residual, long long ldr, T *y, long long ldy) {
     constexpr int SEG = seg_of(V);
-    constexpr int U = 2;  // rows in flight
+    constexpr int U = V > 1 ? 4 : 2;  // rows in flight
     const long long R = static_cast<long long>(T_) * J;
     const int unit = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     const int t = unit / segments;
@@ -257,34 +311,31 @@ combine_kernel(int T_, int J, int packs, int segments, const int *__restrict__ r
             const bool in = r >= 0 && r < R;
             if (in) w[u] = weights != nullptr ? wt[j0 + u] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < SEG; ++i) {
-                if (in && c0 + 32 * i < packs) {
-                    v[u][i] = load<T, V>(ys + r * ldys + static_cast<long long>(c0 + 32 * i) * V);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) v[u][i].v[k] = from_f<T>(0.0f);
-                }
-            }
+            for (int i = 0; i < SEG; ++i)
+                v[u][i] = load_if<T, V>(in && c0 + 32 * i < packs, ys + r * ldys + static_cast<long long>(c0 + 32 * i) * V);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < SEG; ++i)
+            for (int i = 0; i < SEG; ++i) {
+                float f[V];
+                v[u][i].get(f);
 #pragma unroll
-                for (int k = 0; k < V; ++k) sum[i][k] = fmaf(w[u], to_f(v[u][i].v[k]), sum[i][k]);
+                for (int k = 0; k < V; ++k) sum[i][k] = fmaf(w[u], f[k], sum[i][k]);
+            }
     }
 #pragma unroll
     for (int i = 0; i < SEG; ++i) {
         const long long c = static_cast<long long>(c0 + 32 * i) * V;
         if (c0 + 32 * i >= packs) continue;
         if (residual != nullptr) {
-            const Pack<T, V> r = load<T, V>(residual + t * ldr + c);
+            float f[V];
+            load<T, V>(residual + t * ldr + c).get(f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) sum[i][k] += to_f(r.v[k]);
+            for (int k = 0; k < V; ++k) sum[i][k] += f[k];
         }
         Pack<T, V> o;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o.v[k] = from_f<T>(sum[i][k]);
+        o.set(sum[i]);
         store<T, V>(y + t * ldy + c, o);
     }
 }
@@ -313,17 +364,19 @@ combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__
     const T *d = dy + i / J * lddy, *s = ys + r * ldys;
     T *o = dys + r * lddys;
     float dot = 0.0f;
-#pragma unroll seg_of(V)
+#pragma unroll(V > 1 ? 4 : 8)
     for (int p = lane; p < packs; p += 32) {
-        const Pack<T, V> g = load<T, V>(d + static_cast<long long>(p) * V);
-        if (dweights != nullptr) {
-            const Pack<T, V> v = load<T, V>(s + static_cast<long long>(p) * V);
+        float g[V], f[V];
+        const Pack<T, V> gv = load<T, V>(d + static_cast<long long>(p) * V);
+        const Pack<T, V> fv = load_if<T, V>(dweights != nullptr, s + static_cast<long long>(p) * V);
+        gv.get(g);
+        fv.get(f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) dot = fmaf(to_f(g.v[k]), to_f(v.v[k]), dot);
-        }
+        for (int k = 0; k < V; ++k) dot = fmaf(g[k], f[k], dot);
+#pragma unroll
+        for (int k = 0; k < V; ++k) g[k] *= w;
         Pack<T, V> q;
-#pragma unroll
-        for (int k = 0; k < V; ++k) q.v[k] = from_f<T>(w * to_f(g.v[k]));
+        q.set(g);
         store<T, V>(o + static_cast<long long>(p) * V, q);
     }
     if (dweights != nullptr) {

@@ -117,9 +117,8 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
     tc::grid_wait();
-    // the weight one group of steps ahead of the products
-    Words<ORDER ? 4 : 2> wv[UNROLL][ORDER ? TILES : 4], next[UNROLL][ORDER ? TILES : 4];
-    auto load_w = [&](int s, Words<ORDER ? 4 : 2>(&v)[UNROLL][ORDER ? TILES : 4]) {
+    for (int s = s0; s < s1; s += UNROLL) {
+        Words<ORDER ? 4 : 2> wv[UNROLL][ORDER ? TILES : 4];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int k = (s + u) * STEP + t * XN;
@@ -128,19 +127,15 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
                     const int f = f0 + 8 * i + g;
-                    v[u][i] = fetch16<8, VEC>(w + f * p.ldw + k, in && f < p.F ? p.K - k : 0);
+                    wv[u][i] = fetch16<8, VEC>(w + f * p.ldw + k, in && f < p.F ? p.K - k : 0);
                 }
             } else {
                 const int f = f0 + 4 * g;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[u][i] = fetch16<4, VEC>(w + (k + i) * p.ldw + f, in && k + i < p.K ? p.F - f : 0);
+                    wv[u][i] = fetch16<4, VEC>(w + (k + i) * p.ldw + f, in && k + i < p.K ? p.F - f : 0);
             }
         }
-    };
-    load_w(s0, wv);
-    for (int s = s0; s < s1; s += UNROLL) {
-        load_w(s + UNROLL, next);
         Words<XN / 2> lo[UNROLL], hi[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
@@ -165,10 +160,6 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
                     }
                 }
             }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-            for (int i = 0; i < (ORDER ? TILES : 4); ++i) wv[u][i] = next[u][i];
     }
     // fragment (g, t): tokens g and g + 8, columns 2 t and 2 t + 1 of each tile
 #pragma unroll

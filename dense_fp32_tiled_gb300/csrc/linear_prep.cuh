@@ -10,11 +10,17 @@
 namespace linear_prep {
 
 // `planes` matrices of `outer` rows of `inner` values (row stride ld, plane
-// stride plane, in elements), copied to dst with rows of up8(inner) values.
-// FP32: as three bf16 pieces, piece i of matrix e at
+// stride plane, in elements), to be copied to dst with rows of up8(inner)
+// values.  FP32: as three bf16 pieces, piece i of matrix e at
 // dst + (i*planes + e) * outer * up8(inner).
-cudaError_t copy_operand(int type, const void *src, long long ld, long long plane, int inner, int outer, int planes,
-                         void *dst, cudaStream_t stream);
+struct Copy {
+    const void *src;
+    long long ld, plane;
+    int inner, outer, planes;
+    void *dst;
+};
+// One or two of them in one launch.
+cudaError_t copy_operands(int type, const Copy *copies, int n, cudaStream_t stream);
 
 // Workspace of activation_gradient's column sums.
 size_t sums_bytes(int M, int N, int E);
