@@ -513,6 +513,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             int s = 0;
             for (int idx = unit; idx < tiles; idx += units) {
                 const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+                const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
                 for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0, ++g) {
                     const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
                     const uint32_t set = g & 1;
@@ -545,7 +546,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             advance();
                         }
                         waiter.wait(full0 + 8u * s, ph);
-                        if (p.mode == K_BY_EXPERT && kt + 1 == w.k1)  // rows that a copying warp cleared
+                        if (kt == tail_kt)  // rows that the tail warps cleared, here and in the other CTA
                             asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
                         tc::fence_after();
                         __syncwarp();
@@ -612,10 +613,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         }
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(acc_empty0 + 8u * set);
+                    if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
                 }
             }
             const uint32_t set = g & 1;
+            bool freed = false;  // the accumulators are reported read
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
             if (S > 1 && !w.none) {
                 // hand this CTA's part over: wait until the last one is read, store, tell all
@@ -687,7 +689,14 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = next[i];
                     const bool more = any && c + 16 < n_warp;
-                    if (more) tc::tmem_ld_frag(t_set + c + 16, next);  // arrives while these are finished
+                    if (more) {
+                        tc::tmem_ld_frag(t_set + c + 16, next);  // arrives while these are finished
+                    } else if (any) {  // all read: the accumulators are free while the rest is finished
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                        freed = true;
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] += b[2 * (i >> 3) + (i >> 1 & 1)];
                     if (p.z != nullptr)
@@ -721,9 +730,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 }
             }
             if (!F32 && any) {
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(acc_empty0 + 8u * set);
+                if (!freed) {
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                }
                 ++g;
             }
             if (S > 1 && !w.none) {

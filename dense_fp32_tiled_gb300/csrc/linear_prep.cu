@@ -240,15 +240,24 @@ cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offse
     const long long blocks = (static_cast<long long>(M) + CHUNK - 1) / CHUNK * strips;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
-    lt::with_activation(act, [&](auto a) {
-        constexpr int ACT = decltype(a)::value;
+    auto launch = [&](auto kernel) {
+        kernel<<<grid, GWARPS * 32, 0, stream>>>(M, N, E, offsets, static_cast<const T *>(dy), lddy,
+                                                 static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
+    };
+    auto pick = [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
         if (vec)
-            activation_gradient_kernel<T, V, ACT><<<grid, GWARPS * 32, 0, stream>>>(
-                M, N, E, offsets, static_cast<const T *>(dy), lddy, static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
+            launch(activation_gradient_kernel<T, V, ACT>);
         else
-            activation_gradient_kernel<T, 1, ACT><<<grid, GWARPS * 32, 0, stream>>>(
-                M, N, E, offsets, static_cast<const T *>(dy), lddy, static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
-    });
+            launch(activation_gradient_kernel<T, 1, ACT>);
+    };
+    switch (act) {
+        case LINEAR_ACT_RELU: pick(lt::Int<LINEAR_ACT_RELU>{}); break;
+        case LINEAR_ACT_SILU: pick(lt::Int<LINEAR_ACT_SILU>{}); break;
+        case LINEAR_ACT_GELU: pick(lt::Int<LINEAR_ACT_GELU>{}); break;
+        case LINEAR_ACT_GELU_TANH: pick(lt::Int<LINEAR_ACT_GELU_TANH>{}); break;
+        default: pick(lt::Int<LINEAR_ACT_NONE>{}); break;
+    }
     cudaError_t err = cudaPeekAtLastError();
     if (err == cudaSuccess && sums != nullptr) {
         const dim3 g2(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(E < 0 ? 1 : E));

@@ -66,31 +66,60 @@ __device__ __forceinline__ void pieces(float x, __nv_bfloat16 &a, __nv_bfloat16 
 
 inline int type_bytes(int type) { return type == LINEAR_F32 ? 4 : 2; }
 
-// EXACT (FP32 tensors): the library's accurate exponential and division; the
-// 16-bit types round to 8 or 11 bits afterwards, so there the fast forms (a
-// few units in the last place of FP32) change nothing that is kept.
-template <bool EXACT>
-__device__ __forceinline__ float exp_of(float x) {
-    return EXACT ? expf(x) : __expf(x);
+// EXACT (FP32 tensors): the library's exponential and division.  The 16-bit
+// types round to 8 or 11 bits afterwards, so there the hardware's approximate
+// instructions do, 2^-22 of the value, in the form that takes subnormal numbers
+// for 0 (the other one, which __expf and __fdividef compile to, scales around
+// them and costs an epilogue of a tile about as much again).
+__device__ __forceinline__ float fast_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-template <bool EXACT>
-__device__ __forceinline__ float quotient(float a, float b) {
-    return EXACT ? a / b : __fdividef(a, b);
+__device__ __forceinline__ float fast_reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
+constexpr float kLog2E = 1.4426950408889634f;
 template <bool EXACT>
 __device__ __forceinline__ float logistic(float x) {
-    return quotient<EXACT>(1.0f, 1.0f + exp_of<EXACT>(-x));
+    return EXACT ? 1.0f / (1.0f + expf(-x)) : fast_reciprocal(1.0f + fast_exp2(-kLog2E * x));
 }
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi): (1 + tanh u) / 2 = logistic(2 u)
 constexpr float kGeluB = 0.044715f;
 constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
+// The normal distribution's upper tail at |z|, erfc(|z| / sqrt 2) / 2, and
+// exp(-z^2 / 2) on the way, for the 16-bit types: exp(-z^2 / 2) times a
+// polynomial in t = 1 / (1 + |z| / 5), fitted to the scaled tail erfcx / 2 with
+// least largest relative error (1.3e-6 for |z| up to 14, where the tail has
+// long left their range).  One exponential and one quotient, where erff takes
+// both of its branches in a warp.
+__device__ __forceinline__ float normal_tail(float z, float &gauss) {
+    const float a = fabsf(z);
+    gauss = fast_exp2((-0.5f * kLog2E) * a * a);
+    const float t = fast_reciprocal(fmaf(0.2f, a, 1.0f));
+    float q = fmaf(t, 0.2790941894f, -0.3868259490f);
+    q = fmaf(t, q, 0.4469392002f);
+    q = fmaf(t, q, -0.1231861413f);
+    q = fmaf(t, q, 0.1325369924f);
+    q = fmaf(t, q, 0.0710921586f);
+    q = fmaf(t, q, 0.0803501904f);
+    return q * t * gauss;
+}
+
 template <int ACT, bool EXACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == LINEAR_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
     if constexpr (ACT == LINEAR_ACT_SILU) return z * logistic<EXACT>(z);
-    if constexpr (ACT == LINEAR_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+    if constexpr (ACT == LINEAR_ACT_GELU) {
+        if constexpr (EXACT) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+        float gauss;
+        const float tail = z * normal_tail(z, gauss);
+        return z < 0.0f ? tail : z - tail;
+    }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) return z * logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
     return z;
 }
@@ -102,8 +131,12 @@ __device__ __forceinline__ float slope(float z) {
         const float p = logistic<EXACT>(z);
         return p * (1.0f + z * (1.0f - p));
     }
-    if constexpr (ACT == LINEAR_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * exp_of<EXACT>(-0.5f * z * z);
+    if constexpr (ACT == LINEAR_ACT_GELU) {
+        if constexpr (EXACT) return 0.5f * (1.0f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+        float gauss;
+        const float tail = normal_tail(z, gauss);
+        return (z < 0.0f ? tail : 1.0f - tail) + z * kInvSqrt2Pi * gauss;
+    }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) {
         const float p = logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
         return p + z * p * (1.0f - p) * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
@@ -111,13 +144,13 @@ __device__ __forceinline__ float slope(float z) {
     return 1.0f;
 }
 
-// f(std::integral_constant-like tag) for the activation `act`.
+// f(tag) for the activation `act`, the tag's value a constant.
 template <int V>
 struct Int {
     static constexpr int value = V;
 };
 template <typename F>
-__host__ __device__ __forceinline__ void with_activation(int act, F &&f) {
+__device__ __forceinline__ void with_activation(int act, F &&f) {
     switch (act) {
         case LINEAR_ACT_RELU: f(Int<LINEAR_ACT_RELU>{}); break;
         case LINEAR_ACT_SILU: f(Int<LINEAR_ACT_SILU>{}); break;

@@ -65,6 +65,12 @@ __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes)
 __device__ __forceinline__ void mbar_arrive(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
+// Arrive on a barrier of any CTA of the cluster without handing over anything
+// that this thread wrote (tensor memory read empty: the tcgen05 fences order
+// that).  A release would first wait for the thread's stores to reach L2.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
+}
 // CLUSTER: what the arriving threads of other CTAs wrote themselves is to be
 // seen.  What copies and products wrote needs no more than the CTA's scope,
 // and the wider one costs each wait some hundred nanoseconds.
