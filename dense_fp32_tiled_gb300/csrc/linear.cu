@@ -44,6 +44,7 @@ constexpr int PROWS = 128;                   // features per CTA
 constexpr int P_BYTES = PROWS * BK * 2;      // 16 KiB
 constexpr int MN_BOX_BYTES = 64 * BK * 2;    // an MN-major box: 64 operand rows x 64 K
 constexpr int MAX_STAGES = 12;
+constexpr int SORTED_EXPERTS = 256;         // of more, sorting by rows would take longer than it saves
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_SPLITS = 8;                // the portable cluster size
 constexpr int EPI_WARPS = 8;                 // warp w: tensor-memory lanes 32 (w % 4).., column half w / 4
@@ -73,7 +74,7 @@ struct Product {
     int nt, nf;               // tiles in tokens (DENSE, K_BY_EXPERT) and in features
     int splits;               // CTAs of a cluster that share the K of a tile (CG = 1)
     int stages, stage_bytes, q_bytes;
-    int epi_offset;           // of the epilogue's buffers in dynamic shared memory
+    int epi_offset, epi_bytes;  // the epilogue's buffers in dynamic shared memory, per warp
     int p_mn, q_mn;
     const void *bias, *residual;
     void *z, *out;
@@ -96,11 +97,19 @@ struct Tile {
 
 // Experts' tables in shared memory: clamped first rows and, for
 // ROWS_BY_EXPERT, the first tile of each (group E: the rows of no expert).
+// K_BY_EXPERT: the experts in falling order of rows.
 struct Tables {
     const int *begin;  // E + 2
     const int *first;  // E + 2
 };
 
+// The unit's tile after idx: the same place in the next round of `units` tiles,
+// or, where tiles come in falling order of length, back and forth, so that no
+// unit always gets the longer ones.
+__device__ __forceinline__ int next_tile(int idx, int unit, int units, bool snake) {
+    const int round = idx / units;
+    return (round + 1) * units + (snake && (round & 1) == 0 ? units - 1 - unit : unit);
+}
 __device__ __forceinline__ void raster(int idx, int nt, int nf, int &tt, int &ft) {
     // 8 token tiles at a time: the tiles in flight share few panels of both operands
     const int per_group = 8 * nf;
@@ -146,8 +155,9 @@ __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &
         }
     } else {
         const int per = p.nt * p.nf;
-        w.e = idx / per;
-        raster(idx - w.e * per, p.nt, p.nf, tt, ft);
+        const int at = idx / per;
+        w.e = tb.first[at];
+        raster(idx - at * per, p.nt, p.nf, tt, ft);
         w.t0 = tt * p.bt;
         w.t_end = p.T;
         w.kbase = tb.begin[w.e];
@@ -226,7 +236,7 @@ __device__ __forceinline__ void finish16(const float (&acc)[16], const Product &
 }
 
 // ---- the 16-bit types' epilogue ------------------------------------------------
-// A warp takes 32 features (the lanes of tensor memory that it may read) and 16
+// A warp takes 32 features (the lanes of tensor memory that it may read) and 32
 // tokens at a time, as 8 x 8 fragments.  A token's 32 features are 64
 // contiguous bytes of out, so the fragments go through shared memory,
 // transposed on the way by stmatrix, and leave in 16-byte stores, 8 tokens an
@@ -234,8 +244,10 @@ __device__ __forceinline__ void finish16(const float (&acc)[16], const Product &
 // while the tile is still being multiplied.  A row of the buffer is 64 bytes,
 // its four 16-byte chunks XORed with half the row number, so that the eight
 // rows of a matrix fall on different banks.
-constexpr int STAGE16 = 16 * 64;               // bytes of 16 tokens x 32 features
-constexpr int EPI_BYTES = STAGE16, EPI_BYTES_RESIDUAL = 3 * STAGE16;  // per warp: z and out; two residual buffers
+constexpr int EPI_T = 32;                      // tokens of a step
+constexpr int STAGE16 = EPI_T * 64;            // bytes of a step's 32 x 32 values
+// per warp: out, z, and two buffers of the residual
+inline int epi_bytes(bool z, bool residual) { return STAGE16 * (1 + (z ? 1 : 0) + (residual ? 2 : 0)); }
 
 __device__ __forceinline__ uint32_t stage16(uint32_t buf, int row, int chunk) {
     return buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
@@ -244,7 +256,7 @@ __device__ __forceinline__ uint32_t stage16(uint32_t buf, int row, int chunk) {
 template <typename T>
 __device__ __forceinline__ void fetch16(const Product &p, uint32_t buf, long long row0, int n, int f0, int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < EPI_T / 8; ++i) {
         const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
         if (row < n && f < p.F) {
             const T *src = static_cast<const T *>(p.residual) + (row0 + row) * p.ldr + f;
@@ -261,49 +273,51 @@ __device__ __forceinline__ void fetch16(const Product &p, uint32_t buf, long lon
     }
     tc::cp_async_commit();
 }
-// Asks for all the residual of a warp's n tokens in L2, when its tile begins:
-// from HBM it would arrive long after the two buffers' 32 tokens are done.
+// Asks for the residual of a warp's n tokens in L2 one tile ahead: from HBM it
+// would arrive long after the step before has been finished.
 template <typename T>
 __device__ __forceinline__ void prefetch_residual(const Product &p, long long row0, int n, int f0, int lane) {
     const char *base = reinterpret_cast<const char *>(static_cast<const T *>(p.residual) + row0 * p.ldr + f0);
     for (int r = lane; r < n; r += 32)
         asm volatile("prefetch.global.L2 [%0];\n" ::"l"(base + r * p.ldr * static_cast<long long>(sizeof(T))) : "memory");
 }
-// 16 tokens x 32 features (fragments, rounded) to rows row0 .. row0 + n of dst.
+// 32 tokens x 32 features (fragments, rounded) into a buffer, and from there to
+// rows row0 .. row0 + n of dst.
 template <typename T>
-__device__ __forceinline__ void put16(const float (&v)[16], uint32_t buf, T *dst, long long ld, bool vec, long long row0,
-                                      int n, int f0, int F, int lane) {
-    __syncwarp();  // the buffer's last contents have been read
+__device__ __forceinline__ void stage_fragments(const float (&v)[2][16], uint32_t buf, int lane) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
         uint32_t r[4];
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
-            const int i = 8 * (o >> 1) + 4 * j + 2 * (o & 1);
-            r[o] = lt::pack2<T>(v[i], v[i + 1]);
+            const int i = 8 * (o >> 1) + 4 * (j & 1) + 2 * (o & 1);
+            r[o] = lt::pack2<T>(v[j >> 1][i], v[j >> 1][i + 1]);
         }
         tc::stmatrix_t(stage16(buf, 8 * j + (lane & 7), lane >> 3), r);
     }
-    __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld, bool vec, long long row0, int n, int f0,
+                                             int F, int lane) {
+    const int chunk = lane & 3, f = f0 + 8 * chunk;
+    uint32_t w[EPI_T / 8][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
-        if (row < n && f < F) {
-            uint32_t a, b, c, d;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                         : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-                         : "r"(stage16(buf, row, chunk))
-                         : "memory");
-            T *o = dst + (row0 + row) * ld + f;
-            if (vec && f + 8 <= F) {
-                *reinterpret_cast<uint4 *>(o) = make_uint4(a, b, c, d);
-            } else {
-                const uint32_t w[4] = {a, b, c, d};
+    for (int i = 0; i < EPI_T / 8; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                     : "r"(stage16(buf, (lane >> 2) + 8 * i, chunk))
+                     : "memory");
+    T *o = dst + (row0 + (lane >> 2)) * ld + f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (f + k < F)
-                        reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[k >> 1] >> (16 * (k & 1)));
-            }
+    for (int i = 0; i < EPI_T / 8; ++i, o += 8 * ld) {
+        if ((lane >> 2) + 8 * i >= n || f >= F) continue;
+        if (vec && f + 8 <= F) {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (f + k < F)
+                    reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[i][k >> 1] >> (16 * (k & 1)));
         }
     }
 }
@@ -345,8 +359,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     float *partial = reinterpret_cast<float *>(sgen + static_cast<size_t>(p.stages) * p.stage_bytes);
     int *tables = reinterpret_cast<int *>(partial + (S > 1 ? p.bt * PROWS : 0));
     const Tables tb{tables, tables + p.E + 2};
-    const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset +
-                         (warp < EPI_WARPS ? warp : 0) * (p.residual != nullptr ? EPI_BYTES_RESIDUAL : EPI_BYTES);
+    const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset + (warp < EPI_WARPS ? warp : 0) * p.epi_bytes;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -385,7 +398,20 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 high = __shfl_sync(0xffffffffu, b, 31);
             }
             __syncwarp();
-            if (p.mode == ROWS_BY_EXPERT)
+            if (p.mode == K_BY_EXPERT) {
+                for (int e = lane; e < p.E; e += 32) {
+                    int at = e;
+                    if (p.E <= SORTED_EXPERTS) {
+                        const int n = tables[e + 1] - tables[e];
+                        at = 0;
+                        for (int o = 0; o < p.E; ++o) {
+                            const int m = tables[o + 1] - tables[o];
+                            at += m > n || (m == n && o < e) ? 1 : 0;
+                        }
+                    }
+                    tables[p.E + 2 + at] = e;
+                }
+            } else
                 for (int e0 = 0; e0 < p.E + 2; e0 += 32) {
                     const int e = e0 + lane;
                     const int n = e <= p.E ? (tables[e + 1] - tables[e] + p.bt - 1) / p.bt * p.nf : 0;
@@ -409,6 +435,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         tiles = tb.first[p.E + 1];
     else if (p.mode == K_BY_EXPERT)
         tiles *= p.E;
+    const bool snake = p.mode == K_BY_EXPERT;
     tc::Waiter waiter(p.timeout_flag);
 
     // One thread issues the copies and one the products, so what they run per
@@ -425,7 +452,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
         uint32_t ph = 1;
         int s = 0, issued = 0;  // stage; how many of the ring are in use, at most
-        for (int idx = unit; idx < tiles; idx += units) {
+        for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
             const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
             const int f0 = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS;
             const int tq = w.t0 + static_cast<int>(CG == 2 ? rank : 0) * q_rows;
@@ -481,7 +508,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const int boxes = (P_BYTES + p.q_bytes) / MN_BOX_BYTES;
             uint32_t phases = 0;  // of tail_bar, a bit per stage
             int s = 0;
-            for (int idx = unit; idx < tiles; idx += units) {
+            for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
                 const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
                 const int left = w.k_rows % BK;  // both operands are MN-major: a box row is one K
                 const bool tail = left != 0 && w.k0 <= w.k_rows / BK && w.k_rows / BK < w.k1;
@@ -511,7 +538,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
             uint32_t ph = 0, g = 0;
             int s = 0;
-            for (int idx = unit; idx < tiles; idx += units) {
+            for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
                 const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
                 const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
                 for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0, ++g) {
@@ -545,9 +572,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             second = s;
                             advance();
                         }
-                        waiter.wait(full0 + 8u * s, ph);
-                        if (kt == tail_kt)  // rows that the tail warps cleared, here and in the other CTA
-                            asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+                        if (kt == tail_kt)  // with rows that the tail warps cleared, here and in the other CTA
+                            waiter.wait<true>(full0 + 8u * s, ph);
+                        else
+                            waiter.wait(full0 + 8u * s, ph);
                         tc::fence_after();
                         __syncwarp();
                         if (tc::elect()) {
@@ -579,7 +607,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         const uint32_t t_off = (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(col0);
         const uint32_t acc_empty0 = tc::peer_addr(tc::smem_u32(&acc_empty[0]), lead);
         uint32_t g = 0, handed = 0;
-        for (int idx = unit; idx < tiles; idx += units) {
+        for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
             const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
             const int fl = 32 * q + lane;           // feature within the CTA's 128
             const int f = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS + fl;
@@ -662,71 +690,96 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 #pragma unroll
                 for (int o = 0; o < 4; ++o) b[o] = __shfl_sync(0xffffffffu, bias, 8 * o + (lane >> 2));
                 const bool res = p.residual != nullptr && !w.none;
+                const uint32_t obuf = epi, zbuf = epi + STAGE16, rbuf0 = epi + (p.z != nullptr ? 2 : 1) * STAGE16;
                 if (res && n_warp > 0) {
-                    fetch16<T>(p, epi + STAGE16, row0, n_warp, f0, lane);
-                    if (n_warp > 16) prefetch_residual<T>(p, row0 + 16, n_warp - 16, f0, lane);
+                    fetch16<T>(p, rbuf0, row0, n_warp, f0, lane);
+                    if (idx == unit && n_warp > EPI_T) prefetch_residual<T>(p, row0 + EPI_T, n_warp - EPI_T, f0, lane);
                 }
                 if (any) {
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
                     __syncwarp();
                     tc::fence_after();
                 }
-                float next[16];
+                float next[2][16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) next[i] = 0.0f;
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) next[h][i] = 0.0f;
                 if (any && n_warp > 0) {
-                    tc::tmem_ld_frag(t_set, next);
-                    tc::tmem_ld_wait(next);
+                    tc::tmem_ld_frag(t_set, next[0]);
+                    tc::tmem_ld_frag(t_set + 16, next[1]);
+                    tc::tmem_ld_wait(next[0]);
+                    tc::tmem_ld_wait(next[1]);
                 }
-                for (int c = 0; c < n_warp; c += 16) {
-                    const uint32_t obuf = epi, rbuf = epi + (1 + (c >> 4 & 1)) * STAGE16;
-                    if (res) {  // the next 16 tokens' residual, into the buffer read last time
+                if (p.residual != nullptr && next_tile(idx, unit, units, snake) < tiles) {  // the next tile's, a whole tile ahead
+                    const Tile nw = locate<CG>(next_tile(idx, unit, units, snake), p, tb, static_cast<int>(rank));
+                    const int nf0 = nw.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS + 32 * q;
+                    if (nf0 < p.F && !nw.none)
+                        prefetch_residual<T>(p, static_cast<long long>(nw.t0) + col0, min(cols, min(p.bt, nw.t_end - nw.t0) - col0), nf0, lane);
+                }
+                for (int c = 0; c < n_warp; c += EPI_T) {
+                    const uint32_t rbuf = rbuf0 + (c / EPI_T & 1) * STAGE16;
+                    if (res) {  // the next step's residual, into the buffer read last time
                         __syncwarp();
-                        if (c + 16 < n_warp)
-                            fetch16<T>(p, epi + (2 - (c >> 4 & 1)) * STAGE16, row0 + c + 16, n_warp - c - 16, f0, lane);
+                        if (c + EPI_T < n_warp)
+                            fetch16<T>(p, rbuf0 + ((c / EPI_T & 1) ^ 1) * STAGE16, row0 + c + EPI_T, n_warp - c - EPI_T, f0, lane);
                     }
-                    float v[16];
+                    float v[2][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = next[i];
-                    const bool more = any && c + 16 < n_warp;
-                    if (more) {
-                        tc::tmem_ld_frag(t_set + c + 16, next);  // arrives while these are finished
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[h][i] = next[h][i];
+                    const bool more = any && c + EPI_T < n_warp;
+                    if (more) {  // arrives while these are finished
+                        tc::tmem_ld_frag(t_set + c + EPI_T, next[0]);
+                        tc::tmem_ld_frag(t_set + c + EPI_T + 16, next[1]);
                     } else if (any) {  // all read: the accumulators are free while the rest is finished
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
                         freed = true;
                     }
+                    __syncwarp();  // the buffers' last contents have been read
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += b[2 * (i >> 3) + (i >> 1 & 1)];
-                    if (p.z != nullptr)
-                        put16<T>(v, obuf, static_cast<T *>(p.z), p.ldz, (p.vec & VEC_Z) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[h][i] += b[2 * (i >> 3) + (i >> 1 & 1)];
+                    if (p.z != nullptr) stage_fragments<T>(v, zbuf, lane);
                     if (!w.none)
                         lt::with_activation(p.act, [&](auto a) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = lt::activate<decltype(a)::value, F32>(v[i]);
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[h][i] = lt::activate<decltype(a)::value, F32>(v[h][i]);
                         });
                     if (res) {
-                        if (c + 16 < n_warp)
+                        if (c + EPI_T < n_warp)
                             tc::cp_async_wait<1>();
                         else
                             tc::cp_async_wait<0>();
                         __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < 4; ++j) {
                             uint32_t r[4];
                             tc::ldmatrix_t(stage16(rbuf, 8 * j + (lane & 7), lane >> 3), r);
 #pragma unroll
                             for (int o = 0; o < 4; ++o) {
-                                const int i = 8 * (o >> 1) + 4 * j + 2 * (o & 1);
+                                const int i = 8 * (o >> 1) + 4 * (j & 1) + 2 * (o & 1);
                                 const float2 x = lt::unpack2<T>(r[o]);
-                                v[i] += x.x;
-                                v[i + 1] += x.y;
+                                v[j >> 1][i] += x.x;
+                                v[j >> 1][i + 1] += x.y;
                             }
                         }
                     }
-                    put16<T>(v, obuf, out, p.ldo, (p.vec & VEC_OUT) != 0, row0 + c, n_warp - c, f0, p.F, lane);
-                    if (more) tc::tmem_ld_wait(next);
+                    stage_fragments<T>(v, obuf, lane);
+                    __syncwarp();
+                    if (p.z != nullptr)
+                        store_staged<T>(zbuf, static_cast<T *>(p.z), p.ldz, (p.vec & VEC_Z) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                    store_staged<T>(obuf, out, p.ldo, (p.vec & VEC_OUT) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                    if (more) {
+                        tc::tmem_ld_wait(next[0]);
+                        tc::tmem_ld_wait(next[1]);
+                    }
                 }
             }
             if (!F32 && any) {
@@ -935,6 +988,10 @@ const Tune &tune() {
     return t;
 }
 
+// Bytes of Q's tile: rows of 64 K, or whole boxes of 64 rows (the last one, of
+// which fewer may be wanted, is copied whole).
+int q_bytes_of(int rows, bool mn) { return mn ? (rows + 63) / 64 * MN_BOX_BYTES : rows * 128; }
+
 // Time of a plan in SM clocks.  A K tile of a CTA (128 features, bt tokens, 64
 // K; FP32: three stages of pieces) takes the longest of three: the tensor cores' bt/2 clocks per 16 K (2.2 bt
 // measured for the four with bt = 256), the bytes that it copies at what L2
@@ -950,7 +1007,7 @@ Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
     for (int cg = 2; cg >= 1; --cg)
         for (int bt : bts) {
             if (cg == 2 && (bt < 64 || bt % 32 != 0)) continue;
-            if ((p.q_mn && bt / cg % 64 != 0) || (f32 && bt > 2 * F32_COLS)) continue;
+            if (f32 && bt > 2 * F32_COLS) continue;
             if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
             double nt, ktiles = (p.K + BK - 1) / BK;
             if (p.mode == ROWS_BY_EXPERT) {
@@ -967,7 +1024,7 @@ Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
             }
             const double tiles = nt * ((p.F + PROWS * cg - 1) / (PROWS * cg));
             double per = 370.0;
-            const double copy = (P_BYTES + bt / cg * 128) / 62.0;
+            const double copy = (P_BYTES + q_bytes_of(bt / cg, p.q_mn != 0)) / 62.0;
             if (copy > per) per = copy;
             if (f32) per *= PIECES;
             const double mma = (f32 ? PRODUCTS : 1) * 2.2 * bt;
@@ -1025,7 +1082,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     if (pl.cost > 1e299) pl = choose(p, d, type, Tune());
     p.bt = pl.bt;
     p.splits = pl.splits;
-    p.q_bytes = p.bt / pl.cg * 128;
+    p.q_bytes = q_bytes_of(p.bt / pl.cg, Q.mn);
     p.stage_bytes = P_BYTES + p.q_bytes;
     const int per_unit = PROWS * pl.cg;
     p.nf = (p.F + per_unit - 1) / per_unit;
@@ -1036,7 +1093,8 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     if (tiles > INT_MAX / 2) return SGEMM_ERR_INVALID_DIM;
     const int tables = p.mode == DENSE ? 0 : 2 * (p.E + 2) * 4;
     const int part = p.splits > 1 ? p.bt * PROWS * 4 : 0;
-    const int epi = type == LINEAR_F32 ? 0 : EPI_WARPS * (p.residual != nullptr ? EPI_BYTES_RESIDUAL : EPI_BYTES) + 128;
+    p.epi_bytes = epi_bytes(p.z != nullptr, p.residual != nullptr && p.splits == 1);  // split: only zero rows go there
+    const int epi = type == LINEAR_F32 ? 0 : EPI_WARPS * p.epi_bytes + 128;
     p.stages = (SMEM_MAX - 2048 - tables - part - epi) / p.stage_bytes;
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     const size_t used = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
