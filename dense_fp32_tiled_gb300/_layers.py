@@ -17,25 +17,38 @@ from ._binding import SGEMM_OK, SgemmError, load_library
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
-# The calls are short next to what they launch (a decoding step's product takes
-# a few microseconds), so the checks below run in as few Python steps as they
-# can: torch and the library are looked up once, a call on the current stream
-# enters no context, and 16-bit operands whose rows are 16-byte aligned, which
-# need no workspace, do not ask for its size.
+# What these calls launch is short (a decoding step's product takes a few
+# microseconds), so calls on the current device and stream whose arguments are
+# as they should be go through an extension (csrc/fast_call.c) that takes the
+# same steps without the interpreter.  It answers NotImplemented to anything
+# else, which the functions below then serve or refuse, and a status of the
+# library as a number.
 torch = None
 _lib = None
 _types = {}
 _raw_stream = None
+_fast = None
 
 
 def _load():
-    global torch, _lib, _raw_stream
+    global torch, _lib, _raw_stream, _fast
     if _lib is None:
         import torch as _torch
         torch = _torch
         _types.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _lib = load_library()
+        try:
+            from . import _fast_call
+        except ImportError:  # built without Python's headers
+            return _lib
+        names = [f for op in ("linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward",
+                              "expert_sort") for f in (op, op + "_workspace_size")]
+        names += ["expert_gather", "expert_combine", "expert_combine_backward"]
+        _fast_call.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},
+                        (torch.Tensor, torch.empty, _raw_stream, torch._C._cuda_getDevice, _workspace, ACTIVATIONS,
+                         (torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.int64))
+        _fast = _fast_call
     return _lib
 
 
@@ -142,6 +155,12 @@ def _check(st, what):
         raise SgemmError(st, what)
 
 
+def _answer(r, what):
+    if type(r) is int:
+        raise SgemmError(r, what)
+    return r
+
+
 # ---- the product with its epilogue ---------------------------------------------
 def linear(x, w, bias=None, residual=None, activation="none", preact=None, out=None, stream=None):
     """act(x @ w + bias) + residual.
@@ -151,6 +170,10 @@ def linear(x, w, bias=None, residual=None, activation="none", preact=None, out=N
     residual and out are (M, N).  ``preact``, an (M, N) tensor, receives
     x @ w + bias for linear_backward.  ``out`` may be ``residual`` itself.
     """
+    if stream is None and _fast is not None:
+        r = _fast.forward(x, w, None, bias, residual, activation, preact, out)
+        if r is not NotImplemented:
+            return _answer(r, "linear_forward")
     return _forward(x, w, None, bias, residual, activation, preact, out, stream)
 
 
@@ -159,6 +182,10 @@ def expert_linear(x, w, offsets, bias=None, residual=None, activation="none", pr
     offsets[e + 1] of x (R, K) meet w[e] and bias[e] of w (E, K, N) and bias
     (E, N).  offsets is int32 (E + 1,) on the device, as expert_sort makes it,
     and is not read on the host.  Rows of no expert give 0."""
+    if stream is None and _fast is not None and offsets is not None:
+        r = _fast.forward(x, w, offsets, bias, residual, activation, preact, out)
+        if r is not NotImplemented:
+            return _answer(r, "expert_linear_forward")
     return _forward(x, w, offsets, bias, residual, activation, preact, out, stream)
 
 
@@ -205,12 +232,20 @@ def linear_backward(dy, x, w, preact=None, activation="none", need_dx=True, need
     """(dx, dw, dbias) of linear for the gradient dy of its result (that of the
     residual is dy itself).  preact is what linear saved, needed unless the
     activation is "none".  dw has the memory order of w; what is not needed is None."""
+    if stream is None and _fast is not None:
+        r = _fast.backward(dy, x, w, None, preact, activation, need_dx, need_dw, need_dbias)
+        if r is not NotImplemented:
+            return _answer(r, "linear_backward")
     return _backward(dy, x, w, None, preact, activation, need_dx, need_dw, need_dbias, stream)
 
 
 def expert_linear_backward(dy, x, w, offsets, preact=None, activation="none", need_dx=True, need_dw=True,
                            need_dbias=True, stream=None):
     """(dx, dw, dbias) of expert_linear.  Rows of no expert have a dx of 0, experts without rows a dw and dbias of 0."""
+    if stream is None and _fast is not None and offsets is not None:
+        r = _fast.backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbias)
+        if r is not NotImplemented:
+            return _answer(r, "expert_linear_backward")
     return _backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbias, stream)
 
 
@@ -276,6 +311,10 @@ def expert_sort(choices, experts, stream=None):
     token (one outside 0 .. experts - 1 is dropped).  rows, int32 (T, J), is
     each choice's place among all T*J sorted by expert, then token and choice,
     or -1; places offsets[e] to offsets[e + 1] belong to expert e."""
+    if stream is None and _fast is not None:
+        r = _fast.sort(choices, experts)
+        if r is not NotImplemented:
+            return _answer(r, "expert_sort")
     lib = _lib or _load()
     dtype = getattr(choices, "dtype", None)
     if dtype is torch.int32:
@@ -315,6 +354,10 @@ def _order(rows, offsets, T, dev):
 
 def expert_gather(x, rows, offsets, out=None, stream=None):
     """The token rows in expert order: out[rows[t, j]] = x[t], (T*J, H); places in no use are 0."""
+    if stream is None and _fast is not None:
+        r = _fast.gather(x, rows, offsets, out)
+        if r is not NotImplemented:
+            return _answer(r, "expert_gather")
     lib = _lib or _load()
     kind = _type_of(x, "x")
     if x.dim() != 2:
@@ -335,6 +378,10 @@ def expert_gather(x, rows, offsets, out=None, stream=None):
 def expert_combine(ys, rows, weights=None, residual=None, out=None, stream=None):
     """Each token's sum over its choices: residual[t] + sum_j weights[t, j] * ys[rows[t, j]].
     weights is float32 (T, J); None weighs all by 1.  Dropped choices add nothing."""
+    if stream is None and _fast is not None:
+        r = _fast.combine(ys, rows, weights, residual, out)
+        if r is not NotImplemented:
+            return _answer(r, "expert_combine")
     lib = _lib or _load()
     kind = _type_of(ys, "ys")
     if ys.dim() != 2 or rows.dim() != 2:
@@ -363,6 +410,10 @@ def expert_combine_backward(dy, ys, rows, weights, offsets, need_dweights=True, 
     """(dys, dweights) of expert_combine (the residual's gradient is dy itself):
     dys[rows[t, j]] = weights[t, j] * dy[t], 0 in the places in no use, and
     dweights[t, j] = dy[t] . ys[rows[t, j]], float32, 0 for a dropped choice."""
+    if stream is None and _fast is not None:
+        r = _fast.combine_backward(dy, ys, rows, weights, offsets, need_dweights)
+        if r is not NotImplemented:
+            return _answer(r, "expert_combine_backward")
     lib = _lib or _load()
     kind = _type_of(dy, "dy")
     if dy.dim() != 2:

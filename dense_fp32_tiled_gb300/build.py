@@ -1,4 +1,5 @@
-"""Build step for the CUDA library libsgemm_f32.so (sm_103a only).
+"""Build step for the CUDA library libsgemm_f32.so (sm_103a only) and for
+_fast_call.so, the Python extension that marshals the common layer calls.
 
 Compiles every csrc/*.cu to an object file, all in parallel (one nvcc
 process each), and links them into the package directory (in-tree, so the
@@ -13,12 +14,14 @@ import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsgemm_f32.so")
+FAST_CALL = os.path.join(PKG, "_fast_call.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # flags that shape the generated code (hashed into the stamps; no paths, so a
@@ -35,6 +38,32 @@ def _nvcc() -> str:
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_fast_call() -> str | None:
+    """Compile csrc/fast_call.c against this interpreter (None without its headers:
+    the calls then go through _layers.py)."""
+    include = sysconfig.get_path("include")
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    src = os.path.join(CSRC, "fast_call.c")
+    cmd = ["gcc", "-O2", "-Wall", "-Werror", "-fPIC", "-shared", f"-I{include}", src]
+    with open(src, "rb") as f:
+        stamp = hashlib.sha256(f.read() + " ".join(cmd[:-1] + [sys.version]).encode()).hexdigest()
+    stamp_file = os.path.join(BUILD_DIR, "fast_call.stamp")
+    if os.path.exists(FAST_CALL) and os.path.exists(stamp_file):
+        with open(stamp_file) as f:
+            if f.read().strip() == stamp:
+                return FAST_CALL
+    tmp = os.path.join(BUILD_DIR, f"_fast_call.{os.getpid()}.so")
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("gcc failed building _fast_call.so")
+    os.replace(tmp, FAST_CALL)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
+    return FAST_CALL
 
 
 def _stamp() -> str:
@@ -62,6 +91,7 @@ def kernel_stamp(names) -> str:
 
 def build(force: bool = False, quiet: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
+    build_fast_call()
     stamp_file = os.path.join(BUILD_DIR, "libsgemm_f32.stamp")
     stamp = _stamp()
     if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
