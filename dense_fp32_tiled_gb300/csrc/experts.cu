@@ -170,45 +170,69 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
 }
 
 // ---- rows --------------------------------------------------------------------------
-// V values (16 bytes, or one) of a row, as the words they travel in: a load
+// V values (16, 8, 4 or 2 bytes) of a row, as the word they travel in: a load
 // that may not happen is then one predicated instruction, and the next ones
 // follow it at once.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+    using type = uint4;
+};
+template <>
+struct Word<8> {
+    using type = uint2;
+};
+template <>
+struct Word<4> {
+    using type = uint32_t;
+};
+template <>
+struct Word<2> {
+    using type = uint16_t;
+};
 template <typename T, int V>
 struct Pack {
-    using Raw = typename std::conditional<V != 1, uint4, typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type>::type;
+    static constexpr int BYTES = V * static_cast<int>(sizeof(T));
+    using Raw = typename Word<BYTES>::type;
     Raw raw;
-    __device__ __forceinline__ void clear() {
-        if constexpr (V != 1)
-            raw = make_uint4(0u, 0u, 0u, 0u);
-        else
-            raw = 0;
+    __device__ __forceinline__ void clear() { raw = Raw{}; }
+    __device__ __forceinline__ uint32_t word(int i) const {
+        if constexpr (BYTES == 16) return i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
+        if constexpr (BYTES == 8) return i == 0 ? raw.x : raw.y;
+        if constexpr (BYTES <= 4) return raw;
     }
     __device__ __forceinline__ void get(float (&f)[V]) const {
-        if constexpr (V == 1) {
+        if constexpr (BYTES == 2) {
             f[0] = to_f(*reinterpret_cast<const T *>(&raw));
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(word(i));
         } else {
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v = lt::unpack2<T>(w[i]);
-                    f[2 * i] = v.x;
-                    f[2 * i + 1] = v.y;
-                }
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 v = lt::unpack2<T>(word(i));
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
             }
         }
     }
     __device__ __forceinline__ void set(const float (&f)[V]) {
-        if constexpr (V == 1) {
+        if constexpr (BYTES == 2) {
             const T v = from_f<T>(f[0]);
             raw = *reinterpret_cast<const Raw *>(&v);
-        } else if constexpr (sizeof(T) == 4) {
-            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
         } else {
-            raw = make_uint4(lt::pack2<T>(f[0], f[1]), lt::pack2<T>(f[2], f[3]), lt::pack2<T>(f[4], f[5]), lt::pack2<T>(f[6], f[7]));
+            uint32_t w[BYTES / 4];
+#pragma unroll
+            for (int i = 0; i < BYTES / 4; ++i) {
+                if constexpr (sizeof(T) == 4)
+                    w[i] = __float_as_uint(f[i]);
+                else
+                    w[i] = lt::pack2<T>(f[2 * i], f[2 * i + 1]);
+            }
+            if constexpr (BYTES == 16) raw = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (BYTES == 8) raw = make_uint2(w[0], w[1]);
+            if constexpr (BYTES == 4) raw = w[0];
         }
     }
 };
@@ -250,16 +274,16 @@ __device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long 
 // A warp takes a segment of one token's row: SEG accesses per lane.  With 16-byte
 // ones a single access per lane and four of the token's rows in flight serve the
 // sum best (16384 tokens, 4 choices, 4096 wide in bf16: 134 us; two accesses and
-// two rows 137, four and two 183: fewer registers, more warps); single values
-// want eight (5000 tokens, 6 choices, 1001 wide in FP32: 27 us, one 48).
-__host__ __device__ constexpr int seg_of(int V) { return V > 1 ? 1 : 8; }
+// two rows 137, four and two 183: fewer registers, more warps); narrow ones want
+// eight (5000 tokens, 6 choices, 1001 wide in FP32: 27 us, one 48).
+__host__ __device__ constexpr int seg_of(int bytes) { return bytes == 16 ? 1 : bytes == 8 ? 2 : 8; }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(ROW_THREADS)
 gather_kernel(int T_, int J, int packs, int segments, int E, const int *__restrict__ rows,
               const int *__restrict__ offsets, const T *__restrict__ x, long long ldx, T *__restrict__ xs,
               long long ldxs, int blocks) {
-    constexpr int SEG = seg_of(V);
+    constexpr int SEG = seg_of(Pack<T, V>::BYTES);
     const long long R = static_cast<long long>(T_) * J;
     if (static_cast<int>(blockIdx.x) >= blocks) {
         clear_rest<T, V>(xs, ldxs, offsets[E], R, packs, blockIdx.x - blocks);
@@ -287,8 +311,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(ROW_THREADS)
 combine_kernel(int T_, int J, int packs, int segments, const int *__restrict__ rows, const float *__restrict__ weights,
                const T *__restrict__ ys, long long ldys, const T *residual, long long ldr, T *y, long long ldy) {
-    constexpr int SEG = seg_of(V);
-    constexpr int U = V > 1 ? 4 : 2;  // rows in flight
+    constexpr int SEG = seg_of(Pack<T, V>::BYTES);
+    constexpr int U = SEG <= 2 ? 4 : 2;  // rows in flight
     const long long R = static_cast<long long>(T_) * J;
     const int unit = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     const int t = unit / segments;
@@ -364,7 +388,7 @@ combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__
     const T *d = dy + i / J * lddy, *s = ys + r * ldys;
     T *o = dys + r * lddys;
     float dot = 0.0f;
-#pragma unroll(V > 1 ? 4 : 8)
+#pragma unroll(V * sizeof(T) > 8 ? 4 : 8)
     for (int p = lane; p < packs; p += 32) {
         float g[V], f[V];
         const Pack<T, V> gv = load<T, V>(d + static_cast<long long>(p) * V);
@@ -407,23 +431,33 @@ int check_sizes(int type, int T, int J, int H, long long E) {
         return SGEMM_ERR_INVALID_DIM;
     return SGEMM_OK;
 }
-bool wide(const void *p, long long ld, int type) {
-    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * lt::type_bytes(type) % 16 == 0);
+// The widest access (16, 8, 4 or 2 bytes) that rows of this address and stride allow.
+int width_of(const void *p, long long ld, int type) {
+    if (p == nullptr) return 16;
+    const unsigned long long bits = reinterpret_cast<uintptr_t>(p) | static_cast<unsigned long long>(ld) * lt::type_bytes(type) | 16;
+    return static_cast<int>(bits & (0 - bits));
 }
+int narrower(int a, int b) { return a < b ? a : b; }
 int launched() {
     if (cudaPeekAtLastError() == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
 }
-// f(element, values per access) for the type and whether rows allow 16 bytes.
+// f(element, values per access) for the type and the bytes of an access.
 template <typename F>
-int with_rows(int type, bool vec, F &&f) {
-    if (type == LINEAR_F32) return vec ? f(float(), lt::Int<4>{}) : f(float(), lt::Int<1>{});
-    if (type == LINEAR_BF16) return vec ? f(__nv_bfloat16(), lt::Int<8>{}) : f(__nv_bfloat16(), lt::Int<1>{});
-    return vec ? f(__half(), lt::Int<8>{}) : f(__half(), lt::Int<1>{});
+int with_rows(int type, int bytes, F &&f) {
+    if (type == LINEAR_F32)
+        return bytes == 16 ? f(float(), lt::Int<4>{}) : bytes == 8 ? f(float(), lt::Int<2>{}) : f(float(), lt::Int<1>{});
+    auto half = [&](auto el) {
+        return bytes == 16  ? f(el, lt::Int<8>{})
+               : bytes == 8 ? f(el, lt::Int<4>{})
+               : bytes == 4 ? f(el, lt::Int<2>{})
+                            : f(el, lt::Int<1>{});
+    };
+    return type == LINEAR_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
-int segments_of(int packs, bool vec) {
-    const int seg = 32 * seg_of(vec ? 4 : 1);
+int segments_of(int packs, int bytes) {
+    const int seg = 32 * seg_of(bytes);
     return packs / seg + (packs % seg != 0);
 }
 long long blocks_for(long long warps) { return (warps + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32); }
@@ -504,14 +538,12 @@ extern "C" int expert_gather(int type, int T, int J, int H, int E, const int *ro
     const Span so = span(xs, R, H, ldxs, b);
     if (overlap(so, span(x, T, H, ldx, b)) || overlap(so, span(rows, 1, R, R, 4)) || overlap(so, span(offsets, 1, E + 1, 1, 4)))
         return SGEMM_ERR_ALIAS;
-    const int n = 16 / b;
-    const bool vec = H % n == 0 && wide(x, ldx, type) && wide(xs, ldxs, type);
-    const int packs = vec ? H / n : H;
-    const int segments = segments_of(packs, vec);
+    const int width = narrower(narrower(width_of(x, ldx, type), width_of(xs, ldxs, type)), width_of(x, H, type));
+    const int packs = H / (width / b), segments = segments_of(packs, width);
     const long long blocks = blocks_for(static_cast<long long>(T) * segments);
     if (static_cast<long long>(T) * segments > INT_MAX - ROW_THREADS) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: gather");
-    return with_rows(type, vec, [&](auto el, auto v) {
+    return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
         gather_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
             T, J, packs, segments, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks));
@@ -535,14 +567,13 @@ extern "C" int expert_combine(int type, int T, int J, int H, const int *rows, co
     if (overlap(so, span(ys, R, H, ldys, b)) || overlap(so, span(rows, 1, R, R, 4)) || overlap(so, span(weights, 1, R, R, 4)) ||
         (!in_place && overlap(so, span(residual, T, H, ldr, b))))
         return SGEMM_ERR_ALIAS;
-    const int n = 16 / b;
-    const bool vec = H % n == 0 && wide(ys, ldys, type) && wide(y, ldy, type) && wide(residual, ldr, type);
-    const int packs = vec ? H / n : H;
-    const int segments = segments_of(packs, vec);
+    const int width = narrower(narrower(width_of(ys, ldys, type), width_of(residual, ldr, type)),
+                            narrower(width_of(y, ldy, type), width_of(y, H, type)));
+    const int packs = H / (width / b), segments = segments_of(packs, width);
     const long long blocks = blocks_for(static_cast<long long>(T) * segments);
     if (static_cast<long long>(T) * segments > INT_MAX - ROW_THREADS) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: combine");
-    return with_rows(type, vec, [&](auto el, auto v) {
+    return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
         combine_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks), ROW_THREADS, 0, stream>>>(
             T, J, packs, segments, rows, weights, static_cast<const El *>(ys), ldys, static_cast<const El *>(residual), ldr,
@@ -572,13 +603,13 @@ extern "C" int expert_combine_backward(int type, int T, int J, int H, int E, con
         for (const Span &i : in)
             if (overlap(o, i)) return SGEMM_ERR_ALIAS;
     if (overlap(out[0], out[1])) return SGEMM_ERR_ALIAS;
-    const int n = 16 / b;
-    const bool vec = H % n == 0 && wide(dy, lddy, type) && (dweights == nullptr || wide(ys, ldys, type)) && wide(dys, lddys, type);
-    const int packs = vec ? H / n : H;
+    const int width = narrower(narrower(width_of(dy, lddy, type), dweights == nullptr ? 16 : width_of(ys, ldys, type)),
+                            narrower(width_of(dys, lddys, type), width_of(dy, H, type)));
+    const int packs = H / (width / b);
     const long long blocks = blocks_for(R);
     if (blocks + ZERO_BLOCKS > INT_MAX) return SGEMM_ERR_INVALID_DIM;
     sg_nvtx::Range r("experts: combine backward");
-    return with_rows(type, vec, [&](auto el, auto v) {
+    return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
         combine_backward_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
             T, J, packs, E, rows, offsets, weights, static_cast<const El *>(dy), lddy, static_cast<const El *>(ys), ldys,

@@ -281,6 +281,15 @@ __device__ __forceinline__ void prefetch_residual(const Product &p, long long ro
     for (int r = lane; r < n; r += 32)
         asm volatile("prefetch.global.L2 [%0];\n" ::"l"(base + r * p.ldr * static_cast<long long>(sizeof(T))) : "memory");
 }
+// The residual of the same warp's part of tile idx (a call of its own: inlined, it costs the epilogue registers).
+template <int CG, typename T>
+__device__ __noinline__ void prefetch_next(int idx, const Product &p, const Tables &tb, int rank, int col0, int cols, int lane0,
+                                           int lane) {
+    const Tile w = locate<CG>(idx, p, tb, rank);
+    const int f0 = w.ft * (PROWS * CG) + (CG == 2 ? rank : 0) * PROWS + lane0;
+    if (f0 < p.F && !w.none)
+        prefetch_residual<T>(p, static_cast<long long>(w.t0) + col0, min(cols, min(p.bt, w.t_end - w.t0) - col0), f0, lane);
+}
 // 32 tokens x 32 features (fragments, rounded) into a buffer, and from there to
 // rows row0 .. row0 + n of dst.
 template <typename T>
@@ -300,24 +309,27 @@ template <typename T>
 __device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld, bool vec, long long row0, int n, int f0,
                                              int F, int lane) {
     const int chunk = lane & 3, f = f0 + 8 * chunk;
-    uint32_t w[EPI_T / 8][4];
-#pragma unroll
-    for (int i = 0; i < EPI_T / 8; ++i)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                     : "r"(stage16(buf, (lane >> 2) + 8 * i, chunk))
-                     : "memory");
     T *o = dst + (row0 + (lane >> 2)) * ld + f;
 #pragma unroll
-    for (int i = 0; i < EPI_T / 8; ++i, o += 8 * ld) {
-        if ((lane >> 2) + 8 * i >= n || f >= F) continue;
-        if (vec && f + 8 <= F) {
-            *reinterpret_cast<uint4 *>(o) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-        } else {
+    for (int h = 0; h < 2; ++h) {
+        uint32_t w[2][4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (f + k < F)
-                    reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[i][k >> 1] >> (16 * (k & 1)));
+        for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(stage16(buf, (lane >> 2) + 8 * (2 * h + i), chunk))
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i, o += 8 * ld) {
+            if ((lane >> 2) + 8 * (2 * h + i) >= n || f >= F) continue;
+            if (vec && f + 8 <= F) {
+                *reinterpret_cast<uint4 *>(o) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (f + k < F)
+                        reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[i][k >> 1] >> (16 * (k & 1)));
+            }
         }
     }
 }
@@ -711,12 +723,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     tc::tmem_ld_wait(next[0]);
                     tc::tmem_ld_wait(next[1]);
                 }
-                if (p.residual != nullptr && next_tile(idx, unit, units, snake) < tiles) {  // the next tile's, a whole tile ahead
-                    const Tile nw = locate<CG>(next_tile(idx, unit, units, snake), p, tb, static_cast<int>(rank));
-                    const int nf0 = nw.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS + 32 * q;
-                    if (nf0 < p.F && !nw.none)
-                        prefetch_residual<T>(p, static_cast<long long>(nw.t0) + col0, min(cols, min(p.bt, nw.t_end - nw.t0) - col0), nf0, lane);
-                }
+                if (p.residual != nullptr && next_tile(idx, unit, units, snake) < tiles)
+                    prefetch_next<CG, T>(next_tile(idx, unit, units, snake), p, tb, static_cast<int>(rank), col0, cols, 32 * q, lane);
                 for (int c = 0; c < n_warp; c += EPI_T) {
                     const uint32_t rbuf = rbuf0 + (c / EPI_T & 1) * STAGE16;
                     if (res) {  // the next step's residual, into the buffer read last time

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
     constexpr int OWN = ORDER ? own32(TT) : 4;  // features of a thread
     constexpr int FEATURES = ORDER ? OWN : 32;
     constexpr int STEP = ORDER ? 128 : 4;
-    constexpr int UNROLL = ORDER ? 1 : (!VEC ? 2 : TT > 8 ? 4 : 8);
+    constexpr int UNROLL = ORDER ? 1 : TT > 8 ? 2 : !VEC ? 2 : TT > 4 ? 4 : 8;
     __shared__ float sums[WARPS][TT][FEATURES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int f0 = blockIdx.x * FEATURES;

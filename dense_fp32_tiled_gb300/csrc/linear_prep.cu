@@ -108,6 +108,11 @@ void copy_operands_t(const linear_prep::Copy *copies, int n, cudaStream_t stream
 constexpr int CHUNK = 64;
 constexpr int GWARPS = 8;
 
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Chunk16 {
+    T v[V];
+};
+
 // The expert of `row`: the last e with offsets[e] <= row (E: none).
 __device__ __forceinline__ int expert_of(const int *offsets, int E, int row) {
     int lo = 0, hi = E + 1;
@@ -121,7 +126,10 @@ __device__ __forceinline__ int expert_of(const int *offsets, int E, int row) {
     return lo;
 }
 
-template <typename T, int V, int ACT>
+// ROWS of a warp are loaded together.  With enough blocks to fill the GPU several
+// times over, one row and more warps do better (8192 x 8192 in bf16: 61 us, four
+// rows 120); with few, four (1024 x 1024 in FP32: 5.4 us, one row 7.1).
+template <typename T, int V, int ACT, int ROWS>
 __global__ void __launch_bounds__(GWARPS * 32)
 activation_gradient_kernel(int M, int N, int E, const int *__restrict__ offsets, const T *__restrict__ dy,
                            long long lddy, const T *__restrict__ z, long long ldz, void *__restrict__ dz,
@@ -145,42 +153,42 @@ activation_gradient_kernel(int M, int N, int E, const int *__restrict__ offsets,
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[i] = 0.0f;
         if (counted && col < N)
-            for (int r = row + warp; r < end; r += GWARPS) {
-                T d[V], zz[V];
-                if constexpr (V > 1) {
-                    *reinterpret_cast<Chunk<T> *>(d) = *reinterpret_cast<const Chunk<T> *>(dy + r * lddy + col);
-                    if constexpr (ACT != LINEAR_ACT_NONE)
-                        *reinterpret_cast<Chunk<T> *>(zz) = *reinterpret_cast<const Chunk<T> *>(z + r * ldz + col);
-                } else {
-                    d[0] = dy[r * lddy + col];
-                    if constexpr (ACT != LINEAR_ACT_NONE) zz[0] = z[r * ldz + col];
-                }
-                float g[V];
+            for (int r0 = row + warp; r0 < end; r0 += GWARPS * ROWS) {
+                Chunk16<T, V> d[ROWS], zz[ROWS];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    g[i] = to_f(d[i]);
-                    if constexpr (ACT != LINEAR_ACT_NONE) g[i] *= lt::slope<ACT, F32>(to_f(zz[i]));
-                    sum[i] += g[i];
+                for (int u = 0; u < ROWS; ++u) {
+                    const long long r = r0 + u * GWARPS;
+                    if (r < end) {
+                        d[u] = *reinterpret_cast<const Chunk16<T, V> *>(dy + r * lddy + col);
+                        if constexpr (ACT != LINEAR_ACT_NONE) zz[u] = *reinterpret_cast<const Chunk16<T, V> *>(z + r * ldz + col);
+                    }
                 }
-                if (dz != nullptr) {
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    const long long r = r0 + u * GWARPS;
+                    if (r >= end) break;
+                    float g[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        g[i] = to_f(d[u].v[i]);
+                        if constexpr (ACT != LINEAR_ACT_NONE) g[i] *= lt::slope<ACT, F32>(to_f(zz[u].v[i]));
+                        sum[i] += g[i];
+                    }
+                    if (dz == nullptr) continue;
                     if constexpr (F32) {
                         auto *o = static_cast<__nv_bfloat16 *>(dz) + r * lddz + col;
                         const long long piece = static_cast<long long>(M) * lddz;
-                        struct alignas(2 * V) Out {
-                            __nv_bfloat16 v[V];
-                        } a, b, c;
+                        Chunk16<__nv_bfloat16, V> a, b, c;
 #pragma unroll
                         for (int i = 0; i < V; ++i) pieces(g[i], a.v[i], b.v[i], c.v[i]);
-                        *reinterpret_cast<Out *>(o) = a;
-                        *reinterpret_cast<Out *>(o + piece) = b;
-                        *reinterpret_cast<Out *>(o + 2 * piece) = c;
+                        *reinterpret_cast<Chunk16<__nv_bfloat16, V> *>(o) = a;
+                        *reinterpret_cast<Chunk16<__nv_bfloat16, V> *>(o + piece) = b;
+                        *reinterpret_cast<Chunk16<__nv_bfloat16, V> *>(o + 2 * piece) = c;
                     } else {
-                        struct alignas(sizeof(T) * V) Out {
-                            T v[V];
-                        } a;
+                        Chunk16<T, V> a;
 #pragma unroll
                         for (int i = 0; i < V; ++i) a.v[i] = from_f<T>(g[i]);
-                        *reinterpret_cast<Out *>(static_cast<T *>(dz) + r * lddz + col) = a;
+                        *reinterpret_cast<Chunk16<T, V> *>(static_cast<T *>(dz) + r * lddz + col) = a;
                     }
                 }
             }
@@ -246,10 +254,12 @@ cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offse
     };
     auto pick = [&](auto tag) {
         constexpr int ACT = decltype(tag)::value;
-        if (vec)
-            launch(activation_gradient_kernel<T, V, ACT>);
+        if (!vec)
+            launch(activation_gradient_kernel<T, 1, ACT, 4>);
+        else if (blocks < 4 * 152)
+            launch(activation_gradient_kernel<T, V, ACT, 4>);
         else
-            launch(activation_gradient_kernel<T, 1, ACT>);
+            launch(activation_gradient_kernel<T, V, ACT, 1>);
     };
     switch (act) {
         case LINEAR_ACT_RELU: pick(lt::Int<LINEAR_ACT_RELU>{}); break;
