@@ -71,7 +71,8 @@ template <typename I>
 __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(const I *__restrict__ choices, long long R, int E,
                                                                   int range, int warps, int *__restrict__ counts) {
     extern __shared__ int shared[];
-    tc::grid_trigger();  // the second kernel counts its ranges meanwhile
+    tc::grid_wait();
+    tc::grid_trigger();  // the second kernel counts its ranges meanwhile (the choices are there now)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < warps * E; i += SORT_THREADS) shared[i] = 0;
     __syncthreads();
@@ -102,6 +103,7 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
     int *mine = earlier + E;             // warps x E
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (warps + 2) * E; i += SORT_THREADS) totals[i] = 0;
+    if (blocks == 1) tc::grid_wait();  // else the first kernel has waited for the choices
     __syncthreads();
     const long long begin = static_cast<long long>(blockIdx.x) * range;
     const long long end = begin + range < R ? begin + range : R;
@@ -285,6 +287,8 @@ gather_kernel(int T_, int J, int packs, int segments, int E, const int *__restri
               long long ldxs, int blocks) {
     constexpr int SEG = seg_of(Pack<T, V>::BYTES);
     const long long R = static_cast<long long>(T_) * J;
+    tc::grid_trigger();
+    tc::grid_wait();
     if (static_cast<int>(blockIdx.x) >= blocks) {
         clear_rest<T, V>(xs, ldxs, offsets[E], R, packs, blockIdx.x - blocks);
         return;
@@ -314,6 +318,8 @@ combine_kernel(int T_, int J, int packs, int segments, const int *__restrict__ r
     constexpr int SEG = seg_of(Pack<T, V>::BYTES);
     constexpr int U = SEG <= 2 ? 4 : 2;  // rows in flight
     const long long R = static_cast<long long>(T_) * J;
+    tc::grid_trigger();
+    tc::grid_wait();
     const int unit = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     const int t = unit / segments;
     if (t >= T_) return;
@@ -372,6 +378,8 @@ combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__
                         const T *__restrict__ ys, long long ldys, T *__restrict__ dys, long long lddys,
                         float *__restrict__ dweights, int blocks) {
     const long long R = static_cast<long long>(T_) * J;
+    tc::grid_trigger();
+    tc::grid_wait();
     if (static_cast<int>(blockIdx.x) >= blocks) {
         clear_rest<T, V>(dys, lddys, offsets[E], R, packs, blockIdx.x - blocks);
         return;
@@ -438,8 +446,8 @@ int width_of(const void *p, long long ld, int type) {
     return static_cast<int>(bits & (0 - bits));
 }
 int narrower(int a, int b) { return a < b ? a : b; }
-int launched() {
-    if (cudaPeekAtLastError() == cudaSuccess) return SGEMM_OK;
+int launched(cudaError_t err) {
+    if (err == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
 }
@@ -472,27 +480,14 @@ int sort(long long R, int E, const I *choices, int *rows, int *offsets, int *cou
         return SGEMM_ERR_DEVICE;
     }
     sg_nvtx::Range r("experts: sort");
+    cudaError_t err = cudaSuccess;
     if (s.blocks > 1)
-        sort_count_kernel<I><<<s.blocks, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, counts);
-    if (s.blocks == 1) {
-        sort_place_kernel<I><<<1, SORT_THREADS, s.smem, stream>>>(choices, R, E, s.range, s.warps, 1, counts, rows, offsets);
-        return launched();
-    }
-    // the choices are those the first kernel has waited for, so the second may start beside it
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(s.blocks));
-    cfg.blockDim = dim3(SORT_THREADS);
-    cfg.dynamicSmemBytes = s.smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, sort_place_kernel<I>, choices, R, E, s.range, s.warps, s.blocks,
-                                               static_cast<const int *>(counts), rows, offsets);
-    const int st = launched();
-    return st == SGEMM_OK && err != cudaSuccess ? SGEMM_ERR_LAUNCH : st;
+        err = tc::launch(sort_count_kernel<I>, static_cast<unsigned>(s.blocks), dim3(SORT_THREADS), s.smem, stream, choices, R,
+                         E, s.range, s.warps, counts);
+    if (err == cudaSuccess)
+        err = tc::launch(sort_place_kernel<I>, static_cast<unsigned>(s.blocks), dim3(SORT_THREADS), s.smem, stream, choices, R,
+                         E, s.range, s.warps, s.blocks, static_cast<const int *>(counts), rows, offsets);
+    return launched(err);
 }
 
 }  // namespace
@@ -545,9 +540,8 @@ extern "C" int expert_gather(int type, int T, int J, int H, int E, const int *ro
     sg_nvtx::Range r("experts: gather");
     return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
-        gather_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
-            T, J, packs, segments, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks));
-        return launched();
+        return launched(tc::launch(gather_kernel<El, decltype(v)::value>, static_cast<unsigned>(blocks + ZERO_BLOCKS), dim3(ROW_THREADS), 0, stream,
+            T, J, packs, segments, E, rows, offsets, static_cast<const El *>(x), ldx, static_cast<El *>(xs), ldxs, static_cast<int>(blocks)));
     });
 }
 
@@ -575,10 +569,9 @@ extern "C" int expert_combine(int type, int T, int J, int H, const int *rows, co
     sg_nvtx::Range r("experts: combine");
     return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
-        combine_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks), ROW_THREADS, 0, stream>>>(
+        return launched(tc::launch(combine_kernel<El, decltype(v)::value>, static_cast<unsigned>(blocks), dim3(ROW_THREADS), 0, stream,
             T, J, packs, segments, rows, weights, static_cast<const El *>(ys), ldys, static_cast<const El *>(residual), ldr,
-            static_cast<El *>(y), ldy);
-        return launched();
+            static_cast<El *>(y), ldy));
     });
 }
 
@@ -611,9 +604,8 @@ extern "C" int expert_combine_backward(int type, int T, int J, int H, int E, con
     sg_nvtx::Range r("experts: combine backward");
     return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
-        combine_backward_kernel<El, decltype(v)::value><<<static_cast<unsigned>(blocks + ZERO_BLOCKS), ROW_THREADS, 0, stream>>>(
+        return launched(tc::launch(combine_backward_kernel<El, decltype(v)::value>, static_cast<unsigned>(blocks + ZERO_BLOCKS), dim3(ROW_THREADS), 0, stream,
             T, J, packs, E, rows, offsets, weights, static_cast<const El *>(dy), lddy, static_cast<const El *>(ys), ldys,
-            static_cast<El *>(dys), lddys, dweights, static_cast<int>(blocks));
-        return launched();
+            static_cast<El *>(dys), lddys, dweights, static_cast<int>(blocks)));
     });
 }

@@ -46,7 +46,7 @@ constexpr int MN_BOX_BYTES = 64 * BK * 2;    // an MN-major box: 64 operand rows
 constexpr int MAX_STAGES = 12;
 constexpr int SORTED_EXPERTS = 256;         // of more, sorting by rows would take longer than it saves
 constexpr int TMEM_COLS = 512;
-constexpr int MAX_SPLITS = 8;                // the portable cluster size
+constexpr int MAX_SPLITS = 4;                // CTAs of a cluster that share a tile's K; 8 took longer wherever tried
 constexpr int EPI_WARPS = 8;                 // warp w: tensor-memory lanes 32 (w % 4).., column half w / 4
 constexpr int COPY_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1, TAIL_WARP = EPI_WARPS + 2;
 constexpr int THREADS = (EPI_WARPS + 3) * 32;

@@ -260,16 +260,8 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
 
 template <typename K>
 cudaError_t launch(K kernel, int features, int threads, const Few &p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((p.F + features - 1) / features));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return tc::launch(kernel, static_cast<unsigned>((p.F + features - 1) / features), dim3(static_cast<unsigned>(threads)), 0,
+                      stream, p);
 }
 bool aligned(const void *q, long long ld, int element, int bytes) {
     return reinterpret_cast<uintptr_t>(q) % bytes == 0 && ld * element % bytes == 0;

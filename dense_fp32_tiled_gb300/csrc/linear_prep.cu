@@ -69,7 +69,8 @@ __device__ __forceinline__ void copy8(const Job &job, long long u) {
 }
 template <typename T>
 __global__ void __launch_bounds__(256) copy_operands_kernel(const Job a, const Job b) {
-    tc::grid_trigger();  // a product may set itself up meanwhile; it waits for this grid before it reads
+    tc::grid_trigger();  // the next kernel may set itself up meanwhile; it waits for this grid before it reads
+    tc::grid_wait();
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
     for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < a.units + b.units; u += step) {
         if (u < a.units)
@@ -89,14 +90,14 @@ Job job_of(const linear_prep::Copy &c) {
     return j;
 }
 template <typename T>
-void copy_operands_t(const linear_prep::Copy *copies, int n, cudaStream_t stream) {
+cudaError_t copy_operands_t(const linear_prep::Copy *copies, int n, cudaStream_t stream) {
     const Job a = job_of<T>(copies[0]);
     Job b = a;
     b.units = 0;
     if (n > 1) b = job_of<T>(copies[1]);
     long long blocks = (a.units + b.units + 255) / 256;
     if (blocks > 152 * 64) blocks = 152 * 64;
-    copy_operands_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, b);
+    return tc::launch(copy_operands_kernel<T>, static_cast<unsigned>(blocks), dim3(256), 0, stream, a, b);
 }
 
 // ---- dz = dy * act'(z), and its column sums -------------------------------------------
@@ -137,6 +138,7 @@ activation_gradient_kernel(int M, int N, int E, const int *__restrict__ offsets,
     constexpr bool F32 = std::is_same<T, float>::value;
     __shared__ float part[GWARPS][32 * V];
     tc::grid_trigger();
+    tc::grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = blockIdx.x / strips, strip = blockIdx.x - chunk * strips;
     const int col = strip * 32 * V + lane * V;
@@ -212,10 +214,12 @@ activation_gradient_kernel(int M, int N, int E, const int *__restrict__ offsets,
 // Block (32, 8) per 32 columns of an expert: warp y adds chunks y, y + 8, ...
 template <typename T>
 __global__ void __launch_bounds__(256) column_sums_kernel(int M, int N, int E, const int *__restrict__ offsets,
-                                                          const float *__restrict__ sums, T *__restrict__ dbias) {
+                                                          const float *__restrict__ sums, T *__restrict__ dbias,
+                                                          int strips) {
     __shared__ float part[8][32];
     tc::grid_trigger();
-    const int e = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
+    tc::grid_wait();
+    const int e = blockIdx.x / strips, col = (blockIdx.x - e * strips) * 32 + threadIdx.x;
     int b = 0, end = M;
     if (E >= 0) {
         b = min(max(offsets[e], 0), M);
@@ -248,9 +252,10 @@ cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offse
     const long long blocks = (static_cast<long long>(M) + CHUNK - 1) / CHUNK * strips;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned grid = static_cast<unsigned>(blocks);
+    cudaError_t err = cudaSuccess;
     auto launch = [&](auto kernel) {
-        kernel<<<grid, GWARPS * 32, 0, stream>>>(M, N, E, offsets, static_cast<const T *>(dy), lddy,
-                                                 static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
+        err = tc::launch(kernel, grid, dim3(GWARPS * 32), 0, stream, M, N, E, offsets, static_cast<const T *>(dy), lddy,
+                         static_cast<const T *>(z), ldz, dz, lddz, sums, strips);
     };
     auto pick = [&](auto tag) {
         constexpr int ACT = decltype(tag)::value;
@@ -268,11 +273,12 @@ cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offse
         case LINEAR_ACT_GELU_TANH: pick(lt::Int<LINEAR_ACT_GELU_TANH>{}); break;
         default: pick(lt::Int<LINEAR_ACT_NONE>{}); break;
     }
-    cudaError_t err = cudaPeekAtLastError();
     if (err == cudaSuccess && sums != nullptr) {
-        const dim3 g2(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(E < 0 ? 1 : E));
-        column_sums_kernel<T><<<g2, dim3(32, 8), 0, stream>>>(M, N, E, offsets, sums, static_cast<T *>(dbias));
-        err = cudaPeekAtLastError();
+        const int strips32 = (N + 31) / 32;
+        const long long total = static_cast<long long>(strips32) * (E < 0 ? 1 : E);
+        if (total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        err = tc::launch(column_sums_kernel<T>, static_cast<unsigned>(total), dim3(32, 8), 0, stream, M, N, E, offsets,
+                         static_cast<const float *>(sums), static_cast<T *>(dbias), strips32);
     }
     return err;
 }
@@ -284,13 +290,9 @@ namespace linear_prep {
 cudaError_t copy_operands(int type, const Copy *copies, int n, cudaStream_t stream) {
     if (n == 0) return cudaSuccess;
     sg_nvtx::Range r("linear: operand copies");
-    if (type == LINEAR_F32)
-        copy_operands_t<float>(copies, n, stream);
-    else if (type == LINEAR_BF16)
-        copy_operands_t<__nv_bfloat16>(copies, n, stream);
-    else
-        copy_operands_t<__half>(copies, n, stream);
-    return cudaPeekAtLastError();
+    return type == LINEAR_F32    ? copy_operands_t<float>(copies, n, stream)
+           : type == LINEAR_BF16 ? copy_operands_t<__nv_bfloat16>(copies, n, stream)
+                                 : copy_operands_t<__half>(copies, n, stream);
 }
 
 size_t sums_bytes(int M, int N, int E) {
