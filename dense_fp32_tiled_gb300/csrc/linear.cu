@@ -81,6 +81,10 @@ struct Product {
     long long ldr, ldz, ldo, out_expert;
     int act;
     int vec;                  // VEC_* of what has 16-byte aligned rows
+    // a bias gradient to add up from the chunks' column sums on the side (see column_sum)
+    const float *sums;
+    void *dbias;
+    int sums_M, sums_N, sums_E;
     unsigned *timeout_flag;
 };
 constexpr int VEC_OUT = 1, VEC_Z = 2, VEC_RESIDUAL = 4;
@@ -349,8 +353,8 @@ __device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld,
 // K_BY_EXPERT: the last K tile of an expert also holds rows of the next one.
 // It is copied on a barrier of its own, tail_bar[s], and warp 10 clears those
 // rows in both operands (a NaN times 0 would be one) and then reports the stage
-// full, while the copies go on (the copying warp doing it itself stalled them:
-// 203 us for the weight gradient of 16 uneven experts, 16384 x 2048 x 4096).
+// full, while the copies go on.  Before that, the same warp adds up the bias
+// gradient, where the product is the first of a backward pass.
 template <int CG, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
@@ -505,7 +509,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 }
             }
         }
-        // this CTA's last copies are read before it can exit
+        // this CTA's last copies are read before it can exit; after a wait that ran out, they
+        // are given one more limit to land
+        waiter.gave_up = false;
         for (; issued > 0; --issued) {
             if (s == 0) {
                 s = stages;
@@ -515,6 +521,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             waiter.wait(empty0 + 8u * s, ph ^ 1);
         }
     } else if (warp == TAIL_WARP) {
+        if (p.dbias != nullptr) {
+            const int strips = (p.sums_N + 31) / 32;
+            const long long jobs = static_cast<long long>(strips) * (p.sums_E < 0 ? 1 : p.sums_E);
+            for (long long j = blockIdx.x; j < jobs; j += gridDim.x) {
+                const int e = static_cast<int>(j / strips), col = static_cast<int>(j - static_cast<long long>(e) * strips) * 32 + lane;
+                const float t = linear_prep::column_sum(p.sums, p.sums_M, p.sums_N, p.sums_E, p.offsets, e, col, 0, 1);
+                if (col < p.sums_N) static_cast<T *>(p.dbias)[static_cast<long long>(e) * p.sums_N + col] = from_f<T>(t);
+            }
+        }
         if (p.mode == K_BY_EXPERT) {
             const uint32_t full0 = tc::peer_addr(tc::smem_u32(&full_bar[0]), lead);
             const int boxes = (P_BYTES + p.q_bytes) / MN_BOX_BYTES;
@@ -1416,6 +1431,8 @@ int backward(const Call &c) {
     char *ws = static_cast<char *>(c.ws);
     const bool products = (want.dx || want.dw) && c.K > 0;
     const bool empty = c.M == 0 || c.N == 0 || c.E == 0;
+    Product p;
+    memset(&p, 0, sizeof p);
     // the weight and x, where they need a copy (the weight, then x), dz and the column sums
     Operand P_dx, X;
     if (!empty && products) {
@@ -1439,10 +1456,18 @@ int backward(const Call &c) {
             dz.plane = c.M * dz.ld;
             if (c.type == LINEAR_F32) dz.planes = 3;
         }
-        void *sums = ws + need.dz;
-        const cudaError_t err = linear_prep::activation_gradient(
-            c.type, c.act, c.M, c.N, c.E, c.offsets, c.dy, c.lddy, c.preact_in, c.ldz, make ? ws : nullptr, dz.ld,
-            want.dbias ? sums : nullptr, c.dbias, c.stream);
+        float *sums = want.dbias ? reinterpret_cast<float *>(ws + need.dz) : nullptr;
+        cudaError_t err = linear_prep::activation_gradient(c.type, c.act, c.M, c.N, c.E, c.offsets, c.dy, c.lddy,
+                                                           c.preact_in, c.ldz, make ? ws : nullptr, dz.ld, sums, c.stream);
+        if (want.dbias && products) {  // a warp of the first product adds them up
+            p.sums = sums;
+            p.dbias = c.dbias;
+            p.sums_M = c.M;
+            p.sums_N = c.N;
+            p.sums_E = c.E;
+        } else if (want.dbias && err == cudaSuccess) {
+            err = linear_prep::column_sums(c.type, c.M, c.N, c.E, c.offsets, sums, c.dbias, c.stream);
+        }
         if (err != cudaSuccess) {
             (void)cudaGetLastError();
             return SGEMM_ERR_LAUNCH;
@@ -1454,8 +1479,6 @@ int backward(const Call &c) {
         }
     }
     if (!products) return SGEMM_OK;
-    Product p;
-    memset(&p, 0, sizeof p);
     p.offsets = c.offsets;
     p.E = c.E > 0 ? c.E : 0;
     if (want.dx && c.M > 0) {
@@ -1469,6 +1492,7 @@ int backward(const Call &c) {
         p.ldo = c.lddx;
         st = run_product(c.type, p, P_dx, Q, d, c.stream);
         if (st != SGEMM_OK) return st;
+        p.dbias = nullptr;
     }
     if (want.dw && c.N > 0 && c.E != 0) {
         Operand Z = dz;

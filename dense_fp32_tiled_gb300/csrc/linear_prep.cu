@@ -101,12 +101,10 @@ cudaError_t copy_operands_t(const linear_prep::Copy *copies, int n, cudaStream_t
 }
 
 // ---- dz = dy * act'(z), and its column sums -------------------------------------------
-// A block takes CHUNK rows of 32 * V columns; warp w its rows w, w + 8, ...
-// Rows of different experts are summed apart: the rows of expert e in chunk c
-// go to partial sum c + e, which no other pair of the two shares, as both only
-// grow along the rows.  A second kernel adds each expert's partial sums in
-// chunk order, so the sums do not depend on timing.
-constexpr int CHUNK = 64;
+// A block takes a chunk of rows of 32 * V columns; warp w its rows w, w + 8, ...
+// Rows of different experts are summed apart; the chunks' sums are added up
+// afterwards, in chunk order, so they do not depend on timing.
+using linear_prep::CHUNK;
 constexpr int GWARPS = 8;
 
 template <typename T, int V>
@@ -220,15 +218,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(int M, int N, int E, c
     tc::grid_trigger();
     tc::grid_wait();
     const int e = blockIdx.x / strips, col = (blockIdx.x - e * strips) * 32 + threadIdx.x;
-    int b = 0, end = M;
-    if (E >= 0) {
-        b = min(max(offsets[e], 0), M);
-        end = min(max(offsets[e + 1], b), M);
-    }
-    float t = 0.0f;
-    if (col < N && end > b)
-        for (int c = b / CHUNK + threadIdx.y; c <= (end - 1) / CHUNK; c += 8)
-            t += sums[static_cast<long long>(c + e) * N + col];
+    float t = linear_prep::column_sum(sums, M, N, E, offsets, e, col, threadIdx.y, 8);
     part[threadIdx.y][threadIdx.x] = t;
     __syncthreads();
     if (threadIdx.y == 0 && col < N) {
@@ -241,7 +231,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(int M, int N, int E, c
 
 template <typename T>
 cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offsets, const void *dy, long long lddy,
-                                  const void *z, long long ldz, void *dz, long long lddz, float *sums, void *dbias,
+                                  const void *z, long long ldz, void *dz, long long lddz, float *sums,
                                   cudaStream_t stream) {
     if (dz == nullptr && sums == nullptr) return cudaSuccess;
     constexpr int V = 16 / static_cast<int>(sizeof(T));
@@ -273,14 +263,16 @@ cudaError_t activation_gradient_t(int act, int M, int N, int E, const int *offse
         case LINEAR_ACT_GELU_TANH: pick(lt::Int<LINEAR_ACT_GELU_TANH>{}); break;
         default: pick(lt::Int<LINEAR_ACT_NONE>{}); break;
     }
-    if (err == cudaSuccess && sums != nullptr) {
-        const int strips32 = (N + 31) / 32;
-        const long long total = static_cast<long long>(strips32) * (E < 0 ? 1 : E);
-        if (total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        err = tc::launch(column_sums_kernel<T>, static_cast<unsigned>(total), dim3(32, 8), 0, stream, M, N, E, offsets,
-                         static_cast<const float *>(sums), static_cast<T *>(dbias), strips32);
-    }
     return err;
+}
+
+template <typename T>
+cudaError_t column_sums_t(int M, int N, int E, const int *offsets, const float *sums, void *dbias, cudaStream_t stream) {
+    const int strips = (N + 31) / 32;
+    const long long blocks = static_cast<long long>(strips) * (E < 0 ? 1 : E);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return tc::launch(column_sums_kernel<T>, static_cast<unsigned>(blocks), dim3(32, 8), 0, stream, M, N, E, offsets, sums,
+                      static_cast<T *>(dbias), strips);
 }
 
 }  // namespace
@@ -301,15 +293,22 @@ size_t sums_bytes(int M, int N, int E) {
 }
 
 cudaError_t activation_gradient(int type, int act, int M, int N, int E, const int *offsets, const void *dy,
-                                long long lddy, const void *z, long long ldz, void *dz, long long lddz, void *sums,
-                                void *dbias, cudaStream_t stream) {
+                                long long lddy, const void *z, long long ldz, void *dz, long long lddz, float *sums,
+                                cudaStream_t stream) {
     sg_nvtx::Range r("linear: activation gradient");
-    float *s = static_cast<float *>(sums);
     if (type == LINEAR_F32)
-        return activation_gradient_t<float>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
+        return activation_gradient_t<float>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, sums, stream);
     if (type == LINEAR_BF16)
-        return activation_gradient_t<__nv_bfloat16>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
-    return activation_gradient_t<__half>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, s, dbias, stream);
+        return activation_gradient_t<__nv_bfloat16>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, sums, stream);
+    return activation_gradient_t<__half>(act, M, N, E, offsets, dy, lddy, z, ldz, dz, lddz, sums, stream);
+}
+
+cudaError_t column_sums(int type, int M, int N, int E, const int *offsets, const float *sums, void *dbias,
+                        cudaStream_t stream) {
+    sg_nvtx::Range r("linear: column sums");
+    return type == LINEAR_F32    ? column_sums_t<float>(M, N, E, offsets, sums, dbias, stream)
+           : type == LINEAR_BF16 ? column_sums_t<__nv_bfloat16>(M, N, E, offsets, sums, dbias, stream)
+                                 : column_sums_t<__half>(M, N, E, offsets, sums, dbias, stream);
 }
 
 }  // namespace linear_prep
