@@ -85,8 +85,15 @@ struct Product {
     const float *sums;
     void *dbias;
     int sums_M, sums_N, sums_E;
+    int order;                // ORDER_*
     unsigned *timeout_flag;
 };
+// A backward pass's two products need the same earlier kernels and not each
+// other.  The first lets the second start once it has waited for those
+// (ORDER_FIRST); the second takes the SMs that the first leaves or never had,
+// and waits for it before it ends (ORDER_BESIDE), so that what follows in the
+// stream still comes after both.
+enum Order { ORDER_ALONE = 0, ORDER_FIRST = 1, ORDER_BESIDE = 2 };
 constexpr int VEC_OUT = 1, VEC_Z = 2, VEC_RESIDUAL = 4;
 struct Maps {
     CUtensorMap p, q;
@@ -394,7 +401,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         tc::tma_prefetch(&maps.q);
     }
     if (warp == MMA_WARP) tc::tmem_alloc<CG, TMEM_COLS>(tc::smem_u32(&tmem_slot));
-    tc::grid_wait();  // nothing of global memory is touched before the earlier kernels are done
+    // nothing of global memory is touched before the earlier kernels are done
+    if (p.order != ORDER_BESIDE) tc::grid_wait();
+    if (p.order == ORDER_FIRST) tc::grid_trigger();
     int tiles = p.nt * p.nf;
     if (p.mode != DENSE) {
         // clamp: non-decreasing and inside the rows, whatever the offsets hold
@@ -818,49 +827,59 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_ready), threadIdx.x));
                 waiter.wait<true>(tc::smem_u32(&part_ready), handed & 1);
                 // the parts' sum in rank order, four features of a token per thread, shared out over
-                // all CTAs; the parts' loads are in flight together
+                // all CTAs, two such at a time with their loads in flight together
                 const uint32_t mine = tc::smem_u32(partial);
                 const int fb = w.ft * PROWS;
-                for (int i = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i < n_tile * (PROWS / 4);
-                     i += S * EPI_THREADS) {
-                    const int fi = fb + 4 * (i & (PROWS / 4 - 1));
-                    if (fi >= p.F) continue;
-                    float4 part[MAX_SPLITS];
-#pragma unroll
-                    for (int s = 0; s < MAX_SPLITS; ++s)
-                        part[s] = s < S ? tc::ld_cluster_f32x4(tc::peer_addr(mine + 16u * i, s)) : make_float4(0, 0, 0, 0);
-                    const long long row = static_cast<long long>(w.t0) + i / (PROWS / 4);
-                    const T *bp = p.bias == nullptr ? nullptr
+                const T *bias_e = p.bias == nullptr ? nullptr
                                                     : static_cast<const T *>(p.bias) +
-                                                          (p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + fi;
-                    const T *rp = p.residual == nullptr ? nullptr : static_cast<const T *>(p.residual) + row * p.ldr + fi;
-                    float v[4], b[4] = {0, 0, 0, 0}, r[4] = {0, 0, 0, 0};
+                                                          (p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0);
+                constexpr int U = 2;
+                const int items = n_tile * (PROWS / 4), step = S * EPI_THREADS;
+                for (int i0 = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i0 < items; i0 += U * step) {
+                    float4 part[U][MAX_SPLITS];
+                    float b[U][4], r[U][4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (fi + k < p.F) {
-                            if (bp != nullptr) b[k] = to_f(bp[k]);
-                            if (rp != nullptr) r[k] = to_f(rp[k]);
+                    for (int u = 0; u < U; ++u) {
+                        const int i = i0 + u * step, fi = fb + 4 * (i & (PROWS / 4 - 1));
+                        const bool in = i < items && fi < p.F;
+#pragma unroll
+                        for (int s = 0; s < MAX_SPLITS; ++s)
+                            part[u][s] = in && s < S ? tc::ld_cluster_f32x4(tc::peer_addr(mine + 16u * i, s)) : make_float4(0, 0, 0, 0);
+                        const T *rp = static_cast<const T *>(p.residual) +
+                                      (static_cast<long long>(w.t0) + i / (PROWS / 4)) * p.ldr + fi;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool ok = in && fi + k < p.F;
+                            b[u][k] = ok && bias_e != nullptr ? to_f(bias_e[fi + k]) : 0.0f;
+                            r[u][k] = ok && p.residual != nullptr ? to_f(rp[k]) : 0.0f;
                         }
-                    v[0] = part[0].x, v[1] = part[0].y, v[2] = part[0].z, v[3] = part[0].w;
+                    }
 #pragma unroll
-                    for (int s = 1; s < MAX_SPLITS; ++s)
-                        v[0] += part[s].x, v[1] += part[s].y, v[2] += part[s].z, v[3] += part[s].w;
+                    for (int u = 0; u < U; ++u) {
+                        const int i = i0 + u * step, fi = fb + 4 * (i & (PROWS / 4 - 1));
+                        if (i >= items || fi >= p.F) continue;
+                        const long long row = static_cast<long long>(w.t0) + i / (PROWS / 4);
+                        float v[4] = {part[u][0].x, part[u][0].y, part[u][0].z, part[u][0].w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] += b[k];
-                    if (p.z != nullptr) {
-                        T *z = static_cast<T *>(p.z) + row * p.ldz + fi;
+                        for (int s = 1; s < MAX_SPLITS; ++s)
+                            v[0] += part[u][s].x, v[1] += part[u][s].y, v[2] += part[u][s].z, v[3] += part[u][s].w;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] += b[u][k];
+                        if (p.z != nullptr) {
+                            T *z = static_cast<T *>(p.z) + row * p.ldz + fi;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (fi + k < p.F) z[k] = from_f<T>(v[k]);
+                        }
+                        lt::with_activation(p.act, [&](auto a) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[k] = lt::activate<decltype(a)::value, F32>(v[k]);
+                        });
+                        T *o = out + row * p.ldo + fi;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (fi + k < p.F) z[k] = from_f<T>(v[k]);
+                            if (fi + k < p.F) o[k] = from_f<T>(p.residual != nullptr ? v[k] + r[u][k] : v[k]);
                     }
-                    lt::with_activation(p.act, [&](auto a) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = lt::activate<decltype(a)::value, F32>(v[k]);
-                    });
-                    T *o = out + row * p.ldo + fi;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (fi + k < p.F) o[k] = from_f<T>(rp != nullptr ? v[k] + r[k] : v[k]);
                 }
                 epi_bar();
                 if (threadIdx.x < S) tc::mbar_arrive(tc::peer_addr(tc::smem_u32(&part_read), threadIdx.x));
@@ -868,6 +887,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             }
         }
     }
+    if (p.order == ORDER_BESIDE) tc::grid_wait();
     tc::fence_before();
     __syncthreads();
     tc::cluster_sync();  // no remote arrive and no read of this CTA's memory is still pending
@@ -1490,9 +1510,12 @@ int backward(const Call &c) {
         p.mode = c.E >= 0 && !empty ? ROWS_BY_EXPERT : DENSE;
         p.out = c.dx;
         p.ldo = c.lddx;
+        const bool two = !empty && want.dw;  // without rows there may be many more products
+        p.order = two ? ORDER_FIRST : ORDER_ALONE;
         st = run_product(c.type, p, P_dx, Q, d, c.stream);
         if (st != SGEMM_OK) return st;
         p.dbias = nullptr;
+        p.order = two ? ORDER_BESIDE : ORDER_ALONE;
     }
     if (want.dw && c.N > 0 && c.E != 0) {
         Operand Z = dz;
