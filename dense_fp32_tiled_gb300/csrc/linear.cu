@@ -118,16 +118,29 @@ struct Tables {
 // or, where tiles come in falling order of length, back and forth, so that no
 // unit always gets the longer ones.
 __device__ __forceinline__ int next_tile(int idx, int unit, int units, bool snake) {
+    if (!snake) return idx + units;
     const int round = idx / units;
-    return (round + 1) * units + (snake && (round & 1) == 0 ? units - 1 - unit : unit);
+    return (round + 1) * units + ((round & 1) == 0 ? units - 1 - unit : unit);
 }
+// Tile idx of nt x nf, 8 token tiles at a time: the tiles in flight share few
+// panels of both operands.  Divisions only where they are needed: the first
+// tile's copies wait for this.
 __device__ __forceinline__ void raster(int idx, int nt, int nf, int &tt, int &ft) {
-    // 8 token tiles at a time: the tiles in flight share few panels of both operands
-    const int per_group = 8 * nf;
-    const int g = idx / per_group, r = idx - g * per_group;
+    int g = 0, r = idx;
+    if (nt > 8) {
+        const int per_group = 8 * nf;
+        g = idx / per_group;
+        r = idx - g * per_group;
+    }
     const int rows = min(8, nt - 8 * g);
-    tt = 8 * g + r % rows;
-    ft = r / rows;
+    if (rows == 8) {
+        ft = r >> 3;
+    } else if (rows == 1) {
+        ft = r;
+    } else {
+        ft = r / rows;
+    }
+    tt = 8 * g + r - ft * rows;
 }
 
 // The same value, known to the compiler as one for the whole warp: what the
@@ -374,7 +387,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     const uint32_t sbase = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *sgen = smem_raw + (sbase - tc::smem_u32(smem_raw));
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t rank = tc::cluster_rank();
+    const uint32_t rank = uniform(static_cast<int>(tc::cluster_rank()));
     const int S = CG == 1 ? p.splits : 1;
     const int cluster = CG == 2 ? 2 : S;
     const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
@@ -384,23 +397,26 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     const Tables tb{tables, tables + p.E + 2};
     const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset + (warp < EPI_WARPS ? warp : 0) * p.epi_bytes;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            tc::mbar_init(tc::smem_u32(&full_bar[s]), CG);
-            tc::mbar_init(tc::smem_u32(&empty_bar[s]), 1);
-            tc::mbar_init(tc::smem_u32(&tail_bar[s]), 1);
+    if (warp == 0) {  // a barrier or three per lane: one thread would take as long as a copy from L2
+        if (lane < p.stages) {
+            tc::mbar_init(tc::smem_u32(&full_bar[lane]), CG);
+            tc::mbar_init(tc::smem_u32(&empty_bar[lane]), 1);
+            tc::mbar_init(tc::smem_u32(&tail_bar[lane]), 1);
+        } else if (lane < MAX_STAGES + 2) {
+            const int b = lane - MAX_STAGES;
+            if (b >= 0) {
+                tc::mbar_init(tc::smem_u32(&acc_full[b]), 1);
+                tc::mbar_init(tc::smem_u32(&acc_empty[b]), CG * EPI_WARPS);
+            }
+        } else if (lane == MAX_STAGES + 2) {
+            tc::mbar_init(tc::smem_u32(&part_ready), S);
+            tc::mbar_init(tc::smem_u32(&part_read), S);
         }
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(tc::smem_u32(&acc_full[b]), 1);
-            tc::mbar_init(tc::smem_u32(&acc_empty[b]), CG * EPI_WARPS);
-        }
-        tc::mbar_init(tc::smem_u32(&part_ready), S);
-        tc::mbar_init(tc::smem_u32(&part_read), S);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    } else if (warp == COPY_WARP && lane == 0) {
         tc::tma_prefetch(&maps.p);
         tc::tma_prefetch(&maps.q);
     }
-    if (warp == MMA_WARP) tc::tmem_alloc<CG, TMEM_COLS>(tc::smem_u32(&tmem_slot));
     // nothing of global memory is touched before the earlier kernels are done
     if (p.order != ORDER_BESIDE) tc::grid_wait();
     if (p.order == ORDER_FIRST) tc::grid_trigger();
@@ -451,11 +467,17 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 }
         }
     }
-    tc::fence_before();
     __syncthreads();
     tc::cluster_sync();  // the barriers of all CTAs exist before any remote arrive or copy
-    tc::fence_after();
-    const uint32_t tmem = uniform(static_cast<int>(tmem_slot));
+    // the first copies are on their way while tensor memory is allocated
+    uint32_t tmem = 0;
+    if (warp < EPI_WARPS || warp == MMA_WARP) {
+        if (warp == MMA_WARP) tc::tmem_alloc<CG, TMEM_COLS>(tc::smem_u32(&tmem_slot));
+        tc::fence_before();
+        asm volatile("bar.sync 2, %0;\n" ::"n"(EPI_THREADS + 32) : "memory");
+        tc::fence_after();
+        tmem = uniform(static_cast<int>(tmem_slot));
+    }
     if (p.mode == ROWS_BY_EXPERT)
         tiles = tb.first[p.E + 1];
     else if (p.mode == K_BY_EXPERT)
