@@ -80,7 +80,7 @@ struct Product {
     void *z, *out;
     long long ldr, ldz, ldo, out_expert;
     int act;
-    int vec;                  // VEC_* of what has 16-byte aligned rows
+    int widths;               // see OUT_SHIFT
     // a bias gradient to add up from the chunks' column sums on the side (see column_sum)
     const float *sums;
     void *dbias;
@@ -94,7 +94,8 @@ struct Product {
 // and waits for it before it ends (ORDER_BESIDE), so that what follows in the
 // stream still comes after both.
 enum Order { ORDER_ALONE = 0, ORDER_FIRST = 1, ORDER_BESIDE = 2 };
-constexpr int VEC_OUT = 1, VEC_Z = 2, VEC_RESIDUAL = 4;
+// Bytes of an access that all rows of out, z and the residual allow (16, 4 or 2), in Product::widths.
+constexpr int OUT_SHIFT = 0, Z_SHIFT = 8, RESIDUAL_SHIFT = 16;
 struct Maps {
     CUtensorMap p, q;
 };
@@ -276,24 +277,63 @@ inline int epi_bytes(bool z, bool residual) { return STAGE16 * (1 + (z ? 1 : 0) 
 __device__ __forceinline__ uint32_t stage16(uint32_t buf, int row, int chunk) {
     return buf + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
+// Rows that allow no 16-byte access move in narrower ones, 4 bytes if they can,
+// but always with the lanes along the row: two rows or one an instruction.
+// (Eight 2-byte stores of each lane's 16 bytes touch 32 rows' sectors each:
+// 6783 x 1417 x 256 in bf16 with residual and saved argument took 117 us, so 60.)
+// The rows' functions for narrow accesses are calls of their own: inlined, they cost the epilogue registers.
+template <typename T>
+__device__ __noinline__ void fetch_narrow(const T *base, long long ld, int F, int width, uint32_t buf, int n, int f0, int lane) {
+    if (width == 4) {
+        const int col = (lane & 15) * 2, f = f0 + col;
+#pragma unroll 4
+        for (int row = lane >> 4; row < n && row < EPI_T; row += 2) {
+            const T *src = base + row * ld + col;
+            const uint32_t dst = stage16(buf, row, col >> 3) + 2 * (col & 7);
+            if (f + 1 < F)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+            else if (f < F)
+                asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst), "h"(*reinterpret_cast<const unsigned short *>(src)) : "memory");
+        }
+    } else {  // no asynchronous copy moves 2 bytes: 16 rows' loads together, then their stores
+        const bool in = f0 + lane < F;
+        const unsigned short *src = reinterpret_cast<const unsigned short *>(base) + lane;
+#pragma unroll
+        for (int h = 0; h < EPI_T; h += 16) {
+            unsigned short v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = in && h + i < n ? src[(h + i) * ld] : static_cast<unsigned short>(0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(stage16(buf, h + i, lane >> 3) + 2 * (lane & 7)), "h"(v[i])
+                             : "memory");
+        }
+    }
+}
 // Residual rows row0 .. row0 + n of features f0 .. f0 + 31 into a buffer.
 template <typename T>
 __device__ __forceinline__ void fetch16(const Product &p, uint32_t buf, long long row0, int n, int f0, int lane) {
+    const int width = (p.widths >> RESIDUAL_SHIFT) & 255;
+    const T *base = static_cast<const T *>(p.residual) + row0 * p.ldr + f0;
+    if (width == 16) {
 #pragma unroll
-    for (int i = 0; i < EPI_T / 8; ++i) {
-        const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
-        if (row < n && f < p.F) {
-            const T *src = static_cast<const T *>(p.residual) + (row0 + row) * p.ldr + f;
-            const uint32_t dst = stage16(buf, row, chunk);
-            if ((p.vec & VEC_RESIDUAL) && f + 8 <= p.F) {
-                tc::cp_async16(dst, src);
-            } else {
-                for (int k = 0; k < 8 && f + k < p.F; ++k)
-                    asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + 2 * k),
-                                 "h"(*reinterpret_cast<const unsigned short *>(src + k))
-                                 : "memory");
+        for (int i = 0; i < EPI_T / 8; ++i) {
+            const int row = (lane >> 2) + 8 * i, chunk = lane & 3, f = f0 + 8 * chunk;
+            if (row < n && f < p.F) {
+                const T *src = base + row * p.ldr + 8 * chunk;
+                const uint32_t dst = stage16(buf, row, chunk);
+                if (f + 8 <= p.F) {
+                    tc::cp_async16(dst, src);
+                } else {
+                    for (int k = 0; k < 8 && f + k < p.F; ++k)
+                        asm volatile("st.shared.b16 [%0], %1;\n" ::"r"(dst + 2 * k),
+                                     "h"(*reinterpret_cast<const unsigned short *>(src + k))
+                                     : "memory");
+                }
             }
         }
+    } else {
+        fetch_narrow<T>(base, p.ldr, p.F, width, buf, n, f0, lane);
     }
     tc::cp_async_commit();
 }
@@ -330,31 +370,55 @@ __device__ __forceinline__ void stage_fragments(const float (&v)[2][16], uint32_
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld, bool vec, long long row0, int n, int f0,
+__device__ __noinline__ void store_narrow(uint32_t buf, T *dst, long long ld, int width, int n, int f0, int F, int lane) {
+    const int across = width == 4 ? 16 : 32, per = 32 / across;
+    const int col = (lane & (across - 1)) * (32 / across), f = f0 + col;
+    int row = width == 4 ? lane >> 4 : 0;
+    T *o = dst + row * ld + col;
+#pragma unroll 8
+    for (; row < n && row < EPI_T; row += per, o += per * ld) {
+        const uint32_t at = stage16(buf, row, col >> 3) + 2 * (col & 7);
+        if (width == 4 && f + 1 < F) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+            *reinterpret_cast<uint32_t *>(o) = v;
+        } else if (f < F) {
+            unsigned short v;
+            asm volatile("ld.shared.b16 %0, [%1];\n" : "=h"(v) : "r"(at) : "memory");
+            *reinterpret_cast<unsigned short *>(o) = v;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld, int width, long long row0, int n, int f0,
                                              int F, int lane) {
-    const int chunk = lane & 3, f = f0 + 8 * chunk;
-    T *o = dst + (row0 + (lane >> 2)) * ld + f;
+    if (width == 16) {
+        const int chunk = lane & 3, f = f0 + 8 * chunk;
+        T *o = dst + (row0 + (lane >> 2)) * ld + f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t w[2][4];
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                         : "r"(stage16(buf, (lane >> 2) + 8 * (2 * h + i), chunk))
-                         : "memory");
+            for (int i = 0; i < 2; ++i)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                             : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                             : "r"(stage16(buf, (lane >> 2) + 8 * (2 * h + i), chunk))
+                             : "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i, o += 8 * ld) {
-            if ((lane >> 2) + 8 * (2 * h + i) >= n || f >= F) continue;
-            if (vec && f + 8 <= F) {
-                *reinterpret_cast<uint4 *>(o) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-            } else {
+            for (int i = 0; i < 2; ++i, o += 8 * ld) {
+                if ((lane >> 2) + 8 * (2 * h + i) >= n || f >= F) continue;
+                if (f + 8 <= F) {
+                    *reinterpret_cast<uint4 *>(o) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (f + k < F)
-                        reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[i][k >> 1] >> (16 * (k & 1)));
+                    for (int k = 0; k < 8; ++k)
+                        if (f + k < F)
+                            reinterpret_cast<unsigned short *>(o)[k] = static_cast<unsigned short>(w[i][k >> 1] >> (16 * (k & 1)));
+                }
             }
         }
+    } else {
+        store_narrow<T>(buf, dst + row0 * ld + f0, ld, width, n, f0, F, lane);
     }
 }
 
@@ -828,8 +892,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     stage_fragments<T>(v, obuf, lane);
                     __syncwarp();
                     if (p.z != nullptr)
-                        store_staged<T>(zbuf, static_cast<T *>(p.z), p.ldz, (p.vec & VEC_Z) != 0, row0 + c, n_warp - c, f0, p.F, lane);
-                    store_staged<T>(obuf, out, p.ldo, (p.vec & VEC_OUT) != 0, row0 + c, n_warp - c, f0, p.F, lane);
+                        store_staged<T>(zbuf, static_cast<T *>(p.z), p.ldz, (p.widths >> Z_SHIFT) & 255, row0 + c, n_warp - c, f0, p.F, lane);
+                    store_staged<T>(obuf, out, p.ldo, (p.widths >> OUT_SHIFT) & 255, row0 + c, n_warp - c, f0, p.F, lane);
                     if (more) {
                         tc::tmem_ld_wait(next[0]);
                         tc::tmem_ld_wait(next[1]);
@@ -1165,9 +1229,12 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     const size_t used = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part + tables;
     p.epi_offset = static_cast<int>((used + 127) / 128 * 128);
     const size_t smem = used + epi;
-    auto rows16 = [&](const void *base, long long ld) { return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld % 8 == 0; };
-    p.vec = (rows16(p.out, p.ldo) && p.out_expert % 8 == 0 ? VEC_OUT : 0) | (rows16(p.z, p.ldz) ? VEC_Z : 0) |
-            (rows16(p.residual, p.ldr) ? VEC_RESIDUAL : 0);
+    auto width = [&](const void *base, long long ld, long long expert) {
+        const unsigned long long bits = reinterpret_cast<uintptr_t>(base) | static_cast<unsigned long long>(ld | expert) * 2;
+        return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    };
+    p.widths = width(p.out, p.ldo, p.out_expert) << OUT_SHIFT | width(p.z, p.ldz, 0) << Z_SHIFT |
+               width(p.residual, p.ldr, 0) << RESIDUAL_SHIFT;
     Maps maps;
     memset(&maps, 0, sizeof maps);
     const bool f16 = type == LINEAR_F16;
