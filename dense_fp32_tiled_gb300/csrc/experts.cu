@@ -275,9 +275,9 @@ __device__ __forceinline__ void clear_rest(T *out, long long ld, int used, long 
 
 // A warp takes a segment of one token's row: SEG accesses per lane.  With 16-byte
 // ones a single access per lane and four of the token's rows in flight serve the
-// sum best (16384 tokens, 4 choices, 4096 wide in bf16: 134 us; two accesses and
-// two rows 137, four and two 183: fewer registers, more warps); narrow ones want
-// eight (5000 tokens, 6 choices, 1001 wide in FP32: 27 us, one 48).
+// sum best (16384 tokens, 4 choices, 4096 wide in bf16: 134 us, 6.0 TB/s; two
+// accesses and two rows 137, four and two 183: fewer registers, more warps); narrow
+// ones want eight (5000 tokens, 6 choices, 1001 wide in FP32: 27 us, one 48).
 __host__ __device__ constexpr int seg_of(int bytes) { return bytes == 16 ? 1 : bytes == 8 ? 2 : 8; }
 
 template <typename T, int V>

@@ -345,9 +345,9 @@ __device__ __forceinline__ void prefetch_residual(const Product &p, long long ro
     for (int r = lane; r < n; r += 32)
         asm volatile("prefetch.global.L2 [%0];\n" ::"l"(base + r * p.ldr * static_cast<long long>(sizeof(T))) : "memory");
 }
-// The residual of the same warp's part of tile idx (a call of its own: inlined, it costs the epilogue registers).
+// The residual of the same warp's part of tile idx.
 template <int CG, typename T>
-__device__ __noinline__ void prefetch_next(int idx, const Product &p, const Tables &tb, int rank, int col0, int cols, int lane0,
+__device__ __forceinline__ void prefetch_next(int idx, const Product &p, const Tables &tb, int rank, int col0, int cols, int lane0,
                                            int lane) {
     const Tile w = locate<CG>(idx, p, tb, rank);
     const int f0 = w.ft * (PROWS * CG) + (CG == 2 ? rank : 0) * PROWS + lane0;
@@ -1127,8 +1127,8 @@ int q_bytes_of(int rows, bool mn) { return mn ? (rows + 63) / 64 * MN_BOX_BYTES 
 // gives an SM when all copy (62 a clock measured), and the issue of a stage
 // (370 clocks measured with narrow tiles).  Whole waves of tiles count, and
 // between filling the pipeline and draining the last accumulator about 6000
-// clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 78, 256 wide 86,
-// 128 wide 97; single CTAs 256 wide 102, 128 wide 135.
+// clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 73, 256 wide 82,
+// 128 wide 95; single CTAs 256 wide 93, 128 wide 126.
 Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
     const bool f32 = type == LINEAR_F32;
     Plan best;

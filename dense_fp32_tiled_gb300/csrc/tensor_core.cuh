@@ -52,7 +52,7 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 // Arrive and announce `bytes` of copies on a barrier of this CTA, or (CG = 2)
 // of either CTA of the pair.  Relaxed: the waiting thread is to see what the copies wrote, and
 // they order that themselves; a release here waits out the thread's earlier
-// copies' issue, about 0.9 us a stage.
+// copies' issue, about 0.4 us a stage.
 template <int CG>
 __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
     if constexpr (CG == 2)
