@@ -56,6 +56,26 @@ template <int WORDS>
 struct alignas(4 * WORDS) Words {
     uint32_t v[WORDS];
 };
+// A weight's 16 or 8 bytes, read once: not kept in L1, and L2 fetches the 256
+// bytes around them at once, which other steps of the warp (order 0: the
+// neighbouring blocks) read next, as an access takes only 64 bytes of a row (one
+// token, 8192 x 8192, 16 bits: 30 us without, 25 with).  Volatile keeps it behind
+// grid_wait.
+template <int WORDS>
+__device__ __forceinline__ Words<WORDS> stream(const void *p, bool in) {
+    Words<WORDS> r;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) r.v[i] = 0u;
+    if (in) {
+        if constexpr (WORDS == 4)
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3])
+                         : "l"(p));
+        else
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.b32 {%0, %1}, [%2];\n" : "=r"(r.v[0]), "=r"(r.v[1]) : "l"(p));
+    }
+    return r;
+}
 template <int N, bool VEC>
 __device__ __forceinline__ Words<N / 2> fetch16(const void *p, int left) {
     Words<N / 2> r;
@@ -83,6 +103,14 @@ __device__ __forceinline__ float4 fetch32(const float *p, int left) {
         if (left > 3) r.w = p[3];
     }
     return r;
+}
+
+// fetch32 for a weight, see stream
+template <bool VEC>
+__device__ __forceinline__ float4 stream32(const float *p, int left) {
+    if constexpr (!VEC) return fetch32<false>(p, left);
+    const Words<4> r = stream<4>(p, left > 0);
+    return make_float4(__uint_as_float(r.v[0]), __uint_as_float(r.v[1]), __uint_as_float(r.v[2]), __uint_as_float(r.v[3]));
 }
 
 template <typename T>
@@ -127,13 +155,20 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
                     const int f = f0 + 8 * i + g;
-                    wv[u][i] = fetch16<8, VEC>(w + f * p.ldw + k, in && f < p.F ? p.K - k : 0);
+                    if constexpr (VEC)
+                        wv[u][i] = stream<4>(w + f * p.ldw + k, in && f < p.F && k < p.K);
+                    else
+                        wv[u][i] = fetch16<8, false>(w + f * p.ldw + k, in && f < p.F ? p.K - k : 0);
                 }
             } else {
                 const int f = f0 + 4 * g;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    wv[u][i] = fetch16<4, VEC>(w + (k + i) * p.ldw + f, in && k + i < p.K ? p.F - f : 0);
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (VEC)
+                        wv[u][i] = stream<2>(w + (k + i) * p.ldw + f, in && k + i < p.K && f < p.F);
+                    else
+                        wv[u][i] = fetch16<4, false>(w + (k + i) * p.ldw + f, in && k + i < p.K ? p.F - f : 0);
+                }
             }
         }
         Words<XN / 2> lo[UNROLL], hi[UNROLL];
@@ -207,7 +242,7 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
             const int k = s * STEP + 4 * lane;
             float4 wv[OWN];
 #pragma unroll
-            for (int i = 0; i < OWN; ++i) wv[i] = fetch32<VEC>(w + (f0 + i) * p.ldw + k, f0 + i < p.F ? p.K - k : 0);
+            for (int i = 0; i < OWN; ++i) wv[i] = stream32<VEC>(w + (f0 + i) * p.ldw + k, f0 + i < p.F ? p.K - k : 0);
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
                 const float4 xv = fetch32<VEC>(x + j * p.ldx + k, j < p.T ? p.K - k : 0);
@@ -221,7 +256,7 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
                 const int k = (s + u) * STEP + r;
-                wv[u] = fetch32<VEC>(w + k * p.ldw + f, s + u < s1 && k < p.K ? p.F - f : 0);
+                wv[u] = stream32<VEC>(w + k * p.ldw + f, s + u < s1 && k < p.K ? p.F - f : 0);
             }
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
