@@ -1400,7 +1400,7 @@ Matrix row_matrix(const void *p, int rows, int width, long long ld) {
     return m;
 }
 
-bool few_tokens(const Call &c) { return c.E < 0 && c.M <= linear_few::MAX_TOKENS && c.K > 0; }
+bool few_tokens(const Call &c) { return c.E < 0 && c.M <= linear_few::max_tokens(c.type) && c.K > 0; }
 
 size_t forward_bytes(const Call &c) {
     if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.K == 0 || c.E == 0 || few_tokens(c)) return 0;
@@ -1442,7 +1442,7 @@ int forward(const Call &c) {
         linear_few::Few p;
         p.T = c.M, p.F = c.N, p.K = c.K, p.x = c.x, p.w = c.w, p.bias = c.bias, p.residual = c.residual;
         p.z = c.preact, p.out = c.y, p.ldx = c.ldx, p.ldw = c.ldw, p.ldr = c.ldr, p.ldz = c.ldz, p.ldo = c.ldy;
-        p.order = c.w_order, p.act = c.act;
+        p.order = c.w_order, p.act = c.act, p.sms = d.sms;
         if (linear_few::run(c.type, p, c.stream) == cudaSuccess) return SGEMM_OK;
         (void)cudaGetLastError();
         return SGEMM_ERR_LAUNCH;

@@ -1,4 +1,4 @@
-// linear_few.cu -- y = act(x.w + bias) + residual for up to 16 tokens.
+// linear_few.cu -- y = act(x.w + bias) + residual for up to 16 tokens, in FP32 64.
 //
 // Such a product reads each weight once and does next to nothing with it, so
 // what counts is that loads of the weight start at once and keep coming: no
@@ -15,9 +15,15 @@
 //   order 0 (features contiguous): it takes features 4 g .. 4 g + 3 of the four
 //     K from 4 t on, paired up in registers into the shares of four fragments
 //     (features 4 g + i for fragment i).
-// FP32: fused multiply-adds, one per token and weight (splitting a weight into
-// pieces for the tensor cores costs more than 16 of them: 45 us measured for
-// 4096 x 4096 whatever the tokens).
+// FP32, up to 4 tokens: fused multiply-adds, one per token and weight (4 x 8192 x
+// 8192 50 us; on the tensor cores 54).  More tokens: mma.sync on three bf16 pieces
+// that each warp makes of its values in registers, so that the weight is read once
+// in FP32, where the product kernel's operand copies read 4 bytes of it and write
+// and read 6.  us, K contiguous, multiply-adds / product kernel / this:
+//   8 x 4096^2 24 / 54 / 17.6      16 x 4096^2 38 / 54 / 21   16 x 8192^2 107 / 180 / 67
+//   32 x 4096^2 - / 55 / 27        32 x 8192^2 - / 183 / 92   48 x 8192^2 - / 186 / 132
+//   64 x 4096^2 - / 57 / 49        64 x 8192^2 - / 186 / 172  64 x 1000 x 1024 - / 19 / 11
+// mma.sync bounds it from about 16 tokens on (10 to 12 cycles a scheduler for each).
 #include "linear_few.cuh"
 
 #include <cstdint>
@@ -214,16 +220,15 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
 }
 
 // TT tokens (at least p.T).  Order 1: 8 warps share out K, each lane 4 K of the
-// block's 8 features at a time (4 of them for more than 4 tokens).  Order 0: 16 warps; lane (r, q) takes K r of
-// four and features 4 q .. 4 q + 3 of the block's 32.
-__host__ __device__ constexpr int own32(int tokens) { return tokens > 4 ? 4 : 8; }
+// block's 8 features at a time.  Order 0: 16 warps; lane (r, q) takes K r of four
+// and features 4 q .. 4 q + 3 of the block's 32.
 template <int ORDER, int TT, bool VEC>
 __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel(const Few p) {
     constexpr int WARPS = ORDER ? 8 : 16;
-    constexpr int OWN = ORDER ? own32(TT) : 4;  // features of a thread
+    constexpr int OWN = ORDER ? 8 : 4;  // features of a thread
     constexpr int FEATURES = ORDER ? OWN : 32;
     constexpr int STEP = ORDER ? 128 : 4;
-    constexpr int UNROLL = ORDER ? 1 : TT > 8 ? 2 : !VEC ? 2 : TT > 4 ? 4 : 8;
+    constexpr int UNROLL = ORDER ? 1 : VEC ? 8 : 2;
     __shared__ float sums[WARPS][TT][FEATURES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int f0 = blockIdx.x * FEATURES;
@@ -293,6 +298,150 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
     }
 }
 
+// FP32, more than four tokens: mma.sync on the three bf16 pieces that the warp
+// makes of its values (lt::pieces), six products, features as rows and tokens as
+// columns (8 NT of them).  A warp's step is 32 features x 16 K; the K of a
+// fragment are a thread's four from 4 t on, and its rows:
+//   order 1: features g + 8 r, r = 0 .. 3, each by its own 16 bytes of K
+//   order 0: features 4 g + r, by 16 bytes of features for each K
+// rows 2 i and 2 i + 1 being fragment i's rows g and g + 8.  128 K are summed on
+// the tensor cores, those sums in FP32.
+// Where there are few features a cluster of up to 8 CTAs shares a tile's K (SPLIT)
+// and adds their sums in order of their rank: 32 x 256 x 8192 49 -> 12.6 us.
+template <int NT>
+struct FewTile {
+    static constexpr int WARPS = NT <= 2 ? 16 : 8;   // accumulators: 16 NT registers
+    static constexpr int DEPTH = NT <= 4 ? 2 : 1;    // steps whose loads are in flight
+};
+// x and y as three bf16 pieces each (x in the low halves), cut rather than
+// rounded: x = a + b + c exactly, 8 bits each, by whole-word instructions (5.5 a
+// value; with lt::pieces, 8 x 4096 x 4096 took 30 us for 18).  The products left
+// out are below 2^-21 of the full one.  An infinity leaves NaN in b and c.
+__device__ __forceinline__ void cut2(float x, float y, uint32_t (&r)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+        r[i] = __byte_perm(u, v, 0x7632);
+        x -= __uint_as_float(u & 0xffff0000u);
+        y -= __uint_as_float(v & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float part(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+template <int ORDER, int NT, bool VEC, bool SPLIT>
+__global__ void __launch_bounds__(FewTile<NT>::WARPS * 32, 1) few32_mma_kernel(const Few p) {
+    constexpr int WARPS = FewTile<NT>::WARPS, DEPTH = FewTile<NT>::DEPTH;
+    const int split = SPLIT ? p.split : 1;
+    constexpr int PAIR = NT > 1 ? 2 : 1;
+    __shared__ float sums[WARPS][8 * PAIR][33];
+    __shared__ float own[8 * NT][32];  // this CTA's sums, for its cluster
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rank = blockIdx.x % split, f0 = static_cast<int>(blockIdx.x / split) * 32;
+    const float *x = static_cast<const float *>(p.x) + g * p.ldx + 4 * t, *w = static_cast<const float *>(p.w);
+    const int steps = (p.K + 15) / 16;
+    const int s0 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp) / (WARPS * split));
+    const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp + 1) / (WARPS * split));
+    w += ORDER ? (f0 + g) * p.ldw + 4 * t : f0 + 4 * g + 4 * t * p.ldw;
+    float4 wv[DEPTH][4], xv[DEPTH][NT];
+    float acc[NT][2][4], total[NT][2][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j][i >> 2][i & 3] = total[j][i >> 2][i & 3] = 0.0f;
+    auto load = [&](int s, int d) {
+        const int k = 16 * s + 4 * t;
+        const bool in = s < s1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (ORDER)
+                wv[d][r] = stream32<VEC>(w + 8 * r * p.ldw + 16 * s, in && f0 + g + 8 * r < p.F ? p.K - k : 0);
+            else
+                wv[d][r] = stream32<VEC>(w + (16ll * s + r) * p.ldw, in && k + r < p.K ? p.F - (f0 + 4 * g) : 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) xv[d][j] = fetch32<VEC>(x + 8 * j * p.ldx + 16 * s, in && 8 * j + g < p.T ? p.K - k : 0);
+    };
+    tc::grid_wait();
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(s0 + d, d);
+    for (int s = s0; s < s1; s += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            uint32_t a[2][4][3];  // fragment, register, piece
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    cut2(ORDER ? part(wv[d][r], 2 * h) : part(wv[d][2 * h], r),
+                            ORDER ? part(wv[d][r], 2 * h + 1) : part(wv[d][2 * h + 1], r), a[r >> 1][(r & 1) + 2 * h]);
+#pragma unroll
+            for (int j = 0; j < NT; j += PAIR) {
+                uint32_t b[PAIR][2][3];
+#pragma unroll
+                for (int q = 0; q < PAIR; ++q) {
+                    cut2(xv[d][j + q].x, xv[d][j + q].y, b[q][0]);
+                    cut2(xv[d][j + q].z, xv[d][j + q].w, b[q][1]);
+                }
+                constexpr int WP[6] = {2, 0, 1, 1, 0, 0}, XP[6] = {0, 2, 1, 0, 1, 0};  // the small products first
+#pragma unroll
+                for (int m = 0; m < 6; ++m)
+#pragma unroll
+                    for (int q = 0; q < PAIR; ++q)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t av[4] = {a[i][0][WP[m]], a[i][1][WP[m]], a[i][2][WP[m]], a[i][3][WP[m]]};
+                            mma<__nv_bfloat16>(acc[j + q][i], av, b[q][0][XP[m]], b[q][1][XP[m]]);
+                        }
+            }
+            load(s + DEPTH + d, d);
+        }
+        if ((s - s0) % 8 == 8 - DEPTH || s + DEPTH >= s1) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    total[j][i >> 2][i & 3] += acc[j][i >> 2][i & 3];
+                    acc[j][i >> 2][i & 3] = 0.0f;
+                }
+        }
+    }
+    // fragment (g, t): rows g and g + 8, tokens 2 t and 2 t + 1
+#pragma unroll
+    for (int j = 0; j < NT; j += PAIR) {
+        if (j > 0) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PAIR; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 2 * i + (k >> 1);
+                    sums[warp][8 * q + 2 * t + (k & 1)][ORDER ? g + 8 * r : 4 * g + r] = total[j + q][i][k];
+                }
+        __syncthreads();
+        for (int o = threadIdx.x; o < 8 * PAIR * 32; o += WARPS * 32) {
+            const int token = 8 * j + o / 32, col = o % 32, f = f0 + col;
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) v += sums[i][o / 32][col];
+            if (split > 1)
+                own[token][col] = v;
+            else if (token < p.T && f < p.F)
+                finish<float>(p, token, f, v);
+        }
+    }
+    if (split == 1) return;
+    tc::cluster_sync();
+    for (int o = rank * WARPS * 32 + threadIdx.x; o < 8 * NT * 32; o += split * WARPS * 32) {
+        const int token = o / 32, f = f0 + o % 32;
+        if (token >= p.T || f >= p.F) continue;
+        float v = 0.0f;
+        for (int r = 0; r < split; ++r) v += tc::ld_cluster_f32(tc::peer_addr(tc::smem_u32(&own[token][o % 32]), r));
+        finish<float>(p, token, f, v);
+    }
+    tc::cluster_sync();  // no CTA ends while another reads its sums
+}
+
 template <typename K>
 cudaError_t launch(K kernel, int features, int threads, const Few &p, cudaStream_t stream) {
     return tc::launch(kernel, static_cast<unsigned>((p.F + features - 1) / features), dim3(static_cast<unsigned>(threads)), 0,
@@ -314,10 +463,26 @@ template <int TT>
 cudaError_t run32(const Few &p, cudaStream_t stream) {
     if (p.order) {
         const bool vec = p.K % 4 == 0 && aligned(p.x, p.ldx, 4, 16) && aligned(p.w, p.ldw, 4, 16);
-        return launch(vec ? few32_kernel<1, TT, true> : few32_kernel<1, TT, false>, own32(TT), 256, p, stream);
+        return launch(vec ? few32_kernel<1, TT, true> : few32_kernel<1, TT, false>, 8, 256, p, stream);
     }
     const bool vec = p.F % 4 == 0 && aligned(p.w, p.ldw, 4, 16);
     return launch(vec ? few32_kernel<0, TT, true> : few32_kernel<0, TT, false>, 32, 512, p, stream);
+}
+template <int ORDER, int NT>
+cudaError_t run32_mma(bool vec, Few p, cudaStream_t stream) {
+    constexpr int WARPS = FewTile<NT>::WARPS;
+    const long long tiles = (p.F + 31ll) / 32, steps = (p.K + 15ll) / 16;
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split * tiles <= p.sms && steps >= 2 * p.split * WARPS * FewTile<NT>::DEPTH) p.split *= 2;
+    const auto kernel = p.split > 1 ? (vec ? few32_mma_kernel<ORDER, NT, true, true> : few32_mma_kernel<ORDER, NT, false, true>)
+                                    : (vec ? few32_mma_kernel<ORDER, NT, true, false> : few32_mma_kernel<ORDER, NT, false, false>);
+    return tc::launch_clusters(kernel, static_cast<unsigned>(p.split), static_cast<unsigned>(tiles * p.split),
+                               dim3(WARPS * 32), 0, stream, p);
+}
+template <int NT>
+cudaError_t run32_mma(const Few &p, cudaStream_t stream) {
+    const bool vec = p.K % 4 == 0 && aligned(p.x, p.ldx, 4, 16) && aligned(p.w, p.ldw, 4, 16);
+    return p.order ? run32_mma<1, NT>(vec, p, stream) : run32_mma<0, NT>(vec && p.F % 4 == 0, p, stream);
 }
 
 }  // namespace
@@ -326,7 +491,9 @@ cudaError_t run(int type, const Few &p, cudaStream_t stream) {
     sg_nvtx::Range r("linear: few tokens");
     if (type == LINEAR_BF16) return run16<__nv_bfloat16>(p, stream);
     if (type == LINEAR_F16) return run16<__half>(p, stream);
-    return p.T <= 1 ? run32<1>(p, stream) : p.T <= 4 ? run32<4>(p, stream) : p.T <= 8 ? run32<8>(p, stream) : run32<16>(p, stream);
+    if (p.T <= 4) return p.T <= 1 ? run32<1>(p, stream) : run32<4>(p, stream);
+    if (p.T <= 16) return p.T <= 8 ? run32_mma<1>(p, stream) : run32_mma<2>(p, stream);
+    return p.T <= 32 ? run32_mma<4>(p, stream) : p.T <= 48 ? run32_mma<6>(p, stream) : run32_mma<8>(p, stream);
 }
 
 }  // namespace linear_few

@@ -36,6 +36,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t smem_addr, uint32_t rank)
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -277,20 +282,28 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 // A launch whose kernel may be set up while the one before it still runs; it
-// waits with grid_wait before it touches memory.
+// waits with grid_wait before it touches memory.  `cluster` CTAs in a row form a
+// cluster (1: none).
 template <typename... P, typename... A>
-inline cudaError_t launch(void (*kernel)(P...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+inline cudaError_t launch_clusters(void (*kernel)(P...), unsigned cluster, unsigned grid, dim3 block, size_t smem,
+                                   cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+inline cudaError_t launch(void (*kernel)(P...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    return launch_clusters(kernel, 1u, grid, block, smem, stream, args...);
 }
 
 }  // namespace tc

@@ -19,7 +19,8 @@
  * (and of preact, where it is saved) is in FP32.  dz is rounded to the
  * tensors' type before the products that use it; dbias is summed in FP32
  * from the unrounded values.  LINEAR_F32 splits each operand into three bf16
- * pieces (x = x1 + x2 + x3 to 2^-27) and adds the six products that matter;
+ * pieces (x = x1 + x2 + x3 to 2^-27) and adds the six products that matter
+ * (up to 4 tokens of linear_forward: it multiplies in FP32);
  * the tensor cores sum blocks of 128 K, which are added in FP32 with
  * round-to-nearest: the error is that of an FP32 product.  An infinity or a
  * NaN in an FP32 operand makes every element of the result that it enters

@@ -29,7 +29,7 @@ def forward(lib, type=BF16, M=16, N=16, K=16, x=A, ldx=16, w=B, ldw=16, order=0,
     (dict(res=D, ldr=15), -2), (dict(z=D, ldz=15), -2),
     (dict(x=None), -3), (dict(w=None), -3), (dict(y=None), -3),
     (dict(x=A + 2), -3),                                        # needs a copy, and there is no workspace
-    (dict(type=F32), -3),                                       # so do FP32's pieces (more than 16 tokens)
+    (dict(type=F32, M=65), -3),                                 # so do FP32's pieces (more than 64 tokens)
     (dict(x=A + 1, ws=WS, bytes=1 << 20), -7),                  # not aligned to its element
     (dict(y=C + 1), -7), (dict(bias=D + 1), -7),
     (dict(x=A + 2, ws=WS + 128, bytes=1 << 20), -7),            # workspace not 256-byte aligned
