@@ -58,6 +58,7 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 // N consecutive values, `left` of them in the matrix (the others 0).  VEC: one
 // aligned load, all or nothing (sizes are multiples of N), so that it is a
 // predicated instruction and nothing keeps the next ones from following at once.
+// fetch16 has a form for even sizes between: 2, by pairs of values.
 template <int WORDS>
 struct alignas(4 * WORDS) Words {
     uint32_t v[WORDS];
@@ -82,13 +83,17 @@ __device__ __forceinline__ Words<WORDS> stream(const void *p, bool in) {
     }
     return r;
 }
-template <int N, bool VEC>
+template <int N, int VEC>
 __device__ __forceinline__ Words<N / 2> fetch16(const void *p, int left) {
     Words<N / 2> r;
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) r.v[i] = 0u;
-    if constexpr (VEC) {
+    if constexpr (VEC == 1) {
         if (left > 0) r = *static_cast<const Words<N / 2> *>(p);
+    } else if constexpr (VEC == 2) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            if (2 * i < left) r.v[i] = static_cast<const uint32_t *>(p)[i];
     } else {
         const unsigned short *q = static_cast<const unsigned short *>(p);
 #pragma unroll
@@ -128,21 +133,39 @@ __device__ __forceinline__ void finish(const Few &p, int token, int f, float v) 
     static_cast<T *>(p.out)[token * p.ldo + f] = from_f<T>(v);
 }
 
+// A cluster's CTAs add their sums of a tile in order of their rank, each for its
+// share of the outputs.
+template <typename T, int THREADS, int TOKENS, int FEATURES>
+__device__ __forceinline__ void join(const Few &p, const float (&own)[TOKENS][FEATURES], int f0, int rank) {
+    tc::cluster_sync();
+    for (int o = rank * THREADS + threadIdx.x; o < TOKENS * FEATURES; o += p.split * THREADS) {
+        const int token = o / FEATURES, col = o % FEATURES, f = f0 + col;
+        if (token >= p.T || f >= p.F) continue;
+        float v = 0.0f;
+        for (int r = 0; r < p.split; ++r) v += tc::ld_cluster_f32(tc::peer_addr(tc::smem_u32(&own[token][col]), r));
+        finish<T>(p, token, f, v);
+    }
+    tc::cluster_sync();  // no CTA ends while another reads its sums
+}
+
 // A block has 16 (order 1) or 32 features.
-template <typename T, int ORDER, bool VEC>
-__global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel(const Few p) {
-    constexpr int WARPS = ORDER ? 8 : 16;
+template <typename T, int ORDER, int WARPS, int VEC, bool SPLIT>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few16_kernel(const Few p) {
     constexpr int TILES = ORDER ? 2 : 4;
-    constexpr int STEP = ORDER ? 32 : 16;       // K of a warp's step
-    constexpr int UNROLL = VEC ? 4 : 1;  // steps whose loads are in flight together
-    constexpr int XN = STEP / 4;                // consecutive K of a thread
-    __shared__ float sums[WARPS][16][8 * TILES + 1];
+    constexpr int STEP = ORDER ? 32 : 16;                        // K of a warp's step
+    constexpr int UNROLL = VEC == 1 ? 4 : 1;              // steps whose loads are in flight together
+    constexpr int ROWS = ORDER ? TILES : 4;                      // loads of a thread's step
+    constexpr int XN = STEP / 4;                                 // consecutive K of a thread
+    constexpr int FEATURES = 8 * TILES;
+    __shared__ float sums[WARPS][16][FEATURES + 1];
+    __shared__ float own[16][FEATURES];  // this CTA's sums, for its cluster
+    const int split = SPLIT ? p.split : 1, rank = blockIdx.x % split;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int f0 = blockIdx.x * 8 * TILES;
+    const int f0 = static_cast<int>(blockIdx.x / split) * FEATURES;
     const T *x = static_cast<const T *>(p.x), *w = static_cast<const T *>(p.w);
     const int steps = (p.K + STEP - 1) / STEP;
-    const int s0 = static_cast<int>(static_cast<long long>(steps) * warp / WARPS);
-    const int s1 = static_cast<int>(static_cast<long long>(steps) * (warp + 1) / WARPS);
+    const int s0 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp) / (WARPS * split));
+    const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp + 1) / (WARPS * split));
     const T *x_lo = x + (g < p.T ? g : 0) * p.ldx, *x_hi = x + (g + 8 < p.T ? g + 8 : 0) * p.ldx;
     const int lo_k = g < p.T ? p.K : 0, hi_k = g + 8 < p.T ? p.K : 0;  // a missing token is zeros
     float acc[TILES][4];
@@ -152,29 +175,20 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
         for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
     tc::grid_wait();
     for (int s = s0; s < s1; s += UNROLL) {
-        Words<ORDER ? 4 : 2> wv[UNROLL][ORDER ? TILES : 4];
+        Words<ORDER ? 4 : 2> wv[UNROLL][ROWS];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int k = (s + u) * STEP + t * XN;
             const bool in = s + u < s1;
-            if constexpr (ORDER) {
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) {
-                    const int f = f0 + 8 * i + g;
-                    if constexpr (VEC)
-                        wv[u][i] = stream<4>(w + f * p.ldw + k, in && f < p.F && k < p.K);
-                    else
-                        wv[u][i] = fetch16<8, false>(w + f * p.ldw + k, in && f < p.F ? p.K - k : 0);
-                }
-            } else {
-                const int f = f0 + 4 * g;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (VEC)
-                        wv[u][i] = stream<2>(w + (k + i) * p.ldw + f, in && k + i < p.K && f < p.F);
-                    else
-                        wv[u][i] = fetch16<4, false>(w + (k + i) * p.ldw + f, in && k + i < p.K ? p.F - f : 0);
-                }
+            for (int i = 0; i < ROWS; ++i) {
+                const int f = ORDER ? f0 + 8 * i + g : f0 + 4 * g, kk = ORDER ? k : k + i;
+                const T *q = w + (ORDER ? f * p.ldw + kk : kk * p.ldw + f);
+                const bool here = in && f < p.F && kk < p.K;
+                if constexpr (VEC == 1)
+                    wv[u][i] = stream<ORDER ? 4 : 2>(q, here);
+                else
+                    wv[u][i] = fetch16<ORDER ? 8 : 4, VEC>(q, here ? ORDER ? p.K - kk : p.F - f : 0);
             }
         }
         Words<XN / 2> lo[UNROLL], hi[UNROLL];
@@ -211,12 +225,18 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few16_kernel
             sums[warp][g + 8 * (k >> 1)][ORDER ? 8 * i + n : 4 * n + i] = acc[i][k];
         }
     __syncthreads();
-    const int token = threadIdx.x / (8 * TILES), col = threadIdx.x % (8 * TILES), f = f0 + col;
-    if (token >= p.T || f >= p.F) return;
-    float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) v += sums[i][token][col];
-    finish<T>(p, token, f, v);
+    for (int o = threadIdx.x; o < 16 * FEATURES; o += WARPS * 32) {
+        const int token = o / FEATURES, col = o % FEATURES, f = f0 + col;
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) v += sums[i][token][col];
+        if (SPLIT)
+            own[token][col] = v;
+        else if (token < p.T && f < p.F)
+            finish<T>(p, token, f, v);
+    }
+    if (SPLIT) join<T, WARPS * 32>(p, own, f0, rank);
 }
 
 // TT tokens (at least p.T).  Order 1: 8 warps share out K, each lane 4 K of the
@@ -424,22 +444,13 @@ __global__ void __launch_bounds__(FewTile<NT>::WARPS * 32, 1) few32_mma_kernel(c
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) v += sums[i][o / 32][col];
-            if (split > 1)
+            if (SPLIT)
                 own[token][col] = v;
             else if (token < p.T && f < p.F)
                 finish<float>(p, token, f, v);
         }
     }
-    if (split == 1) return;
-    tc::cluster_sync();
-    for (int o = rank * WARPS * 32 + threadIdx.x; o < 8 * NT * 32; o += split * WARPS * 32) {
-        const int token = o / 32, f = f0 + o % 32;
-        if (token >= p.T || f >= p.F) continue;
-        float v = 0.0f;
-        for (int r = 0; r < split; ++r) v += tc::ld_cluster_f32(tc::peer_addr(tc::smem_u32(&own[token][o % 32]), r));
-        finish<float>(p, token, f, v);
-    }
-    tc::cluster_sync();  // no CTA ends while another reads its sums
+    if (SPLIT) join<float, WARPS * 32>(p, own, f0, rank);
 }
 
 template <typename K>
@@ -450,14 +461,42 @@ cudaError_t launch(K kernel, int features, int threads, const Few &p, cudaStream
 bool aligned(const void *q, long long ld, int element, int bytes) {
     return reinterpret_cast<uintptr_t>(q) % bytes == 0 && ld * element % bytes == 0;
 }
+// CTAs that share a tile's K: as many as find room at once, at most a portable
+// cluster's 8, each of their warps keeping `least` steps (16 x 2048 x 11008 bf16
+// 22 -> 16.7 us, K contiguous 15.6 -> 14.1; 1 x 256 x 8192 15.6 -> 6.7 and 10.8 ->
+// 6.7; with half the steps 1 x 2048 x 2048 took 6.6 us for 5.8).
+int shares(long long tiles, long long places, long long steps, int warps, int least) {
+    int split = 1;
+    while (split < 8 && 2 * split * tiles <= places && steps >= 2ll * split * warps * least) split *= 2;
+    return split;
+}
+template <typename T, int ORDER, int WARPS, bool SPLIT>
+cudaError_t launch16(int vec, const Few &p, long long tiles, cudaStream_t stream) {
+    return tc::launch_clusters(vec == 1   ? few16_kernel<T, ORDER, WARPS, 1, SPLIT>
+                               : vec == 2 ? few16_kernel<T, ORDER, WARPS, 2, SPLIT>
+                                          : few16_kernel<T, ORDER, WARPS, 0, SPLIT>,
+                               SPLIT ? static_cast<unsigned>(p.split) : 1u, static_cast<unsigned>(tiles * p.split),
+                               dim3(WARPS * 32), 0, stream, p);
+}
+// Whether the operands can be read by n values of K of x, and of w's rows.
+bool read_by(const Few &p, int n) {
+    return p.K % n == 0 && (p.order || p.F % n == 0) && aligned(p.x, p.ldx, 2, 2 * n) && aligned(p.w, p.ldw, 2, 2 * n);
+}
 template <typename T>
-cudaError_t run16(const Few &p, cudaStream_t stream) {
+cudaError_t run16(Few p, cudaStream_t stream) {
+    const int vec = read_by(p, p.order ? 8 : 4) ? 1 : read_by(p, 2) ? 2 : 0;
     if (p.order) {
-        const bool vec = p.K % 8 == 0 && aligned(p.x, p.ldx, 2, 16) && aligned(p.w, p.ldw, 2, 16);
-        return launch(vec ? few16_kernel<T, 1, true> : few16_kernel<T, 1, false>, 16, 256, p, stream);
+        const long long tiles = (p.F + 15ll) / 16;
+        p.split = shares(tiles, 2ll * p.sms, (p.K + 31ll) / 32, 8, 8);
+        return p.split > 1 ? launch16<T, 1, 8, true>(vec, p, tiles, stream) : launch16<T, 1, 8, false>(vec, p, tiles, stream);
     }
-    const bool vec = p.K % 4 == 0 && p.F % 4 == 0 && aligned(p.x, p.ldx, 2, 8) && aligned(p.w, p.ldw, 2, 8);
-    return launch(vec ? few16_kernel<T, 0, true> : few16_kernel<T, 0, false>, 32, 512, p, stream);
+    // 16 warps while each tile has an SM (1 x 4096 x 4096 11.1 us, with 8 warps and
+    // twice the shares of K 12.2), else 8, two blocks an SM (1 x 8192 x 8192 29; 34)
+    const long long tiles = (p.F + 31ll) / 32;
+    p.split = 1;
+    if (tiles > p.sms) return launch16<T, 0, 8, false>(vec, p, tiles, stream);
+    p.split = shares(tiles, p.sms, (p.K + 15ll) / 16, 16, 4);
+    return p.split > 1 ? launch16<T, 0, 16, true>(vec, p, tiles, stream) : launch16<T, 0, 16, false>(vec, p, tiles, stream);
 }
 template <int TT>
 cudaError_t run32(const Few &p, cudaStream_t stream) {
@@ -472,8 +511,7 @@ template <int ORDER, int NT>
 cudaError_t run32_mma(bool vec, Few p, cudaStream_t stream) {
     constexpr int WARPS = FewTile<NT>::WARPS;
     const long long tiles = (p.F + 31ll) / 32, steps = (p.K + 15ll) / 16;
-    p.split = 1;
-    while (p.split < 8 && 2 * p.split * tiles <= p.sms && steps >= 2 * p.split * WARPS * FewTile<NT>::DEPTH) p.split *= 2;
+    p.split = shares(tiles, p.sms, steps, WARPS, FewTile<NT>::DEPTH);
     const auto kernel = p.split > 1 ? (vec ? few32_mma_kernel<ORDER, NT, true, true> : few32_mma_kernel<ORDER, NT, false, true>)
                                     : (vec ? few32_mma_kernel<ORDER, NT, true, false> : few32_mma_kernel<ORDER, NT, false, false>);
     return tc::launch_clusters(kernel, static_cast<unsigned>(p.split), static_cast<unsigned>(tiles * p.split),

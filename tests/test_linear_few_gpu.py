@@ -50,6 +50,14 @@ def test_few_features(dtype, order, size):
     _check(*size, L.TYPES[dtype], order)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("order", [0, 1])
+@pytest.mark.parametrize("N,K,pad,offset", [(30, 1030, 0, 0), (262, 778, 2, 2), (30, 500, 4, 0), (36, 500, 4, 4), (5000, 98, 2, 0),
+                                            (5001, 99, 0, 0), (5004, 100, 0, 0)])
+def test_even_and_odd_rows(dtype, order, N, K, pad, offset):
+    _check(11, N, K, L.TYPES[dtype], order, pad=pad, offset=offset)
+
+
 @pytest.mark.parametrize("dtype", L.TYPES)
 @pytest.mark.parametrize("M", [3, 12, 40])
 def test_infinities_stay_in_their_row_and_column(dtype, M):
