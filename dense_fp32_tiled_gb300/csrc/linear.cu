@@ -1400,7 +1400,15 @@ Matrix row_matrix(const void *p, int rows, int width, long long ld) {
     return m;
 }
 
-bool few_tokens(const Call &c) { return c.E < 0 && c.M <= linear_few::max_tokens(c.type) && c.K > 0; }
+linear_few::Few few(const Call &c) {
+    linear_few::Few p;
+    memset(&p, 0, sizeof p);
+    p.T = c.M, p.F = c.N, p.K = c.K, p.x = c.x, p.w = c.w, p.bias = c.bias, p.residual = c.residual;
+    p.z = c.preact, p.out = c.y, p.ldx = c.ldx, p.ldw = c.ldw, p.ldr = c.ldr, p.ldz = c.ldz, p.ldo = c.ldy;
+    p.order = c.w_order, p.act = c.act;
+    return p;
+}
+bool few_tokens(const Call &c) { return c.E < 0 && c.K > 0 && linear_few::takes(c.type, few(c)); }
 
 size_t forward_bytes(const Call &c) {
     if (check_sizes(c) != SGEMM_OK || c.M == 0 || c.N == 0 || c.K == 0 || c.E == 0 || few_tokens(c)) return 0;
@@ -1439,10 +1447,8 @@ int forward(const Call &c) {
     st = set_up(&d);
     if (st != SGEMM_OK) return st;
     if (few_tokens(c)) {
-        linear_few::Few p;
-        p.T = c.M, p.F = c.N, p.K = c.K, p.x = c.x, p.w = c.w, p.bias = c.bias, p.residual = c.residual;
-        p.z = c.preact, p.out = c.y, p.ldx = c.ldx, p.ldw = c.ldw, p.ldr = c.ldr, p.ldz = c.ldz, p.ldo = c.ldy;
-        p.order = c.w_order, p.act = c.act, p.sms = d.sms;
+        linear_few::Few p = few(c);
+        p.sms = d.sms;
         if (linear_few::run(c.type, p, c.stream) == cudaSuccess) return SGEMM_OK;
         (void)cudaGetLastError();
         return SGEMM_ERR_LAUNCH;

@@ -1,4 +1,5 @@
-// linear_few.cu -- y = act(x.w + bias) + residual for up to 16 tokens, in FP32 64.
+// linear_few.cu -- y = act(x.w + bias) + residual for up to 16 tokens, and up to 64
+// in FP32 or with few weights.
 //
 // Such a product reads each weight once and does next to nothing with it, so
 // what counts is that loads of the weight start at once and keep coming: no
@@ -318,8 +319,116 @@ __global__ void __launch_bounds__(ORDER ? 256 : 512, ORDER ? 2 : 1) few32_kernel
     }
 }
 
+// The warps' sums of 32 features as rows (rows 2 i and 2 i + 1 of a thread are
+// fragment i's rows g and g + 8: features g + 8 r, order 0: 4 g + r), 8 NT tokens
+// as columns, added in order of the warps, two tiles of tokens at a time.
+template <typename T, int ORDER, int NT, int WARPS, bool SPLIT>
+__device__ __forceinline__ void add_warps(const Few &p, const float (&total)[NT][2][4], int f0, int rank) {
+    constexpr int PAIR = NT > 1 ? 2 : 1;
+    __shared__ float sums[WARPS][8 * PAIR][33];
+    __shared__ float own[8 * NT][32];  // this CTA's sums, for its cluster
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NT; j += PAIR) {
+        if (j > 0) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PAIR; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 2 * i + (k >> 1);
+                    sums[warp][8 * q + 2 * t + (k & 1)][ORDER ? g + 8 * r : 4 * g + r] = total[j + q][i][k];
+                }
+        __syncthreads();
+        for (int o = threadIdx.x; o < 8 * PAIR * 32; o += WARPS * 32) {
+            const int token = 8 * j + o / 32, col = o % 32, f = f0 + col;
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) v += sums[i][o / 32][col];
+            if (SPLIT)
+                own[token][col] = v;
+            else if (token < p.T && f < p.F)
+                finish<T>(p, token, f, v);
+        }
+    }
+    if (SPLIT) join<T, WARPS * 32>(p, own, f0, rank);
+}
+
+// 16-bit types, 17 to 64 tokens (see takes): features as rows, so that a fragment of the weight
+// serves all tokens, 8 NT of them as columns.  A warp's step is 32 features x 32 K;
+// a thread's K are the eight from 8 t on, four for each of two fragments' columns:
+//   order 1: features g + 8 r, r = 0 .. 3, each by 16 bytes of K
+//   order 0: features 4 g + r, by 8 bytes of features for each K, paired up
+template <typename T, int ORDER, int NT, bool SPLIT>
+__global__ void __launch_bounds__(256, NT <= 4 ? 2 : 1) rows16_kernel(const Few p) {
+    constexpr int WARPS = 8, DEPTH = 2;
+    const int split = SPLIT ? p.split : 1, rank = blockIdx.x % split;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int f0 = static_cast<int>(blockIdx.x / split) * 32;
+    const T *x = static_cast<const T *>(p.x) + g * p.ldx + 8 * t, *w = static_cast<const T *>(p.w);
+    const int steps = (p.K + 31) / 32;
+    const int s0 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp) / (WARPS * split));
+    const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank * WARPS + warp + 1) / (WARPS * split));
+    w += ORDER ? (f0 + g) * p.ldw + 8 * t : f0 + 4 * g + 8 * t * p.ldw;
+    uint32_t wv[DEPTH][16];
+    Words<4> xv[DEPTH][NT];
+    float acc[NT][2][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j][i >> 2][i & 3] = 0.0f;
+    auto load = [&](int s, int d) {
+        const bool in = s < s1 && 32 * s + 8 * t < p.K;
+        if constexpr (ORDER) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const Words<4> v = stream<4>(w + 8 * r * p.ldw + 32 * s, in && f0 + g + 8 * r < p.F);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) wv[d][4 * r + q] = v.v[q];
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const Words<2> v = stream<2>(w + (32ll * s + r) * p.ldw, in && f0 + 4 * g < p.F);
+                wv[d][2 * r] = v.v[0], wv[d][2 * r + 1] = v.v[1];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) xv[d][j] = fetch16<8, 1>(x + 8 * j * p.ldx + 32 * s, in && 8 * j + g < p.T ? 8 : 0);
+    };
+    // K 8 t + 4 h + 2 pair and the next one of row r
+    auto value = [&](int d, int h, int r, int pair) {
+        if constexpr (ORDER) {
+            return wv[d][4 * r + 2 * h + pair];
+        } else {
+            const int k = 4 * h + 2 * pair;
+            return __byte_perm(wv[d][2 * k + r / 2], wv[d][2 * k + 2 + r / 2], r & 1 ? 0x7632 : 0x5410);
+        }
+    };
+    tc::grid_wait();
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(s0 + d, d);
+    for (int s = s0; s < s1; s += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t a[4] = {value(d, h, 2 * i, 0), value(d, h, 2 * i + 1, 0), value(d, h, 2 * i, 1),
+                                           value(d, h, 2 * i + 1, 1)};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma<T>(acc[j][i], a, xv[d][j].v[2 * h], xv[d][j].v[2 * h + 1]);
+                }
+            load(s + DEPTH + d, d);
+        }
+    }
+    add_warps<T, ORDER, NT, WARPS, SPLIT>(p, acc, f0, rank);
+}
+
 // FP32, more than four tokens: mma.sync on the three bf16 pieces that the warp
-// makes of its values (lt::pieces), six products, features as rows and tokens as
+// cuts its values into, six products, features as rows and tokens as
 // columns (8 NT of them).  A warp's step is 32 features x 16 K; the K of a
 // fragment are a thread's four from 4 t on, and its rows:
 //   order 1: features g + 8 r, r = 0 .. 3, each by its own 16 bytes of K
@@ -353,8 +462,6 @@ __global__ void __launch_bounds__(FewTile<NT>::WARPS * 32, 1) few32_mma_kernel(c
     constexpr int WARPS = FewTile<NT>::WARPS, DEPTH = FewTile<NT>::DEPTH;
     const int split = SPLIT ? p.split : 1;
     constexpr int PAIR = NT > 1 ? 2 : 1;
-    __shared__ float sums[WARPS][8 * PAIR][33];
-    __shared__ float own[8 * NT][32];  // this CTA's sums, for its cluster
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % split, f0 = static_cast<int>(blockIdx.x / split) * 32;
     const float *x = static_cast<const float *>(p.x) + g * p.ldx + 4 * t, *w = static_cast<const float *>(p.w);
@@ -425,32 +532,7 @@ __global__ void __launch_bounds__(FewTile<NT>::WARPS * 32, 1) few32_mma_kernel(c
                 }
         }
     }
-    // fragment (g, t): rows g and g + 8, tokens 2 t and 2 t + 1
-#pragma unroll
-    for (int j = 0; j < NT; j += PAIR) {
-        if (j > 0) __syncthreads();
-#pragma unroll
-        for (int q = 0; q < PAIR; ++q)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = 2 * i + (k >> 1);
-                    sums[warp][8 * q + 2 * t + (k & 1)][ORDER ? g + 8 * r : 4 * g + r] = total[j + q][i][k];
-                }
-        __syncthreads();
-        for (int o = threadIdx.x; o < 8 * PAIR * 32; o += WARPS * 32) {
-            const int token = 8 * j + o / 32, col = o % 32, f = f0 + col;
-            float v = 0.0f;
-#pragma unroll
-            for (int i = 0; i < WARPS; ++i) v += sums[i][o / 32][col];
-            if (SPLIT)
-                own[token][col] = v;
-            else if (token < p.T && f < p.F)
-                finish<float>(p, token, f, v);
-        }
-    }
-    if (SPLIT) join<float, WARPS * 32>(p, own, f0, rank);
+    add_warps<float, ORDER, NT, WARPS, SPLIT>(p, total, f0, rank);
 }
 
 template <typename K>
@@ -482,8 +564,20 @@ cudaError_t launch16(int vec, const Few &p, long long tiles, cudaStream_t stream
 bool read_by(const Few &p, int n) {
     return p.K % n == 0 && (p.order || p.F % n == 0) && aligned(p.x, p.ldx, 2, 2 * n) && aligned(p.w, p.ldw, 2, 2 * n);
 }
+template <typename T, int ORDER, int NT>
+cudaError_t rows16(Few p, cudaStream_t stream) {
+    const long long tiles = (p.F + 31ll) / 32;
+    p.split = shares(tiles, p.sms, (p.K + 31ll) / 32, 8, 2);
+    return tc::launch_clusters(p.split > 1 ? rows16_kernel<T, ORDER, NT, true> : rows16_kernel<T, ORDER, NT, false>,
+                               static_cast<unsigned>(p.split), static_cast<unsigned>(tiles * p.split), dim3(256), 0, stream, p);
+}
+template <typename T, int ORDER>
+cudaError_t rows16(const Few &p, cudaStream_t stream) {
+    return p.T <= 32 ? rows16<T, ORDER, 4>(p, stream) : rows16<T, ORDER, 8>(p, stream);
+}
 template <typename T>
 cudaError_t run16(Few p, cudaStream_t stream) {
+    if (p.T > 16) return p.order ? rows16<T, 1>(p, stream) : rows16<T, 0>(p, stream);
     const int vec = read_by(p, p.order ? 8 : 4) ? 1 : read_by(p, 2) ? 2 : 0;
     if (p.order) {
         const long long tiles = (p.F + 15ll) / 16;
@@ -524,6 +618,19 @@ cudaError_t run32_mma(const Few &p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// More than 16 tokens.  FP32: beyond 64, cutting the operands once for the product
+// kernel costs less than in each CTA.  16 bits: each CTA reads all of x, so the
+// product kernel, about 10 us whatever its size, is left behind only below about
+// 8 million weights (us, product kernel / rows16_kernel: 32 x 512 x 512 11.0 / 5.5,
+// 24 x 1024 x 1024 11.2 / 7.2, 32 x 256 x 8192 17.9 / 8.2, 48 x 2048 x 2048 12.9 /
+// 10.5; 48 x 4096 x 4096 16.4 / 17.0, 64 x 8192 x 8192 32 / 59).
+bool takes(int type, const Few &p) {
+    if (p.T <= 16) return true;
+    if (type == LINEAR_F32) return p.T <= 64;
+    return p.T <= 64 && static_cast<long long>(p.F) * p.K <= 1 << 23 && p.K % 8 == 0 && (p.order || p.F % 8 == 0) &&
+           aligned(p.x, p.ldx, 2, 16) && aligned(p.w, p.ldw, 2, 16);
+}
 
 cudaError_t run(int type, const Few &p, cudaStream_t stream) {
     sg_nvtx::Range r("linear: few tokens");

@@ -7,10 +7,6 @@
 
 namespace linear_few {
 
-// Most tokens that run takes (FP32: beyond it, splitting the operands once for the
-// product kernel costs less than splitting them in each CTA).
-inline int max_tokens(int type) { return type == LINEAR_F32 ? 64 : 16; }
-
 struct Few {
     int T, F, K;
     const void *x, *w, *bias, *residual;
@@ -20,6 +16,8 @@ struct Few {
     int sms, split;  // of the device; CTAs that share a tile's K (set by run)
 };
 
+// Whether run does this product (its sizes, w, x and order are looked at).
+bool takes(int type, const Few &p);
 cudaError_t run(int type, const Few &p, cudaStream_t stream);
 
 }  // namespace linear_few

@@ -43,7 +43,7 @@ def test_tokens(dtype, order, M):
 
 @pytest.mark.parametrize("dtype", L.TYPES)
 @pytest.mark.parametrize("order", [0, 1])
-@pytest.mark.parametrize("size", [(1, 8, 9000), (7, 32, 8192), (12, 200, 4100), (16, 33, 5003), (30, 256, 8192),
+@pytest.mark.parametrize("size", [(1, 8, 9000), (7, 32, 8192), (12, 200, 4100), (16, 33, 5003), (30, 256, 8192), (17, 2048, 2048), (64, 8, 16384),
                                   (40, 1, 6001), (64, 1000, 1024), (50, 600, 2048), (16, 1100, 1024)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_few_features(dtype, order, size):
