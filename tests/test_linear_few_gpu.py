@@ -96,3 +96,25 @@ def test_same_bits_every_time(dtype):
         x, w = L.randn(g, (M, K), dt), L.randn(g, (K, N), dt)
         first = sg.linear(x, w)
         assert all(torch.equal(first, sg.linear(x, w)) for _ in range(5))
+
+
+@pytest.mark.parametrize("dtype", L.TYPES)
+def test_in_a_graph(dtype):
+    """Clusters and programmatic launches captured and replayed, one product's result the next one's input."""
+    g = L.rng(6)
+    dt = L.TYPES[dtype]
+    for M in (3, 16, 40):
+        x = L.randn(g, (M, 4096), dt)
+        w1, w2 = L.randn(g, (4096, 96), dt, 1 / 64), L.randn(g, (96, 72), dt, 1 / 8)
+        h, y = torch.empty((M, 96), dtype=dt, device="cuda"), torch.empty((M, 72), dtype=dt, device="cuda")
+        want = sg.linear(sg.linear(x, w1, activation="relu"), w2)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sg.linear(x, w1, activation="relu", out=h)
+            sg.linear(h, w2, out=y)
+        for _ in range(3):
+            h.zero_(), y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
