@@ -46,10 +46,15 @@ def _load():
                               "expert_sort") for f in (op, op + "_workspace_size")]
         names += ["expert_gather", "expert_combine", "expert_combine_backward"]
         _fast_call.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},
-                        (torch.Tensor, torch.empty, _raw_stream, torch._C._cuda_getDevice, _workspace, ACTIVATIONS,
-                         (torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.int64))
+                        bound(torch, _raw_stream, torch._C._cuda_getDevice))
         _fast = _fast_call
     return _lib
+
+
+def bound(torch, raw_stream, get_device):
+    """What the extension's calls need of torch."""
+    return (torch.Tensor, torch.empty, raw_stream, get_device, ACTIVATIONS, (torch.float32, torch.bfloat16, torch.float16),
+            torch.int32, torch.int64, torch.uint8)
 
 
 def _type_of(t, name):
@@ -125,22 +130,13 @@ def _on(device, stream):
     return _NOWHERE
 
 
-_workspaces = {}
-
-
-def _workspace(device, stream, nbytes):
-    """Address of scratch for the calls of one stream, which are ordered and so
-    can share it.  It is allocated with that stream current, so it belongs to
-    it.  One that has become too small is kept, as a captured graph may hold
-    its address; each is at least twice the one before, so all of them
-    together take no more than the last one does."""
-    if not nbytes:
-        return None
-    held = _workspaces.setdefault((device, stream), [])
-    if not held or held[-1].numel() < nbytes:
-        size = max(nbytes, 2 * held[-1].numel() if held else 1 << 16)
-        held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{device}"))
-    return held[-1].data_ptr()
+def _scratch(nbytes, device):
+    """Scratch of one call, or None.  It is the call's own: allocated with the
+    call's stream current and given back to torch's allocator when all its
+    kernels are enqueued, which hands it on in the order of that stream only.
+    So no two threads' calls have the same at a time, and a captured graph's
+    is memory of that graph."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _act(name):
@@ -212,16 +208,17 @@ def _forward(x, w, offsets, bias, residual, activation, preact, out, stream):
         else:
             yp, ldy = _rows(out, M, N, dtype, dev, "out")
         raw = _raw_stream(dev)
-        nbytes, ws = 0, None
+        nbytes, ws, wsp = 0, None, None
         if kind == 0 or (xp | wp) & 15 or (ldx | ldw | step) & 7:
             nbytes = (lib.expert_linear_forward_workspace_size(kind, M, N, K, E, xp, ldx, wp, ldw, step, order) if grouped
                       else lib.linear_forward_workspace_size(kind, M, N, K, xp, ldx, wp, ldw, order))
-            ws = _workspace(dev, raw, nbytes)
+            ws = _scratch(nbytes, x.device)
+            wsp = ws.data_ptr() if nbytes else None
         if grouped:
             st = lib.expert_linear_forward(kind, M, N, K, E, op, xp, ldx, wp, ldw, step, order, bp, rp, ldr, act, zp, ldz,
-                                           yp, ldy, ws, nbytes, raw)
+                                           yp, ldy, wsp, nbytes, raw)
         else:
-            st = lib.linear_forward(kind, M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, act, zp, ldz, yp, ldy, ws, nbytes,
+            st = lib.linear_forward(kind, M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, act, zp, ldz, yp, ldy, wsp, nbytes,
                                     raw)
     if st:
         _check(st, "expert_linear_forward" if grouped else "linear_forward")
@@ -286,13 +283,15 @@ def _backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbia
         if grouped:
             nbytes = lib.expert_linear_backward_workspace_size(kind, M, N, K, E, gp, lddy, xp, ldx, wp, ldw, step, order,
                                                                act, need_dx, need_dw, need_dbias)
+            ws = _scratch(nbytes, x.device)
             st = lib.expert_linear_backward(kind, M, N, K, E, op, gp, lddy, xp, ldx, wp, ldw, step, order, zp, ldz, act, hp,
-                                            ldh, vp, ldv, stepv, bp, _workspace(dev, raw, nbytes), nbytes, raw)
+                                            ldh, vp, ldv, stepv, bp, ws.data_ptr() if nbytes else None, nbytes, raw)
         else:
             nbytes = lib.linear_backward_workspace_size(kind, M, N, K, gp, lddy, xp, ldx, wp, ldw, order, act, need_dx,
                                                         need_dw, need_dbias)
+            ws = _scratch(nbytes, x.device)
             st = lib.linear_backward(kind, M, N, K, gp, lddy, xp, ldx, wp, ldw, order, zp, ldz, act, hp, ldh, vp, ldv, bp,
-                                     _workspace(dev, raw, nbytes), nbytes, raw)
+                                     ws.data_ptr() if nbytes else None, nbytes, raw)
     if st:
         _check(st, "expert_linear_backward" if grouped else "linear_backward")
     return dx, dw, dbias
@@ -333,8 +332,9 @@ def expert_sort(choices, experts, stream=None):
         offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=choices.device)
         raw = _raw_stream(dev)
         nbytes = lib.expert_sort_workspace_size(T, J, E)
+        ws = _scratch(nbytes, choices.device)
         st = lib.expert_sort(T, J, E, choices.data_ptr(), width, rows.data_ptr(), offsets.data_ptr(),
-                             _workspace(dev, raw, nbytes), nbytes, raw)
+                             ws.data_ptr() if nbytes else None, nbytes, raw)
     if st:
         _check(st, "expert_sort")
     return rows, offsets

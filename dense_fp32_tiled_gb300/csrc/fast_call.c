@@ -49,7 +49,7 @@ static const char *const lib_names[] = {"linear_forward", "linear_forward_worksp
                                         "expert_gather", "expert_combine", "expert_combine_backward"};
 
 /* What bind() keeps: torch's own objects, for the life of the process. */
-static PyObject *tensor_type, *empty, *raw_stream, *get_device, *workspace, *activations, *kinds[3], *int32_type, *int64_type;
+static PyObject *tensor_type, *empty, *raw_stream, *get_device, *activations, *kinds[3], *int32_type, *int64_type, *uint8_type;
 static PyObject *s_dtype, *s_device, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_transpose;
 static PyObject *empty_names, *minus1, *minus2;
 
@@ -181,15 +181,14 @@ done:
     Py_DECREF(shape);
     return r;
 }
-static int scratch(int64_t device, stream_t stream, size_t bytes, void **data) {
+/* Scratch of this call alone (*hold, to be let go after the launches; NULL: none needed). */
+static int scratch(size_t bytes, PyObject *like, PyObject **hold, void **data) {
+    *hold = NULL;
     *data = NULL;
     if (bytes == 0) return 1;
-    PyObject *r = PyObject_CallFunction(workspace, "LLn", (long long)device, (long long)(intptr_t)stream, (Py_ssize_t)bytes);
-    int64_t p;
-    const int ok = whole(r, &p);
-    Py_XDECREF(r);
-    if (ok) *data = (void *)(intptr_t)p;
-    return ok;
+    const int64_t size[1] = {(int64_t)bytes};
+    *hold = new_tensor(1, size, uint8_type, like, data);
+    return *hold != NULL;
 }
 static int activation(PyObject *name, int *act) {
     PyObject *v = PyDict_GetItemWithError(activations, name);
@@ -240,8 +239,7 @@ static PyObject *forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                                                                            w.data, m.ld, m.expert, m.order)
                                 : lib.linear_forward_workspace_size(kind, (int)M, (int)N, (int)K, x.data, ldx, w.data, m.ld,
                                                                     m.order);
-    PyObject *out = a[7];
-    if (!scratch(device, stream, need, &ws)) UNUSUAL();
+    PyObject *out = a[7], *hold;
     if (out == Py_None) {
         const int64_t size[2] = {M, N};
         out = new_tensor(2, size, dtype, a[0], &y);
@@ -252,11 +250,16 @@ static PyObject *forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         y = t.data;
         Py_INCREF(out);
     }
+    if (!scratch(need, a[0], &hold, &ws)) {
+        Py_DECREF(out);
+        UNUSUAL();
+    }
     const int st =
         grouped ? lib.expert_linear_forward(kind, (int)M, (int)N, (int)K, (int)E, offsets, x.data, ldx, w.data, m.ld, m.expert,
                                             m.order, bias, residual, ldr, act, z, ldz, y, ldy, ws, need, stream)
                 : lib.linear_forward(kind, (int)M, (int)N, (int)K, x.data, ldx, w.data, m.ld, m.order, bias, residual, ldr, act,
                                      z, ldz, y, ldy, ws, need, stream);
+    Py_XDECREF(hold);
     if (st == 0) return out;
     Py_DECREF(out);
     return PyLong_FromLong(st);
@@ -264,7 +267,7 @@ static PyObject *forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 
 /* backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbias) -> (dx, dw, dbias) */
 static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
-    PyObject *dtype, *dx = NULL, *dw = NULL, *db = NULL, *result = NULL;
+    PyObject *dtype, *dx = NULL, *dw = NULL, *db = NULL, *hold = NULL, *result = NULL;
     int64_t device, lddy, ldx, ldz = 0;
     stream_t stream;
     int act;
@@ -297,7 +300,6 @@ static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                                                             w.data, m.ld, m.expert, m.order, act, want_dx, want_dw, want_db)
                 : lib.linear_backward_workspace_size(kind, (int)M, (int)N, (int)K, g.data, lddy, x.data, ldx, w.data, m.ld,
                                                      m.order, act, want_dx, want_dw, want_db);
-    if (!scratch(device, stream, need, &ws)) UNUSUAL();
     const int64_t dx_size[2] = {M, K}, dw_size[3] = {E, m.order ? N : K, m.order ? K : N}, db_size[2] = {E, N};
     if (want_dx && (dx = new_tensor(2, dx_size, dtype, a[1], &dxp)) == NULL) goto unusual;
     if (want_dw && (dw = new_tensor(2 + grouped, dw_size + !grouped, dtype, a[1], &dwp)) == NULL) goto unusual;
@@ -309,12 +311,14 @@ static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         dw = turned;
         if (dw == NULL) goto unusual;
     }
+    if (!scratch(need, a[1], &hold, &ws)) goto unusual;
     const int64_t lddw = m.order ? K : N;
     const int st = grouped ? lib.expert_linear_backward(kind, (int)M, (int)N, (int)K, (int)E, offsets, g.data, lddy, x.data,
                                                         ldx, w.data, m.ld, m.expert, m.order, z, ldz, act, dxp, K, dwp, lddw,
                                                         K * N, dbp, ws, need, stream)
                            : lib.linear_backward(kind, (int)M, (int)N, (int)K, g.data, lddy, x.data, ldx, w.data, m.ld,
                                                  m.order, z, ldz, act, dxp, K, dwp, lddw, dbp, ws, need, stream);
+    Py_XDECREF(hold);
     if (st == 0)
         result = PyTuple_Pack(3, dx != NULL ? dx : Py_None, dw != NULL ? dw : Py_None, db != NULL ? db : Py_None);
     else
@@ -346,15 +350,17 @@ static PyObject *sort(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         UNUSUAL();
     const int T = (int)c.size[0], J = (int)c.size[1];
     const size_t need = lib.expert_sort_workspace_size(T, J, (int)E);
-    if (!scratch(device, stream, need, &ws)) UNUSUAL();
     const int64_t o_size[1] = {E + 1};
     PyObject *rows = new_tensor(2, c.size, int32_type, a[0], &rp);
     PyObject *offsets = rows == NULL ? NULL : new_tensor(1, o_size, int32_type, a[0], &op);
-    if (offsets == NULL) {
+    PyObject *hold = NULL;
+    if (offsets == NULL || !scratch(need, a[0], &hold, &ws)) {
         Py_XDECREF(rows);
+        Py_XDECREF(offsets);
         UNUSUAL();
     }
     const int st = lib.expert_sort(T, J, (int)E, c.data, d == int32_type ? 4 : 8, rp, op, ws, need, stream);
+    Py_XDECREF(hold);
     PyObject *result = st == 0 ? PyTuple_Pack(2, rows, offsets) : PyLong_FromLong(st);
     Py_DECREF(rows);
     Py_DECREF(offsets);
@@ -503,8 +509,8 @@ static PyObject *bind(PyObject *self, PyObject *args) {
         slots[i] = PyLong_AsVoidPtr(v);
         if (slots[i] == NULL) return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "%s", lib_names[i]);
     }
-    if (!PyArg_ParseTuple(objects, "OOOOOO!(OOO)OO", &tensor_type, &empty, &raw_stream, &get_device, &workspace, &PyDict_Type,
-                          &activations, &kinds[0], &kinds[1], &kinds[2], &int32_type, &int64_type))
+    if (!PyArg_ParseTuple(objects, "OOOOO!(OOO)OOO", &tensor_type, &empty, &raw_stream, &get_device, &PyDict_Type, &activations,
+                          &kinds[0], &kinds[1], &kinds[2], &int32_type, &int64_type, &uint8_type))
         return NULL;
     if (!PyType_Check(tensor_type)) return PyErr_Format(PyExc_TypeError, "the tensor type is none");
     Py_INCREF(objects); /* and with it all of them, for good */

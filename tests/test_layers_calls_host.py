@@ -1,0 +1,60 @@
+"""What the layer calls do around their launches, with stand-ins for CUDA
+tensors and for the library (CPU only): through the extension and through the
+interpreter."""
+import gc
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dense_fp32_tiled_gb300 as sg
+from dense_fp32_tiled_gb300 import build as sg_build
+from tests import _stand_ins as S
+
+WITH_SCRATCH = ["linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward", "expert_sort"]
+
+
+@pytest.fixture(scope="module")
+def real():
+    sg_build.build()
+    return sg.load_library()
+
+
+@pytest.fixture(params=["extension", "interpreter"])
+def lib(request, real, monkeypatch, tmp_path):
+    return S.install(monkeypatch, real, request.param, str(tmp_path))
+
+
+def _call(name):
+    """A call of each operator that takes scratch; x is not 16-byte aligned, so every product asks for some."""
+    x, w, dy = S.Tensor((20, 8), address=(1 << 50) + 2), S.Tensor((8, 16)), S.Tensor((20, 16))
+    we, off = S.Tensor((3, 8, 16)), S.Tensor((4,), torch.int32)
+    return {"linear_forward": lambda: sg.linear(x, w), "linear_backward": lambda: sg.linear_backward(dy, x, w),
+            "expert_linear_forward": lambda: sg.expert_linear(x, we, off),
+            "expert_linear_backward": lambda: sg.expert_linear_backward(dy, x, we, off),
+            "expert_sort": lambda: sg.expert_sort(S.Tensor((9000, 2), torch.int32), 4)}[name]
+
+
+@pytest.mark.parametrize("name", WITH_SCRATCH)
+def test_scratch_is_its_calls_own(lib, name):
+    """A call that begins while another one is still enqueueing (another thread's, on the same
+    stream) has other scratch; a call's scratch lives until it has enqueued its kernels, and
+    nothing holds it any longer (a captured graph's then belongs to that graph alone)."""
+    seen, alive, call = [], [], _call(name)
+
+    def addresses():
+        gc.collect()
+        return {t().data_ptr() for t in lib.made if t() is not None and t().dtype is torch.uint8}
+
+    def enqueue(*args):  # ..., workspace, its bytes, stream
+        seen.append(args[-3])
+        if len(seen) == 1:
+            call()
+        alive.append(args[-3] in addresses())
+        return 0
+
+    lib.does[name + "_workspace_size"] = lambda *a: 4096
+    lib.does[name] = enqueue
+    call()
+    assert len(seen) == 2 and seen[0] and seen[1] and seen[0] != seen[1]
+    assert alive == [True, True] and not addresses()
