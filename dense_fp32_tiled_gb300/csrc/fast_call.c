@@ -48,6 +48,15 @@ static const char *const lib_names[] = {"linear_forward", "linear_forward_worksp
                                         "expert_linear_backward_workspace_size", "expert_sort", "expert_sort_workspace_size",
                                         "expert_gather", "expert_combine", "expert_combine_backward"};
 
+/* A launch may wait for room in the stream's queue, and what it waits for, such as a
+ * function on the host, may want the interpreter: it is not held meanwhile. */
+#define LAUNCH(status, call)   \
+    do {                       \
+        Py_BEGIN_ALLOW_THREADS \
+        status = call;         \
+        Py_END_ALLOW_THREADS   \
+    } while (0)
+
 /* What bind() keeps: torch's own objects, for the life of the process. */
 static PyObject *tensor_type, *empty, *raw_stream, *get_device, *activations, *kinds[3], *int32_type, *int64_type, *uint8_type;
 static PyObject *s_dtype, *s_device, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_transpose;
@@ -254,11 +263,11 @@ static PyObject *forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         Py_DECREF(out);
         UNUSUAL();
     }
-    const int st =
-        grouped ? lib.expert_linear_forward(kind, (int)M, (int)N, (int)K, (int)E, offsets, x.data, ldx, w.data, m.ld, m.expert,
-                                            m.order, bias, residual, ldr, act, z, ldz, y, ldy, ws, need, stream)
-                : lib.linear_forward(kind, (int)M, (int)N, (int)K, x.data, ldx, w.data, m.ld, m.order, bias, residual, ldr, act,
-                                     z, ldz, y, ldy, ws, need, stream);
+    int st;
+    LAUNCH(st, grouped ? lib.expert_linear_forward(kind, (int)M, (int)N, (int)K, (int)E, offsets, x.data, ldx, w.data, m.ld,
+                                                   m.expert, m.order, bias, residual, ldr, act, z, ldz, y, ldy, ws, need, stream)
+                       : lib.linear_forward(kind, (int)M, (int)N, (int)K, x.data, ldx, w.data, m.ld, m.order, bias, residual,
+                                            ldr, act, z, ldz, y, ldy, ws, need, stream));
     Py_XDECREF(hold);
     if (st == 0) return out;
     Py_DECREF(out);
@@ -313,11 +322,12 @@ static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     }
     if (!scratch(need, a[1], &hold, &ws)) goto unusual;
     const int64_t lddw = m.order ? K : N;
-    const int st = grouped ? lib.expert_linear_backward(kind, (int)M, (int)N, (int)K, (int)E, offsets, g.data, lddy, x.data,
-                                                        ldx, w.data, m.ld, m.expert, m.order, z, ldz, act, dxp, K, dwp, lddw,
-                                                        K * N, dbp, ws, need, stream)
-                           : lib.linear_backward(kind, (int)M, (int)N, (int)K, g.data, lddy, x.data, ldx, w.data, m.ld,
-                                                 m.order, z, ldz, act, dxp, K, dwp, lddw, dbp, ws, need, stream);
+    int st;
+    LAUNCH(st, grouped ? lib.expert_linear_backward(kind, (int)M, (int)N, (int)K, (int)E, offsets, g.data, lddy, x.data, ldx,
+                                                    w.data, m.ld, m.expert, m.order, z, ldz, act, dxp, K, dwp, lddw, K * N,
+                                                    dbp, ws, need, stream)
+                       : lib.linear_backward(kind, (int)M, (int)N, (int)K, g.data, lddy, x.data, ldx, w.data, m.ld, m.order, z,
+                                             ldz, act, dxp, K, dwp, lddw, dbp, ws, need, stream));
     Py_XDECREF(hold);
     if (st == 0)
         result = PyTuple_Pack(3, dx != NULL ? dx : Py_None, dw != NULL ? dw : Py_None, db != NULL ? db : Py_None);
@@ -359,7 +369,8 @@ static PyObject *sort(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         Py_XDECREF(offsets);
         UNUSUAL();
     }
-    const int st = lib.expert_sort(T, J, (int)E, c.data, d == int32_type ? 4 : 8, rp, op, ws, need, stream);
+    int st;
+    LAUNCH(st, lib.expert_sort(T, J, (int)E, c.data, d == int32_type ? 4 : 8, rp, op, ws, need, stream));
     Py_XDECREF(hold);
     PyObject *result = st == 0 ? PyTuple_Pack(2, rows, offsets) : PyLong_FromLong(st);
     Py_DECREF(rows);
@@ -409,7 +420,8 @@ static PyObject *gather(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         xs = t.data;
         Py_INCREF(out);
     }
-    const int st = lib.expert_gather(kind, (int)T, (int)J, (int)H, (int)E, rows, offsets, x.data, ldx, xs, lds, stream);
+    int st;
+    LAUNCH(st, lib.expert_gather(kind, (int)T, (int)J, (int)H, (int)E, rows, offsets, x.data, ldx, xs, lds, stream));
     if (st == 0) return out;
     Py_DECREF(out);
     return PyLong_FromLong(st);
@@ -455,8 +467,8 @@ static PyObject *combine(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         y = t.data;
         Py_INCREF(out);
     }
-    const int st =
-        lib.expert_combine(kind, (int)T, (int)J, (int)H, rows, weights, s.data, lds, residual, ldr, y, ldy, stream);
+    int st;
+    LAUNCH(st, lib.expert_combine(kind, (int)T, (int)J, (int)H, rows, weights, s.data, lds, residual, ldr, y, ldy, stream));
     if (st == 0) return out;
     Py_DECREF(out);
     return PyLong_FromLong(st);
@@ -489,8 +501,9 @@ static PyObject *combine_backward(PyObject *self, PyObject *const *a, Py_ssize_t
         Py_XDECREF(dys);
         UNUSUAL();
     }
-    const int st = lib.expert_combine_backward(kind, (int)T, (int)J, (int)H, (int)E, rows, offsets, weights, g.data, lddy, ys,
-                                               lds, dysp, H > 1 ? H : 1, dwp, stream);
+    int st;
+    LAUNCH(st, lib.expert_combine_backward(kind, (int)T, (int)J, (int)H, (int)E, rows, offsets, weights, g.data, lddy, ys, lds,
+                                           dysp, H > 1 ? H : 1, dwp, stream));
     PyObject *result = st == 0 ? PyTuple_Pack(2, dys, dw != NULL ? dw : Py_None) : PyLong_FromLong(st);
     Py_DECREF(dys);
     Py_XDECREF(dw);

@@ -1,7 +1,10 @@
 """What the layer calls do around their launches, with stand-ins for CUDA
 tensors and for the library (CPU only): through the extension and through the
 interpreter."""
+import ctypes
 import gc
+import subprocess
+import threading
 
 import pytest
 
@@ -58,3 +61,33 @@ def test_scratch_is_its_calls_own(lib, name):
     call()
     assert len(seen) == 2 and seen[0] and seen[1] and seen[0] != seen[1]
     assert alive == [True, True] and not addresses()
+
+
+WAITS = r"""
+#include <unistd.h>
+int flag;
+int wait_for_flag() {
+    for (int i = 0; i < 3000 && !*(volatile int *)&flag; ++i) usleep(1000);
+    return flag ? 0 : -6;
+}
+"""
+
+
+@pytest.mark.parametrize("name", WITH_SCRATCH + ["expert_gather", "expert_combine", "expert_combine_backward"])
+def test_other_threads_run_while_a_launch_waits(real, monkeypatch, tmp_path, name):
+    """The library's functions may wait for room in a stream's queue, and what runs there may
+    need the interpreter: here another thread sets the flag that the function waits for."""
+    (tmp_path / "waits.c").write_text(WAITS)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(tmp_path / "waits.so"), str(tmp_path / "waits.c")], check=True)
+    waits = ctypes.CDLL(str(tmp_path / "waits.so"))
+    S.install(monkeypatch, real, "extension", str(tmp_path),
+              {name: ctypes.cast(waits.wait_for_flag, ctypes.c_void_p).value})
+    calls = {"expert_gather": lambda: sg.expert_gather(S.Tensor((5, 8)), S.Tensor((5, 2), torch.int32), S.Tensor((3,), torch.int32)),
+             "expert_combine": lambda: sg.expert_combine(S.Tensor((10, 8)), S.Tensor((5, 2), torch.int32)),
+             "expert_combine_backward": lambda: sg.expert_combine_backward(
+                 S.Tensor((5, 8)), S.Tensor((10, 8)), S.Tensor((5, 2), torch.int32), None, S.Tensor((3,), torch.int32))}
+    flag = ctypes.c_int.in_dll(waits, "flag")
+    setter = threading.Timer(0.05, lambda: setattr(flag, "value", 1))
+    setter.start()
+    (calls.get(name) or _call(name))()  # raises SgemmError if the wait ran out
+    setter.join()
