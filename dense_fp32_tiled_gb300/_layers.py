@@ -124,6 +124,8 @@ _NOWHERE = nullcontext()
 def _on(device, stream):
     """The context in which a call allocates and launches: the device and stream it is for."""
     if stream is not None:
+        if stream.device.index != device:
+            raise ValueError(f"stream is on cuda:{stream.device.index}, the tensors on cuda:{device}")
         return torch.cuda.stream(stream)
     if torch.cuda.current_device() != device:
         return torch.cuda.device(device)

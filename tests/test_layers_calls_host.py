@@ -91,3 +91,27 @@ def test_other_threads_run_while_a_launch_waits(real, monkeypatch, tmp_path, nam
     setter.start()
     (calls.get(name) or _call(name))()  # raises SgemmError if the wait ran out
     setter.join()
+
+
+def _given(stream):
+    """Every operator's call with a stream."""
+    x, w, dy = S.Tensor((20, 8)), S.Tensor((8, 16)), S.Tensor((20, 16))
+    we, off, rows = S.Tensor((3, 8, 16)), S.Tensor((4,), torch.int32), S.Tensor((10, 2), torch.int32)
+    return {"linear": lambda: sg.linear(x, w, stream=stream), "linear_backward": lambda: sg.linear_backward(dy, x, w, stream=stream),
+            "expert_linear": lambda: sg.expert_linear(x, we, off, stream=stream),
+            "expert_linear_backward": lambda: sg.expert_linear_backward(dy, x, we, off, stream=stream),
+            "expert_sort": lambda: sg.expert_sort(rows, 3, stream=stream),
+            "expert_gather": lambda: sg.expert_gather(S.Tensor((10, 8)), rows, off, stream=stream),
+            "expert_combine": lambda: sg.expert_combine(x, rows, stream=stream),
+            "expert_gather_backward": lambda: sg.expert_gather_backward(x, rows, stream=stream),
+            "expert_combine_backward": lambda: sg.expert_combine_backward(S.Tensor((10, 8)), x, rows, None, off, stream=stream)}
+
+
+@pytest.mark.parametrize("name", _given(None))
+def test_stream_of_another_device_is_refused(lib, name):
+    with pytest.raises(ValueError, match="stream"):
+        _given(S.Stream(1))[name]()
+    assert not lib.entered and lib.calls == 0
+    own = S.Stream(0)
+    _given(own)[name]()
+    assert lib.entered == [own] and lib.calls == 1
