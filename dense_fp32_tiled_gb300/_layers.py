@@ -64,6 +64,12 @@ def _type_of(t, name):
     return kind
 
 
+def _fits(*sizes):
+    """The C functions' sizes are 32-bit."""
+    if any(abs(n) > 0x7fffffff for n in sizes):
+        raise ValueError(f"sizes must be below 2**31, got {sizes}")
+
+
 def _alike(t, dtype, device, name):
     if getattr(t, "dtype", None) is not dtype or t.get_device() != device:
         raise TypeError(f"{name} must be a {dtype} tensor on cuda:{device}")
@@ -197,6 +203,7 @@ def _forward(x, w, offsets, bias, residual, activation, preact, out, stream):
     xp, ldx = _rows(x, M, K, dtype, dev, "x")
     wp, ldw, order, step = _weight(w, K, dtype, dev, "w")
     N = w.shape[-1]
+    _fits(M, N, K)
     rp, ldr = _rows(residual, M, N, dtype, dev, "residual") if residual is not None else (None, 0)
     zp, ldz = _rows(preact, M, N, dtype, dev, "preact") if preact is not None else (None, 0)
     if grouped:
@@ -258,6 +265,7 @@ def _backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbia
         raise ValueError("preact is needed with an activation, and only then")
     (M, K), dtype, dev = x.shape, x.dtype, x.get_device()
     N = w.shape[-1]
+    _fits(M, N, K)
     gp, lddy = _rows(dy, M, N, dtype, dev, "dy")
     xp, ldx = _rows(x, M, K, dtype, dev, "x")
     wp, ldw, order, step = _weight(w, K, dtype, dev, "w")
@@ -329,6 +337,7 @@ def expert_sort(choices, experts, stream=None):
     if choices.dim() != 2 or not choices.is_contiguous():
         raise ValueError(f"choices must be contiguous with shape (tokens, choices), got {tuple(choices.shape)}")
     (T, J), E, dev = choices.shape, int(experts), choices.get_device()
+    _fits(T, J, E)
     with _on(dev, stream):
         rows = torch.empty((T, J), dtype=torch.int32, device=choices.device)
         offsets = torch.empty((max(E, 0) + 1,), dtype=torch.int32, device=choices.device)
@@ -351,6 +360,7 @@ def _order(rows, offsets, T, dev):
     if offsets is not None:
         E = offsets.shape[0] - 1
         op = _int32(offsets, (E + 1,), dev, "offsets")
+    _fits(J, E)
     return J, E, _int32(rows, (T, J), dev, "rows"), op
 
 
@@ -365,6 +375,7 @@ def expert_gather(x, rows, offsets, out=None, stream=None):
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
     (T, H), dtype, dev = x.shape, x.dtype, x.get_device()
+    _fits(T, H)
     xp, ldx = _rows(x, T, H, dtype, dev, "x")
     J, E, rp, op = _order(rows, offsets, T, dev)
     with _on(dev, stream):
@@ -389,6 +400,7 @@ def expert_combine(ys, rows, weights=None, residual=None, out=None, stream=None)
     if ys.dim() != 2 or rows.dim() != 2:
         raise ValueError(f"ys and rows must be 2-D, got {tuple(ys.shape)} and {tuple(rows.shape)}")
     T, H, dtype, dev = rows.shape[0], ys.shape[1], ys.dtype, ys.get_device()
+    _fits(T, H)
     J, _, rp, _ = _order(rows, None, T, dev)
     sp, lds = _rows(ys, T * J, H, dtype, dev, "ys")
     wp = _vector(weights, (T, J), torch.float32, dev, "weights")
@@ -421,6 +433,7 @@ def expert_combine_backward(dy, ys, rows, weights, offsets, need_dweights=True, 
     if dy.dim() != 2:
         raise ValueError(f"dy must be 2-D, got {tuple(dy.shape)}")
     (T, H), dtype, dev = dy.shape, dy.dtype, dy.get_device()
+    _fits(T, H)
     gp, lddy = _rows(dy, T, H, dtype, dev, "dy")
     J, E, rp, op = _order(rows, offsets, T, dev)
     wp = _vector(weights, (T, J), torch.float32, dev, "weights")

@@ -88,8 +88,8 @@ class Library:
                 self.calls += 1
                 return self.does.get(name, lambda *a: 0)(*args)
 
-            setattr(self, name, call)
             self.callbacks[name] = ctypes.CFUNCTYPE(fn.restype, *fn.argtypes)(call)
+            setattr(self, name, self.callbacks[name])  # arguments are converted as the real one's are
 
     def addresses(self):
         return {n: ctypes.cast(c, ctypes.c_void_p).value for n, c in self.callbacks.items()}

@@ -115,3 +115,28 @@ def test_stream_of_another_device_is_refused(lib, name):
     own = S.Stream(0)
     _given(own)[name]()
     assert lib.entered == [own] and lib.calls == 1
+
+
+BIG = 2 ** 32 + 16  # 16 in 32 bits
+
+
+@pytest.mark.parametrize("name,call", [
+    ("rows of x", lambda: sg.linear(S.Tensor((BIG, 8)), S.Tensor((8, 16)))),
+    ("inputs", lambda: sg.linear(S.Tensor((4, BIG)), S.Tensor((BIG, 16)))),
+    ("outputs", lambda: sg.linear(S.Tensor((4, 8)), S.Tensor((8, BIG)))),
+    ("rows of experts", lambda: sg.expert_linear(S.Tensor((BIG, 8)), S.Tensor((2, 8, 16)), S.Tensor((3,), torch.int32))),
+    ("rows of dy", lambda: sg.linear_backward(S.Tensor((BIG, 16)), S.Tensor((BIG, 8)), S.Tensor((8, 16)))),
+    ("tokens sorted", lambda: sg.expert_sort(S.Tensor((BIG, 2), torch.int32), 4)),
+    ("experts", lambda: sg.expert_sort(S.Tensor((4, 2), torch.int32), BIG)),
+    ("less than no experts", lambda: sg.expert_sort(S.Tensor((4, 2), torch.int32), 16 - 2 ** 32)),
+    ("choices", lambda: sg.expert_sort(S.Tensor((4, BIG), torch.int32), 4)),
+    ("gathered", lambda: sg.expert_gather(S.Tensor((BIG, 8)), S.Tensor((BIG, 2), torch.int32), S.Tensor((4,), torch.int32))),
+    ("width", lambda: sg.expert_gather(S.Tensor((4, BIG)), S.Tensor((4, 2), torch.int32), S.Tensor((4,), torch.int32))),
+    ("combined", lambda: sg.expert_combine(S.Tensor((BIG, 8)), S.Tensor((BIG, 1), torch.int32))),
+    ("spread", lambda: sg.expert_combine_backward(S.Tensor((BIG, 8)), S.Tensor((BIG, 8)), S.Tensor((BIG, 1), torch.int32), None,
+                                                  S.Tensor((4,), torch.int32))),
+])
+def test_sizes_past_32_bits_are_refused(lib, name, call):
+    with pytest.raises(ValueError):
+        call()
+    assert lib.calls == 0
