@@ -124,6 +124,11 @@ def _int32(t, shape, device, name):
     return t.data_ptr()
 
 
+def _grouped(offsets):
+    if offsets is None:
+        raise ValueError("offsets are needed (linear is the product without them)")
+
+
 _NOWHERE = nullcontext()
 
 
@@ -186,7 +191,8 @@ def expert_linear(x, w, offsets, bias=None, residual=None, activation="none", pr
     offsets[e + 1] of x (R, K) meet w[e] and bias[e] of w (E, K, N) and bias
     (E, N).  offsets is int32 (E + 1,) on the device, as expert_sort makes it,
     and is not read on the host.  Rows of no expert give 0."""
-    if stream is None and _fast is not None and offsets is not None:
+    _grouped(offsets)
+    if stream is None and _fast is not None:
         r = _fast.forward(x, w, offsets, bias, residual, activation, preact, out)
         if r is not NotImplemented:
             return _answer(r, "expert_linear_forward")
@@ -248,7 +254,8 @@ def linear_backward(dy, x, w, preact=None, activation="none", need_dx=True, need
 def expert_linear_backward(dy, x, w, offsets, preact=None, activation="none", need_dx=True, need_dw=True,
                            need_dbias=True, stream=None):
     """(dx, dw, dbias) of expert_linear.  Rows of no expert have a dx of 0, experts without rows a dw and dbias of 0."""
-    if stream is None and _fast is not None and offsets is not None:
+    _grouped(offsets)
+    if stream is None and _fast is not None:
         r = _fast.backward(dy, x, w, offsets, preact, activation, need_dx, need_dw, need_dbias)
         if r is not NotImplemented:
             return _answer(r, "expert_linear_backward")

@@ -140,3 +140,12 @@ def test_sizes_past_32_bits_are_refused(lib, name, call):
     with pytest.raises(ValueError):
         call()
     assert lib.calls == 0
+
+
+def test_experts_without_offsets_are_refused(lib):
+    x, w, dy, rows = S.Tensor((20, 8)), S.Tensor((8, 16)), S.Tensor((20, 16)), S.Tensor((10, 2), torch.int32)
+    for call in (lambda: sg.expert_linear(x, w, None), lambda: sg.expert_linear_backward(dy, x, w, None),
+                 lambda: sg.expert_linear(x, w, None, stream=S.Stream()), lambda: sg.expert_linear_backward(dy, x, w, None, stream=S.Stream())):
+        with pytest.raises(ValueError, match="offsets"):
+            call()
+    assert lib.calls == 0
