@@ -117,7 +117,7 @@ __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == LINEAR_ACT_GELU) {
         if constexpr (EXACT) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
         float gauss;
-        const float tail = z * normal_tail(z, gauss);
+        const float tail = fminf(z, 16.0f) * normal_tail(z, gauss);  // 0 from there on, and no inf * 0 at infinity
         return z < 0.0f ? tail : z - tail;
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) return z * logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
