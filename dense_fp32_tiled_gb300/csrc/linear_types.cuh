@@ -156,7 +156,8 @@ __device__ __forceinline__ float slope(float z) {
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) {
         const float p = logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
-        return p + z * p * (1.0f - p) * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+        const float c = fminf(fabsf(z), 100.0f);  // p (1 - p) is 0 long before, and c * c stays finite
+        return p + z * p * (1.0f - p) * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
     }
     return 1.0f;
 }

@@ -82,3 +82,13 @@ def test_slope_of_gelu_f32():
     cdf, density = 0.5 * torch.erfc(-zd * 0.5 ** 0.5), (zd * torch.exp(-0.5 * zd * zd) * 0.3989422804014327).abs()
     bound = 1.5 * 2.0 ** -21 * cdf + (zd * zd / 2 * 2.0 ** -24 + 2.0 ** -21).clamp(max=1) * density + 2.0 ** -24 * want.abs() + FLOOR
     L.assert_within(_slopes(z, "gelu"), want, bound, "slope of gelu")
+
+
+@pytest.mark.parametrize("dtype", L.TYPES)
+@pytest.mark.parametrize("act", L.ACTS)
+def test_slopes(dtype, act):
+    """Every activation's, to the ends of the type's range: terms of at most |slope| + 1, each within act_bound."""
+    z = _arguments(L.TYPES[dtype])
+    want = L.slope(z.double(), act)
+    got = _slopes(z, act) if act != "none" else torch.ones_like(z)
+    L.assert_within(got, want, L.act_bound(1 + want.abs(), z.dtype) + L.rounding(want, z.dtype) + FLOOR, f"slope of {act} {dtype}")
