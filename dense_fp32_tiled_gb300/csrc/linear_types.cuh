@@ -86,6 +86,15 @@ template <bool EXACT>
 __device__ __forceinline__ float logistic(float x) {
     return EXACT ? 1.0f / (1.0f + expf(-x)) : fast_reciprocal(1.0f + fast_exp2(-kLog2E * x));
 }
+// p = logistic(x), and p (1 - p) without the difference, which for large x is as
+// coarse as p: gelu_tanh's slope multiplies it by up to 35 before it vanishes.
+template <bool EXACT>
+__device__ __forceinline__ float logistic(float x, float &pq) {
+    const float e = EXACT ? expf(-fabsf(x)) : fast_exp2(-kLog2E * fabsf(x));
+    const float s = EXACT ? 1.0f / (1.0f + e) : fast_reciprocal(1.0f + e);
+    pq = e * s * s;
+    return x < 0.0f ? e * s : s;
+}
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi): (1 + tanh u) / 2 = logistic(2 u)
 constexpr float kGeluB = 0.044715f;
 constexpr float kSqrtHalf = 0.70710678118654752f;
@@ -142,8 +151,9 @@ template <int ACT, bool EXACT>
 __device__ __forceinline__ float slope(float z) {
     if constexpr (ACT == LINEAR_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
     if constexpr (ACT == LINEAR_ACT_SILU) {
-        const float p = logistic<EXACT>(z);
-        return p * (1.0f + z * (1.0f - p));
+        float pq;
+        const float p = logistic<EXACT>(z, pq);
+        return p + z * pq;
     }
     if constexpr (ACT == LINEAR_ACT_GELU) {
         float gauss;
@@ -155,9 +165,10 @@ __device__ __forceinline__ float slope(float z) {
         return (z < 0.0f ? tail : 1.0f - tail) + z * kInvSqrt2Pi * gauss;
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) {
-        const float p = logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
-        const float c = fminf(fabsf(z), 100.0f);  // p (1 - p) is 0 long before, and c * c stays finite
-        return p + z * p * (1.0f - p) * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
+        float pq;
+        const float p = logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z), pq);
+        const float c = fminf(fabsf(z), 100.0f);  // pq is 0 long before, and c * c stays finite
+        return p + z * pq * kGeluA * (1.0f + 3.0f * kGeluB * c * c);
     }
     return 1.0f;
 }

@@ -29,6 +29,13 @@ def _arguments(dtype):
 # Logistics below the smallest normal number may be 0; times an argument of -12 that is 12 * 2**-126.
 FLOOR = 2.0 ** -122
 
+def _value(z, act):
+    """L.value, with gelu_tanh as z times a logistic: 1 + tanh is 0 in 64 bits from z = -7.5 on, the product is not."""
+    if act == "gelu_tanh":
+        return z / (1 + torch.exp(-2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
+    return L.value(z, act)
+
+
 # few tokens, the product kernel with K in one piece and shared out, and without any K
 ROUTES = [(2, 40), (40, 40), (150, 40), (80, 4096), (70, 0)]
 
@@ -43,7 +50,7 @@ def _through(z, act, M, K):
 @pytest.mark.parametrize("M,K", ROUTES)
 def test_values_16_bit(dtype, act, M, K):
     z = _arguments(L.TYPES[dtype])
-    want = L.value(z.double(), act).expand(M, -1)
+    want = _value(z.double(), act).expand(M, -1)
     L.assert_within(_through(z, act, M, K), want, L.act_bound(want, z.dtype) + L.rounding(want, z.dtype) + FLOOR, f"{act} {dtype} {M} {K}")
 
 
@@ -62,7 +69,7 @@ def _relative_f32(z, act):
 @pytest.mark.parametrize("M,K", ROUTES)
 def test_values_f32(act, M, K):
     z = _arguments(torch.float32)
-    want = L.value(z.double(), act)
+    want = _value(z.double(), act)
     bound = (_relative_f32(z.double(), act) * want.abs() + FLOOR).expand(M, -1)
     L.assert_within(_through(z, act, M, K), want.expand(M, -1), bound, f"{act} {M} {K}")
 
