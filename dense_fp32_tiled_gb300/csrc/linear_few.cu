@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(256, NT <= 4 ? 2 : 1) rows16_kernel(const Few 
 }
 
 // FP32, more than four tokens: mma.sync on the three bf16 pieces that the warp
-// cuts its values into, six products, features as rows and tokens as
+// makes of its values, six products, features as rows and tokens as
 // columns (8 NT of them).  A warp's step is 32 features x 16 K; the K of a
 // fragment are a thread's four from 4 t on, and its rows:
 //   order 1: features g + 8 r, r = 0 .. 3, each by its own 16 bytes of K
@@ -442,17 +442,21 @@ struct FewTile {
     static constexpr int WARPS = NT <= 2 ? 16 : 8;   // accumulators: 16 NT registers
     static constexpr int DEPTH = NT <= 4 ? 2 : 1;    // steps whose loads are in flight
 };
-// x and y as three bf16 pieces each (x in the low halves), cut rather than
-// rounded: x = a + b + c exactly, 8 bits each, by whole-word instructions (5.5 a
-// value; with lt::pieces, 8 x 4096 x 4096 took 30 us for 18).  The products left
-// out are below 2^-21 of the full one.  An infinity leaves NaN in b and c.
-__device__ __forceinline__ void cut2(float x, float y, uint32_t (&r)[3]) {
+// x and y as three bf16 pieces each (x in the low halves), each rounded to nearest,
+// two values an instruction: x = a + b + c to 2^-27, and the products left out are
+// about 2^-24 of the full one at most, either way.  (Cut by masks, that is 2^-21, always
+// towards zero.  us, cut / rounded: K contiguous 16 x 8192^2 59 / 60, 32 x 8192^2 94 / 89,
+// 64 x 4096^2 46 / 47; features contiguous 63 / 70, 96 / 103, 48 / 45.)  The first piece stops at bf16's largest value where
+// rounding would overflow; an infinity passes into the second, and the third is a NaN.
+__device__ __forceinline__ void pieces2(float x, float y, uint32_t (&r)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
-        r[i] = __byte_perm(u, v, 0x7632);
-        x -= __uint_as_float(u & 0xffff0000u);
-        y -= __uint_as_float(v & 0xffff0000u);
+        if (i == 0)
+            asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;\n" : "=r"(r[i]) : "f"(y), "f"(x));
+        else
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r[i]) : "f"(y), "f"(x));
+        x -= __uint_as_float(r[i] << 16);
+        y -= __uint_as_float(r[i] & 0xffff0000u);
     }
 }
 __device__ __forceinline__ float part(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -499,15 +503,15 @@ __global__ void __launch_bounds__(FewTile<NT>::WARPS * 32, 1) few32_mma_kernel(c
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    cut2(ORDER ? part(wv[d][r], 2 * h) : part(wv[d][2 * h], r),
+                    pieces2(ORDER ? part(wv[d][r], 2 * h) : part(wv[d][2 * h], r),
                             ORDER ? part(wv[d][r], 2 * h + 1) : part(wv[d][2 * h + 1], r), a[r >> 1][(r & 1) + 2 * h]);
 #pragma unroll
             for (int j = 0; j < NT; j += PAIR) {
                 uint32_t b[PAIR][2][3];
 #pragma unroll
                 for (int q = 0; q < PAIR; ++q) {
-                    cut2(xv[d][j + q].x, xv[d][j + q].y, b[q][0]);
-                    cut2(xv[d][j + q].z, xv[d][j + q].w, b[q][1]);
+                    pieces2(xv[d][j + q].x, xv[d][j + q].y, b[q][0]);
+                    pieces2(xv[d][j + q].z, xv[d][j + q].w, b[q][1]);
                 }
                 constexpr int WP[6] = {2, 0, 1, 1, 0, 0}, XP[6] = {0, 2, 1, 0, 1, 0};  // the small products first
 #pragma unroll
@@ -619,7 +623,7 @@ cudaError_t run32_mma(const Few &p, cudaStream_t stream) {
 
 }  // namespace
 
-// More than 16 tokens.  FP32: beyond 64, cutting the operands once for the product
+// More than 16 tokens.  FP32: beyond 64, splitting the operands once for the product
 // kernel costs less than in each CTA.  16 bits: each CTA reads all of x, so the
 // product kernel, about 10 us whatever its size, is left behind only below about
 // 8 million weights (us, product kernel / rows16_kernel: 32 x 512 x 512 11.0 / 5.5,
