@@ -492,7 +492,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             int high = 0, tile0 = 0;
             for (int e0 = 0; e0 < p.E + 2; e0 += 32) {
                 const int e = e0 + lane;
-                int b = e <= p.E ? min(max(p.offsets[e], 0), rows) : rows;
+                int b = rows > 0 && e <= p.E ? min(max(p.offsets[e], 0), rows) : rows;  // without rows there may be no offsets
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int o = __shfl_up_sync(0xffffffffu, b, d);
@@ -1605,7 +1605,7 @@ int backward(const Call &c) {
         p.mode = c.E >= 0 && !empty ? ROWS_BY_EXPERT : DENSE;
         p.out = c.dx;
         p.ldo = c.lddx;
-        const bool two = !empty && want.dw;  // without rows there may be many more products
+        const bool two = !empty && want.dw;
         p.order = two ? ORDER_FIRST : ORDER_ALONE;
         st = run_product(c.type, p, P_dx, Q, d, c.stream);
         if (st != SGEMM_OK) return st;
@@ -1619,19 +1619,10 @@ int backward(const Call &c) {
         p.T = c.w_order ? c.N : c.K;
         p.F = c.w_order ? c.K : c.N;
         p.K = empty ? 0 : c.M;
-        p.mode = c.E >= 0 && !empty ? K_BY_EXPERT : DENSE;
+        p.mode = c.E >= 0 ? K_BY_EXPERT : DENSE;  // without rows every expert's is zero
         p.out = c.dw;
         p.ldo = c.lddw;
         p.out_expert = c.E > 1 ? c.dw_expert : 0;
-        if (empty && c.E > 1) {  // no rows: every expert's is zero
-            for (int e = 0; e < c.E; ++e) {
-                Product q = p;
-                q.out = static_cast<char *>(c.dw) + static_cast<long long>(e) * c.dw_expert * b;
-                st = run_product(c.type, q, X, Z, d, c.stream);
-                if (st != SGEMM_OK) return st;
-            }
-            return SGEMM_OK;
-        }
         st = run_product(c.type, p, c.w_order ? X : Z, c.w_order ? Z : X, d, c.stream);
         if (st != SGEMM_OK) return st;
     }

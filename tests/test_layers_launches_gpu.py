@@ -1,0 +1,52 @@
+"""How many kernels the layer calls launch, and what another stream may see of
+them (needs a GB300)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import dense_fp32_tiled_gb300 as sg
+from tests import _layers as L
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dense_fp32_tiled_gb300 import build
+    build.build()
+    sg.load_library()
+    yield
+    assert sg.linear_timeouts() == 0
+
+
+def _products(call):
+    """The product kernels that a call launches."""
+    for _ in range(2):  # a process's first profile may come out empty
+        with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+            call()
+            torch.cuda.synchronize()
+    return sum(e.count for e in prof.key_averages() if "product_kernel" in e.key)
+
+
+@pytest.mark.parametrize("dtype", L.TYPES)
+@pytest.mark.parametrize("order", [0, 1])
+@pytest.mark.parametrize("E", [1, 5, 300])
+def test_no_rows_over_many_experts(dtype, order, E):
+    """Every expert's gradient is zero, in one launch."""
+    dt = L.TYPES[dtype]
+    dy, x = torch.empty(0, 72, dtype=dt, device="cuda"), torch.empty(0, 40, dtype=dt, device="cuda")
+    w = L.weight(L.rng(E), 40, 72, dt, order, (E,))
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        junk = torch.full((E, 72, 40), 7.0, dtype=dt, device="cuda")  # what dw's memory may hold
+        del junk
+        dx, dw, db = sg.expert_linear_backward(dy, x, w, offsets)
+        assert dx.shape == (0, 40) and dw.shape == (E, 40, 72) and (dw == 0).all() and (db == 0).all()
+    assert _products(lambda: sg.expert_linear_backward(dy, x, w, offsets)) == 1
