@@ -20,6 +20,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -1094,10 +1095,11 @@ struct Plan {
     double cost = 1e300;
 };
 
-// LINEAR_TUNE="cg=1|2,bt=16..256,splits=1..8", read once at the first call,
+// LINEAR_TUNE="cg=1|2,bt=16..256,splits=1..4", read once at the first call,
 // limits the plans of every product to those values, for sweeps without a
-// rebuild (a limit that leaves no plan is not applied).  It changes how the
-// work is split, not what is computed.
+// rebuild.  Limits that leave a product no plan are not applied to it, and the
+// first time that is said on stderr.  It changes how the work is split, not
+// what is computed.
 struct Tune {
     int cg = 0, bt = 0, splits = 0;
 };
@@ -1208,7 +1210,13 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.q_mn = Q.mn;
     p.timeout_flag = d.timeout_flag;
     Plan pl = choose(p, d, type, tune());
-    if (pl.cost > 1e299) pl = choose(p, d, type, Tune());
+    if (pl.cost > 1e299) {
+        static std::once_flag told;
+        std::call_once(told, [&] {
+            fprintf(stderr, "LINEAR_TUNE leaves no plan for a product of %d x %d x %d and is not applied to it\n", p.T, p.F, p.K);
+        });
+        pl = choose(p, d, type, Tune());
+    }
     p.bt = pl.bt;
     p.splits = pl.splits;
     p.q_bytes = q_bytes_of(p.bt / pl.cg, Q.mn);

@@ -50,3 +50,14 @@ def test_no_rows_over_many_experts(dtype, order, E):
         dx, dw, db = sg.expert_linear_backward(dy, x, w, offsets)
         assert dx.shape == (0, 40) and dw.shape == (E, 40, 72) and (dw == 0).all() and (db == 0).all()
     assert _products(lambda: sg.expert_linear_backward(dy, x, w, offsets)) == 1
+
+
+@pytest.mark.parametrize("limit,heard", [("splits=8", True), ("cg=1,bt=20", True), ("cg=1,bt=64,splits=4", False), ("", False)])
+def test_limits_that_leave_no_plan_are_reported(limit, heard):
+    code = ("import torch, dense_fp32_tiled_gb300 as sg; x, w = torch.ones(100, 4096, device='cuda'), torch.ones(4096, 72, device='cuda');"
+            "assert (sg.linear(x, w) == 4096).all() and (sg.linear(x, w) == 4096).all()")
+    env = {k: v for k, v in os.environ.items() if k != "LINEAR_TUNE"}
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env={**env, **({"LINEAR_TUNE": limit} if limit else {})},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stderr.count("LINEAR_TUNE leaves no plan") == int(heard)
