@@ -61,3 +61,21 @@ def test_limits_that_leave_no_plan_are_reported(limit, heard):
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stderr.count("LINEAR_TUNE leaves no plan") == int(heard)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_another_stream_behind_an_event_sees_both_products(dtype):
+    """An event recorded after a backward pass comes after its second product, which waits for its first."""
+    g, dt = L.rng(5), L.TYPES[dtype]
+    x, dy = L.randn(g, (4096, 2048), dt), L.randn(g, (4096, 1024), dt)
+    w = L.weight(g, 2048, 1024, dt, 1)
+    want = [t.clone() for t in sg.linear_backward(dy, x, w)]
+    side, event = torch.cuda.Stream(), torch.cuda.Event()
+    for _ in range(20):
+        got = sg.linear_backward(dy, x, w)
+        event.record()
+        side.wait_event(event)
+        with torch.cuda.stream(side):
+            copies = [t.clone() for t in got]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(copies, want))
