@@ -24,7 +24,9 @@ using lt::to_f;
 // kernel counts each range's choices by expert; the second adds up what lies
 // before its range, counts its own range warp by warp and gives each choice
 // its place: places before the expert + before the range + before the warp +
-// in the warp.  No atomics, so the order is that of the choices.
+// in the warp.  Nothing there depends on which thread runs first, so the order is
+// that of the choices; only the ranges' counts are added up by atomics, and sums
+// of whole numbers are the same in any order.
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_ALONE = 4096;   // choices that one block sorts in one launch
 constexpr int SORT_RANGE = 1024;   // choices of a block, with more: one step of its 32 warps
