@@ -97,9 +97,6 @@ __device__ __forceinline__ float logistic(float x, float &pq) {
 }
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi): (1 + tanh u) / 2 = logistic(2 u)
 constexpr float kGeluB = 0.044715f;
-constexpr float kSqrtHalf = 0.70710678118654752f;
-constexpr float kSqrtHalfRest = static_cast<float>(0.70710678118654752440 - static_cast<double>(kSqrtHalf));
-constexpr float kInvSqrtPi = 0.5641895835477563f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
 // The normal distribution's upper tail at |z|, erfc(|z| / sqrt 2) / 2, and
@@ -123,16 +120,27 @@ __device__ __forceinline__ float normal_tail(float z, float &gauss) {
     return q * t * gauss;
 }
 
-// The normal distribution function of z and exp(-z^2 / 2), for FP32: erfc(-z / sqrt 2) / 2,
-// which keeps its relative accuracy where 1 + erf cancels (at z = -5 that is 4 % off), and
-// what the rounding of its argument h leaves, l, by the derivative (without it 180 x 2^-24
-// of the value at z = -12, with it 2 x 2^-24 beside erfcf's own error).  From |z| = 20 on
-// both ends are reached; cut there, infinities leave no inf - inf.
-__device__ __forceinline__ float normal_cdf(float z, float &gauss) {
-    const float c = fminf(fmaxf(z, -20.0f), 20.0f);
-    const float h = -c * kSqrtHalf, l = fmaf(-c, kSqrtHalf, -h) - c * kSqrtHalfRest;
-    gauss = expf(-0.5f * c * c);
-    return fmaf(-kInvSqrtPi * gauss, l, 0.5f * erfcf(h));
+// The same for FP32, with t = 1 / (1 + 0.4 |z|) (fit: 2e-8) and what rounding leaves of
+// z^2 / 2 and of t put back: 6.5 x 2^-24 of the tail and expf's error, where (1 + erf) / 2
+// cancels (at z = -5 it is 4 % off).  erfcf is as exact with the same correction and three
+// times as long (1000 x 1030 x 777 with gelu 28.8 us, with this @).  From |z| = 20 on the
+// tail is 0; cut there, an infinity leaves no inf - inf.
+__device__ __forceinline__ float normal_tail_f32(float z, float &gauss) {
+    const float a = fminf(fabsf(z), 20.0f), h = 0.5f * a * a, e = expf(-h);
+    gauss = fmaf(-e, fmaf(0.5f * a, a, -h), e);
+    const float d = fmaf(0.4f, a, 1.0f);
+    float t = fast_reciprocal(d);
+    t = fmaf(t, fmaf(-d, t, 1.0f), t);
+    float q = fmaf(t, 0.03242806717753410f, -0.17794845998287201f);
+    q = fmaf(t, q, 0.38489249348640442f);
+    q = fmaf(t, q, -0.37734243273735046f);
+    q = fmaf(t, q, 0.12209832668304443f);
+    q = fmaf(t, q, -0.02815046161413193f);
+    q = fmaf(t, q, 0.09175224602222443f);
+    q = fmaf(t, q, 0.13305851817131042f);
+    q = fmaf(t, q, 0.15963622927665710f);
+    q = fmaf(t, q, 0.15957549214363098f);
+    return q * t * gauss;
 }
 
 template <int ACT, bool EXACT>
@@ -141,8 +149,7 @@ __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == LINEAR_ACT_SILU) return z * logistic<EXACT>(z);
     if constexpr (ACT == LINEAR_ACT_GELU) {
         float gauss;
-        if constexpr (EXACT) return z * normal_cdf(z, gauss);
-        const float tail = fminf(z, 16.0f) * normal_tail(z, gauss);  // 0 from there on, and no inf * 0 at infinity
+        const float tail = fminf(z, 20.0f) * (EXACT ? normal_tail_f32(z, gauss) : normal_tail(z, gauss));  // no inf * 0 at infinity
         return z < 0.0f ? tail : z - tail;
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) return z * logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
@@ -159,11 +166,7 @@ __device__ __forceinline__ float slope(float z) {
     }
     if constexpr (ACT == LINEAR_ACT_GELU) {
         float gauss;
-        if constexpr (EXACT) {
-            const float cdf = normal_cdf(z, gauss);
-            return cdf + z * kInvSqrt2Pi * gauss;
-        }
-        const float tail = normal_tail(z, gauss);
+        const float tail = EXACT ? normal_tail_f32(z, gauss) : normal_tail(z, gauss);
         return (z < 0.0f ? tail : 1.0f - tail) + z * kInvSqrt2Pi * gauss;
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) {

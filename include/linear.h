@@ -17,14 +17,20 @@
  * Types: all tensors of a call have one type.  LINEAR_BF16 and LINEAR_F16
  * multiply exactly and add in FP32; everything up to the one rounding of y
  * (and of preact, where it is saved) is in FP32.  dz is rounded to the
- * tensors' type before the products that use it; dbias is summed in FP32
- * from the unrounded values.  LINEAR_F32 splits each operand into three bf16
- * pieces (x = x1 + x2 + x3 to 2^-27) and adds the six products that matter
- * (up to 4 tokens of linear_forward: it multiplies in FP32);
- * the tensor cores sum blocks of 128 K, which are added in FP32 with
- * round-to-nearest: the error is that of an FP32 product.  An infinity or a
- * NaN in an FP32 operand makes every element of the result that it enters
- * NaN or infinite.
+ * tensors' type before the products that use it (bf16: the root mean square
+ * error of dx and dw is 2.3e-3 of them instead of the 1.7e-3 that rounding
+ * them once leaves); dbias is summed in FP32 from the unrounded values.
+ * LINEAR_F32 splits each operand into three bf16 pieces and adds the six
+ * products that matter (up to 4 tokens of linear_forward: it multiplies in
+ * FP32).  x = x1 + x2 + x3 to 2^-27 of x, and to 2^-134 where |x| is below
+ * 2^-107, as the pieces have bf16's exponents; the products left out are
+ * 1.5 x 2^-24 of the full one at most, of either sign.  The tensor cores sum
+ * blocks of 128 K, which are added in FP32 with round-to-nearest.  In a block
+ * they cut what they add to 24 bits: the error of sums with terms of both
+ * signs is that of an FP32 product (4096^3, normal numbers: 3.4e-7 of the
+ * result's root mean square; added in FP32: 6.5e-7), sums of terms of one
+ * sign come out up to 5e-7 too small.  An infinity or a NaN in an FP32
+ * operand makes every element of the result that it enters NaN or infinite.
  *
  * All sums have a fixed order: a call gives the same bits every time.
  *
