@@ -122,25 +122,33 @@ __device__ __forceinline__ float normal_tail(float z, float &gauss) {
 
 // The same for FP32, with t = 1 / (1 + 0.4 |z|) (fit: 2e-8) and what rounding leaves of
 // z^2 / 2 and of t put back: 6.5 x 2^-24 of the tail and expf's error, where (1 + erf) / 2
-// cancels (at z = -5 it is 4 % off).  erfcf is as exact with the same correction and three
-// times as long (1000 x 1030 x 777 with gelu 28.8 us, with this 25.7).  From |z| = 20 on the
-// tail is 0; cut there, an infinity leaves no inf - inf.
+// cancels (at z = -5 it is 4 % off).  erfcf with the same correction is as exact and takes
+// longer (1000 x 1030 x 777 with gelu, one call among others: 28.8 us for 25.7).  From
+// |z| = 20 on the tail is 0; cut there, an infinity leaves no inf - inf.
 __device__ __forceinline__ float normal_tail_f32(float z, float &gauss) {
     const float a = fminf(fabsf(z), 20.0f), h = 0.5f * a * a, e = expf(-h);
     gauss = fmaf(-e, fmaf(0.5f * a, a, -h), e);
     const float d = fmaf(0.4f, a, 1.0f);
     float t = fast_reciprocal(d);
     t = fmaf(t, fmaf(-d, t, 1.0f), t);
-    float q = fmaf(t, 0.03242806717753410f, -0.17794845998287201f);
-    q = fmaf(t, q, 0.38489249348640442f);
-    q = fmaf(t, q, -0.37734243273735046f);
-    q = fmaf(t, q, 0.12209832668304443f);
-    q = fmaf(t, q, -0.02815046161413193f);
-    q = fmaf(t, q, 0.09175224602222443f);
-    q = fmaf(t, q, 0.13305851817131042f);
-    q = fmaf(t, q, 0.15963622927665710f);
-    q = fmaf(t, q, 0.15957549214363098f);
+    // by pairs of powers: the chain is what an epilogue with few warps waits for
+    const float t2 = t * t, t4 = t2 * t2;
+    const float p0 = fmaf(t, 0.15963622927665710f, 0.15957549214363098f), p2 = fmaf(t, 0.09175224602222443f, 0.13305851817131042f);
+    const float p4 = fmaf(t, 0.12209832668304443f, -0.02815046161413193f), p6 = fmaf(t, 0.38489249348640442f, -0.37734243273735046f);
+    const float p8 = fmaf(t, 0.03242806717753410f, -0.17794845998287201f);
+    const float q = fmaf(t4, fmaf(t4, p8, fmaf(t2, p6, p4)), fmaf(t2, p2, p0));
     return q * t * gauss;
+}
+
+// z Phi(z) from the tail; z - z tail would be a NaN at infinity.
+__device__ __forceinline__ float gelu_of(float z, float tail) { return z * (z < 0.0f ? tail : 1.0f - tail); }
+// A call of its own: the FP32 product's epilogue unrolls it 112 times beside as many
+// accumulators, and inlined it took registers and instruction fetches from the rest
+// (4096^3 573 us, as a call 510; with erff inlined 524, and 1000 x 1030 x 777 with the
+// saved argument 37.3, 33 and 35.7).
+static __device__ __noinline__ float gelu_f32(float z) {
+    float gauss;
+    return gelu_of(z, normal_tail_f32(z, gauss));
 }
 
 template <int ACT, bool EXACT>
@@ -148,9 +156,9 @@ __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == LINEAR_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
     if constexpr (ACT == LINEAR_ACT_SILU) return z * logistic<EXACT>(z);
     if constexpr (ACT == LINEAR_ACT_GELU) {
+        if constexpr (EXACT) return gelu_f32(z);
         float gauss;
-        const float tail = fminf(z, 20.0f) * (EXACT ? normal_tail_f32(z, gauss) : normal_tail(z, gauss));  // no inf * 0 at infinity
-        return z < 0.0f ? tail : z - tail;
+        return gelu_of(z, normal_tail(z, gauss));
     }
     if constexpr (ACT == LINEAR_ACT_GELU_TANH) return z * logistic<EXACT>(kGeluA * (z + kGeluB * z * z * z));
     return z;
