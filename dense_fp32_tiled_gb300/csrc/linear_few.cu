@@ -21,9 +21,9 @@
 // that each warp makes of its values in registers, so that the weight is read once
 // in FP32, where the product kernel's operand copies read 4 bytes of it and write
 // and read 6.  us, K contiguous, multiply-adds / product kernel / this:
-//   8 x 4096^2 24 / 54 / 17.6      16 x 4096^2 38 / 54 / 21   16 x 8192^2 107 / 180 / 67
-//   32 x 4096^2 - / 55 / 27        32 x 8192^2 - / 183 / 92   48 x 8192^2 - / 186 / 132
-//   64 x 4096^2 - / 57 / 49        64 x 8192^2 - / 186 / 172  64 x 1000 x 1024 - / 19 / 11
+//   8 x 4096^2 24 / 54 / 18.1      16 x 4096^2 38 / 54 / 22.8  16 x 8192^2 107 / 180 / 66.7
+//   32 x 4096^2 - / 55 / 27.5      32 x 8192^2 - / 183 / 92.3  48 x 8192^2 - / 186 / 128
+//   64 x 4096^2 - / 57 / 52.7      64 x 8192^2 - / 186 / 185   64 x 1000 x 1024 - / 19 / 10.5
 // mma.sync bounds it from about 16 tokens on (10 to 12 cycles a scheduler for each).
 #include "linear_few.cuh"
 
@@ -446,8 +446,9 @@ struct FewTile {
 // two values an instruction: x = a + b + c to 2^-27, and the products left out are
 // about 2^-24 of the full one at most, either way.  (Cut by masks, that is 2^-21, always
 // towards zero.  us, cut / rounded: K contiguous 16 x 8192^2 59 / 60, 32 x 8192^2 94 / 89,
-// 64 x 4096^2 46 / 47; features contiguous 63 / 70, 96 / 103, 48 / 45.)  The first piece stops at bf16's largest value where
-// rounding would overflow; an infinity passes into the second, and the third is a NaN.
+// 64 x 4096^2 46 / 47; features contiguous 63 / 70, 96 / 103, 48 / 45.)  The first piece
+// stops at bf16's largest value where rounding would overflow; an infinity passes into the
+// second, and the third is a NaN.
 __device__ __forceinline__ void pieces2(float x, float y, uint32_t (&r)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {

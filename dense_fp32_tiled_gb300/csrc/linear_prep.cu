@@ -101,6 +101,9 @@ cudaError_t copy_operands_t(const linear_prep::Copy *copies, int n, cudaStream_t
 }
 
 // ---- dz = dy * act'(z), and its column sums -------------------------------------------
+// dz of the 16-bit types is rounded to them, as a chain of 16-bit tensors would hold it:
+// dx and dw are then 2.35e-3 off in the root mean square in bf16, 2.9e-4 in float16
+// (rounded once 1.66e-3 and 2.1e-4).  A second piece of dz would take both products twice.
 // A block takes a chunk of rows of 32 * V columns; warp w its rows w, w + 8, ...
 // Rows of different experts are summed apart; the chunks' sums are added up
 // afterwards, in chunk order, so they do not depend on timing.
