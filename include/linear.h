@@ -26,10 +26,10 @@
  * 2^-107, as the pieces have bf16's exponents; the products left out are
  * 1.5 x 2^-24 of the full one at most, of either sign.  The tensor cores sum
  * blocks of 128 K, which are added in FP32 with round-to-nearest.  In a block
- * they cut what they add to 24 bits: the error of sums with terms of both
- * signs is that of an FP32 product (4096^3, normal numbers: 3.4e-7 of the
- * result's root mean square; added in FP32: 6.5e-7), sums of terms of one
- * sign come out up to 5e-7 too small.  An infinity or a NaN in an FP32
+ * they cut what they add to 24 bits: of normal numbers the error's root mean
+ * square is 3e-7 to 6e-7 of the result's at any K (added in FP32: 1e-7 at a
+ * K of some hundred, 6.5e-7 at 4096^3), and sums of terms of one sign come
+ * out up to 5e-7 too small.  An infinity or a NaN in an FP32
  * operand makes every element of the result that it enters NaN or infinite.
  *
  * All sums have a fixed order: a call gives the same bits every time.
