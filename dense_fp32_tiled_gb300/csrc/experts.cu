@@ -12,12 +12,12 @@
 #include "experts.h"
 #include "linear_types.cuh"
 #include "nvtx_range.cuh"
+#include "rows.cuh"
 #include "tensor_core.cuh"
 
 namespace {
 
-using lt::from_f;
-using lt::to_f;
+using namespace rows;
 
 // ---- sort ------------------------------------------------------------------------
 // Choices are cut into `blocks` equal ranges.  With more than one, a first
@@ -174,91 +174,6 @@ sort_place_kernel(const I *__restrict__ choices, long long R, int E, int range, 
 }
 
 // ---- rows --------------------------------------------------------------------------
-// V values (16, 8, 4 or 2 bytes) of a row, as the word they travel in: a load
-// that may not happen is then one predicated instruction, and the next ones
-// follow it at once.
-template <int BYTES>
-struct Word;
-template <>
-struct Word<16> {
-    using type = uint4;
-};
-template <>
-struct Word<8> {
-    using type = uint2;
-};
-template <>
-struct Word<4> {
-    using type = uint32_t;
-};
-template <>
-struct Word<2> {
-    using type = uint16_t;
-};
-template <typename T, int V>
-struct Pack {
-    static constexpr int BYTES = V * static_cast<int>(sizeof(T));
-    using Raw = typename Word<BYTES>::type;
-    Raw raw;
-    __device__ __forceinline__ void clear() { raw = Raw{}; }
-    __device__ __forceinline__ uint32_t word(int i) const {
-        if constexpr (BYTES == 16) return i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
-        if constexpr (BYTES == 8) return i == 0 ? raw.x : raw.y;
-        if constexpr (BYTES <= 4) return raw;
-    }
-    __device__ __forceinline__ void get(float (&f)[V]) const {
-        if constexpr (BYTES == 2) {
-            f[0] = to_f(*reinterpret_cast<const T *>(&raw));
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(word(i));
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float2 v = lt::unpack2<T>(word(i));
-                f[2 * i] = v.x;
-                f[2 * i + 1] = v.y;
-            }
-        }
-    }
-    __device__ __forceinline__ void set(const float (&f)[V]) {
-        if constexpr (BYTES == 2) {
-            const T v = from_f<T>(f[0]);
-            raw = *reinterpret_cast<const Raw *>(&v);
-        } else {
-            uint32_t w[BYTES / 4];
-#pragma unroll
-            for (int i = 0; i < BYTES / 4; ++i) {
-                if constexpr (sizeof(T) == 4)
-                    w[i] = __float_as_uint(f[i]);
-                else
-                    w[i] = lt::pack2<T>(f[2 * i], f[2 * i + 1]);
-            }
-            if constexpr (BYTES == 16) raw = make_uint4(w[0], w[1], w[2], w[3]);
-            if constexpr (BYTES == 8) raw = make_uint2(w[0], w[1]);
-            if constexpr (BYTES == 4) raw = w[0];
-        }
-    }
-};
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load(const T *p) {
-    Pack<T, V> v;
-    v.raw = *reinterpret_cast<const typename Pack<T, V>::Raw *>(p);
-    return v;
-}
-// The values at p, or zeros.
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_if(bool in, const T *p) {
-    Pack<T, V> v;
-    v.clear();
-    if (in) v.raw = *reinterpret_cast<const typename Pack<T, V>::Raw *>(p);
-    return v;
-}
-template <typename T, int V>
-__device__ __forceinline__ void store(T *p, const Pack<T, V> &v) {
-    *reinterpret_cast<typename Pack<T, V>::Raw *>(p) = v.raw;
-}
-
 constexpr int ROW_THREADS = 256;
 constexpr int ZERO_BLOCKS = 64;  // blocks that clear the places in no use
 
@@ -421,50 +336,12 @@ combine_backward_kernel(int T_, int J, int packs, int E, const int *__restrict__
 }
 
 // ---- host ----------------------------------------------------------------------------
-struct Span {
-    uintptr_t lo = 0, hi = 0;
-};
-Span span(const void *p, long long rows, long long width, long long ld, long long bytes) {
-    Span s;
-    if (p == nullptr || rows <= 0 || width <= 0) return s;
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + static_cast<uintptr_t>(((rows - 1) * ld + width) * bytes);
-    return s;
-}
-bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
-bool misaligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
-
 int check_sizes(int type, int T, int J, int H, long long E) {
     if (type < LINEAR_F32 || type > LINEAR_F16) return SGEMM_ERR_INVALID_ARG;
     if (T < 0 || J < 0 || H < 0 || E < 0 || E > LINEAR_MAX_EXPERTS || J > EXPERTS_MAX_CHOICES ||
         static_cast<long long>(T) * J > INT_MAX)
         return SGEMM_ERR_INVALID_DIM;
     return SGEMM_OK;
-}
-// The widest access (16, 8, 4 or 2 bytes) that rows of this address and stride allow.
-int width_of(const void *p, long long ld, int type) {
-    if (p == nullptr) return 16;
-    const unsigned long long bits = reinterpret_cast<uintptr_t>(p) | static_cast<unsigned long long>(ld) * lt::type_bytes(type) | 16;
-    return static_cast<int>(bits & (0 - bits));
-}
-int narrower(int a, int b) { return a < b ? a : b; }
-int launched(cudaError_t err) {
-    if (err == cudaSuccess) return SGEMM_OK;
-    (void)cudaGetLastError();
-    return SGEMM_ERR_LAUNCH;
-}
-// f(element, values per access) for the type and the bytes of an access.
-template <typename F>
-int with_rows(int type, int bytes, F &&f) {
-    if (type == LINEAR_F32)
-        return bytes == 16 ? f(float(), lt::Int<4>{}) : bytes == 8 ? f(float(), lt::Int<2>{}) : f(float(), lt::Int<1>{});
-    auto half = [&](auto el) {
-        return bytes == 16  ? f(el, lt::Int<8>{})
-               : bytes == 8 ? f(el, lt::Int<4>{})
-               : bytes == 4 ? f(el, lt::Int<2>{})
-                            : f(el, lt::Int<1>{});
-    };
-    return type == LINEAR_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
 int segments_of(int packs, int bytes) {
     const int seg = 32 * seg_of(bytes);
