@@ -22,11 +22,15 @@ from ._binding import (SGEMM_OK, WAIT_SELFTESTS, SgemmError, bank_pattern_probe,
                        tc_timeouts, tc_workspace_size, transpose, transpose_f32, transpose_smem_request,
                        transpose_status_string, wait_selftest, workspace_size, workspace_size_for,
                        ws_schedule)
-from ._layers import (ACTIVATIONS, expert_combine, expert_combine_backward, expert_gather, expert_gather_backward,
-                      expert_linear, expert_linear_backward, expert_sort, linear, linear_backward, linear_timeouts)
+from ._layers import (ACTIVATIONS, SCORINGS, expert_choose, expert_choose_backward, expert_combine,
+                      expert_combine_backward, expert_gather, expert_gather_backward, expert_linear,
+                      expert_linear_backward, expert_sort, layer_norm, layer_norm_backward, linear, linear_backward,
+                      linear_cross_entropy, linear_cross_entropy_backward, linear_timeouts)
 
-__all__ = ["ACTIVATIONS", "expert_combine", "expert_combine_backward", "expert_gather", "expert_gather_backward",
-           "expert_linear", "expert_linear_backward", "expert_sort", "linear", "linear_backward", "linear_timeouts",
+__all__ = ["ACTIVATIONS", "SCORINGS", "expert_choose", "expert_choose_backward", "layer_norm", "layer_norm_backward",
+           "expert_combine", "expert_combine_backward", "expert_gather", "expert_gather_backward",
+           "expert_linear", "expert_linear_backward", "expert_sort", "linear", "linear_backward", "linear_cross_entropy",
+           "linear_cross_entropy_backward", "linear_timeouts",
            "SGEMM_OK", "WAIT_SELFTESTS", "SgemmError", "bank_pattern_probe", "bank_stride_probe", "copy_timeouts", "declared_functions", "host_workspace_size",
            "load_library", "sgemm", "sgemm_f32", "sgemm_f32_3xtf32", "sgemm_f32_host", "sgemm_host",
            "sgemm_tc", "tc_timeouts", "tc_workspace_size",

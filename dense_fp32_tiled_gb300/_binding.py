@@ -16,7 +16,9 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "sgemm_f32.h")
 HEADER_PATHS = [HEADER_PATH, os.path.join(os.path.dirname(_PKG), "include", "transpose_f32.h"),
                 os.path.join(os.path.dirname(_PKG), "include", "smem_bank_probe.h"),
                 os.path.join(os.path.dirname(_PKG), "include", "linear.h"),
-                os.path.join(os.path.dirname(_PKG), "include", "experts.h")]
+                os.path.join(os.path.dirname(_PKG), "include", "experts.h"),
+                os.path.join(os.path.dirname(_PKG), "include", "norm.h"),
+                os.path.join(os.path.dirname(_PKG), "include", "cross_entropy.h")]
 
 SGEMM_OK = 0
 _lib = None
@@ -109,8 +111,29 @@ def load_library():
     lib.expert_gather.argtypes = [i32, i32, i32, i32, i32, p, p, p, i64, p, i64, p]
     lib.expert_combine.argtypes = [i32, i32, i32, i32, p, p, p, i64, p, i64, p, i64, p]
     lib.expert_combine_backward.argtypes = [i32, i32, i32, i32, i32, p, p, p, p, i64, p, i64, p, i64, p, p]
+    f32 = ctypes.c_float
+    # type, sizes; logits; bias; scoring; groups; renormalize; scale; chosen; weights; stream
+    lib.expert_choose.argtypes = [i32, i32, i32, i32, p, i64, p, i32, i32, i32, i32, i32, f32, p, p, p]
+    lib.expert_choose_backward.argtypes = [i32, i32, i32, i32, p, p, p, i64, i32, i32, f32, p, i64, p]
+    # type, sizes; x; weight; bias; eps; statistics; y; stream
+    lib.layer_norm_forward.argtypes = [i32, i32, i32, p, i64, p, p, f32, p, p, i64, p]
+    # type, sizes; dy; x; weight; statistics; dx; dweight; dbias; workspace; stream
+    lib.layer_norm_backward.argtypes = [i32, i32, i32, p, i64, p, i64, p, p, p, i64, p, p, p, size, p]
+    lib.layer_norm_backward_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.layer_norm_backward_workspace_size.restype = size
+    # type, sizes; x; w; targets; loss; lse; workspace; stream
+    lib.linear_cross_entropy_forward.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32, p, i32, p, p, p, size, p]
+    lib.linear_cross_entropy_forward_workspace_size.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32]
+    # type, sizes; dloss; dlse; x; w; targets; lse; dx; dw; workspace; stream
+    lib.linear_cross_entropy_backward.argtypes = [i32, i32, i32, i32, p, p, p, i64, p, i64, i32, p, i32, p, p, i64, p, i64, p,
+                                                  size, p]
+    lib.linear_cross_entropy_backward_workspace_size.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32, i32, i32]
+    for name in ("linear_cross_entropy_forward", "linear_cross_entropy_backward"):
+        getattr(lib, name).restype = i32
+        getattr(lib, name + "_workspace_size").restype = size
     for name in ("linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward",
-                 "linear_timeouts", "expert_sort", "expert_gather", "expert_combine", "expert_combine_backward"):
+                 "linear_timeouts", "expert_sort", "expert_gather", "expert_combine", "expert_combine_backward",
+                 "expert_choose", "expert_choose_backward", "layer_norm_forward", "layer_norm_backward"):
         getattr(lib, name).restype = i32
     for name in ("linear_forward", "linear_backward", "expert_linear_forward", "expert_linear_backward", "expert_sort"):
         getattr(lib, name + "_workspace_size").restype = size
@@ -124,7 +147,7 @@ def declared_functions() -> list[str]:
     for path in HEADER_PATHS:
         with open(path) as f:
             text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
-        names |= set(re.findall(r"\b((?:sgemm|transpose)_f32\w*|smem_bank_\w+|linear_\w+|expert_\w+)\s*\(", text))
+        names |= set(re.findall(r"\b((?:sgemm|transpose)_f32\w*|smem_bank_\w+|linear_\w+|expert_\w+|layer_norm_\w+)\s*\(", text))
     return sorted(names)
 
 

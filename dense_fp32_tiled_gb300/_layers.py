@@ -1,5 +1,6 @@
-"""Layer operators on torch tensors: argument marshalling for include/linear.h
-and include/experts.h.  As in ``_binding``, every arithmetic step runs in the
+"""Layer operators on torch tensors: argument marshalling for include/linear.h,
+include/experts.h, include/norm.h and
+include/cross_entropy.h.  As in ``_binding``, every arithmetic step runs in the
 CUDA library; PyTorch supplies device memory, strides and the current stream.
 
 Every function runs on ``stream`` (a torch.cuda.Stream) or the current one, is
@@ -16,6 +17,7 @@ from contextlib import nullcontext
 from ._binding import SGEMM_OK, SgemmError, load_library
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORINGS = {"softmax": 0, "sigmoid": 1}
 
 # What these calls launch is short (a decoding step's product takes a few
 # microseconds), so calls on the current device and stream whose arguments are
@@ -321,7 +323,208 @@ def linear_timeouts() -> int:
     return n.value
 
 
+# ---- the loss of a head ----------------------------------------------------------
+def _integers(t, shape, device, name):
+    """(address, bytes of a value) of a contiguous int32 or int64 tensor."""
+    dtype = getattr(t, "dtype", None)
+    if (dtype is not torch.int32 and dtype is not torch.int64) or t.get_device() != device:
+        raise TypeError(f"{name} must be an int32 or int64 tensor on cuda:{device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr(), 4 if dtype is torch.int32 else 8
+
+
+def _head(x, w, targets):
+    kind = _type_of(x, "x")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x and w must be 2-D, got {tuple(x.shape)} and {tuple(w.shape)}")
+    (M, K), dtype, dev = x.shape, x.dtype, x.get_device()
+    xp, ldx = _rows(x, M, K, dtype, dev, "x")
+    wp, ldw, order, _ = _weight(w, K, dtype, dev, "w")
+    N = w.shape[1]
+    _fits(M, N, K)
+    tp, width = _integers(targets, (M,), dev, "targets")
+    return kind, M, N, K, xp, ldx, wp, ldw, order, tp, width
+
+
+def linear_cross_entropy(x, w, targets, stream=None):
+    """(loss, lse): each row's -log softmax(x @ w)[target] and log of its sum of
+    exponentials, float32 (M,), without x @ w in memory.
+
+    x is (M, K), row-major with any row stride; w is (K, N) in either memory
+    order; targets is int32 or int64 (M,).  A target outside 0 .. N - 1 (a
+    padded token's -100) gives a loss of 0.
+    """
+    lib = _lib or _load()
+    kind, M, N, K, xp, ldx, wp, ldw, order, tp, width = _head(x, w, targets)
+    with _on(x.get_device(), stream):
+        loss = torch.empty((M,), dtype=torch.float32, device=x.device)
+        lse = torch.empty((M,), dtype=torch.float32, device=x.device)
+        nbytes = lib.linear_cross_entropy_forward_workspace_size(kind, M, N, K, xp, ldx, wp, ldw, order)
+        ws = _scratch(nbytes, x.device)
+        st = lib.linear_cross_entropy_forward(kind, M, N, K, xp, ldx, wp, ldw, order, tp, width, loss.data_ptr(),
+                                              lse.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
+                                              _raw_stream(x.get_device()))
+    if st:
+        _check(st, "linear_cross_entropy_forward")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, dlse=None, need_dx=True, need_dw=True, stream=None):
+    """(dx, dw) of linear_cross_entropy for the gradients of its losses and (dlse,
+    None for none) of its log sums, float32 (M,); lse is what it returned.  dw
+    has the memory order of w; what is not needed is None."""
+    lib = _lib or _load()
+    kind, M, N, K, xp, ldx, wp, ldw, order, tp, width = _head(x, w, targets)
+    dev = x.get_device()
+    if lse is None:
+        raise ValueError("lse is needed (linear_cross_entropy returns it)")
+    gp, ep = _vector(dloss, (M,), torch.float32, dev, "dloss"), _vector(dlse, (M,), torch.float32, dev, "dlse")
+    lp = _vector(lse, (M,), torch.float32, dev, "lse")
+    dx = dw = hp = vp = None
+    with _on(dev, stream):
+        if need_dx:
+            dx = torch.empty((M, K), dtype=x.dtype, device=x.device)
+            hp = dx.data_ptr()
+        if need_dw:
+            dw = torch.empty((N, K) if order else (K, N), dtype=x.dtype, device=x.device)
+            vp = dw.data_ptr()
+            if order:
+                dw = dw.transpose(0, 1)
+        nbytes = lib.linear_cross_entropy_backward_workspace_size(kind, M, N, K, xp, ldx, wp, ldw, order, bool(need_dx), bool(need_dw))
+        ws = _scratch(nbytes, x.device)
+        st = lib.linear_cross_entropy_backward(kind, M, N, K, gp, ep, xp, ldx, wp, ldw, order, tp, width, lp, hp, K or 1, vp,
+                                               (K if order else N) or 1, ws.data_ptr() if nbytes else None, nbytes,
+                                               _raw_stream(dev))
+    if st:
+        _check(st, "linear_cross_entropy_backward")
+    return dx, dw
+
+
+# ---- layer norm ------------------------------------------------------------------
+def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=None, out=None, stream=None):
+    """(x - mean) / sqrt(variance + eps) * weight + bias over the rows of x.
+
+    x is (M, N), row-major with any row stride; weight and bias are (N,), None
+    for 1 and 0; out is (M, N).  ``stats``, a float32 (M, 2) tensor, receives
+    each row's mean and 1 / sqrt(variance + eps) for layer_norm_backward.
+    """
+    lib = _lib or _load()
+    kind = _type_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    (M, N), dtype, dev = x.shape, x.dtype, x.get_device()
+    _fits(M, N)
+    xp, ldx = _rows(x, M, N, dtype, dev, "x")
+    wp, bp = _vector(weight, (N,), dtype, dev, "weight"), _vector(bias, (N,), dtype, dev, "bias")
+    sp = _vector(stats, (M, 2), torch.float32, dev, "stats")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=x.device)
+        yp, ldy = _rows(out, M, N, dtype, dev, "out")
+        st = lib.layer_norm_forward(kind, M, N, xp, ldx, wp, bp, eps, sp, yp, ldy, _raw_stream(dev))
+    if st:
+        _check(st, "layer_norm_forward")
+    return out
+
+
+def layer_norm_backward(dy, x, weight, stats, need_dx=True, need_dweight=True, need_dbias=True, stream=None):
+    """(dx, dweight, dbias) of layer_norm for the gradient dy of its result.
+    stats is what layer_norm saved; weight may be None (all 1).  What is not
+    needed is None."""
+    lib = _lib or _load()
+    kind = _type_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    (M, N), dtype, dev = x.shape, x.dtype, x.get_device()
+    _fits(M, N)
+    gp, lddy = _rows(dy, M, N, dtype, dev, "dy")
+    xp, ldx = _rows(x, M, N, dtype, dev, "x")
+    wp = _vector(weight, (N,), dtype, dev, "weight")
+    if stats is None:
+        raise ValueError("stats are needed (layer_norm saves them)")
+    sp = _vector(stats, (M, 2), torch.float32, dev, "stats")
+    dx = dweight = dbias = None
+    with _on(dev, stream):
+        if need_dx:
+            dx = torch.empty((M, N), dtype=dtype, device=x.device)
+        if need_dweight:
+            dweight = torch.empty((N,), dtype=dtype, device=x.device)
+        if need_dbias:
+            dbias = torch.empty((N,), dtype=dtype, device=x.device)
+        nbytes = lib.layer_norm_backward_workspace_size(M, N, bool(need_dweight), bool(need_dbias))
+        ws = _scratch(nbytes, x.device)
+        st = lib.layer_norm_backward(kind, M, N, gp, lddy, xp, ldx, wp, sp, dx.data_ptr() if need_dx else None, N or 1,
+                                     dweight.data_ptr() if need_dweight else None, dbias.data_ptr() if need_dbias else None,
+                                     ws.data_ptr() if nbytes else None, nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "layer_norm_backward")
+    return dx, dweight, dbias
+
+
 # ---- tokens to their experts and back --------------------------------------------
+def _scoring(name):
+    scoring = SCORINGS.get(name)
+    if scoring is None:
+        raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}, got {name!r}")
+    return scoring
+
+
+def expert_choose(logits, choices, bias=None, scoring="softmax", groups=1, kept_groups=1, group_top=1, renormalize=True,
+                  scale=1.0, stream=None):
+    """(chosen, weights): each token's experts from a router's logits (T, E), for
+    expert_sort and expert_combine.
+
+    Scores are softmax or sigmoid of the logits.  The ``choices`` experts with
+    the largest score + bias (bias: float32 (E,) or None) are chosen, in falling
+    order, of equal ones the lowest; with ``groups`` > 1 only those of the
+    ``kept_groups`` groups (of E / groups experts in a row) whose ``group_top``
+    (1 or 2) best have the largest sum.  chosen is int32 (T, choices); weights,
+    float32, are scale times the chosen scores, divided by their sum if
+    ``renormalize``.  Experts with a logit of -inf are never chosen; places left
+    over are -1 (which expert_sort drops), their weights 0.
+    """
+    lib = _lib or _load()
+    kind, how = _type_of(logits, "logits"), _scoring(scoring)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D, got {tuple(logits.shape)}")
+    (T, E), J, dtype, dev = logits.shape, int(choices), logits.dtype, logits.get_device()
+    _fits(T, E, J, groups, kept_groups, group_top)
+    lp, ldl = _rows(logits, T, E, dtype, dev, "logits")
+    bp = _vector(bias, (E,), torch.float32, dev, "bias")
+    with _on(dev, stream):
+        chosen = torch.empty((T, max(J, 0)), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, max(J, 0)), dtype=torch.float32, device=logits.device)
+        st = lib.expert_choose(kind, T, E, J, lp, ldl, bp, how, groups, kept_groups, group_top, bool(renormalize), scale,
+                               chosen.data_ptr(), weights.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "expert_choose")
+    return chosen, weights
+
+
+def expert_choose_backward(dweights, logits, chosen, scoring="softmax", renormalize=True, scale=1.0, stream=None):
+    """The gradient of the logits, in their type, from that of expert_choose's
+    weights; chosen, scoring, renormalize and scale as there (the bias has none)."""
+    lib = _lib or _load()
+    kind, how = _type_of(logits, "logits"), _scoring(scoring)
+    if logits.dim() != 2 or getattr(chosen, "ndim", 2) != 2:
+        raise ValueError(f"logits and chosen must be 2-D, got {tuple(logits.shape)} and {tuple(chosen.shape)}")
+    (T, E), J, dtype, dev = logits.shape, chosen.shape[1], logits.dtype, logits.get_device()
+    _fits(T, E, J)
+    lp, ldl = _rows(logits, T, E, dtype, dev, "logits")
+    cp = _int32(chosen, (T, J), dev, "chosen")
+    if dweights is None:
+        raise ValueError("dweights are needed")
+    gp = _vector(dweights, (T, J), torch.float32, dev, "dweights")
+    with _on(dev, stream):
+        dlogits = torch.empty((T, E), dtype=dtype, device=logits.device)
+        st = lib.expert_choose_backward(kind, T, E, J, gp, cp, lp, ldl, how, bool(renormalize), scale, dlogits.data_ptr(),
+                                        E or 1, _raw_stream(dev))
+    if st:
+        _check(st, "expert_choose_backward")
+    return dlogits
+
+
 def expert_sort(choices, experts, stream=None):
     """(rows, offsets): choices is int32 or int64 (T, J), the experts of each
     token (one outside 0 .. experts - 1 is dropped).  rows, int32 (T, J), is

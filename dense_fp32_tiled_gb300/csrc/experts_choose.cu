@@ -1,0 +1,538 @@
+// experts_choose.cu -- a router's choice of each token's experts, and its
+// gradient (C ABI: include/experts.h).
+//
+// A warp takes a token; lane l holds the logits of experts l, l + 32, ...  The
+// J best are picked one after the other: each lane keeps its own best, one
+// warp maximum finds the value, one minimum the lowest expert that has it, and
+// the lane that lost its best looks for the next.  Values are compared as whole
+// numbers of the same order as the floats (0: not to be chosen), so a maximum
+// is one instruction.
+//
+// What is compared.  Scores are increasing in the logits, so without a bias the
+// logits themselves are: no rounding enters.  With a bias (and for the sums of a
+// group's best two) the order is that of the scores in 64 bits.  A warp computes
+// them in 32 with a known bound on the error, and where two values that have to
+// be told apart are closer than that, once more in 64: some tokens in a thousand
+// (all of them in 64 bits: 4 million exponentials at GB300's FP64 rate would take 0.3 ms).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "experts.h"
+#include "linear_types.cuh"
+#include "nvtx_range.cuh"
+#include "rows.cuh"
+#include "tensor_core.cuh"
+
+namespace {
+
+using namespace rows;
+
+constexpr int CHOOSE_WARPS = 4;
+constexpr unsigned ALL = 0xffffffffu;
+
+struct Choose {
+    const void *logits;
+    long long ld;
+    const float *bias;
+    int *chosen;
+    float *weights;
+    int T, E, J, scoring, groups, kept, top, size;  // size: experts of a group
+    unsigned per;                                   // e * per >> 20 = e / size
+    int renormalize;
+    float scale;
+};
+
+// Floats as unsigned numbers of the same order; -0 is taken for 0.
+__device__ __forceinline__ uint32_t rank_of(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_rank(uint32_t r) { return __uint_as_float(r >> 31 ? r & 0x7fffffffu : ~r); }
+__device__ __forceinline__ unsigned long long rank_of(double v) {
+    const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double of_rank(unsigned long long r) {
+    return __longlong_as_double(static_cast<long long>(r >> 63 ? r & 0x7fffffffffffffffull : ~r));
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(ALL, v); }
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(ALL, v, k);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(ALL, v, k);
+    return v;
+}
+__device__ __forceinline__ float warp_max_f(float v) {
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, k));
+    return v;
+}
+// logistic(l), small ones included
+__device__ __forceinline__ float sigmoid(float l) {
+    const float e = expf(-fabsf(l));
+    return l < 0.0f ? e / (1.0f + e) : 1.0f / (1.0f + e);
+}
+__device__ __forceinline__ double sigmoid(double l) {
+    const double e = exp(-fabs(l));
+    return l < 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);
+}
+template <typename T>
+__device__ __forceinline__ float logit(const Choose &c, const T *row, int e) {
+    return to_f(row[e]);
+}
+
+// The sum of the two largest of a warp's values (ranks; each lane gives its own best two; 0: none).
+template <typename R, typename F>
+__device__ __forceinline__ F best_two(R first, R second, bool two, R *any) {
+    const R high = warp_max(first);
+    *any = high;
+    if (high == 0) return 0;
+    F sum = of_rank(high);
+    if (two) {
+        const int owner = __ffs(__ballot_sync(ALL, first == high)) - 1;
+        const R next = warp_max(static_cast<int>(threadIdx.x & 31) == owner ? second : first);
+        if (next != 0) sum += of_rank(next);
+    }
+    return sum;
+}
+
+// Everything of the choice in 64 bits, for a token whose values are too close
+// for 32.  `held` is the warp's room for E ranks.  Returns this lane's picks
+// (pick j at lane j % 32, in mine[j / 32]).
+template <typename T>
+__device__ __noinline__ void choose_in_64(const Choose &c, const T *row, unsigned long long *held, int lane, int (&mine)[2]) {
+    mine[0] = mine[1] = -1;
+    double m = -INFINITY, z = 0.0;
+    if (c.scoring == EXPERTS_SOFTMAX) {
+        for (int e = lane; e < c.E; e += 32) m = fmax(m, static_cast<double>(logit(c, row, e)));
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmax(m, __shfl_xor_sync(ALL, m, k));
+        for (int e = lane; e < c.E; e += 32) z += exp(static_cast<double>(logit(c, row, e)) - m);
+        z = warp_sum(z);
+    }
+    for (int e = lane; e < c.E; e += 32) {
+        const float l = logit(c, row, e);
+        double v = c.scoring == EXPERTS_SOFTMAX ? exp(l - m) / z : sigmoid(static_cast<double>(l));
+        bool in = l > -INFINITY;
+        if (c.bias != nullptr) {
+            v += static_cast<double>(c.bias[e]);
+            in = in && v > -INFINITY;
+        }
+        held[e] = in ? rank_of(v) : 0ull;
+    }
+    __syncwarp();
+    if (c.groups > 1) {
+        unsigned long long total = 0;  // lane g: of group g
+        for (int g = 0; g < c.groups; ++g) {
+            unsigned long long first = 0, second = 0, any;
+            for (int i = lane; i < c.size; i += 32) {
+                const unsigned long long r = held[g * c.size + i];
+                second = r > first ? first : r > second ? r : second;
+                first = r > first ? r : first;
+            }
+            const double sum = best_two<unsigned long long, double>(first, second, c.top > 1, &any);
+            if (lane == g && any != 0) total = rank_of(sum);
+        }
+        int before = 0;
+        for (int g = 0; g < c.groups; ++g) {
+            const unsigned long long o = __shfl_sync(ALL, total, g);
+            before += o > total || (o == total && g < lane) ? 1 : 0;
+        }
+        const unsigned keep = __ballot_sync(ALL, lane < c.groups && before < c.kept && total != 0);
+        for (int e = lane; e < c.E; e += 32)
+            if ((keep >> (e * c.per >> 20) & 1) == 0) held[e] = 0;
+    }
+    if (c.bias == nullptr)
+        for (int e = lane; e < c.E; e += 32)
+            if (held[e] != 0) held[e] = rank_of(static_cast<double>(logit(c, row, e)));
+    __syncwarp();
+    for (int j = 0; j < c.J; ++j) {
+        unsigned long long best = 0;
+        int at = INT_MAX;
+        for (int e = lane; e < c.E; e += 32)
+            if (held[e] > best) {
+                best = held[e];
+                at = e;
+            }
+        const unsigned long long high = warp_max(best);
+        if (high == 0) break;
+        const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
+        if (who == at) held[at] = 0;
+        if ((j & 31) == lane) mine[j >> 5] = who;
+        __syncwarp();
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_constant__ Choose c) {
+    extern __shared__ unsigned long long held[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * CHOOSE_WARPS + warp;
+    tc::grid_trigger();
+    tc::grid_wait();
+    if (t >= c.T) return;
+    const T *row = static_cast<const T *>(c.logits) + t * c.ld;
+    const bool softmax = c.scoring == EXPERTS_SOFTMAX;
+    float l[NV];
+    float m = -INFINITY;
+    bool wrong = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = i * 32 + lane;
+        l[i] = e < c.E ? logit(c, row, e) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        wrong = wrong || l[i] != l[i];
+        m = fmaxf(m, l[i]);
+    }
+    m = warp_max_f(m);
+    wrong = __any_sync(ALL, wrong) || (softmax && m == INFINITY);
+    const bool summed = c.groups > 1 && c.top > 1;   // groups by sums of scores
+    float z = 1.0f;
+    if (softmax && (c.bias != nullptr || !c.renormalize || summed) && m > -INFINITY) {
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) z += expf(l[i] - m);
+        z = warp_sum(z);
+    }
+    // How far the difference of two scores may be off.  expf is within 4 units of 2^-24 of its value, sums
+    // and quotients within 1.  Sigmoid: 4 units a score.  Softmax, of the largest score 1 / z: 4 of its own
+    // exponential, less than 1 of the rounding of l - m (x exp(-x) < 0.4), and those of z: 36 of up to 31
+    // sums in a lane and 5 across, 11 of the exponentials (4, and the rounding of l - m at a mean of
+    // up to log 1024); 2 of quotient and product.
+    const float most = softmax ? 1.0f / z : 1.0f;
+    const float slack = softmax ? most * 0x1p-17f : 0x1p-21f;
+    auto value = [&](int i) {
+        const float s = softmax ? expf(l[i] - m) * most : sigmoid(l[i]);
+        return c.bias != nullptr && i * 32 + lane < c.E ? s + c.bias[i * 32 + lane] : s;
+    };
+    uint32_t key[NV];
+    float size = 1.0f;  // of what groups' sums add up
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        key[i] = 0;
+        if (l[i] > -INFINITY && !wrong) {
+            const float v = c.bias != nullptr ? value(i) : l[i];
+            if (v > -INFINITY) {
+                key[i] = rank_of(v);
+                if (c.bias != nullptr) size = fmaxf(size, fabsf(v));
+            }
+        }
+    }
+    bool doubt = false;
+    if (c.groups > 1) {
+        uint32_t total = 0;
+        for (int g = 0; g < c.groups; ++g) {
+            uint32_t first = 0, second = 0, any;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = i * 32 + lane;
+                if ((e * c.per >> 20) == static_cast<unsigned>(g) && key[i] != 0) {
+                    const uint32_t r = summed && c.bias == nullptr ? rank_of(value(i)) : key[i];
+                    second = r > first ? first : r > second ? r : second;
+                    first = r > first ? r : first;
+                }
+            }
+            const float sum = best_two<uint32_t, float>(first, second, c.top > 1, &any);
+            if (lane == g && any != 0) total = rank_of(sum);
+        }
+        int before = 0;
+        for (int g = 0; g < c.groups; ++g) {
+            const uint32_t o = __shfl_sync(ALL, total, g);
+            before += o > total || (o == total && g < lane) ? 1 : 0;
+        }
+        const bool stays = lane < c.groups && before < c.kept && total != 0;
+        const unsigned keep = __ballot_sync(ALL, stays);
+        if (summed || c.bias != nullptr) {
+            const uint32_t low = __reduce_min_sync(ALL, stays ? total : 0xffffffffu);
+            size = warp_max_f(size);
+            const uint32_t out = warp_max(lane < c.groups && !stays ? total : 0u);
+            if (out != 0) {
+                const float a = of_rank(low), b = of_rank(out);
+                doubt = !(a - b >= 2.0f * slack + 0x1p-21f * size);  // 4 scores; 4 sums with biases, 2 of two values
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((keep >> ((i * 32 + lane) * c.per >> 20 & 31) & 1) == 0) key[i] = 0;
+    }
+    int mine[2] = {-1, -1};
+    uint32_t best = 0;
+    int at = INT_MAX;
+    auto look = [&] {
+        best = 0;
+        at = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i * 32 + lane;
+            }
+    };
+    look();
+    float last = 0.0f;
+    int last_who = -1;
+    const int rounds = c.bias != nullptr ? c.J + 1 : c.J;  // one more: the best that is left out
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t high = warp_max(best);
+        if (high == 0) break;
+        const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
+        if (c.bias != nullptr) {
+            const float v = of_rank(high);
+            // values of equal logits and biases are equal in 64 bits too
+            if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)) &&  // 2 scores, 2 sums with the bias
+                !(logit(c, row, who) == logit(c, row, last_who) && c.bias[who] == c.bias[last_who]))
+                doubt = true;
+            last = v;
+            last_who = who;
+        }
+        if (j < c.J && (j & 31) == lane) mine[j >> 5] = who;
+        if (who == at) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i * 32 + lane == who) key[i] = 0;
+            look();
+        }
+    }
+    if (doubt) choose_in_64(c, row, held + static_cast<size_t>(warp) * c.E, lane, mine);
+
+    // weights of the picks
+    float lj[2], w[2];
+    float high = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        lj[s] = mine[s] >= 0 ? logit(c, row, mine[s]) : -INFINITY;
+        high = fmaxf(high, lj[s]);
+    }
+    float sum = 0.0f;
+    if (c.renormalize) {
+        // relative to the largest pick, so that no pick's score is lost below the smallest number
+        high = warp_max_f(high);
+        const float ref = softmax ? high : fminf(high, 0.0f);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            w[s] = softmax || lj[s] < 0.0f ? expf(lj[s] - ref) : 1.0f;
+            if (!softmax) w[s] /= 1.0f + expf(-fabsf(lj[s]));
+            if (mine[s] < 0) w[s] = 0.0f;
+            sum += w[s];
+        }
+        sum = warp_sum(sum);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (c.renormalize)
+            w[s] /= sum;
+        else
+            w[s] = softmax ? expf(lj[s] - m) * most : sigmoid(lj[s]);
+        w[s] = wrong ? __int_as_float(0x7fffffff) : mine[s] < 0 ? 0.0f : w[s] * c.scale;
+        const int j = s * 32 + lane;
+        if (j < c.J) {
+            c.chosen[static_cast<long long>(t) * c.J + j] = mine[s];
+            c.weights[static_cast<long long>(t) * c.J + j] = w[s];
+        }
+    }
+}
+
+// ---- gradient -----------------------------------------------------------------------
+struct ChooseBackward {
+    const float *dweights;
+    const int *chosen;
+    const void *logits;
+    void *dlogits;
+    long long ld, ldd;
+    int T, E, J, scoring, renormalize;
+    float scale;
+};
+
+// A warp takes a token: lane j works out the gradient of pick j (and of j + 32),
+// then each lane gathers those of its experts, in the order of the picks.
+template <typename T, int NV>
+__global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_backward_kernel(const __grid_constant__ ChooseBackward c) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * CHOOSE_WARPS + (threadIdx.x >> 5);
+    tc::grid_trigger();
+    tc::grid_wait();
+    if (t >= c.T) return;
+    const T *row = static_cast<const T *>(c.logits) + t * c.ld;
+    const bool softmax = c.scoring == EXPERTS_SOFTMAX, all = softmax && !c.renormalize;
+    int e[2];
+    float l[2], p[2], g[2];
+    float high = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int j = s * 32 + lane;
+        const long long at = static_cast<long long>(t) * c.J + j;
+        e[s] = j < c.J ? c.chosen[at] : -1;
+        if (e[s] < 0 || e[s] >= c.E) e[s] = -1;
+        g[s] = e[s] >= 0 ? c.dweights[at] * c.scale : 0.0f;
+        l[s] = e[s] >= 0 ? to_f(row[e[s]]) : -INFINITY;
+        high = fmaxf(high, l[s]);
+    }
+    const bool any = __any_sync(ALL, e[0] >= 0 || e[1] >= 0);
+    float x[NV];
+    float z = 1.0f;
+    if (all) {
+        high = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = i * 32 + lane < c.E ? to_f(row[i * 32 + lane]) : -INFINITY;
+            high = fmaxf(high, x[i]);
+        }
+        high = warp_max_f(high);
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i] = expf(x[i] - high);
+            z += x[i];
+        }
+        z = warp_sum(z);
+    } else {
+        high = warp_max_f(high);
+    }
+    // the picks' shares of what they are divided by, and with those the mean of the weights' gradients
+    const float ref = softmax ? high : fminf(high, 0.0f);
+    float sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        p[s] = softmax || l[s] < 0.0f ? expf(l[s] - ref) : 1.0f;
+        if (!softmax) p[s] /= 1.0f + expf(-fabsf(l[s]));
+        if (e[s] < 0) p[s] = 0.0f;
+        sum += p[s];
+    }
+    const float whole = all ? z : warp_sum(sum);
+    float mean = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        p[s] /= any ? whole : 1.0f;
+        mean += p[s] * g[s];
+    }
+    mean = softmax || c.renormalize ? warp_sum(mean) : 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const float far = sigmoid(-l[s]);  // 1 - sigmoid(l)
+        if (all)
+            ;  // joined with the other experts below
+        else if (softmax)
+            g[s] = p[s] * (g[s] - mean);
+        else if (c.renormalize)
+            g[s] = p[s] * far * (g[s] - mean);
+        else
+            g[s] *= sigmoid(l[s]) * far;
+        if (e[s] < 0) g[s] = 0.0f;
+    }
+    float d[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) d[i] = 0.0f;
+    for (int j = 0; j < c.J; ++j) {
+        const int who = __shfl_sync(ALL, j < 32 ? e[0] : e[1], j & 31);
+        const float what = __shfl_sync(ALL, j < 32 ? g[0] : g[1], j & 31);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i * 32 + lane == who) d[i] += what;
+    }
+    T *out = static_cast<T *>(c.dlogits) + t * c.ldd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (all) d[i] = any ? x[i] / z * (d[i] - mean) : 0.0f;
+        if (i * 32 + lane < c.E) out[i * 32 + lane] = from_f<T>(d[i]);
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------
+// f(values per lane) for E experts.
+template <typename F>
+int with_experts(int E, F &&f) {
+    return E <= 32    ? f(lt::Int<1>{})
+           : E <= 64  ? f(lt::Int<2>{})
+           : E <= 128 ? f(lt::Int<4>{})
+           : E <= 256 ? f(lt::Int<8>{})
+           : E <= 512 ? f(lt::Int<16>{})
+                      : f(lt::Int<32>{});
+}
+int check_choice(int type, int T, int E, int J, int scoring) {
+    if (type < LINEAR_F32 || type > LINEAR_F16 || (scoring != EXPERTS_SOFTMAX && scoring != EXPERTS_SIGMOID))
+        return SGEMM_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > EXPERTS_MAX_CHOOSE || J < 0 || J > E || J > EXPERTS_MAX_CHOICES ||
+        T > INT_MAX - CHOOSE_WARPS || static_cast<long long>(T) * J > INT_MAX)
+        return SGEMM_ERR_INVALID_DIM;
+    return SGEMM_OK;
+}
+unsigned token_blocks(int T) { return static_cast<unsigned>((T + CHOOSE_WARPS - 1) / CHOOSE_WARPS); }
+
+}  // namespace
+
+extern "C" int expert_choose(int type, int T, int E, int J, const void *logits, int64_t ldl, const float *bias, int scoring,
+                             int groups, int kept_groups, int group_top, int renormalize, float scale, int *chosen,
+                             float *weights, cudaStream_t stream) {
+    int st = check_choice(type, T, E, J, scoring);
+    if (st != SGEMM_OK) return st;
+    if (groups < 1 || groups > EXPERTS_MAX_GROUPS || E % groups != 0 || kept_groups < 1 || kept_groups > groups ||
+        (group_top != 1 && group_top != 2))
+        return SGEMM_ERR_INVALID_ARG;
+    if (ldl < E) return SGEMM_ERR_INVALID_LD;
+    if (T == 0 || J == 0) return SGEMM_OK;
+    if (logits == nullptr || chosen == nullptr || weights == nullptr) return SGEMM_ERR_NULL_PTR;
+    const int b = lt::type_bytes(type);
+    if (misaligned(logits, b) || misaligned(bias, 4) || misaligned(chosen, 4) || misaligned(weights, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    const long long R = static_cast<long long>(T) * J;
+    const Span sl = span(logits, T, E, ldl, b), sb = span(bias, 1, E, E, 4), sc = span(chosen, 1, R, R, 4),
+               sw = span(weights, 1, R, R, 4);
+    if (overlap(sc, sl) || overlap(sc, sb) || overlap(sw, sl) || overlap(sw, sb) || overlap(sc, sw)) return SGEMM_ERR_ALIAS;
+    Choose c{};
+    c.logits = logits, c.ld = ldl, c.bias = bias, c.chosen = chosen, c.weights = weights, c.T = T, c.E = E, c.J = J;
+    c.scoring = scoring, c.groups = groups, c.kept = kept_groups, c.top = group_top, c.size = E / groups;
+    c.per = (1u << 20) / static_cast<unsigned>(c.size) + 1;  // exact for e * size < 2^20
+    c.renormalize = renormalize != 0, c.scale = scale;
+    if (groups == 1) c.top = 1;
+    const bool in_64 = bias != nullptr || (groups > 1 && group_top > 1);
+    const size_t smem = in_64 ? sizeof(unsigned long long) * CHOOSE_WARPS * static_cast<size_t>(E) : 0;
+    sg_nvtx::Range r("experts: choose");
+    return with_experts(E, [&](auto n) {
+        constexpr int NV = decltype(n)::value;
+        auto run = [&](auto kernel) { return launched(tc::launch(kernel, token_blocks(T), dim3(CHOOSE_WARPS * 32), smem, stream, c)); };
+        return type == LINEAR_F32    ? run(choose_kernel<float, NV>)
+               : type == LINEAR_BF16 ? run(choose_kernel<__nv_bfloat16, NV>)
+                                     : run(choose_kernel<__half, NV>);
+    });
+}
+
+extern "C" int expert_choose_backward(int type, int T, int E, int J, const float *dweights, const int *chosen,
+                                      const void *logits, int64_t ldl, int scoring, int renormalize, float scale,
+                                      void *dlogits, int64_t ldd, cudaStream_t stream) {
+    int st = check_choice(type, T, E, J, scoring);
+    if (st != SGEMM_OK) return st;
+    if (ldl < E || ldd < E) return SGEMM_ERR_INVALID_LD;
+    if (T == 0) return SGEMM_OK;
+    if (logits == nullptr || dlogits == nullptr || (J > 0 && (chosen == nullptr || dweights == nullptr))) return SGEMM_ERR_NULL_PTR;
+    const int b = lt::type_bytes(type);
+    if (misaligned(logits, b) || misaligned(dlogits, b) || misaligned(chosen, 4) || misaligned(dweights, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    const long long R = static_cast<long long>(T) * J;
+    const Span so = span(dlogits, T, E, ldd, b);
+    if (overlap(so, span(logits, T, E, ldl, b)) || overlap(so, span(chosen, 1, R, R, 4)) || overlap(so, span(dweights, 1, R, R, 4)))
+        return SGEMM_ERR_ALIAS;
+    ChooseBackward c{};
+    c.dweights = dweights, c.chosen = chosen, c.logits = logits, c.dlogits = dlogits, c.ld = ldl, c.ldd = ldd;
+    c.T = T, c.E = E, c.J = J, c.scoring = scoring, c.renormalize = renormalize != 0, c.scale = scale;
+    sg_nvtx::Range r("experts: choose backward");
+    return with_experts(E, [&](auto n) {
+        constexpr int NV = decltype(n)::value;
+        auto run = [&](auto kernel) { return launched(tc::launch(kernel, token_blocks(T), dim3(CHOOSE_WARPS * 32), 0, stream, c)); };
+        return type == LINEAR_F32    ? run(choose_backward_kernel<float, NV>)
+               : type == LINEAR_BF16 ? run(choose_backward_kernel<__nv_bfloat16, NV>)
+                                     : run(choose_backward_kernel<__half, NV>);
+    });
+}

@@ -24,11 +24,9 @@ __device__ unsigned g_linear_timeout;
 std::mutex g_mutex;
 Device g_devices[64];
 
-template <int CG, typename T>
-bool opt_in() {
-    return cudaFuncSetAttribute(product_kernel<CG, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) ==
-           cudaSuccess;
-}
+}  // namespace
+
+namespace product {
 
 int set_up(Device *out) {
     int dev = 0;
@@ -49,9 +47,9 @@ int set_up(Device *out) {
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10 ||
-            minor != 3 || d.sms < 2 || encode_fn() == nullptr || !opt_in<1, float>() || !opt_in<2, float>() ||
-            !opt_in<1, __nv_bfloat16>() || !opt_in<2, __nv_bfloat16>() || !opt_in<1, __half>() ||
-            !opt_in<2, __half>() ||
+            minor != 3 || d.sms < 2 || encode_fn() == nullptr || !opt_in<1, float, LAYER>() || !opt_in<2, float, LAYER>() ||
+            !opt_in<1, __nv_bfloat16, LAYER>() || !opt_in<2, __nv_bfloat16, LAYER>() || !opt_in<1, __half, LAYER>() ||
+            !opt_in<2, __half, LAYER>() ||
             cudaGetSymbolAddress(reinterpret_cast<void **>(&d.timeout_flag), g_linear_timeout) != cudaSuccess)
             st = SGEMM_ERR_DEVICE;
         d.pairs = d.sms / 2;
@@ -78,6 +76,14 @@ int set_up(Device *out) {
     *out = d;
     return d.state > 0 ? SGEMM_OK : d.state;
 }
+
+int run_layer(int type, const Product &p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream) {
+    return run_product<LAYER>(type, p, P, Q, d, stream);
+}
+
+}  // namespace product
+
+namespace {
 
 // Everything of a call, dense (E < 0) or by expert.
 struct Call {
@@ -213,7 +219,7 @@ int forward(const Call &c) {
     p.ldz = c.ldz;
     p.ldo = c.ldy;
     p.act = c.act;
-    return run_product(c.type, p, P, Q, d, c.stream);
+    return run_layer(c.type, p, P, Q, d, c.stream);
 }
 
 struct Wanted {
@@ -343,7 +349,7 @@ int backward(const Call &c) {
         p.ldo = c.lddx;
         const bool two = !empty && want.dw;
         p.order = two ? ORDER_FIRST : ORDER_ALONE;
-        st = run_product(c.type, p, P_dx, Q, d, c.stream);
+        st = run_layer(c.type, p, P_dx, Q, d, c.stream);
         if (st != SGEMM_OK) return st;
         p.dbias = nullptr;
         p.order = two ? ORDER_BESIDE : ORDER_ALONE;
@@ -359,7 +365,7 @@ int backward(const Call &c) {
         p.out = c.dw;
         p.ldo = c.lddw;
         p.out_expert = c.E > 1 ? c.dw_expert : 0;
-        st = run_product(c.type, p, c.w_order ? X : Z, c.w_order ? Z : X, d, c.stream);
+        st = run_layer(c.type, p, c.w_order ? X : Z, c.w_order ? Z : X, d, c.stream);
         if (st != SGEMM_OK) return st;
     }
     return SGEMM_OK;

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -66,6 +67,38 @@ constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles
 
 enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
 
+// What becomes of a tile.
+//   LAYER             out = act(product + bias) + residual
+// and, for the loss of a head over a vocabulary, with its tokens as features
+// (a thread of the epilogue then owns a token) and its vocabulary as tokens:
+//   LOG_SUM           nothing is stored but, of each token, the maximum and the
+//                     sum of exponentials of its part of the tile, and the
+//                     value at its target
+//   SOFTMAX_GRADIENT  out = a exp(product - lse) - g [target] (FP32: in pieces)
+//   SCALED_SUM        out = alpha (product + acc), or acc += product
+// The last three have no splits and no experts.
+enum Epilogue { LAYER = 0, LOG_SUM = 1, SOFTMAX_GRADIENT = 2, SCALED_SUM = 3 };
+struct Token {  // of SOFTMAX_GRADIENT
+    float lse;  // 16-bit types: times log2(e)
+    float a, g;
+    int target;  // -1: none
+};
+struct Loss {
+    // LOG_SUM
+    float2 *parts;        // two per tile of the vocabulary: [2 * tile + half][token]
+    const void *targets;  // 4 or 8 bytes each
+    float *hit;
+    int target_bytes;
+    // SOFTMAX_GRADIENT: tokens, and where the piece of the vocabulary begins
+    const Token *tokens;
+    int begin;
+    long long piece;      // elements between FP32's pieces in out
+    // SCALED_SUM
+    float *acc;           // T x F
+    const float *alpha;
+    int first, last;      // acc holds nothing yet; out is wanted
+};
+
 struct Product {
     int T, F, K;              // K_BY_EXPERT: K = all rows, shared out by offsets
     int mode, E;
@@ -87,6 +120,7 @@ struct Product {
     int sums_M, sums_N, sums_E;
     int order;                // ORDER_*
     unsigned *timeout_flag;
+    Loss loss;
 };
 // A backward pass's two products need the same earlier kernels and not each
 // other.  The first lets the second start once it has waited for those
@@ -422,6 +456,157 @@ __device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld,
     }
 }
 
+// ---- the loss's epilogues --------------------------------------------------------
+// log2(e) times what is left to the largest value: the difference first, as the
+// product of each would lose what the largest has above the rest.
+__device__ __forceinline__ float exp_of(float d) { return lt::fast_exp2(lt::kLog2E * d); }
+__device__ __forceinline__ long long target_of(const Loss &l, int token) {
+    return l.target_bytes == 8 ? static_cast<const long long *>(l.targets)[token]
+                               : static_cast<long long>(static_cast<const int *>(l.targets)[token]);
+}
+// The running maximum and sum of exponentials of a token, 16 of its values (n of them valid) at a time.
+struct LogSum {
+    float high = -INFINITY, sum = 0.0f;
+    __device__ __forceinline__ void add(float (&v)[16], int n) {
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i >= n) v[i] = -INFINITY;
+        }
+        float m = high;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, v[i]);
+        const float ref = m == -INFINITY ? 0.0f : m;  // -inf - -inf would be a NaN
+        sum *= exp_of(high - ref);
+        high = m;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i & 3] += exp_of(v[i] - ref);
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+    }
+};
+// One tile of LOG_SUM, SOFTMAX_GRADIENT or SCALED_SUM, of this thread's lane of
+// tensor memory: token (feature) f, columns col0 .. col0 + n of the tile.
+// read(c, v) gives columns col0 + c .. col0 + c + 15.
+template <typename T, int EPI, typename Read>
+__device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f, bool f_ok, int col0, int n, Read &&read) {
+    if constexpr (EPI == LOG_SUM) {
+        LogSum ls;
+        long long t = -1;
+        if (f_ok) t = target_of(p.loss, f) - (static_cast<long long>(w.t0) + col0);
+        for (int c = 0; c < n; c += 16) {
+            float v[16];
+            read(c, v);
+            if (t >= c && t < c + 16 && t < n) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i == static_cast<int>(t)) p.loss.hit[f] = v[i];
+            }
+            ls.add(v, n - c);
+        }
+        const long long part = 2 * static_cast<long long>(w.t0 / p.bt) + (col0 != 0 ? 1 : 0);
+        if (f_ok) p.loss.parts[part * p.F + f] = make_float2(ls.high, ls.sum);
+    } else if constexpr (EPI == SOFTMAX_GRADIENT) {  // FP32; the 16-bit types' is below
+        Token k = {0.0f, 0.0f, 0.0f, -1};
+        if (f_ok) k = p.loss.tokens[f];
+        const int t = k.target < 0 ? -1 : k.target - p.loss.begin - (w.t0 + col0);
+        for (int c = 0; c < n; c += 16) {
+            float v[16];
+            read(c, v);
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<long long>(w.t0) + col0 + c) * p.ldo + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (c + i >= n || !f_ok) break;
+                __nv_bfloat16 x, y, z;
+                lt::pieces(fmaf(expf(v[i] - k.lse), k.a, c + i == t ? -k.g : 0.0f), x, y, z);
+                o[i * p.ldo] = x;
+                o[i * p.ldo + p.loss.piece] = y;
+                o[i * p.ldo + 2 * p.loss.piece] = z;
+            }
+        }
+    } else {
+        const float alpha = p.loss.alpha != nullptr ? *p.loss.alpha : 1.0f;
+        for (int c = 0; c < n; c += 16) {
+            float v[16], before[16];
+            const long long row = static_cast<long long>(w.t0) + col0 + c;
+            float *acc = p.loss.acc + row * p.F + f;
+            if (!p.loss.first && f_ok) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < n) before[i] = acc[static_cast<long long>(i) * p.F];
+            }
+            read(c, v);
+            if (!f_ok) continue;
+            T *o = static_cast<T *>(p.out) + row * p.ldo + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < n) {
+                    const float s = p.loss.first ? v[i] : v[i] + before[i];
+                    if (p.loss.last)
+                        o[i * p.ldo] = from_f<T>(s * alpha);
+                    else
+                        acc[static_cast<long long>(i) * p.F] = s;
+                }
+        }
+    }
+}
+
+// SOFTMAX_GRADIENT of the 16-bit types: fragments through shared memory as in the
+// layer's epilogue, four tokens a thread (8 o + lane / 4), so that rows of 32
+// tokens leave in 16-byte stores.
+template <typename T>
+__device__ __forceinline__ void gradient_tile(const Product &p, const Tile &w, int f, bool f_ok, int col0, int n, bool any,
+                                              uint32_t t_set, uint32_t buf, int lane) {
+    if (n <= 0) return;
+    Token mine = {0.0f, 0.0f, 0.0f, -1};
+    if (f_ok) mine = p.loss.tokens[f];
+    int t = mine.target < 0 ? -1 : mine.target - p.loss.begin - (w.t0 + col0);
+    if (t < 0 || t >= n) t = -1;
+    Token k[4];
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+        k[o].lse = __shfl_sync(0xffffffffu, mine.lse, 8 * o + (lane >> 2));
+        k[o].a = __shfl_sync(0xffffffffu, mine.a, 8 * o + (lane >> 2));
+        k[o].g = __shfl_sync(0xffffffffu, mine.g, 8 * o + (lane >> 2));
+        k[o].target = __shfl_sync(0xffffffffu, t, 8 * o + (lane >> 2));
+    }
+    const long long row0 = static_cast<long long>(w.t0) + col0;
+    for (int c = 0; c < n; c += EPI_T) {
+        float v[2][16];
+        if (any) {
+            tc::tmem_ld_frag(t_set + c, v[0]);
+            tc::tmem_ld_frag(t_set + c + 16, v[1]);
+            tc::tmem_ld_wait(v[0]);
+            tc::tmem_ld_wait(v[1]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[h][i] = 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const Token &q = k[2 * (i >> 3) + (i >> 1 & 1)];
+                v[h][i] = q.a * lt::fast_exp2(fmaf(v[h][i], lt::kLog2E, -q.lse));
+            }
+        if (__any_sync(0xffffffffu, t >= c && t < c + EPI_T)) {  // a target among these
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const Token &q = k[2 * (i >> 3) + (i >> 1 & 1)];
+                    if (q.target == c + 16 * h + 8 * (i >> 2 & 1) + 2 * (lane & 3) + (i & 1)) v[h][i] -= q.g;
+                }
+        }
+        __syncwarp();  // the buffer's last contents have been read
+        stage_fragments<T>(v, buf, lane);
+        __syncwarp();
+        store_staged<T>(buf, static_cast<T *>(p.out), p.ldo, (p.widths >> OUT_SHIFT) & 255, row0 + c, n - c, f - lane, p.F, lane);
+    }
+}
+
 // A persistent grid of CTA pairs (CG = 2, tiles of 256 features) or of
 // clusters of `splits` CTAs (CG = 1, 128 features, the K of a tile shared
 // out).  Per CTA, warp 8 issues the tensor copies into a ring of stages, one
@@ -439,7 +624,7 @@ __device__ __forceinline__ void store_staged(uint32_t buf, T *dst, long long ld,
 // rows in both operands (a NaN times 0 would be one) and then reports the stage
 // full, while the copies go on.  Before that, the same warp adds up the bias
 // gradient, where the product is the first of a backward pass.
-template <int CG, typename T>
+template <int CG, typename T, int EPI = LAYER>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
     constexpr bool F32 = std::is_same<T, float>::value;
@@ -769,6 +954,43 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t set = g & 1;
             bool freed = false;  // the accumulators are reported read
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
+            if constexpr (EPI != LAYER) {
+                const int n = f - lane < p.F ? min(cols, n_tile - col0) : 0;
+                if (!F32 && any) {
+                    waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                    __syncwarp();
+                    tc::fence_after();
+                }
+                if constexpr (EPI == SOFTMAX_GRADIENT && !F32) {
+                    gradient_tile<T>(p, w, f, f_ok, col0, n, any, t_set, epi, lane);
+                } else {
+                    auto read = [&](int c, float (&v)[16]) {
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int b = 0; b < F32_COLS; b += 16)
+                                if (b == c) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) v[i] = total[b + i];
+                                }
+                        } else if (any) {
+                            __syncwarp();  // the loads are the whole warp's
+                            tc::tmem_ld16(t_set + c, v);
+                            tc::tmem_ld_wait(v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        }
+                    };
+                    loss_tile<T, EPI>(p, w, f, f_ok, col0, n, read);
+                }
+                if (!F32 && any) {
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                    ++g;
+                }
+                continue;
+            }
             if (S > 1 && !w.none) {
                 // hand this CTA's part over: wait until the last one is read, store, tell all
                 if (handed > 0) waiter.wait<true>(tc::smem_u32(&part_read), (handed - 1) & 1);
@@ -1030,6 +1252,8 @@ inline bool encode(CUtensorMap &map, const Operand &o, bool f16, int box_outer) 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Narrowest tile of LOG_SUM: the room for its parts is known without a plan.
+constexpr int LOG_SUM_COLS = 64;
 struct Plan {
     int cg = 2, bt = 256, splits = 1, units = 1;
     double cost = 1e300;
@@ -1071,13 +1295,13 @@ inline int q_bytes_of(int rows, bool mn) { return mn ? (rows + 63) / 64 * MN_BOX
 // between filling the pipeline and draining the last accumulator about 6000
 // clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 73, 256 wide 82,
 // 128 wide 95; single CTAs 256 wide 93, 128 wide 126.
-inline Plan choose(const Product &p, const Device &d, int type, const Tune &only) {
+inline Plan choose(const Product &p, const Device &d, int type, const Tune &only, int least = 0) {
     const bool f32 = type == LINEAR_F32;
     Plan best;
     const int bts[] = {256, 224, 192, 160, 128, 96, 64, 32, 16};
     for (int cg = 2; cg >= 1; --cg)
         for (int bt : bts) {
-            if (cg == 2 && (bt < 64 || bt % 32 != 0)) continue;
+            if (bt < least || (cg == 2 && (bt < 64 || bt % 32 != 0))) continue;
             if (f32 && bt > 2 * F32_COLS) continue;
             if ((only.cg != 0 && only.cg != cg) || (only.bt != 0 && only.bt != bt)) continue;
             double nt, ktiles = (p.K + BK - 1) / BK;
@@ -1123,7 +1347,7 @@ inline Plan choose(const Product &p, const Device &d, int type, const Tune &only
     return best;
 }
 
-template <int CG, typename T>
+template <int CG, typename T, int EPI>
 cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -1140,22 +1364,29 @@ cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cu
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, product_kernel<CG, T>, maps, p);
+    return cudaLaunchKernelEx(&cfg, product_kernel<CG, T, EPI>, maps, p);
 }
 
 // Enqueue one product: P and Q as 16-bit operands (FP32: three planes each).
-inline int run_product(int type, Product p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream) {
+template <int EPI>
+int run_product(int type, Product p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream,
+                int *token_tiles = nullptr) {
     if (p.T == 0 || p.F == 0 || (p.mode == K_BY_EXPERT && p.E == 0)) return SGEMM_OK;
     p.p_mn = P.mn;
     p.q_mn = Q.mn;
     p.timeout_flag = d.timeout_flag;
-    Plan pl = choose(p, d, type, tune());
+    Tune only = tune();
+    if (EPI != LAYER) only.splits = 1;
+    if (EPI == LOG_SUM && only.bt < LOG_SUM_COLS) only.bt = 0;
+    Plan pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     if (pl.cost > 1e299) {
         static std::once_flag told;
         std::call_once(told, [&] {
             fprintf(stderr, "LINEAR_TUNE leaves no plan for a product of %d x %d x %d and is not applied to it\n", p.T, p.F, p.K);
         });
-        pl = choose(p, d, type, Tune());
+        only = Tune();
+        if (EPI != LAYER) only.splits = 1;
+        pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     }
     p.bt = pl.bt;
     p.splits = pl.splits;
@@ -1164,6 +1395,7 @@ inline int run_product(int type, Product p, const Operand &P, const Operand &Q, 
     const int per_unit = PROWS * pl.cg;
     p.nf = (p.F + per_unit - 1) / per_unit;
     p.nt = (p.T + p.bt - 1) / p.bt;
+    if (token_tiles != nullptr) *token_tiles = p.nt;
     long long tiles = static_cast<long long>(p.nt) * p.nf;
     if (p.mode == ROWS_BY_EXPERT) tiles = (static_cast<long long>(p.nt) + p.E + 1) * p.nf;  // at most
     if (p.mode == K_BY_EXPERT) tiles *= p.E;
@@ -1191,15 +1423,16 @@ inline int run_product(int type, Product p, const Operand &P, const Operand &Q, 
     const int units = static_cast<int>(tiles < pl.units ? tiles : pl.units);
     const int grid = units * (pl.cg == 2 ? 2 : p.splits);
     sg_nvtx::Range r("linear: product");
-    cudaError_t err;
-    if (pl.cg == 2)
-        err = type == LINEAR_F32    ? launch<2, float>(maps, p, grid, smem, stream)
-              : type == LINEAR_BF16 ? launch<2, __nv_bfloat16>(maps, p, grid, smem, stream)
-                                    : launch<2, __half>(maps, p, grid, smem, stream);
-    else
-        err = type == LINEAR_F32    ? launch<1, float>(maps, p, grid, smem, stream)
-              : type == LINEAR_BF16 ? launch<1, __nv_bfloat16>(maps, p, grid, smem, stream)
-                                    : launch<1, __half>(maps, p, grid, smem, stream);
+    cudaError_t err = cudaErrorInvalidValue;
+    if (type == LINEAR_F32) {
+        if constexpr (EPI != SCALED_SUM)
+            err = pl.cg == 2 ? launch<2, float, EPI>(maps, p, grid, smem, stream) : launch<1, float, EPI>(maps, p, grid, smem, stream);
+    } else if (type == LINEAR_BF16) {
+        err = pl.cg == 2 ? launch<2, __nv_bfloat16, EPI>(maps, p, grid, smem, stream)
+                         : launch<1, __nv_bfloat16, EPI>(maps, p, grid, smem, stream);
+    } else {
+        err = pl.cg == 2 ? launch<2, __half, EPI>(maps, p, grid, smem, stream) : launch<1, __half, EPI>(maps, p, grid, smem, stream);
+    }
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
@@ -1290,6 +1523,18 @@ inline Matrix row_matrix(const void *p, int rows, int width, long long ld) {
     m.ld = ld;
     m.plane = rows * ld;
     return m;
+}
+
+// ---- in linear.cu ------------------------------------------------------------------------
+// The current device's set-up, made at its first call.
+int set_up(Device *out);
+// A product with the layer's epilogue.
+int run_layer(int type, const Product &p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream);
+// Allows this kernel all the shared memory that a product may use.
+template <int CG, typename T, int EPI>
+bool opt_in() {
+    return cudaFuncSetAttribute(product_kernel<CG, T, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) ==
+           cudaSuccess;
 }
 
 }  // namespace product

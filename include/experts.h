@@ -1,6 +1,6 @@
 /*
  * experts.h -- C ABI of the tokens' way to their experts and back
- * (libsgemm_f32.so): the stable sort of the routers' choices by expert, the
+ * (libsgemm_f32.so): a router's choice, the stable sort of the choices by expert, the
  * copy of the token rows into that order, the weighted sum of the experts'
  * rows per token, and the gradients.
  *
@@ -26,6 +26,47 @@ extern "C" {
 
 /* Most choices per token. */
 #define EXPERTS_MAX_CHOICES 64
+/* Most experts and groups of expert_choose. */
+#define EXPERTS_MAX_CHOOSE 1024
+#define EXPERTS_MAX_GROUPS 32
+
+typedef enum { EXPERTS_SOFTMAX = 0, EXPERTS_SIGMOID = 1 } experts_scoring;
+
+/*
+ * expert_choose -- each token's J experts and their weights from a router's logits l.
+ *     s = softmax(l) or 1 / (1 + exp(-l)),  v = s + bias
+ * The E experts form `groups` equal groups in a row; those kept_groups compete
+ * whose group_top (1 or 2) best v have the largest sum.  Of their experts the J
+ * with the largest v are chosen, in falling order; of equal values the lowest
+ * number comes first, for groups as for experts.  Without a bias the order is
+ * that of the logits (and that of a group its best logit, if group_top is 1);
+ * else it is that of v computed in 64 bits.
+ *     weights[t*J + j] = scale * s, or scale * s / sum of the chosen s (renormalize)
+ * The bias decides the choice and enters no weight.
+ *   logits, ldl : T x E of `type`, ldl >= E.
+ *   bias        : E FP32 values, or NULL.
+ *   chosen      : T*J 32-bit values (out).     weights : T*J FP32 values (out).
+ * An expert with a logit or a bias of minus infinity (or a bias that is no
+ * number) is never chosen.  Places for which no expert is left have chosen -1,
+ * which expert_sort drops, and weight 0: a token whose logits are all minus
+ * infinity goes to no expert.  A token with a NaN among its logits, or with
+ * softmax plus infinity, chooses none, and its weights are NaN.
+ * E is at most EXPERTS_MAX_CHOOSE, J at most EXPERTS_MAX_CHOICES and E, groups
+ * at most EXPERTS_MAX_GROUPS and a divisor of E.
+ */
+int expert_choose(int type, int T, int E, int J, const void *logits, int64_t ldl, const float *bias, int scoring,
+                  int groups, int kept_groups, int group_top, int renormalize, float scale, int *chosen,
+                  float *weights, cudaStream_t stream);
+
+/*
+ * expert_choose_backward -- the logits' gradient from the weights'.
+ *   dweights, chosen : T*J values; a choice outside 0 .. E-1 counts for nothing.
+ *   dlogits, ldd     : T x E of `type`, written whole: 0 for experts that the
+ *                      weights do not depend on.
+ */
+int expert_choose_backward(int type, int T, int E, int J, const float *dweights, const int *chosen,
+                           const void *logits, int64_t ldl, int scoring, int renormalize, float scale,
+                           void *dlogits, int64_t ldd, cudaStream_t stream);
 
 /*
  * expert_sort -- rows and offsets from the choices.
