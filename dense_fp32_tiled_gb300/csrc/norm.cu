@@ -2,10 +2,15 @@
 // HBM: the forward pass reads and writes each value once, the gradient reads
 // two and writes one.
 //
-// A row is held in the registers of `threads` threads (a warp, or a block) while
-// its sums go round: thread k has packs k, k + threads, ... of V values.  The
-// mean is rounded; the differences to it are summed again, which gives what the
-// rounding left, and squared for the variance, which so has no cancellation.
+// A row is held in the registers of a warp, or a block, while its sums go round:
+// of each warp's 32 * PPT packs of V values, lane k has k, k + 32, ...  (Steps of a
+// constant size: one address serves all of a thread's accesses to a row.)  The mean is rounded; the
+// differences to it are summed again, which gives what the rounding left, and
+// squared for the variance, which so has no cancellation.
+//
+// At HBM's rate an SM has 0.9 clocks for a value of the forward pass and 1.4 for
+// one of the gradient, so instructions count: arithmetic on pairs, no
+// division in a row, and registers no larger than leave the SM its warps.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -22,33 +27,122 @@ namespace {
 
 using namespace rows;
 
-constexpr int WARP_ROWS = 4;       // rows of a block, if a warp holds one
-constexpr int MOST_THREADS = 1024;
+constexpr int MOST_THREADS = 512;       // of a row held in registers
+constexpr int BACKWARD_THREADS = 768;   // of the gradient's block, if they hold 16 values each
+constexpr int MOST_WARPS = 24;
 
 // The sums of N values over the threads of a row (blockDim.x of them), the same
-// in each: across the warp, then over the warps in their order.  `part` has two
-// sets, used in turn (`turn`), so that one barrier a sum is enough.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[32][4], int &turn) {
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
-    if (blockDim.x == 32) return;
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) part[turn][threadIdx.x >> 5][i] = v[i];
-    __syncthreads();
+// in each: across the warp, then over the warps, in a fixed order.  The lanes
+// share the values out first (of three, lanes 0-7 add up the first, 8-15 the
+// second, 16-23 the third), which takes 6 exchanges for 15.  `part` has two sets,
+// used in turn (`turn`), so that one barrier a sum is enough.  SEVERAL: the
+// block's rows (threadIdx.y) have barriers of their own.  (A barrier whose number
+// is not a constant takes all 16 of a block, and an SM has them for four blocks.)
+__device__ __forceinline__ float across(float v, int k) { return v + __shfl_xor_sync(0xffffffffu, v, k); }
+template <bool SEVERAL, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[MOST_WARPS][4], int &turn) {
+    constexpr int SHARE = N == 1 ? 32 : N == 2 ? 16 : 8;  // lanes of a value
     const int lane = threadIdx.x & 31;
+    float t;
+    if constexpr (N == 1) {
+        t = across(v[0], 16);
+        t = across(t, 8);
+    } else {
+        const bool upper = (lane & 16) != 0;
+        if constexpr (N == 2) {
+            t = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
+            t = across(t, 8);
+        } else {
+            const float a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[2], 16);
+            const float b = across(v[1], 16);
+            const bool odd = (lane & 8) != 0;
+            t = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+        }
+    }
+    t = across(t, 4);
+    t = across(t, 2);
+    t = across(t, 1);
+    if (blockDim.x > 32) {
+        const int warps = blockDim.x >> 5, first = threadIdx.y * warps;
+        if ((lane & (SHARE - 1)) == 0) part[turn][first + (threadIdx.x >> 5)][lane / SHARE] = t;
+        if constexpr (SEVERAL)
+            asm volatile("bar.sync %0, %1;\n" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+        else
+            __syncthreads();
+        t = 0.0f;
+        for (int w = lane & 7; w < warps; w += 8) t += part[turn][first + w][N == 1 ? 0 : lane / SHARE];
+        t = across(t, 4);
+        t = across(t, 2);
+        t = across(t, 1);
+        turn ^= 1;
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < warps ? part[turn][lane][i] : 0.0f;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
-    turn ^= 1;
+    for (int i = 0; i < N; ++i) v[i] = N == 1 ? t : __shfl_sync(0xffffffffu, t, i * SHARE);
 }
+
+// The packs of a thread's next row, on their way while it works on this one: in
+// slots of shared memory that only this thread reads, so no barrier is needed
+// (2-byte packs, which no asynchronous copy moves: in registers).  COUNT matrices
+// of PPT packs each; two rows' room.  (Two rows ahead took longer, for the L1 that
+// their room takes from the weights: 16384 x 4096 bf16 62 us for 47, its gradient 88 for 84.)
+template <typename T, int V, int PPT, int COUNT, int THREADS>
+struct Ahead {
+    using P = Pack<T, V>;
+    static constexpr bool ASYNC = P::BYTES >= 4;
+    static constexpr int SLOT = ASYNC ? P::BYTES : 0;
+    static constexpr int APART = THREADS * SLOT, ROOM = COUNT * PPT * APART;
+    uint32_t at;    // this thread's first slot of the row at work
+    int other;      // how far from it the next row's is
+    P held[ASYNC ? 1 : COUNT * PPT], next[ASYNC ? 1 : COUNT * PPT];
+    __device__ __forceinline__ explicit Ahead(void *room) {
+        at = tc::smem_u32(room) + (threadIdx.y * blockDim.x + threadIdx.x) * SLOT + ROOM;
+        other = -ROOM;
+    }
+    __device__ __forceinline__ void ask(int m, int i, bool in, const T *src) {
+        if constexpr (ASYNC) {
+            const uint32_t to = at + other + (m * PPT + i) * APART;
+            if constexpr (P::BYTES == 16) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(src), "r"(in ? 16 : 0) : "memory");
+            } else {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(P::BYTES < 4 ? 4 : P::BYTES),
+                             "r"(in ? P::BYTES : 0)
+                             : "memory");
+            }
+        } else {
+            next[m * PPT + i] = load_if<T, V>(in, src);
+        }
+    }
+    // A row has been asked for whole.
+    __device__ __forceinline__ void asked() {
+        if constexpr (ASYNC) tc::cp_async_commit();
+    }
+    // The row at work is over, the one asked for is next.
+    __device__ __forceinline__ void turn() {
+        if constexpr (ASYNC) {
+            at += other;
+            other = -other;
+            tc::cp_async_wait<0>();
+        } else {
+#pragma unroll
+            for (int i = 0; i < COUNT * PPT; ++i) held[i] = next[i];
+        }
+    }
+    __device__ __forceinline__ P get(int m, int i) const {
+        if constexpr (ASYNC) {
+            const uint32_t from = at + (m * PPT + i) * APART;
+            P p;
+            if constexpr (P::BYTES == 16)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(p.raw.x), "=r"(p.raw.y), "=r"(p.raw.z), "=r"(p.raw.w) : "r"(from));
+            else if constexpr (P::BYTES == 8)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(p.raw.x), "=r"(p.raw.y) : "r"(from));
+            else if constexpr (P::BYTES == 4)
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(p.raw) : "r"(from));
+            return p;
+        } else {
+            return held[m * PPT + i];
+        }
+    }
+};
 
 struct Forward {
     const void *x, *weight, *bias;
@@ -56,130 +150,185 @@ struct Forward {
     float *stats;
     long long ldx, ldy;
     int M, N, packs;
-    float eps;
+    float eps, inverse;  // 1 / N
 };
 
+// What the passes over a row's packs do.
 template <typename T, int V>
-__device__ __forceinline__ void finish(const Pack<T, V> &x, const Pack<T, V> &w, const Pack<T, V> &b, bool has_w, float mean,
-                                       float rest, float rstd, T *y) {
-    float f[V], fw[V], fb[V];
-    x.get(f);
-    w.get(fw);
-    b.get(fb);
+struct Row {
+    using L = Lanes<V>;
+    using Num = typename L::Num;
+    using P = Pack<T, V>;
+    static __device__ __forceinline__ void add_up(const P &x, Num (&f)[L::N], Num &s) {
+        get<T, V>(x, f);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const float h = (f[k] - mean - rest) * rstd;
-        f[k] = fmaf(h, has_w ? fw[k] : 1.0f, fb[k]);
+        for (int k = 0; k < L::N; ++k) s = add(s, f[k]);
     }
-    Pack<T, V> o;
-    o.set(f);
-    store<T, V>(y, o);
+    // the differences to the mean, their sum and that of their squares
+    static __device__ __forceinline__ void spread(Num (&f)[L::N], Num minus_mean, Num &s, Num &q) {
+#pragma unroll
+        for (int k = 0; k < L::N; ++k) {
+            f[k] = add(f[k], minus_mean);
+            s = add(s, f[k]);
+            q = fma_of(f[k], f[k], q);
+        }
+    }
+    // (d rstd - rest rstd) w + b
+    static __device__ __forceinline__ void finish(Num (&f)[L::N], const P &w, const P &b, Num rstd, Num minus_rest, T *y) {
+        Num fw[L::N], fb[L::N];
+        get<T, V>(w, fw);
+        get<T, V>(b, fb);
+#pragma unroll
+        for (int k = 0; k < L::N; ++k) f[k] = fma_of(fma_of(f[k], rstd, minus_rest), fw[k], fb[k]);
+        store<T, V>(y, pack_of<T, V>(f));
+    }
+    // sums of g w, of g w d and of d
+    static __device__ __forceinline__ void means(const P &x, const P &g, const P &w, Num minus_mean, Num &sg, Num &sgd, Num &sd) {
+        Num fx[L::N], fg[L::N], fw[L::N];
+        get<T, V>(x, fx);
+        get<T, V>(g, fg);
+        get<T, V>(w, fw);
+#pragma unroll
+        for (int k = 0; k < L::N; ++k) {
+            const Num d = add(fx[k], minus_mean), gw = mul(fg[k], fw[k]);
+            sg = add(sg, gw);
+            sgd = fma_of(gw, d, sgd);
+            sd = add(sd, d);
+        }
+    }
+    // dx = rstd g w + (a d + b), and the columns' sums of g h and g
+    static __device__ __forceinline__ P gradient(const P &x, const P &g, const P &w, Num minus_mean, Num rstd, Num minus_rest, Num a,
+                                                 Num b, Num (&dw)[L::N], Num (&db)[L::N]) {
+        Num fx[L::N], fg[L::N], fw[L::N];
+        get<T, V>(x, fx);
+        get<T, V>(g, fg);
+        get<T, V>(w, fw);
+#pragma unroll
+        for (int k = 0; k < L::N; ++k) {
+            const Num d = add(fx[k], minus_mean);
+            dw[k] = fma_of(fg[k], fma_of(d, rstd, minus_rest), dw[k]);
+            db[k] = add(db[k], fg[k]);
+            fx[k] = fma_of(mul(fg[k], fw[k]), rstd, fma_of(d, a, b));
+        }
+        return pack_of<T, V>(fx);
+    }
+};
+
+struct Spread {
+    float rest, rstd;
+};
+__device__ __forceinline__ Spread spread_of(const Forward &c, const float (&q)[2]) {
+    const float rest = q[0] * c.inverse, var = fmaf(-rest, rest, q[1] * c.inverse);
+    return {rest, 1.0f / sqrtf(fmaxf(var, 0.0f) + c.eps)};
 }
 
-// PPT packs a thread.
-template <typename T, int V, int PPT>
-__global__ void __launch_bounds__(MOST_THREADS) forward_kernel(const __grid_constant__ Forward c) {
-    __shared__ float part[2][32][4];
-    const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+// PPT packs a thread.  FAST: all threads have as many, and there are a weight and a
+// bias (the gradient: a weight and dx), so nothing is asked in a row.  A block takes every
+// blocks-th row (of each of its threadIdx.y) and asks for its next row before it
+// sums up this one.  Weight and bias come from L1 for each row.
+template <typename T, int V, int PPT, int THREADS, bool FAST>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const __grid_constant__ Forward c) {
+    using R = Row<T, V>;
+    using Num = typename R::Num;
+    __shared__ __align__(16) float part[2][MOST_WARPS][4];
+    extern __shared__ __align__(16) uint8_t room[];
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+    long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const T *wp = static_cast<const T *>(c.weight), *bp = static_cast<const T *>(c.bias);
+    Ahead<T, V, PPT, 1, THREADS> ahead(room);
+    const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
+    auto mine = [&](int i) { return FAST || p0 + 32 * i < c.packs; };
+    auto ask = [&](long long row) {
+        if (row < c.M) {
+            const T *x = static_cast<const T *>(c.x) + row * c.ldx + p0 * V;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i) ahead.ask(0, i, mine(i), mine(i) ? x + 32 * i * V : static_cast<const T *>(c.x));
+        }
+        ahead.asked();
+    };
     tc::grid_trigger();
     tc::grid_wait();
-    if (r >= c.M) return;
-    const T *row = static_cast<const T *>(c.x) + r * c.ldx;
-    const T *wp = static_cast<const T *>(c.weight), *bp = static_cast<const T *>(c.bias);
-    Pack<T, V> x[PPT], w[PPT], b[PPT];
+    ask(r);
     int turn = 0;
+    for (; r < c.M; r += step) {
+        ahead.turn();
+        Num f[PPT][R::L::N], sum = all<Num>(0.0f), square = sum;
 #pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
-        x[i] = load_if<T, V>(p < c.packs, row + static_cast<long long>(p) * V);
-        w[i] = load_if<T, V>(p < c.packs && wp != nullptr, wp + static_cast<long long>(p) * V);
-        b[i] = load_if<T, V>(p < c.packs && bp != nullptr, bp + static_cast<long long>(p) * V);
-    }
-    float s[1] = {0.0f};
+        for (int i = 0; i < PPT; ++i) R::add_up(ahead.get(0, i), f[i], sum);
+        ask(r + step);
+        float s[1] = {sum_of(sum)};
+        row_sum<false>(s, part, turn);
+        const float mean = s[0] * c.inverse;
+        const Num minus_mean = all<Num>(-mean);
+        sum = all<Num>(0.0f);
 #pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-        float f[V];
-        x[i].get(f);
+        for (int i = 0; i < PPT; ++i)
+            if (mine(i)) R::spread(f[i], minus_mean, sum, square);
+        float q[2] = {sum_of(sum), sum_of(square)};
+        row_sum<false>(q, part, turn);
+        const Spread sp = spread_of(c, q);
+        if (c.stats != nullptr && threadIdx.x == 0) {
+            c.stats[2 * r] = mean + sp.rest;
+            c.stats[2 * r + 1] = sp.rstd;
+        }
+        const Num rstd = all<Num>(sp.rstd), minus_rest = all<Num>(-sp.rest * sp.rstd);
+        T *y = static_cast<T *>(c.y) + r * c.ldy;
 #pragma unroll
-        for (int k = 0; k < V; ++k) s[0] += f[k];
-    }
-    row_sum(s, part, turn);
-    const float mean = s[0] / static_cast<float>(c.N);
-    float q[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-        float f[V];
-        x[i].get(f);
-        if (threadIdx.x + i * blockDim.x < c.packs)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = f[k] - mean;
-                q[0] += d;
-                q[1] = fmaf(d, d, q[1]);
-            }
-    }
-    row_sum(q, part, turn);
-    const float rest = q[0] / static_cast<float>(c.N);
-    const float var = fmaf(-rest, rest, q[1] / static_cast<float>(c.N));
-    const float rstd = 1.0f / sqrtf(fmaxf(var, 0.0f) + c.eps);
-    if (c.stats != nullptr && threadIdx.x == 0) {
-        c.stats[2 * r] = mean + rest;
-        c.stats[2 * r + 1] = rstd;
-    }
-    T *y = static_cast<T *>(c.y) + r * c.ldy;
-#pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
-        if (p < c.packs) finish<T, V>(x[i], w[i], b[i], wp != nullptr, mean, rest, rstd, y + static_cast<long long>(p) * V);
+        for (int i = 0; i < PPT; ++i) {
+            const int p = p0 + 32 * i;
+            if (mine(i))
+                R::finish(f[i], load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V), load_if<T, V>(FAST || bp != nullptr, bp + p * V),
+                          rstd, minus_rest, y + p * V);
+        }
     }
 }
 
 // Rows that no block's registers hold: read three times, the later ones from L2.
 template <typename T, int V>
 __global__ void __launch_bounds__(MOST_THREADS) forward_wide_kernel(const __grid_constant__ Forward c) {
-    __shared__ float part[2][32][4];
+    using R = Row<T, V>;
+    using Num = typename R::Num;
+    __shared__ __align__(16) float part[2][MOST_WARPS][4];
     const long long r = blockIdx.x;
     tc::grid_trigger();
     tc::grid_wait();
     const T *row = static_cast<const T *>(c.x) + r * c.ldx;
     const T *wp = static_cast<const T *>(c.weight), *bp = static_cast<const T *>(c.bias);
     int turn = 0;
-    float s[1] = {0.0f};
+    Num sum = all<Num>(0.0f), square = sum;
 #pragma unroll 4
     for (int p = threadIdx.x; p < c.packs; p += blockDim.x) {
-        float f[V];
-        load<T, V>(row + static_cast<long long>(p) * V).get(f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) s[0] += f[k];
+        Num f[R::L::N];
+        R::add_up(load<T, V>(row + static_cast<long long>(p) * V), f, sum);
     }
-    row_sum(s, part, turn);
-    const float mean = s[0] / static_cast<float>(c.N);
-    float q[2] = {0.0f, 0.0f};
+    float s[1] = {sum_of(sum)};
+    row_sum<false>(s, part, turn);
+    const float mean = s[0] * c.inverse;
+    const Num minus_mean = all<Num>(-mean);
+    sum = all<Num>(0.0f);
 #pragma unroll 4
     for (int p = threadIdx.x; p < c.packs; p += blockDim.x) {
-        float f[V];
-        load<T, V>(row + static_cast<long long>(p) * V).get(f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float d = f[k] - mean;
-            q[0] += d;
-            q[1] = fmaf(d, d, q[1]);
-        }
+        Num f[R::L::N];
+        get<T, V>(load<T, V>(row + static_cast<long long>(p) * V), f);
+        R::spread(f, minus_mean, sum, square);
     }
-    row_sum(q, part, turn);
-    const float rest = q[0] / static_cast<float>(c.N);
-    const float var = fmaf(-rest, rest, q[1] / static_cast<float>(c.N));
-    const float rstd = 1.0f / sqrtf(fmaxf(var, 0.0f) + c.eps);
+    float q[2] = {sum_of(sum), sum_of(square)};
+    row_sum<false>(q, part, turn);
+    const Spread sp = spread_of(c, q);
     if (c.stats != nullptr && threadIdx.x == 0) {
-        c.stats[2 * r] = mean + rest;
-        c.stats[2 * r + 1] = rstd;
+        c.stats[2 * r] = mean + sp.rest;
+        c.stats[2 * r + 1] = sp.rstd;
     }
+    const Num rstd = all<Num>(sp.rstd), minus_rest = all<Num>(-sp.rest * sp.rstd);
     T *y = static_cast<T *>(c.y) + r * c.ldy;
 #pragma unroll 4
     for (int p = threadIdx.x; p < c.packs; p += blockDim.x) {
         const long long at = static_cast<long long>(p) * V;
-        finish<T, V>(load<T, V>(row + at), load_if<T, V>(wp != nullptr, wp + at), load_if<T, V>(bp != nullptr, bp + at),
-                     wp != nullptr, mean, rest, rstd, y + at);
+        Num f[R::L::N];
+        get<T, V>(load<T, V>(row + at), f);
+#pragma unroll
+        for (int k = 0; k < R::L::N; ++k) f[k] = add(f[k], minus_mean);
+        R::finish(f, load_or_ones<T, V>(wp != nullptr, wp + at), load_if<T, V>(bp != nullptr, bp + at), rstd, minus_rest, y + at);
     }
 }
 
@@ -192,173 +341,147 @@ struct Backward {
     float *rest;  // wide rows: what rounding left of their mean
     long long lddy, ldx, lddx;
     int M, N, packs, blocks;
+    float inverse;  // 1 / N
 };
 
-// Of a row: the sums of g, of g d and of d (d = x - mean) give, with rest = mean of d,
-// the two means that dx needs.
+// Of a row's sums of g, of g d and of d (d = x - mean): with rest, the mean of d,
+// h = (d - rest) rstd, and dx = rstd (g - mean g - h mean(g h)) = rstd g + a d + b.
 struct RowMeans {
-    float rest, g, gh;
+    float rest, a, b;
 };
-__device__ __forceinline__ RowMeans row_means(const float (&q)[3], float n, float rstd) {
-    RowMeans m;
-    m.rest = q[2] / n;
-    m.g = q[0] / n;
-    m.gh = (q[1] / n - m.rest * m.g) * rstd;
-    return m;
+__device__ __forceinline__ RowMeans row_means(const float (&q)[3], float inverse, float rstd) {
+    const float rest = q[2] * inverse, g = q[0] * inverse;
+    const float gh = fmaf(q[1], inverse, -rest * g) * rstd;
+    const float a = -rstd * rstd * gh;
+    return {rest, a, fmaf(-rest, a, -rstd * g)};
 }
 
-// A grid of `blocks` blocks takes the rows in turn; a thread keeps the sums of
-// its columns in registers and writes them at the end.
-template <typename T, int V, int PPT, int THREADS>
+// A grid of `blocks` blocks, one an SM, takes the rows in turn, one each of their
+// threadIdx.y at a time; a thread keeps the sums of its columns in registers, and
+// the block's are joined in shared memory at the end.  Each row's packs are read
+// from their slots twice, before and after its means are known.
+template <typename T, int V, int PPT, int THREADS, bool FAST>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Backward c) {
-    __shared__ float part[2][32][4];
-    extern __shared__ float joined[];  // WARP_ROWS warps' sums
-    float dw[PPT][V], db[PPT][V];
+    using R = Row<T, V>;
+    using Num = typename R::Num;
+    constexpr int LN = R::L::N;
+    __shared__ __align__(16) float part[2][MOST_WARPS][4];
+    extern __shared__ __align__(16) uint8_t room[];
+    Num dw[PPT][LN], db[PPT][LN];
 #pragma unroll
     for (int i = 0; i < PPT; ++i)
 #pragma unroll
-        for (int k = 0; k < V; ++k) dw[i][k] = db[i][k] = 0.0f;
+        for (int k = 0; k < LN; ++k) dw[i][k] = db[i][k] = all<Num>(0.0f);
+    const T *wp = static_cast<const T *>(c.weight);
+    const long long step = static_cast<long long>(c.blocks) * blockDim.y;
+    long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    Ahead<T, V, PPT, 2, THREADS> ahead(room);
+    const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto mine = [&](int i) { return FAST || p0 + 32 * i < c.packs; };
+    auto ask = [&](long long row) {
+        if (row < c.M) {
+            const T *xr = static_cast<const T *>(c.x) + row * c.ldx + p0 * V, *gr = static_cast<const T *>(c.dy) + row * c.lddy + p0 * V;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i) {
+                ahead.ask(0, i, mine(i), mine(i) ? xr + 32 * i * V : static_cast<const T *>(c.x));
+                ahead.ask(1, i, mine(i), mine(i) ? gr + 32 * i * V : static_cast<const T *>(c.dy));
+            }
+            next_mean = c.stats[2 * row];
+            next_rstd = c.stats[2 * row + 1];
+        }
+        ahead.asked();
+    };
     tc::grid_trigger();
     tc::grid_wait();
-    const T *wp = static_cast<const T *>(c.weight);
-    const float n = static_cast<float>(c.N);
+    ask(r);
     int turn = 0;
-    for (long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; r < c.M;
-         r += static_cast<long long>(c.blocks) * blockDim.y) {
-        const T *xr = static_cast<const T *>(c.x) + r * c.ldx, *gr = static_cast<const T *>(c.dy) + r * c.lddy;
-        Pack<T, V> x[PPT], g[PPT];
+    for (; r < c.M; r += step) {
+        ahead.turn();
+        const float rstd = next_rstd;
+        const Num minus_mean = all<Num>(-next_mean);
+        ask(r + step);
+        Num sg = all<Num>(0.0f), sgd = sg, sd = sg;
 #pragma unroll
         for (int i = 0; i < PPT; ++i) {
-            const int p = threadIdx.x + i * blockDim.x;
-            x[i] = load_if<T, V>(p < c.packs, xr + static_cast<long long>(p) * V);
-            g[i] = load_if<T, V>(p < c.packs, gr + static_cast<long long>(p) * V);
+            const int p = p0 + 32 * i;
+            if (mine(i)) R::means(ahead.get(0, i), ahead.get(1, i), load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V), minus_mean, sg, sgd, sd);
         }
-        const float mean = c.stats[2 * r], rstd = c.stats[2 * r + 1];
-        float q[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < PPT; ++i) {
-            const int p = threadIdx.x + i * blockDim.x;
-            if (p < c.packs) {
-                float fx[V], fg[V], fw[V];
-                x[i].get(fx);
-                g[i].get(fg);
-                load_if<T, V>(wp != nullptr, wp + static_cast<long long>(p) * V).get(fw);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float d = fx[k] - mean, gw = wp != nullptr ? fg[k] * fw[k] : fg[k];
-                    q[0] += gw;
-                    q[1] = fmaf(gw, d, q[1]);
-                    q[2] += d;
-                }
-            }
-        }
-        row_sum(q, part, turn);
-        const RowMeans m = row_means(q, n, rstd);
+        float q[3] = {sum_of(sg), sum_of(sgd), sum_of(sd)};
+        row_sum<true>(q, part, turn);
+        const RowMeans m = row_means(q, c.inverse, rstd);
+        const Num n_rstd = all<Num>(rstd), minus_rest = all<Num>(-m.rest * rstd), a = all<Num>(m.a), b = all<Num>(m.b);
         T *dx = static_cast<T *>(c.dx) + r * c.lddx;
 #pragma unroll
         for (int i = 0; i < PPT; ++i) {
-            const int p = threadIdx.x + i * blockDim.x;
-            if (p < c.packs) {
-                float fx[V], fg[V], fw[V];
-                x[i].get(fx);
-                g[i].get(fg);
-                load_if<T, V>(wp != nullptr, wp + static_cast<long long>(p) * V).get(fw);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float h = (fx[k] - mean - m.rest) * rstd;
-                    dw[i][k] = fmaf(fg[k], h, dw[i][k]);
-                    db[i][k] += fg[k];
-                    const float gw = wp != nullptr ? fg[k] * fw[k] : fg[k];
-                    fx[k] = rstd * (gw - m.g - h * m.gh);
-                }
-                if (c.dx != nullptr) {
-                    Pack<T, V> o;
-                    o.set(fx);
-                    store<T, V>(dx + static_cast<long long>(p) * V, o);
-                }
+            const int p = p0 + 32 * i;
+            if (mine(i)) {
+                const Pack<T, V> o = R::gradient(ahead.get(0, i), ahead.get(1, i), load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V),
+                                                 minus_mean, n_rstd, minus_rest, a, b, dw[i], db[i]);
+                if (FAST || c.dx != nullptr) store<T, V>(dx + p * V, o);
             }
         }
     }
     if (c.sums == nullptr) return;
-    float *to = c.sums + static_cast<long long>(blockIdx.x) * 2 * c.N;
-    if (blockDim.y > 1) {  // the warps' sums, in their order
-        for (int s = 0; s < 2; ++s) {
-            __syncthreads();
+    // the rows' sums, in their order: V values of a thread lie together, so no two threads share any
+    float *joined = reinterpret_cast<float *>(room);
+    for (int y = 0; y < static_cast<int>(blockDim.y); ++y) {
+        __syncthreads();
+        if (y != static_cast<int>(threadIdx.y)) continue;
 #pragma unroll
-            for (int i = 0; i < PPT; ++i) {
-                const int p = threadIdx.x + i * 32;
-                if (p < c.packs)
+        for (int i = 0; i < PPT; ++i) {
+            const int p = p0 + 32 * i;
+            if (mine(i))
 #pragma unroll
-                    for (int k = 0; k < V; ++k) joined[threadIdx.y * c.N + p * V + k] = s == 0 ? dw[i][k] : db[i][k];
-            }
-            __syncthreads();
-            for (int j = threadIdx.y * 32 + threadIdx.x; j < c.N; j += blockDim.y * 32) {
-                float t = 0.0f;
-                for (int y = 0; y < static_cast<int>(blockDim.y); ++y) t += joined[y * c.N + j];
-                to[s * static_cast<long long>(c.N) + j] = t;
-            }
+                for (int k = 0; k < LN; ++k)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        Num *at = reinterpret_cast<Num *>(joined + s * c.N + p * V) + k;
+                        const Num v = s == 0 ? dw[i][k] : db[i][k];
+                        *at = y == 0 ? v : add(*at, v);
+                    }
         }
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-        const int p = threadIdx.x + i * blockDim.x;
-        if (p < c.packs)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                to[static_cast<long long>(p) * V + k] = dw[i][k];
-                to[c.N + static_cast<long long>(p) * V + k] = db[i][k];
-            }
-    }
+    __syncthreads();
+    float *to = c.sums + static_cast<long long>(blockIdx.x) * 2 * c.N;
+    for (int j = threadIdx.y * blockDim.x + threadIdx.x; j < 2 * c.N; j += blockDim.x * blockDim.y) to[j] = joined[j];
 }
 
 // Wide rows: dx by itself, reading the row twice.
 template <typename T, int V>
 __global__ void __launch_bounds__(MOST_THREADS) backward_wide_kernel(const __grid_constant__ Backward c) {
-    __shared__ float part[2][32][4];
+    using R = Row<T, V>;
+    using Num = typename R::Num;
+    __shared__ __align__(16) float part[2][MOST_WARPS][4];
     const long long r = blockIdx.x;
     tc::grid_trigger();
     tc::grid_wait();
     const T *wp = static_cast<const T *>(c.weight);
     const T *xr = static_cast<const T *>(c.x) + r * c.ldx, *gr = static_cast<const T *>(c.dy) + r * c.lddy;
-    const float mean = c.stats[2 * r], rstd = c.stats[2 * r + 1];
+    const float rstd = c.stats[2 * r + 1];
+    const Num minus_mean = all<Num>(-c.stats[2 * r]);
     int turn = 0;
-    float q[3] = {0.0f, 0.0f, 0.0f};
+    Num sg = all<Num>(0.0f), sgd = sg, sd = sg;
 #pragma unroll 2
     for (int p = threadIdx.x; p < c.packs; p += blockDim.x) {
         const long long at = static_cast<long long>(p) * V;
-        float fx[V], fg[V], fw[V];
-        load<T, V>(xr + at).get(fx);
-        load<T, V>(gr + at).get(fg);
-        load_if<T, V>(wp != nullptr, wp + at).get(fw);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float d = fx[k] - mean, gw = wp != nullptr ? fg[k] * fw[k] : fg[k];
-            q[0] += gw;
-            q[1] = fmaf(gw, d, q[1]);
-            q[2] += d;
-        }
+        R::means(load<T, V>(xr + at), load<T, V>(gr + at), load_or_ones<T, V>(wp != nullptr, wp + at), minus_mean, sg, sgd, sd);
     }
-    row_sum(q, part, turn);
-    const RowMeans m = row_means(q, static_cast<float>(c.N), rstd);
+    float q[3] = {sum_of(sg), sum_of(sgd), sum_of(sd)};
+    row_sum<false>(q, part, turn);
+    const RowMeans m = row_means(q, c.inverse, rstd);
     if (c.rest != nullptr && threadIdx.x == 0) c.rest[r] = m.rest;
     if (c.dx == nullptr) return;
+    const Num n_rstd = all<Num>(rstd), a = all<Num>(m.a), b = all<Num>(m.b);
     T *dx = static_cast<T *>(c.dx) + r * c.lddx;
 #pragma unroll 2
     for (int p = threadIdx.x; p < c.packs; p += blockDim.x) {
         const long long at = static_cast<long long>(p) * V;
-        float fx[V], fg[V], fw[V];
-        load<T, V>(xr + at).get(fx);
-        load<T, V>(gr + at).get(fg);
-        load_if<T, V>(wp != nullptr, wp + at).get(fw);
+        Num unused_w[R::L::N], unused_b[R::L::N];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float h = (fx[k] - mean - m.rest) * rstd, gw = wp != nullptr ? fg[k] * fw[k] : fg[k];
-            fx[k] = rstd * (gw - m.g - h * m.gh);
-        }
-        Pack<T, V> o;
-        o.set(fx);
-        store<T, V>(dx + at, o);
+        for (int k = 0; k < R::L::N; ++k) unused_w[k] = unused_b[k] = all<Num>(0.0f);
+        store<T, V>(dx + at, R::gradient(load<T, V>(xr + at), load<T, V>(gr + at), load_or_ones<T, V>(wp != nullptr, wp + at), minus_mean,
+                                         n_rstd, all<Num>(0.0f), a, b, unused_w, unused_b));
     }
 }
 
@@ -400,7 +523,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ su
     if (to == nullptr) return;
     float t = 0.0f;
     if (j < N) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = threadIdx.y; b < blocks; b += 32) t += sums[(static_cast<long long>(b) * 2 + which) * N + j];
     }
     part[threadIdx.y][threadIdx.x] = t;
@@ -414,17 +537,19 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ su
 
 // ---- host ----------------------------------------------------------------------------
 constexpr int SMS = 152;
-constexpr int MOST_BLOCKS = 2 * SMS;  // of the gradient: their sums are written and read once more
-constexpr int WIDE_BLOCKS = 32;       // row groups of columns_kernel
-constexpr int BACKWARD_THREADS = 512;
+constexpr int WIDE_BLOCKS = 32;            // row groups of columns_kernel
+constexpr size_t ROOM = 200 * 1024;        // of shared memory, for rows on their way and the joined sums
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-// How the gradient's grid shares the rows out, from sizes alone (the workspace depends on it).
-int backward_blocks(int M, int N) {
-    const int rows = N <= 1024 ? WARP_ROWS : 1;
-    const long long groups = (static_cast<long long>(M) + rows - 1) / rows;
-    return static_cast<int>(groups < MOST_BLOCKS ? groups : MOST_BLOCKS);
+// Blocks of the gradient, at most: one an SM (the workspace holds the sums of each).
+int backward_blocks(int M) { return M < SMS ? M : SMS; }
+// The kernel may have `bytes` of shared memory, and (several: more blocks than SMs) an
+// SM's is divided so that all the blocks that its registers allow have theirs.
+template <typename K>
+bool allow_room(K kernel, size_t bytes, bool several) {
+    return (bytes <= 40 * 1024 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ROOM)) == cudaSuccess) &&
+           (!several || cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 75) == cudaSuccess);
 }
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -456,6 +581,7 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
     if (N == 0) return stats == nullptr ? SGEMM_OK : launched(cudaMemsetAsync(stats, 0, sizeof(float) * 2 * static_cast<size_t>(M), stream));
     Forward c{};
     c.x = x, c.weight = weight, c.bias = bias, c.y = y, c.stats = stats, c.ldx = ldx, c.ldy = ldy, c.M = M, c.N = N, c.eps = eps;
+    c.inverse = 1.0f / static_cast<float>(N);
     const int width = narrower(narrower(width_of(x, ldx, type), width_of(y, ldy, type)),
                                narrower(narrower(width_of(weight, 0, type), width_of(bias, 0, type)), width_of(x, N, type)));
     c.packs = N / (width / b);
@@ -463,20 +589,35 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
     return with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
         constexpr int V = decltype(v)::value;
-        auto run = [&](auto kernel, int ppt) {
-            const int threads = round32((c.packs + ppt - 1) / ppt), rows = threads == 32 ? WARP_ROWS : 1;
-            return launched(tc::launch(kernel, static_cast<unsigned>((M + rows - 1) / rows), dim3(threads, rows), 0, stream, c));
+        constexpr int BYTES = V * static_cast<int>(sizeof(El));
+        auto run = [&](auto kernel, int ppt, int block) {
+            const int threads = round32((c.packs + ppt - 1) / ppt), rows = threads == 32 ? 4 : 1;
+            const long long groups = (static_cast<long long>(M) + rows - 1) / rows;
+            const long long most = static_cast<long long>(SMS) * (threads * rows <= 1024 ? 1024 / (threads * rows) : 1);
+            const size_t room = BYTES >= 4 ? static_cast<size_t>(2) * ppt * block * BYTES : 0;
+            if (!allow_room(kernel, room, groups > SMS)) return static_cast<int>(SGEMM_ERR_DEVICE);
+            return launched(tc::launch(kernel, static_cast<unsigned>(groups < most ? groups : most), dim3(threads, rows), room, stream, c));
         };
-        constexpr int SMALL = V >= 8 ? 2 : 4, LARGE = V >= 8 ? 4 : V == 1 ? 16 : 32 / V;
-        if (c.packs <= SMALL * 128) return run(forward_kernel<El, V, SMALL>, SMALL);
-        if (c.packs <= LARGE * MOST_THREADS) return run(forward_kernel<El, V, LARGE>, LARGE);
+        // 32 values of a row a thread (one by one: 16), or a quarter of that of a short one
+        constexpr int LARGE = V > 1 ? 32 / V : 16, SMALL = LARGE / 4;
+        if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128, false>, SMALL, 128);
+        auto pick = [&](auto t) {
+            constexpr int THREADS = decltype(t)::value;
+            if constexpr (BYTES == 16)
+                if (c.packs % (32 * LARGE) == 0 && weight != nullptr && bias != nullptr)
+                    return run(forward_kernel<El, V, LARGE, THREADS, true>, LARGE, THREADS);
+            return run(forward_kernel<El, V, LARGE, THREADS, false>, LARGE, THREADS);
+        };
+        if (c.packs <= LARGE * 128) return pick(lt::Int<128>{});
+        if (c.packs <= LARGE * 256) return pick(lt::Int<256>{});
+        if (c.packs <= LARGE * MOST_THREADS) return pick(lt::Int<MOST_THREADS>{});
         return launched(tc::launch(forward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
     });
 }
 
 extern "C" size_t layer_norm_backward_workspace_size(int M, int N, int want_dweight, int want_dbias) {
     if (M <= 0 || N <= 0 || !(want_dweight || want_dbias)) return 0;
-    const int blocks = backward_blocks(M, N);
+    const int blocks = backward_blocks(M);
     return up256(sizeof(float) * 2 * static_cast<size_t>(blocks) * N) + up256(sizeof(float) * static_cast<size_t>(M));
 }
 
@@ -514,7 +655,8 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
     Backward c{};
     c.dy = dy, c.x = x, c.weight = weight, c.stats = stats, c.dx = dx, c.dweight = dweight, c.dbias = dbias;
     c.lddy = lddy, c.ldx = ldx, c.lddx = lddx, c.M = M, c.N = N;
-    c.blocks = backward_blocks(M, N);
+    c.inverse = 1.0f / static_cast<float>(N);
+    c.blocks = backward_blocks(M);
     if (columns) {
         c.sums = static_cast<float *>(workspace);
         c.rest = reinterpret_cast<float *>(static_cast<char *>(workspace) + up256(sizeof(float) * 2 * static_cast<size_t>(c.blocks) * N));
@@ -526,15 +668,26 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
     const int done = with_rows(type, width, [&](auto el, auto v) {
         using El = decltype(el);
         constexpr int V = decltype(v)::value;
-        auto run = [&](auto kernel, int ppt) {
+        constexpr int BYTES = V * static_cast<int>(sizeof(El));
+        auto run = [&](auto kernel, int ppt, int block) {
             const int threads = round32((c.packs + ppt - 1) / ppt);
-            const int rows = threads == 32 && N <= 1024 ? WARP_ROWS : 1;
-            const size_t smem = rows > 1 && columns ? sizeof(float) * WARP_ROWS * static_cast<size_t>(N) : 0;
-            return launched(tc::launch(kernel, static_cast<unsigned>(c.blocks), dim3(threads, rows), smem, stream, c));
+            int rows = block / threads;
+            if (rows > 15 && threads > 32) rows = 15;  // named barriers
+            const int groups = static_cast<int>((static_cast<long long>(M) + rows - 1) / rows);
+            if (groups < c.blocks) c.blocks = groups;
+            const size_t slots = BYTES >= 4 ? static_cast<size_t>(4) * ppt * block * BYTES : 0, sums = sizeof(float) * 2 * static_cast<size_t>(N);
+            const size_t room = slots > sums ? slots : sums;
+            if (!allow_room(kernel, room, false)) return static_cast<int>(SGEMM_ERR_DEVICE);
+            return launched(tc::launch(kernel, static_cast<unsigned>(c.blocks), dim3(threads, rows), room, stream, c));
         };
-        constexpr int SMALL = V >= 8 ? 2 : 4, LARGE = V >= 8 ? 4 : V >= 4 ? 4 : 16;
-        if (c.packs <= SMALL * 256) return run(backward_kernel<El, V, SMALL, 256>, SMALL);
-        if (c.packs <= LARGE * BACKWARD_THREADS) return run(backward_kernel<El, V, LARGE, BACKWARD_THREADS>, LARGE);
+        // 16 values of a row a thread (one by one: 8), or 32 of a wide one
+        constexpr int SMALL = V > 1 ? 16 / V : 8, LARGE = 2 * SMALL;
+        constexpr int MANY = BACKWARD_THREADS, FEW = sizeof(El) == 4 ? 384 : MOST_THREADS;
+        if constexpr (BYTES == 16)
+            if (c.packs % (32 * SMALL) == 0 && c.packs <= SMALL * MANY && weight != nullptr && dx != nullptr)
+                return run(backward_kernel<El, V, SMALL, MANY, true>, SMALL, MANY);
+        if (c.packs <= SMALL * MANY) return run(backward_kernel<El, V, SMALL, MANY, false>, SMALL, MANY);
+        if (c.packs <= LARGE * FEW) return run(backward_kernel<El, V, LARGE, FEW, false>, LARGE, FEW);
         int s = launched(tc::launch(backward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
         if (s == SGEMM_OK && columns) {
             c.blocks = c.blocks < WIDE_BLOCKS ? c.blocks : WIDE_BLOCKS;

@@ -64,6 +64,10 @@ constexpr int PIECES = 3;
 constexpr int PRODUCTS = 6;
 constexpr int KBLK = 2;
 constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles up to 224 tokens
+// The 16-bit types' LOG_SUM, whose results are FP32, adds in registers too, after
+// LOG_SUM_KBLK tiles of K.
+constexpr int LOG_SUM_KBLK = 4;
+constexpr int LOG_SUM_REGS = 128;
 
 enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
 
@@ -488,29 +492,34 @@ struct LogSum {
 // One tile of LOG_SUM, SOFTMAX_GRADIENT or SCALED_SUM, of this thread's lane of
 // tensor memory: token (feature) f, columns col0 .. col0 + n of the tile.
 // read(c, v) gives columns col0 + c .. col0 + c + 15.
-template <typename T, int EPI, typename Read>
+template <typename T, int EPI, int COLS, typename Read>
 __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f, bool f_ok, int col0, int n, Read &&read) {
     if constexpr (EPI == LOG_SUM) {
         LogSum ls;
         long long t = -1;
         if (f_ok) t = target_of(p.loss, f) - (static_cast<long long>(w.t0) + col0);
-        for (int c = 0; c < n; c += 16) {
-            float v[16];
-            read(c, v);
-            if (t >= c && t < c + 16 && t < n) {
+        const int at = t >= 0 && t < n ? static_cast<int>(t) : -1;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i == static_cast<int>(t)) p.loss.hit[f] = v[i];
+        for (int c = 0; c < COLS; c += 16)
+            if (c < n) {
+                float v[16];
+                read(c, v);
+                if ((at & ~15) == c) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i == at) p.loss.hit[f] = v[i];
+                }
+                ls.add(v, n - c);
             }
-            ls.add(v, n - c);
-        }
         const long long part = 2 * static_cast<long long>(w.t0 / p.bt) + (col0 != 0 ? 1 : 0);
         if (f_ok) p.loss.parts[part * p.F + f] = make_float2(ls.high, ls.sum);
     } else if constexpr (EPI == SOFTMAX_GRADIENT) {  // FP32; the 16-bit types' is below
         Token k = {0.0f, 0.0f, 0.0f, -1};
         if (f_ok) k = p.loss.tokens[f];
         const int t = k.target < 0 ? -1 : k.target - p.loss.begin - (w.t0 + col0);
-        for (int c = 0; c < n; c += 16) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+            if (c >= n) break;
             float v[16];
             read(c, v);
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<long long>(w.t0) + col0 + c) * p.ldo + f;
@@ -629,6 +638,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr bool BF16 = !std::is_same<T, __half>::value;  // FP32's pieces are bf16
+    constexpr bool BLOCKS = F32 || EPI == LOG_SUM;          // K in blocks, added up in registers
+    constexpr int BLOCK = F32 ? KBLK : LOG_SUM_KBLK, COLS = F32 ? F32_COLS : LOG_SUM_REGS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES], acc_full[2], acc_empty[2];
     __shared__ __align__(8) uint64_t tail_bar[MAX_STAGES], part_ready, part_read;
@@ -848,8 +859,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
                 const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
                 const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
-                for (int kb = w.k0; kb < w.k1; kb += F32 ? KBLK : w.k1 - w.k0, ++g) {
-                    const int ke = F32 ? min(kb + KBLK, w.k1) : w.k1;
+                for (int kb = w.k0; kb < w.k1; kb += BLOCKS ? BLOCK : w.k1 - w.k0, ++g) {
+                    const int ke = BLOCKS ? min(kb + BLOCK, w.k1) : w.k1;
                     const uint32_t set = g & 1;
                     waiter.wait(tc::smem_u32(&acc_empty[set]), ((g >> 1) & 1) ^ 1);
                     tc::fence_after();
@@ -925,20 +936,20 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             if (p.bias != nullptr && f_ok && !w.none)
                 bias = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + f]);
             const bool any = w.k1 > w.k0;
-            float total[F32 ? F32_COLS : 1];
-            if constexpr (F32) {
+            float total[BLOCKS ? COLS : 1];
+            if constexpr (BLOCKS) {
                 if (p.residual != nullptr && !w.none && S == 1 && f - lane < p.F)
                     prefetch_residual<T>(p, static_cast<long long>(w.t0) + col0, min(cols, n_tile - col0), f - lane, lane);
 #pragma unroll
-                for (int c = 0; c < F32_COLS; ++c) total[c] = 0.0f;
-                for (int kb = w.k0; kb < w.k1; kb += KBLK, ++g) {
+                for (int c = 0; c < COLS; ++c) total[c] = 0.0f;
+                for (int kb = w.k0; kb < w.k1; kb += BLOCK, ++g) {
                     const uint32_t set = g & 1;
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
                     __syncwarp();
                     tc::fence_after();
                     const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
 #pragma unroll
-                    for (int c = 0; c < F32_COLS; c += 16)
+                    for (int c = 0; c < COLS; c += 16)
                         if (c < cols) {
                             float v[16];
                             tc::tmem_ld16(t_set + c, v);
@@ -956,7 +967,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
             if constexpr (EPI != LAYER) {
                 const int n = f - lane < p.F ? min(cols, n_tile - col0) : 0;
-                if (!F32 && any) {
+                if (!BLOCKS && any) {
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
                     __syncwarp();
                     tc::fence_after();
@@ -965,13 +976,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     gradient_tile<T>(p, w, f, f_ok, col0, n, any, t_set, epi, lane);
                 } else {
                     auto read = [&](int c, float (&v)[16]) {
-                        if constexpr (F32) {
+                        if constexpr (BLOCKS) {
 #pragma unroll
-                            for (int b = 0; b < F32_COLS; b += 16)
-                                if (b == c) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) v[i] = total[b + i];
-                                }
+                            for (int i = 0; i < 16; ++i) v[i] = total[c + i];  // c is a constant there
                         } else if (any) {
                             __syncwarp();  // the loads are the whole warp's
                             tc::tmem_ld16(t_set + c, v);
@@ -981,9 +988,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
                         }
                     };
-                    loss_tile<T, EPI>(p, w, f, f_ok, col0, n, read);
+                    loss_tile<T, EPI, COLS>(p, w, f, f_ok, col0, n, read);
                 }
-                if (!F32 && any) {
+                if (!BLOCKS && any) {
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
@@ -1377,7 +1384,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.timeout_flag = d.timeout_flag;
     Tune only = tune();
     if (EPI != LAYER) only.splits = 1;
-    if (EPI == LOG_SUM && only.bt < LOG_SUM_COLS) only.bt = 0;
+    if (EPI == LOG_SUM && only.bt < LOG_SUM_COLS) only.bt = 0;  // no narrower ones
     Plan pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     if (pl.cost > 1e299) {
         static std::once_flag told;

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "linear.h"
 #include "linear_types.cuh"
@@ -97,6 +98,96 @@ __device__ __forceinline__ Pack<T, V> load_if(bool in, const T *p) {
 template <typename T, int V>
 __device__ __forceinline__ void store(T *p, const Pack<T, V> &v) {
     *reinterpret_cast<typename Pack<T, V>::Raw *>(p) = v.raw;
+}
+
+// The same values, of which the compiler keeps nothing that it made of them
+// before: converting them again costs an instruction, keeping them a register each.
+template <typename T, int V>
+__device__ __forceinline__ void forget(Pack<T, V> &v) {
+    if constexpr (Pack<T, V>::BYTES == 16)
+        asm volatile("" : "+r"(v.raw.x), "+r"(v.raw.y), "+r"(v.raw.z), "+r"(v.raw.w));
+    else if constexpr (Pack<T, V>::BYTES == 8)
+        asm volatile("" : "+r"(v.raw.x), "+r"(v.raw.y));
+    else if constexpr (Pack<T, V>::BYTES == 4)
+        asm volatile("" : "+r"(v.raw));
+    else
+        asm volatile("" : "+h"(v.raw));
+}
+
+// ---- two values at a time ------------------------------------------------------------
+// FP32 arithmetic on pairs: one instruction for two, each rounded as by itself.  A pack of V values is V / 2 pairs, or one float.
+using Pair = float2;
+template <int V>
+struct Lanes {
+    using Num = Pair;
+    static constexpr int N = V / 2;
+};
+template <>
+struct Lanes<1> {
+    using Num = float;
+    static constexpr int N = 1;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ Pair mul(Pair a, Pair b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ Pair fma_of(Pair a, Pair b, Pair c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
+template <typename Num>
+__device__ __forceinline__ Num all(float v) {
+    if constexpr (sizeof(Num) == 8)
+        return make_float2(v, v);
+    else
+        return v;
+}
+__device__ __forceinline__ float sum_of(Pair p) {
+    return p.x + p.y;
+}
+__device__ __forceinline__ float sum_of(float v) { return v; }
+template <typename T, int V>
+__device__ __forceinline__ void get(const Pack<T, V> &p, typename Lanes<V>::Num (&f)[Lanes<V>::N]) {
+    if constexpr (V == 1) {
+        float v[1];
+        p.get(v);
+        f[0] = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 4)
+                f[i] = make_float2(__uint_as_float(p.word(2 * i)), __uint_as_float(p.word(2 * i + 1)));
+            else if constexpr (std::is_same<T, __nv_bfloat16>::value)  // an instruction each
+                f[i] = make_float2(__uint_as_float(p.word(i) << 16), __uint_as_float(p.word(i) & 0xffff0000u));
+            else
+                f[i] = lt::unpack2<T>(p.word(i));
+        }
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> pack_of(const typename Lanes<V>::Num (&f)[Lanes<V>::N]) {
+    float v[V];
+    if constexpr (V == 1) {
+        v[0] = f[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            v[2 * i] = f[i].x;
+            v[2 * i + 1] = f[i].y;
+        }
+    }
+    Pack<T, V> p;
+    p.set(v);
+    return p;
+}
+// The values at p, or ones.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_or_ones(bool in, const T *p) {
+    if (in) return load<T, V>(p);
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 1.0f;
+    Pack<T, V> o;
+    o.set(v);
+    return o;
 }
 
 // ---- host ----------------------------------------------------------------------------
