@@ -49,6 +49,10 @@ def _load():
         names += ["expert_gather", "expert_combine", "expert_combine_backward"]
         _fast_call.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},
                         bound(torch, _raw_stream, torch._C._cuda_getDevice))
+        names = ["layer_norm_forward", "expert_choose", "expert_choose_backward"]
+        names += [f for op in ("layer_norm_backward", "linear_cross_entropy_forward", "linear_cross_entropy_backward")
+                  for f in (op, op + "_workspace_size")]
+        _fast_call.bind_more({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names}, SCORINGS)
         _fast = _fast_call
     return _lib
 
@@ -355,6 +359,10 @@ def linear_cross_entropy(x, w, targets, stream=None):
     order; targets is int32 or int64 (M,).  A target outside 0 .. N - 1 (a
     padded token's -100) gives a loss of 0.
     """
+    if stream is None and _fast is not None:
+        r = _fast.cross_entropy(x, w, targets)
+        if r is not NotImplemented:
+            return _answer(r, "linear_cross_entropy_forward")
     lib = _lib or _load()
     kind, M, N, K, xp, ldx, wp, ldw, order, tp, width = _head(x, w, targets)
     with _on(x.get_device(), stream):
@@ -374,6 +382,10 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, dlse=None, need_dx=
     """(dx, dw) of linear_cross_entropy for the gradients of its losses and (dlse,
     None for none) of its log sums, float32 (M,); lse is what it returned.  dw
     has the memory order of w; what is not needed is None."""
+    if stream is None and _fast is not None:
+        r = _fast.cross_entropy_backward(dloss, x, w, targets, lse, dlse, need_dx, need_dw)
+        if r is not NotImplemented:
+            return _answer(r, "linear_cross_entropy_backward")
     lib = _lib or _load()
     kind, M, N, K, xp, ldx, wp, ldw, order, tp, width = _head(x, w, targets)
     dev = x.get_device()
@@ -409,6 +421,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, stats=None, out=None, stream
     for 1 and 0; out is (M, N).  ``stats``, a float32 (M, 2) tensor, receives
     each row's mean and 1 / sqrt(variance + eps) for layer_norm_backward.
     """
+    if stream is None and _fast is not None:
+        r = _fast.norm(x, weight, bias, eps, stats, out)
+        if r is not NotImplemented:
+            return _answer(r, "layer_norm_forward")
     lib = _lib or _load()
     kind = _type_of(x, "x")
     if x.dim() != 2:
@@ -432,6 +448,10 @@ def layer_norm_backward(dy, x, weight, stats, need_dx=True, need_dweight=True, n
     """(dx, dweight, dbias) of layer_norm for the gradient dy of its result.
     stats is what layer_norm saved; weight may be None (all 1).  What is not
     needed is None."""
+    if stream is None and _fast is not None:
+        r = _fast.norm_backward(dy, x, weight, stats, need_dx, need_dweight, need_dbias)
+        if r is not NotImplemented:
+            return _answer(r, "layer_norm_backward")
     lib = _lib or _load()
     kind = _type_of(x, "x")
     if x.dim() != 2:
@@ -484,6 +504,10 @@ def expert_choose(logits, choices, bias=None, scoring="softmax", groups=1, kept_
     ``renormalize``.  Experts with a logit of -inf are never chosen; places left
     over are -1 (which expert_sort drops), their weights 0.
     """
+    if stream is None and _fast is not None:
+        r = _fast.choose(logits, choices, bias, scoring, groups, kept_groups, group_top, renormalize, scale)
+        if r is not NotImplemented:
+            return _answer(r, "expert_choose")
     lib = _lib or _load()
     kind, how = _type_of(logits, "logits"), _scoring(scoring)
     if logits.dim() != 2:
@@ -505,6 +529,10 @@ def expert_choose(logits, choices, bias=None, scoring="softmax", groups=1, kept_
 def expert_choose_backward(dweights, logits, chosen, scoring="softmax", renormalize=True, scale=1.0, stream=None):
     """The gradient of the logits, in their type, from that of expert_choose's
     weights; chosen, scoring, renormalize and scale as there (the bias has none)."""
+    if stream is None and _fast is not None:
+        r = _fast.choose_backward(dweights, logits, chosen, scoring, renormalize, scale)
+        if r is not NotImplemented:
+            return _answer(r, "expert_choose_backward")
     lib = _lib or _load()
     kind, how = _type_of(logits, "logits"), _scoring(scoring)
     if logits.dim() != 2 or getattr(chosen, "ndim", 2) != 2:

@@ -1,19 +1,23 @@
 // experts_choose.cu -- a router's choice of each token's experts, and its
 // gradient (C ABI: include/experts.h).
 //
-// A warp takes a token; lane l holds the logits of experts l, l + 32, ...  The
-// J best are picked one after the other: each lane keeps its own best, one
-// warp maximum finds the value, one minimum the lowest expert that has it, and
-// the lane that lost its best looks for the next.  Values are compared as whole
-// numbers of the same order as the floats (0: not to be chosen), so a maximum
-// is one instruction.
+// A warp takes a token; lane l holds the logits of experts l * NV to l * NV + NV - 1
+// (in wide accesses where the rows allow them; a group of experts is then some
+// lanes in a row).  The J best are picked one after the other: each lane knows its
+// own best two, one warp maximum finds the value, one minimum the lowest expert
+// that has it, and only a lane that lost both looks for its next two.  Values are
+// compared as whole numbers of the same order as the floats (0: not to be
+// chosen), so a maximum is one instruction.  Bound by the instructions of those
+// rounds.
 //
 // What is compared.  Scores are increasing in the logits, so without a bias the
 // logits themselves are: no rounding enters.  With a bias (and for the sums of a
 // group's best two) the order is that of the scores in 64 bits.  A warp computes
-// them in 32 with a known bound on the error, and where two values that have to
-// be told apart are closer than that, once more in 64: some tokens in a thousand
-// (all of them in 64 bits: 4 million exponentials at GB300's FP64 rate would take 0.3 ms).
+// them in 32, by the hardware's exponential and reciprocal, with a known bound on
+// the error, and where two values that have to be told apart are closer than
+// that, those that may be among the J best once more in 64: some tokens in a
+// hundred, some ten values each.  (All of them in 64 bits: 4 million exponentials
+// at GB300's FP64 rate would take 0.3 ms.)
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -41,6 +45,8 @@ struct Choose {
     float *weights;
     int T, E, J, scoring, groups, kept, top, size;  // size: experts of a group
     unsigned per;                                   // e * per >> 20 = e / size
+    int lanes;                                      // that hold a group, if a power of two of them do; else 0
+    bool wide, wide_bias;                           // rows that allow the widest accesses
     int renormalize;
     float scale;
 };
@@ -87,9 +93,50 @@ __device__ __forceinline__ double sigmoid(double l) {
     const double e = exp(-fabs(l));
     return l < 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);
 }
-template <typename T>
-__device__ __forceinline__ float logit(const Choose &c, const T *row, int e) {
-    return to_f(row[e]);
+// The same for a comparison: see `slack`.
+__device__ __forceinline__ float sigmoid_about(float l) { return lt::fast_reciprocal(1.0f + lt::fast_exp2(-lt::kLog2E * l)); }
+
+// A lane's NV values of a row of E, outside for those that the row has not.
+template <typename T, int NV>
+__device__ __forceinline__ void load_row(const T *row, int lane, int E, bool wide, float outside, float (&f)[NV]) {
+    constexpr int BYTES = NV * static_cast<int>(sizeof(T)) < 16 ? NV * static_cast<int>(sizeof(T)) : 16;
+    constexpr int N = BYTES / static_cast<int>(sizeof(T));
+    if (wide) {
+        Pack<T, N> p[NV / N];
+#pragma unroll
+        for (int a = 0; a < NV / N; ++a) p[a] = load_if<T, N>(lane * NV + a * N < E, row + lane * NV + a * N);
+#pragma unroll
+        for (int a = 0; a < NV / N; ++a) {
+            float v[N];
+            p[a].get(v);
+#pragma unroll
+            for (int k = 0; k < N; ++k) f[a * N + k] = lane * NV + a * N < E ? v[k] : outside;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) f[i] = lane * NV + i < E ? to_f(row[lane * NV + i]) : outside;
+    }
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ void store_row(T *row, int lane, int E, bool wide, const float (&f)[NV]) {
+    constexpr int BYTES = NV * static_cast<int>(sizeof(T)) < 16 ? NV * static_cast<int>(sizeof(T)) : 16;
+    constexpr int N = BYTES / static_cast<int>(sizeof(T));
+    if (wide) {
+#pragma unroll
+        for (int a = 0; a < NV / N; ++a) {
+            float v[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = f[a * N + k];
+            Pack<T, N> p;
+            p.set(v);
+            if (lane * NV + a * N < E) store<T, N>(row + lane * NV + a * N, p);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane * NV + i < E) row[lane * NV + i] = from_f<T>(f[i]);
+    }
 }
 
 // The sum of the two largest of a warp's values (ranks; each lane gives its own best two; 0: none).
@@ -106,77 +153,94 @@ __device__ __forceinline__ F best_two(R first, R second, bool two, R *any) {
     }
     return sum;
 }
+template <typename R>
+__device__ __forceinline__ void keep_two(R r, R &first, R &second) {
+    second = r > first ? first : r > second ? r : second;
+    first = r > first ? r : first;
+}
+// Which groups compete: lane g holds the rank of group g's sum (0: none of its experts may be chosen).
+template <typename R>
+__device__ __forceinline__ bool stays(const Choose &c, R total, int lane) {
+    int before = 0;
+    for (int g = 0; g < c.groups; ++g) {
+        const R o = __shfl_sync(ALL, total, g);
+        before += o > total || (o == total && g < lane) ? 1 : 0;
+    }
+    return lane < c.groups && before < c.kept && total != 0;
+}
+__device__ __forceinline__ unsigned group_of(const Choose &c, int e) { return e * c.per >> 20; }
 
-// Everything of the choice in 64 bits, for a token whose values are too close
-// for 32.  `held` is the warp's room for E ranks.  Returns this lane's picks
-// (pick j at lane j % 32, in mine[j / 32]).
+// A warp's room: ranks and numbers of experts whose values are told apart in 64 bits.
+struct Held {
+    unsigned long long *rank;
+    int *expert;
+};
+
+// The choice in 64 bits, for a token whose values are too close for 32, among the
+// n experts of `held`; their groups too, if `grouped` (then held has all experts
+// in order).  Returns this lane's picks (pick j at lane j % 32, in mine[j / 32]).
 template <typename T>
-__device__ __noinline__ void choose_in_64(const Choose &c, const T *row, unsigned long long *held, int lane, int (&mine)[2]) {
+__device__ __noinline__ void choose_in_64(const Choose &c, const T *row, const Held &held, int n, bool grouped, int lane,
+                                          int (&mine)[2]) {
     mine[0] = mine[1] = -1;
     double m = -INFINITY, z = 0.0;
     if (c.scoring == EXPERTS_SOFTMAX) {
-        for (int e = lane; e < c.E; e += 32) m = fmax(m, static_cast<double>(logit(c, row, e)));
+        for (int e = lane; e < c.E; e += 32) m = fmax(m, static_cast<double>(to_f(row[e])));
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) m = fmax(m, __shfl_xor_sync(ALL, m, k));
-        for (int e = lane; e < c.E; e += 32) z += exp(static_cast<double>(logit(c, row, e)) - m);
+        for (int e = lane; e < c.E; e += 32) z += exp(static_cast<double>(to_f(row[e])) - m);
         z = warp_sum(z);
     }
-    for (int e = lane; e < c.E; e += 32) {
-        const float l = logit(c, row, e);
-        double v = c.scoring == EXPERTS_SOFTMAX ? exp(l - m) / z : sigmoid(static_cast<double>(l));
+    for (int k = lane; k < n; k += 32) {
+        const int e = held.expert[k];
+        const double l = static_cast<double>(to_f(row[e]));
+        double v = c.scoring == EXPERTS_SOFTMAX ? exp(l - m) / z : sigmoid(l);
         bool in = l > -INFINITY;
         if (c.bias != nullptr) {
             v += static_cast<double>(c.bias[e]);
             in = in && v > -INFINITY;
         }
-        held[e] = in ? rank_of(v) : 0ull;
+        held.rank[k] = in ? rank_of(v) : 0ull;
     }
     __syncwarp();
-    if (c.groups > 1) {
+    if (grouped) {
         unsigned long long total = 0;  // lane g: of group g
         for (int g = 0; g < c.groups; ++g) {
             unsigned long long first = 0, second = 0, any;
-            for (int i = lane; i < c.size; i += 32) {
-                const unsigned long long r = held[g * c.size + i];
-                second = r > first ? first : r > second ? r : second;
-                first = r > first ? r : first;
-            }
+            for (int i = lane; i < c.size; i += 32) keep_two(held.rank[g * c.size + i], first, second);
             const double sum = best_two<unsigned long long, double>(first, second, c.top > 1, &any);
             if (lane == g && any != 0) total = rank_of(sum);
         }
-        int before = 0;
-        for (int g = 0; g < c.groups; ++g) {
-            const unsigned long long o = __shfl_sync(ALL, total, g);
-            before += o > total || (o == total && g < lane) ? 1 : 0;
-        }
-        const unsigned keep = __ballot_sync(ALL, lane < c.groups && before < c.kept && total != 0);
-        for (int e = lane; e < c.E; e += 32)
-            if ((keep >> (e * c.per >> 20) & 1) == 0) held[e] = 0;
+        const unsigned keep = __ballot_sync(ALL, stays(c, total, lane));
+        for (int e = lane; e < n; e += 32)
+            if ((keep >> group_of(c, e) & 1) == 0) held.rank[e] = 0;
+        __syncwarp();
     }
     if (c.bias == nullptr)
-        for (int e = lane; e < c.E; e += 32)
-            if (held[e] != 0) held[e] = rank_of(static_cast<double>(logit(c, row, e)));
+        for (int k = lane; k < n; k += 32)
+            if (held.rank[k] != 0) held.rank[k] = rank_of(static_cast<double>(to_f(row[held.expert[k]])));
     __syncwarp();
     for (int j = 0; j < c.J; ++j) {
         unsigned long long best = 0;
-        int at = INT_MAX;
-        for (int e = lane; e < c.E; e += 32)
-            if (held[e] > best) {
-                best = held[e];
-                at = e;
+        int at = -1, who = INT_MAX;
+        for (int k = lane; k < n; k += 32)
+            if (held.rank[k] > best || (held.rank[k] == best && best != 0 && held.expert[k] < who)) {
+                best = held.rank[k];
+                at = k;
+                who = held.expert[k];
             }
         const unsigned long long high = warp_max(best);
         if (high == 0) break;
-        const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
-        if (who == at) held[at] = 0;
-        if ((j & 31) == lane) mine[j >> 5] = who;
+        const int pick = __reduce_min_sync(ALL, best == high ? who : INT_MAX);
+        if (best == high && who == pick) held.rank[at] = 0;
+        if ((j & 31) == lane) mine[j >> 5] = pick;
         __syncwarp();
     }
 }
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_constant__ Choose c) {
-    extern __shared__ unsigned long long held[];
+    extern __shared__ unsigned long long room[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * CHOOSE_WARPS + warp;
     tc::grid_trigger();
@@ -184,14 +248,11 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
     if (t >= c.T) return;
     const T *row = static_cast<const T *>(c.logits) + t * c.ld;
     const bool softmax = c.scoring == EXPERTS_SOFTMAX;
+    const int e0 = lane * NV;
     float l[NV];
+    load_row<T, NV>(row, lane, c.E, c.wide, -INFINITY, l);
     float m = -INFINITY;
     bool wrong = false;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < c.E ? logit(c, row, e) : -INFINITY;
-    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         wrong = wrong || l[i] != l[i];
@@ -199,7 +260,7 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
     }
     m = warp_max_f(m);
     wrong = __any_sync(ALL, wrong) || (softmax && m == INFINITY);
-    const bool summed = c.groups > 1 && c.top > 1;   // groups by sums of scores
+    const bool summed = c.groups > 1 && c.top > 1;  // groups by sums of scores
     float z = 1.0f;
     if (softmax && (c.bias != nullptr || !c.renormalize || summed) && m > -INFINITY) {
         z = 0.0f;
@@ -207,122 +268,167 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
         for (int i = 0; i < NV; ++i) z += expf(l[i] - m);
         z = warp_sum(z);
     }
-    // How far the difference of two scores may be off.  expf is within 4 units of 2^-24 of its value, sums
-    // and quotients within 1.  Sigmoid: 4 units a score.  Softmax, of the largest score 1 / z: 4 of its own
-    // exponential, less than 1 of the rounding of l - m (x exp(-x) < 0.4), and those of z: 36 of up to 31
-    // sums in a lane and 5 across, 11 of the exponentials (4, and the rounding of l - m at a mean of
-    // up to log 1024); 2 of quotient and product.
+    // How far the difference of two scores may be off, in units of 2^-24.  Sigmoid: the exponential is
+    // within 4 of its value and the rounding of its argument moves it by 1.44 |l|, of which a quarter and
+    // 0.33 at most reach the score; the sum adds 1, the reciprocal 2: 5 a score.  Softmax, of the largest
+    // score 1 / z: 4 of its own exponential (expf), less than 1 of the rounding of l - m (x exp(-x) < 0.4),
+    // and those of z: 36 of up to 31 sums in a lane and 5 across, 11 of the exponentials (4, and the
+    // rounding of l - m at a mean of up to log 1024); 2 of quotient and product.
     const float most = softmax ? 1.0f / z : 1.0f;
-    const float slack = softmax ? most * 0x1p-17f : 0x1p-21f;
-    auto value = [&](int i) {
-        const float s = softmax ? expf(l[i] - m) * most : sigmoid(l[i]);
-        return c.bias != nullptr && i * 32 + lane < c.E ? s + c.bias[i * 32 + lane] : s;
-    };
-    uint32_t key[NV];
+    const float slack = softmax ? most * 0x1p-17f : 0x1p-20f;
     float size = 1.0f;  // of what groups' sums add up
+    uint32_t key[NV];
+    float bias[NV];
+    if (c.bias != nullptr) load_row<float, NV>(c.bias, lane, c.E, c.wide_bias, -INFINITY, bias);
+    auto score = [&](int i) { return softmax ? expf(l[i] - m) * most : sigmoid_about(l[i]); };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         key[i] = 0;
         if (l[i] > -INFINITY && !wrong) {
-            const float v = c.bias != nullptr ? value(i) : l[i];
+            const float v = c.bias != nullptr ? score(i) + bias[i] : l[i];
             if (v > -INFINITY) {
                 key[i] = rank_of(v);
                 if (c.bias != nullptr) size = fmaxf(size, fabsf(v));
             }
         }
     }
-    bool doubt = false;
+    bool doubt = false, doubt_groups = false;
     if (c.groups > 1) {
-        uint32_t total = 0;
-        for (int g = 0; g < c.groups; ++g) {
-            uint32_t first = 0, second = 0, any;
+        uint32_t total = 0;  // lane g: of group g
+        auto rank = [&](int i) { return summed && c.bias == nullptr && key[i] != 0 ? rank_of(score(i)) : key[i]; };
+        if (c.lanes > 0) {  // a group is `lanes` lanes, a power of two
+            uint32_t first = 0, second = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = i * 32 + lane;
-                if ((e * c.per >> 20) == static_cast<unsigned>(g) && key[i] != 0) {
-                    const uint32_t r = summed && c.bias == nullptr ? rank_of(value(i)) : key[i];
-                    second = r > first ? first : r > second ? r : second;
-                    first = r > first ? r : first;
-                }
+            for (int i = 0; i < NV; ++i) keep_two(rank(i), first, second);
+            for (int k = 1; k < c.lanes; k <<= 1) {
+                const uint32_t o1 = __shfl_xor_sync(ALL, first, k), o2 = __shfl_xor_sync(ALL, second, k);
+                keep_two(o1, first, second);
+                keep_two(o2, first, second);
             }
-            const float sum = best_two<uint32_t, float>(first, second, c.top > 1, &any);
-            if (lane == g && any != 0) total = rank_of(sum);
+            float sum = of_rank(first);
+            if (c.top > 1 && second != 0) sum += of_rank(second);
+            const uint32_t mine = first != 0 ? rank_of(sum) : 0;
+            total = __shfl_sync(ALL, mine, lane * c.lanes & 31);
+            if (lane >= c.groups) total = 0;
+        } else {
+            for (int g = 0; g < c.groups; ++g) {
+                uint32_t first = 0, second = 0, any;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (group_of(c, e0 + i) == static_cast<unsigned>(g)) keep_two(rank(i), first, second);
+                const float sum = best_two<uint32_t, float>(first, second, c.top > 1, &any);
+                if (lane == g && any != 0) total = rank_of(sum);
+            }
         }
-        int before = 0;
-        for (int g = 0; g < c.groups; ++g) {
-            const uint32_t o = __shfl_sync(ALL, total, g);
-            before += o > total || (o == total && g < lane) ? 1 : 0;
-        }
-        const bool stays = lane < c.groups && before < c.kept && total != 0;
-        const unsigned keep = __ballot_sync(ALL, stays);
+        const bool stay = stays(c, total, lane);
+        const unsigned keep = __ballot_sync(ALL, stay);
         if (summed || c.bias != nullptr) {
-            const uint32_t low = __reduce_min_sync(ALL, stays ? total : 0xffffffffu);
-            size = warp_max_f(size);
-            const uint32_t out = warp_max(lane < c.groups && !stays ? total : 0u);
+            const uint32_t low = __reduce_min_sync(ALL, stay ? total : 0xffffffffu);
+            const uint32_t out = warp_max(lane < c.groups && !stay ? total : 0u);
+            if (c.bias != nullptr) size = warp_max_f(size);
             if (out != 0) {
                 const float a = of_rank(low), b = of_rank(out);
-                doubt = !(a - b >= 2.0f * slack + 0x1p-21f * size);  // 4 scores; 4 sums with biases, 2 of two values
+                doubt_groups = !(a - b >= 2.0f * slack + 0x1p-21f * size);  // 4 scores; 4 sums with biases, 2 of two values
             }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((keep >> ((i * 32 + lane) * c.per >> 20 & 31) & 1) == 0) key[i] = 0;
+            if ((keep >> (group_of(c, e0 + i) & 31) & 1) == 0) key[i] = 0;
     }
     int mine[2] = {-1, -1};
-    uint32_t best = 0;
-    int at = INT_MAX;
+    uint32_t best = 0, second = 0, taken = 0;  // this lane's best two that are left, and which are not
+    int at = INT_MAX, at_second = INT_MAX;
     auto look = [&] {
-        best = 0;
-        at = INT_MAX;
+        best = second = 0;
+        at = at_second = INT_MAX;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i * 32 + lane;
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t k = taken >> i & 1 ? 0u : key[i];
+            if (k > best) {
+                second = best;
+                at_second = at;
+                best = k;
+                at = e0 + i;
+            } else if (k > second) {
+                second = k;
+                at_second = e0 + i;
             }
+        }
     };
     look();
-    float last = 0.0f;
+    float last = 0.0f, floor = 0.0f;
     int last_who = -1;
-    const int rounds = c.bias != nullptr ? c.J + 1 : c.J;  // one more: the best that is left out
+    const int rounds = c.bias != nullptr && !doubt_groups ? c.J + 1 : doubt_groups ? 0 : c.J;  // one more: the best that is left out
     for (int j = 0; j < rounds; ++j) {
         const uint32_t high = warp_max(best);
         if (high == 0) break;
         const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
         if (c.bias != nullptr) {
             const float v = of_rank(high);
-            // values of equal logits and biases are equal in 64 bits too
-            if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)) &&  // 2 scores, 2 sums with the bias
-                !(logit(c, row, who) == logit(c, row, last_who) && c.bias[who] == c.bias[last_who]))
-                doubt = true;
+            // 2 scores, 2 sums with the bias; values of equal logits and biases are equal in 64 bits too
+            if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)))
+                doubt = doubt || !(to_f(row[who]) == to_f(row[last_who]) && c.bias[who] == c.bias[last_who]);
             last = v;
             last_who = who;
+            if (j < c.J) floor = v;
         }
         if (j < c.J && (j & 31) == lane) mine[j >> 5] = who;
         if (who == at) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane == who) key[i] = 0;
-            look();
+            taken |= 1u << (who - e0);
+            if (second != 0) {
+                best = second;
+                at = at_second;
+                second = 0;
+            } else {
+                look();
+            }
         }
     }
-    if (doubt) choose_in_64(c, row, held + static_cast<size_t>(warp) * c.E, lane, mine);
+    if (doubt || doubt_groups) {
+        Held held;
+        held.rank = room + static_cast<size_t>(warp) * c.E;
+        held.expert = reinterpret_cast<int *>(room + static_cast<size_t>(CHOOSE_WARPS) * c.E) + warp * c.E;
+        int n = c.E;
+        if (doubt_groups) {
+            for (int e = lane; e < c.E; e += 32) held.expert[e] = e;
+        } else {  // those that may be among the J best
+            const float low = floor - slack - 0x1p-22f * fabsf(floor);
+            int before = 0, mine_n = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) mine_n += key[i] != 0 && of_rank(key[i]) >= low ? 1 : 0;
+            n = mine_n;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int o = __shfl_up_sync(ALL, n, k);
+                if (lane >= k) n += o;
+            }
+            before = n - mine_n;
+            n = __shfl_sync(ALL, n, 31);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (key[i] != 0 && of_rank(key[i]) >= low) held.expert[before++] = e0 + i;
+        }
+        __syncwarp();
+        choose_in_64(c, row, held, n, doubt_groups, lane, mine);
+    }
 
     // weights of the picks
     float lj[2], w[2];
     float high = -INFINITY;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        lj[s] = mine[s] >= 0 ? logit(c, row, mine[s]) : -INFINITY;
+        lj[s] = mine[s] >= 0 ? to_f(row[mine[s]]) : -INFINITY;
         high = fmaxf(high, lj[s]);
     }
     float sum = 0.0f;
+    const int slots = c.J > 32 ? 2 : 1;
     if (c.renormalize) {
         // relative to the largest pick, so that no pick's score is lost below the smallest number
         high = warp_max_f(high);
         const float ref = softmax ? high : fminf(high, 0.0f);
-#pragma unroll
+        #pragma unroll
         for (int s = 0; s < 2; ++s) {
+            if (s >= slots) break;
             w[s] = softmax || lj[s] < 0.0f ? expf(lj[s] - ref) : 1.0f;
             if (!softmax) w[s] /= 1.0f + expf(-fabsf(lj[s]));
             if (mine[s] < 0) w[s] = 0.0f;
@@ -332,6 +438,7 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+        if (s >= slots) break;
         if (c.renormalize)
             w[s] /= sum;
         else
@@ -353,6 +460,7 @@ struct ChooseBackward {
     void *dlogits;
     long long ld, ldd;
     int T, E, J, scoring, renormalize;
+    bool wide;  // rows that allow the widest accesses
     float scale;
 };
 
@@ -385,11 +493,9 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_backward_kernel(cons
     float z = 1.0f;
     if (all) {
         high = -INFINITY;
+        load_row<T, NV>(row, lane, c.E, c.wide, -INFINITY, x);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            x[i] = i * 32 + lane < c.E ? to_f(row[i * 32 + lane]) : -INFINITY;
-            high = fmaxf(high, x[i]);
-        }
+        for (int i = 0; i < NV; ++i) high = fmaxf(high, x[i]);
         high = warp_max_f(high);
         z = 0.0f;
 #pragma unroll
@@ -440,14 +546,15 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_backward_kernel(cons
         const float what = __shfl_sync(ALL, j < 32 ? g[0] : g[1], j & 31);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (i * 32 + lane == who) d[i] += what;
+            if (lane * NV + i == who) d[i] += what;
     }
     T *out = static_cast<T *>(c.dlogits) + t * c.ldd;
+    if (all) {
+        const float share = 1.0f / z;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (all) d[i] = any ? x[i] / z * (d[i] - mean) : 0.0f;
-        if (i * 32 + lane < c.E) out[i * 32 + lane] = from_f<T>(d[i]);
+        for (int i = 0; i < NV; ++i) d[i] = any ? x[i] * share * (d[i] - mean) : 0.0f;
     }
+    store_row<T, NV>(out, lane, c.E, c.wide, d);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -460,6 +567,11 @@ int with_experts(int E, F &&f) {
            : E <= 256 ? f(lt::Int<8>{})
            : E <= 512 ? f(lt::Int<16>{})
                       : f(lt::Int<32>{});
+}
+// Whether rows of E values allow load_row's accesses with nv values a lane.
+bool wide_rows(const void *p, long long ld, int E, int bytes, int nv) {
+    const int access = nv * bytes < 16 ? nv * bytes : 16;
+    return reinterpret_cast<uintptr_t>(p) % access == 0 && ld * bytes % access == 0 && static_cast<long long>(E) * bytes % access == 0;
 }
 int check_choice(int type, int T, int E, int J, int scoring) {
     if (type < LINEAR_F32 || type > LINEAR_F16 || (scoring != EXPERTS_SOFTMAX && scoring != EXPERTS_SIGMOID))
@@ -498,10 +610,14 @@ extern "C" int expert_choose(int type, int T, int E, int J, const void *logits, 
     c.renormalize = renormalize != 0, c.scale = scale;
     if (groups == 1) c.top = 1;
     const bool in_64 = bias != nullptr || (groups > 1 && group_top > 1);
-    const size_t smem = in_64 ? sizeof(unsigned long long) * CHOOSE_WARPS * static_cast<size_t>(E) : 0;
+    const size_t smem = in_64 ? (sizeof(unsigned long long) + sizeof(int)) * CHOOSE_WARPS * static_cast<size_t>(E) : 0;
     sg_nvtx::Range r("experts: choose");
     return with_experts(E, [&](auto n) {
         constexpr int NV = decltype(n)::value;
+        c.wide = wide_rows(logits, ldl, E, b, NV);
+        c.wide_bias = wide_rows(bias, 0, E, 4, NV);
+        const int lanes = c.size / NV;
+        c.lanes = c.size % NV == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         auto run = [&](auto kernel) { return launched(tc::launch(kernel, token_blocks(T), dim3(CHOOSE_WARPS * 32), smem, stream, c)); };
         return type == LINEAR_F32    ? run(choose_kernel<float, NV>)
                : type == LINEAR_BF16 ? run(choose_kernel<__nv_bfloat16, NV>)
@@ -530,6 +646,7 @@ extern "C" int expert_choose_backward(int type, int T, int E, int J, const float
     sg_nvtx::Range r("experts: choose backward");
     return with_experts(E, [&](auto n) {
         constexpr int NV = decltype(n)::value;
+        c.wide = wide_rows(logits, ldl, E, b, NV) && wide_rows(dlogits, ldd, E, b, NV);
         auto run = [&](auto kernel) { return launched(tc::launch(kernel, token_blocks(T), dim3(CHOOSE_WARPS * 32), 0, stream, c)); };
         return type == LINEAR_F32    ? run(choose_backward_kernel<float, NV>)
                : type == LINEAR_BF16 ? run(choose_backward_kernel<__nv_bfloat16, NV>)

@@ -48,6 +48,32 @@ static const char *const lib_names[] = {"linear_forward", "linear_forward_worksp
                                         "expert_linear_backward_workspace_size", "expert_sort", "expert_sort_workspace_size",
                                         "expert_gather", "expert_combine", "expert_combine_backward"};
 
+/* The operators around the layers, bound by bind_more(). */
+static struct {
+    int (*layer_norm_forward)(int, int, int, const void *, int64_t, const void *, const void *, float, float *, void *, int64_t,
+                              stream_t);
+    int (*layer_norm_backward)(int, int, int, const void *, int64_t, const void *, int64_t, const void *, const float *, void *,
+                               int64_t, void *, void *, void *, size_t, stream_t);
+    size_t (*layer_norm_backward_workspace_size)(int, int, int, int);
+    int (*expert_choose)(int, int, int, int, const void *, int64_t, const float *, int, int, int, int, int, float, int *, float *,
+                         stream_t);
+    int (*expert_choose_backward)(int, int, int, int, const float *, const int *, const void *, int64_t, int, int, float, void *,
+                                  int64_t, stream_t);
+    int (*linear_cross_entropy_forward)(int, int, int, int, const void *, int64_t, const void *, int64_t, int, const void *, int,
+                                        float *, float *, void *, size_t, stream_t);
+    size_t (*linear_cross_entropy_forward_workspace_size)(int, int, int, int, const void *, int64_t, const void *, int64_t, int);
+    int (*linear_cross_entropy_backward)(int, int, int, int, const float *, const float *, const void *, int64_t, const void *,
+                                         int64_t, int, const void *, int, const float *, void *, int64_t, void *, int64_t, void *,
+                                         size_t, stream_t);
+    size_t (*linear_cross_entropy_backward_workspace_size)(int, int, int, int, const void *, int64_t, const void *, int64_t, int,
+                                                           int, int);
+} more;
+static const char *const more_names[] = {"layer_norm_forward", "layer_norm_backward", "layer_norm_backward_workspace_size",
+                                         "expert_choose", "expert_choose_backward", "linear_cross_entropy_forward",
+                                         "linear_cross_entropy_forward_workspace_size", "linear_cross_entropy_backward",
+                                         "linear_cross_entropy_backward_workspace_size"};
+static PyObject *scorings; /* NULL: not bound */
+
 /* A launch may wait for room in the stream's queue, and what it waits for, such as a
  * function on the host, may want the interpreter: it is not held meanwhile. */
 #define LAUNCH(status, call)   \
@@ -510,18 +536,291 @@ static PyObject *combine_backward(PyObject *self, PyObject *const *a, Py_ssize_t
     return result;
 }
 
+/* float32 (M,), or NULL for None; 0 for anything else */
+static int floats_of(PyObject *o, int64_t device, int64_t M, const float **p) {
+    Tensor t;
+    *p = NULL;
+    if (o == Py_None) return 1;
+    if (!look(o, kinds[0], device, &t) || !flat(&t, 1, M, 0)) return 0;
+    *p = t.data;
+    return 1;
+}
+/* A vector (N,) of this type, or NULL for None. */
+static int vector_of(PyObject *o, PyObject *dtype, int64_t device, int64_t N, const void **p) {
+    Tensor t;
+    *p = NULL;
+    if (o == Py_None) return 1;
+    if (!look(o, dtype, device, &t) || !flat(&t, 1, N, 0)) return 0;
+    *p = t.data;
+    return 1;
+}
+static int truth(PyObject *o, int *v) {
+    *v = o == Py_True;
+    return *v || o == Py_False;
+}
+static int scoring_of(PyObject *name, int *v) {
+    int64_t n;
+    if (!whole(PyDict_GetItemWithError(scorings, name), &n)) return 0;
+    *v = (int)n;
+    return 1;
+}
+static int small_number(PyObject *o, int *v) {
+    int64_t n;
+    if (!PyLong_CheckExact(o) || !whole(o, &n) || n < INT32_MIN || n > INT32_MAX) return 0;
+    *v = (int)n;
+    return 1;
+}
+
+/* norm(x, weight, bias, eps, stats, out) -> out */
+static PyObject *norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    PyObject *dtype;
+    int64_t device, ldx, ldy;
+    stream_t stream;
+    Tensor x, t;
+    const void *weight, *bias;
+    float *stats = NULL;
+    void *y;
+    if (n != 6 || scorings == NULL || !PyFloat_CheckExact(a[3])) UNUSUAL();
+    const int kind = kind_of(a[0], &dtype);
+    if (kind < 0 || !here(a[0], &device, &stream) || !look(a[0], dtype, device, &x) || x.dims != 2 ||
+        !rows_of(&x, x.size[0], x.size[1], &ldx) || !small(x.size[0], x.size[1], 0))
+        UNUSUAL();
+    const int64_t M = x.size[0], N = x.size[1];
+    if (!vector_of(a[1], dtype, device, N, &weight) || !vector_of(a[2], dtype, device, N, &bias)) UNUSUAL();
+    if (a[4] != Py_None) {
+        if (!look(a[4], kinds[0], device, &t) || !flat(&t, 2, M, 2)) UNUSUAL();
+        stats = t.data;
+    }
+    PyObject *out = a[5];
+    if (out == Py_None) {
+        out = new_tensor(2, x.size, dtype, a[0], &y);
+        if (out == NULL) UNUSUAL();
+        ldy = N > 1 ? N : 1;
+    } else {
+        if (!look(out, dtype, device, &t) || !rows_of(&t, M, N, &ldy)) UNUSUAL();
+        y = t.data;
+        Py_INCREF(out);
+    }
+    int st;
+    LAUNCH(st, more.layer_norm_forward(kind, (int)M, (int)N, x.data, ldx, weight, bias, (float)PyFloat_AS_DOUBLE(a[3]), stats, y, ldy,
+                                       stream));
+    if (st == 0) return out;
+    Py_DECREF(out);
+    return PyLong_FromLong(st);
+}
+
+/* norm_backward(dy, x, weight, stats, need_dx, need_dweight, need_dbias) -> (dx, dweight, dbias) */
+static PyObject *norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    PyObject *dtype, *made[3] = {NULL, NULL, NULL}, *hold = NULL, *result = NULL;
+    int64_t device, lddy, ldx;
+    stream_t stream;
+    Tensor g, x, t;
+    const void *weight;
+    void *p[3] = {NULL, NULL, NULL}, *ws = NULL;
+    int want[3];
+    if (n != 7 || scorings == NULL) UNUSUAL();
+    const int kind = kind_of(a[1], &dtype);
+    if (kind < 0 || !here(a[1], &device, &stream) || !look(a[1], dtype, device, &x) || !look(a[0], dtype, device, &g) || x.dims != 2)
+        UNUSUAL();
+    const int64_t M = x.size[0], N = x.size[1];
+    if (!small(M, N, 0) || !rows_of(&x, M, N, &ldx) || !rows_of(&g, M, N, &lddy) || !vector_of(a[2], dtype, device, N, &weight) ||
+        !look(a[3], kinds[0], device, &t) || !flat(&t, 2, M, 2) || !truth(a[4], &want[0]) || !truth(a[5], &want[1]) ||
+        !truth(a[6], &want[2]))
+        UNUSUAL();
+    const size_t need = more.layer_norm_backward_workspace_size((int)M, (int)N, want[1], want[2]);
+    int ok = 1;
+    for (int i = 0; i < 3 && ok; ++i)
+        if (want[i]) ok = (made[i] = new_tensor(i == 0 ? 2 : 1, x.size + (i == 0 ? 0 : 1), dtype, a[1], &p[i])) != NULL;
+    if (ok && scratch(need, a[1], &hold, &ws)) {
+        int st;
+        LAUNCH(st, more.layer_norm_backward(kind, (int)M, (int)N, g.data, lddy, x.data, ldx, weight, t.data, p[0], N > 1 ? N : 1, p[1],
+                                            p[2], ws, need, stream));
+        Py_XDECREF(hold);
+        result = st != 0 ? PyLong_FromLong(st)
+                         : PyTuple_Pack(3, want[0] ? made[0] : Py_None, want[1] ? made[1] : Py_None, want[2] ? made[2] : Py_None);
+    }
+    for (int i = 0; i < 3; ++i) Py_XDECREF(made[i]);
+    if (result == NULL) UNUSUAL();
+    return result;
+}
+
+/* choose(logits, choices, bias, scoring, groups, kept_groups, group_top, renormalize, scale) -> (chosen, weights) */
+static PyObject *choose(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    PyObject *dtype;
+    int64_t device, ld;
+    stream_t stream;
+    Tensor l;
+    const float *bias;
+    int J, how, groups, kept, top, renormalize;
+    void *cp, *wp;
+    if (n != 9 || scorings == NULL || !PyFloat_CheckExact(a[8])) UNUSUAL();
+    const int kind = kind_of(a[0], &dtype);
+    if (kind < 0 || !here(a[0], &device, &stream) || !look(a[0], dtype, device, &l) || l.dims != 2 ||
+        !rows_of(&l, l.size[0], l.size[1], &ld) || !small(l.size[0], l.size[1], 0) || !floats_of(a[2], device, l.size[1], &bias) ||
+        !small_number(a[1], &J) || J < 0 || !scoring_of(a[3], &how) || !small_number(a[4], &groups) || !small_number(a[5], &kept) ||
+        !small_number(a[6], &top) || !truth(a[7], &renormalize))
+        UNUSUAL();
+    const int64_t size[2] = {l.size[0], J};
+    PyObject *chosen = new_tensor(2, size, int32_type, a[0], &cp);
+    PyObject *weights = chosen == NULL ? NULL : new_tensor(2, size, kinds[0], a[0], &wp);
+    if (weights == NULL) {
+        Py_XDECREF(chosen);
+        UNUSUAL();
+    }
+    int st;
+    LAUNCH(st, more.expert_choose(kind, (int)l.size[0], (int)l.size[1], J, l.data, ld, bias, how, groups, kept, top, renormalize,
+                                  (float)PyFloat_AS_DOUBLE(a[8]), cp, wp, stream));
+    PyObject *result = st == 0 ? PyTuple_Pack(2, chosen, weights) : PyLong_FromLong(st);
+    Py_DECREF(chosen);
+    Py_DECREF(weights);
+    return result;
+}
+
+/* choose_backward(dweights, logits, chosen, scoring, renormalize, scale) -> dlogits */
+static PyObject *choose_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    PyObject *dtype;
+    int64_t device, ld;
+    stream_t stream;
+    Tensor l, c, g;
+    int how, renormalize;
+    void *dp;
+    if (n != 6 || scorings == NULL || !PyFloat_CheckExact(a[5])) UNUSUAL();
+    const int kind = kind_of(a[1], &dtype);
+    if (kind < 0 || !here(a[1], &device, &stream) || !look(a[1], dtype, device, &l) || l.dims != 2 ||
+        !rows_of(&l, l.size[0], l.size[1], &ld) || !small(l.size[0], l.size[1], 0) || !look(a[2], int32_type, device, &c) ||
+        c.dims != 2 || !flat(&c, 2, l.size[0], c.size[1]) || !small(c.size[1], 0, 0) || !look(a[0], kinds[0], device, &g) ||
+        !flat(&g, 2, l.size[0], c.size[1]) || !scoring_of(a[3], &how) || !truth(a[4], &renormalize))
+        UNUSUAL();
+    PyObject *d = new_tensor(2, l.size, dtype, a[1], &dp);
+    if (d == NULL) UNUSUAL();
+    int st;
+    LAUNCH(st, more.expert_choose_backward(kind, (int)l.size[0], (int)l.size[1], (int)c.size[1], g.data, c.data, l.data, ld, how,
+                                           renormalize, (float)PyFloat_AS_DOUBLE(a[5]), dp, l.size[1] > 1 ? l.size[1] : 1, stream));
+    if (st == 0) return d;
+    Py_DECREF(d);
+    return PyLong_FromLong(st);
+}
+
+/* What both calls of a head's loss take: x, w and targets. */
+typedef struct {
+    PyObject *dtype;
+    int64_t device, M, N, K, ldx;
+    stream_t stream;
+    Tensor x, w, t;
+    Weight m;
+    int kind, target_bytes;
+} Head;
+static int head_of(PyObject *x, PyObject *w, PyObject *targets, Head *h) {
+    h->kind = kind_of(x, &h->dtype);
+    if (h->kind < 0 || !here(x, &h->device, &h->stream) || !look(x, h->dtype, h->device, &h->x) ||
+        !look(w, h->dtype, h->device, &h->w) || h->x.dims != 2 || !weight_of(&h->w, 2, &h->m) ||
+        !rows_of(&h->x, h->x.size[0], h->m.K, &h->ldx) || !PyObject_TypeCheck(targets, (PyTypeObject *)tensor_type))
+        return 0;
+    h->M = h->x.size[0], h->K = h->m.K, h->N = h->m.N;
+    PyObject *d = PyObject_GetAttr(targets, s_dtype);
+    Py_XDECREF(d);
+    h->target_bytes = d == int32_type ? 4 : 8;
+    return (d == int32_type || d == int64_type) && look(targets, d, h->device, &h->t) && flat(&h->t, 1, h->M, 0) &&
+           small(h->M, h->N, h->K);
+}
+
+/* cross_entropy(x, w, targets) -> (loss, lse) */
+static PyObject *cross_entropy(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Head h;
+    void *lp, *ep, *ws;
+    PyObject *hold = NULL;
+    if (n != 3 || scorings == NULL || !head_of(a[0], a[1], a[2], &h)) UNUSUAL();
+    const size_t need = more.linear_cross_entropy_forward_workspace_size(h.kind, (int)h.M, (int)h.N, (int)h.K, h.x.data, h.ldx, h.w.data,
+                                                                         h.m.ld, h.m.order);
+    PyObject *loss = new_tensor(1, &h.M, kinds[0], a[0], &lp);
+    PyObject *lse = loss == NULL ? NULL : new_tensor(1, &h.M, kinds[0], a[0], &ep);
+    if (lse == NULL || !scratch(need, a[0], &hold, &ws)) {
+        Py_XDECREF(loss);
+        Py_XDECREF(lse);
+        UNUSUAL();
+    }
+    int st;
+    LAUNCH(st, more.linear_cross_entropy_forward(h.kind, (int)h.M, (int)h.N, (int)h.K, h.x.data, h.ldx, h.w.data, h.m.ld, h.m.order,
+                                                 h.t.data, h.target_bytes, lp, ep, ws, need, h.stream));
+    Py_XDECREF(hold);
+    PyObject *result = st == 0 ? PyTuple_Pack(2, loss, lse) : PyLong_FromLong(st);
+    Py_DECREF(loss);
+    Py_DECREF(lse);
+    return result;
+}
+
+/* cross_entropy_backward(dloss, x, w, targets, lse, dlse, need_dx, need_dw) -> (dx, dw) */
+static PyObject *cross_entropy_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Head h;
+    const float *dloss, *dlse, *lse;
+    int want_dx, want_dw;
+    void *dxp = NULL, *dwp = NULL, *ws = NULL;
+    PyObject *dx = NULL, *dw = NULL, *hold = NULL, *result = NULL;
+    if (n != 8 || scorings == NULL || a[4] == Py_None || !head_of(a[1], a[2], a[3], &h) || !floats_of(a[0], h.device, h.M, &dloss) ||
+        !floats_of(a[4], h.device, h.M, &lse) || !floats_of(a[5], h.device, h.M, &dlse) || !truth(a[6], &want_dx) ||
+        !truth(a[7], &want_dw))
+        UNUSUAL();
+    const size_t need = more.linear_cross_entropy_backward_workspace_size(h.kind, (int)h.M, (int)h.N, (int)h.K, h.x.data, h.ldx,
+                                                                          h.w.data, h.m.ld, h.m.order, want_dx, want_dw);
+    const int64_t dx_size[2] = {h.M, h.K}, dw_size[2] = {h.m.order ? h.N : h.K, h.m.order ? h.K : h.N};
+    int ok = !want_dx || (dx = new_tensor(2, dx_size, h.dtype, a[1], &dxp)) != NULL;
+    ok = ok && (!want_dw || (dw = new_tensor(2, dw_size, h.dtype, a[1], &dwp)) != NULL);
+    if (ok && want_dw && h.m.order) {
+        PyObject *args[3] = {dw, minus1, minus2};
+        PyObject *turned = PyObject_VectorcallMethod(s_transpose, args, 3 | PY_VECTORCALL_ARGUMENTS_OFFSET, NULL);
+        Py_DECREF(dw);
+        dw = turned;
+        ok = dw != NULL;
+    }
+    if (ok && scratch(need, a[1], &hold, &ws)) {
+        int st;
+        LAUNCH(st, more.linear_cross_entropy_backward(h.kind, (int)h.M, (int)h.N, (int)h.K, dloss, dlse, h.x.data, h.ldx, h.w.data,
+                                                      h.m.ld, h.m.order, h.t.data, h.target_bytes, lse, dxp, h.K, dwp, dw_size[1], ws,
+                                                      need, h.stream));
+        Py_XDECREF(hold);
+        result = st == 0 ? PyTuple_Pack(2, want_dx ? dx : Py_None, want_dw ? dw : Py_None) : PyLong_FromLong(st);
+    }
+    Py_XDECREF(dx);
+    Py_XDECREF(dw);
+    if (result == NULL) UNUSUAL();
+    return result;
+}
+
+static int addresses(PyObject *functions, const char *const *names, size_t n, void **slots) {
+    for (size_t i = 0; i < n; ++i) {
+        PyObject *v = PyDict_GetItemString(functions, names[i]);
+        if (v == NULL) {
+            PyErr_Format(PyExc_KeyError, "%s", names[i]);
+            return 0;
+        }
+        slots[i] = PyLong_AsVoidPtr(v);
+        if (slots[i] == NULL) {
+            if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s", names[i]);
+            return 0;
+        }
+    }
+    return 1;
+}
+
+/* bind_more(functions: dict of addresses, scorings: dict), after bind(); without it
+ * the operators around the layers answer NotImplemented */
+static PyObject *bind_more(PyObject *self, PyObject *args) {
+    PyObject *functions, *names;
+    _Static_assert(sizeof more == sizeof more_names / sizeof *more_names * sizeof(void *), "a name for each function");
+    if (!PyArg_ParseTuple(args, "O!O!", &PyDict_Type, &functions, &PyDict_Type, &names) ||
+        !addresses(functions, more_names, sizeof more_names / sizeof *more_names, (void **)&more))
+        return NULL;
+    scorings = Py_NewRef(names);
+    Py_RETURN_NONE;
+}
+
 /* bind(functions: dict of addresses, objects: tuple) */
 static PyObject *bind(PyObject *self, PyObject *args) {
     PyObject *functions, *objects;
-    if (!PyArg_ParseTuple(args, "O!O!", &PyDict_Type, &functions, &PyTuple_Type, &objects)) return NULL;
-    void **slots = (void **)&lib;
     _Static_assert(sizeof lib == sizeof lib_names / sizeof *lib_names * sizeof(void *), "a name for each function");
-    for (size_t i = 0; i < sizeof lib_names / sizeof *lib_names; ++i) {
-        PyObject *v = PyDict_GetItemString(functions, lib_names[i]);
-        if (v == NULL) return PyErr_Format(PyExc_KeyError, "%s", lib_names[i]);
-        slots[i] = PyLong_AsVoidPtr(v);
-        if (slots[i] == NULL) return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "%s", lib_names[i]);
-    }
+    if (!PyArg_ParseTuple(args, "O!O!", &PyDict_Type, &functions, &PyTuple_Type, &objects) ||
+        !addresses(functions, lib_names, sizeof lib_names / sizeof *lib_names, (void **)&lib))
+        return NULL;
     if (!PyArg_ParseTuple(objects, "OOOOO!(OOO)OOO", &tensor_type, &empty, &raw_stream, &get_device, &PyDict_Type, &activations,
                           &kinds[0], &kinds[1], &kinds[2], &int32_type, &int64_type, &uint8_type))
         return NULL;
@@ -542,6 +841,13 @@ static PyObject *bind(PyObject *self, PyObject *args) {
 }
 
 static PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, NULL},
+                                {"bind_more", bind_more, METH_VARARGS, NULL},
+                                {"norm", (PyCFunction)(void (*)(void))norm, METH_FASTCALL, NULL},
+                                {"norm_backward", (PyCFunction)(void (*)(void))norm_backward, METH_FASTCALL, NULL},
+                                {"choose", (PyCFunction)(void (*)(void))choose, METH_FASTCALL, NULL},
+                                {"choose_backward", (PyCFunction)(void (*)(void))choose_backward, METH_FASTCALL, NULL},
+                                {"cross_entropy", (PyCFunction)(void (*)(void))cross_entropy, METH_FASTCALL, NULL},
+                                {"cross_entropy_backward", (PyCFunction)(void (*)(void))cross_entropy_backward, METH_FASTCALL, NULL},
                                 {"forward", (PyCFunction)(void (*)(void))forward, METH_FASTCALL, NULL},
                                 {"backward", (PyCFunction)(void (*)(void))backward, METH_FASTCALL, NULL},
                                 {"sort", (PyCFunction)(void (*)(void))sort, METH_FASTCALL, NULL},
