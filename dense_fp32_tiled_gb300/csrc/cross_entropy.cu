@@ -31,27 +31,38 @@ namespace {
 using namespace product;
 
 // ---- each token's parts joined ---------------------------------------------------
-// 32 tokens a block: warp y takes parts y, y + 8, ..., and the warps' results are
-// joined in their order.
-constexpr int JOIN_WARPS = 8;
-__device__ __forceinline__ void join(float2 &a, float2 b) {
+// A block takes `tokens` tokens (a power of two, up to 32) and gives each as many
+// threads: thread k takes parts k, k + threads, ..., four at a time, and the
+// threads' results are joined by halves.
+constexpr int JOIN_THREADS = 256;
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.0f : m;
-    a = make_float2(m, a.y * expf(a.x - ref) + b.y * expf(b.x - ref));
+    return make_float2(m, a.y * expf(a.x - ref) + b.y * expf(b.x - ref));
 }
-__global__ void __launch_bounds__(JOIN_WARPS * 32)
-join_kernel(const float2 *__restrict__ parts, int n, int M, int N, const Loss l, float *__restrict__ loss, float *__restrict__ lse) {
-    __shared__ float2 part[JOIN_WARPS][32];
-    const int i = blockIdx.x * 32 + threadIdx.x;
+__global__ void __launch_bounds__(JOIN_THREADS)
+join_kernel(const float2 *__restrict__ parts, int n, int M, int N, int tokens, const Loss l, float *__restrict__ loss,
+            float *__restrict__ lse) {
+    __shared__ float2 part[JOIN_THREADS];
+    const int at = threadIdx.x & (tokens - 1), each = JOIN_THREADS / tokens;
+    const int i = blockIdx.x * tokens + at;
     tc::grid_trigger();
     tc::grid_wait();
-    float2 a = make_float2(-INFINITY, 0.0f);
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    float2 a = none;
     if (i < M)
-        for (int k = threadIdx.y; k < n; k += JOIN_WARPS) join(a, parts[static_cast<long long>(k) * M + i]);
-    part[threadIdx.y][threadIdx.x] = a;
-    __syncthreads();
-    if (threadIdx.y != 0 || i >= M) return;
+        for (int k = threadIdx.x / tokens; k < n; k += 4 * each) {
+            float2 p[4];
 #pragma unroll
-    for (int k = 1; k < JOIN_WARPS; ++k) join(a, part[k][threadIdx.x]);
+            for (int u = 0; u < 4; ++u) p[u] = k + u * each < n ? parts[static_cast<long long>(k + u * each) * M + i] : none;
+            a = join(a, join(join(p[0], p[1]), join(p[2], p[3])));
+        }
+    part[threadIdx.x] = a;
+    for (int k = JOIN_THREADS / 2; k >= tokens; k >>= 1) {
+        __syncthreads();
+        if (threadIdx.x < k) part[threadIdx.x] = join(part[threadIdx.x], part[threadIdx.x + k]);
+    }
+    if (threadIdx.x >= tokens || i >= M) return;
+    a = part[threadIdx.x];
     const float s = a.x + logf(a.y);
     const long long t = target_of(l, i);
     lse[i] = s;
@@ -237,8 +248,11 @@ int forward(const Head &h, float *loss, float *lse, void *workspace, size_t work
         parts *= 2;
     }
     sg_nvtx::Range r("cross entropy: join");
-    const cudaError_t err = tc::launch(join_kernel, static_cast<unsigned>((h.M + 31) / 32), dim3(32, JOIN_WARPS), 0, stream,
-                                       static_cast<const float2 *>(p.loss.parts), parts, h.M, h.N, p.loss, loss, lse);
+    int tokens = 32;  // of a block: fewer where there are few
+    while (tokens > 1 && h.M < tokens * 2 * d.sms) tokens /= 2;
+    const cudaError_t err = tc::launch(join_kernel, static_cast<unsigned>((static_cast<long long>(h.M) + tokens - 1) / tokens),
+                                       dim3(JOIN_THREADS), 0, stream, static_cast<const float2 *>(p.loss.parts), parts, h.M, h.N, tokens,
+                                       p.loss, loss, lse);
     if (err == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
     return SGEMM_ERR_LAUNCH;

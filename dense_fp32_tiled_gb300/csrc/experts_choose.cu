@@ -3,21 +3,20 @@
 //
 // A warp takes a token; lane l holds the logits of experts l * NV to l * NV + NV - 1
 // (in wide accesses where the rows allow them; a group of experts is then some
-// lanes in a row).  The J best are picked one after the other: each lane knows its
-// own best two, one warp maximum finds the value, one minimum the lowest expert
-// that has it, and only a lane that lost both looks for its next two.  Values are
-// compared as whole numbers of the same order as the floats (0: not to be
-// chosen), so a maximum is one instruction.  Bound by the instructions of those
-// rounds.
+// lanes in a row).  The J + 1 lanes with the largest best value give a bound that
+// all picks reach; the some ten experts that do are brought together, one a
+// lane, and each counts those before it: its place.  (Picking one after the
+// other took 36 us for 16384 tokens of 256 experts in 8 groups; this NN.)  Values are compared as
+// whole numbers of the same order as the floats (0: not to be chosen), so a
+// maximum over a warp is one instruction.  Bound by instructions.
 //
 // What is compared.  Scores are increasing in the logits, so without a bias the
 // logits themselves are: no rounding enters.  With a bias (and for the sums of a
 // group's best two) the order is that of the scores in 64 bits.  A warp computes
 // them in 32, by the hardware's exponential and reciprocal, with a known bound on
 // the error, and where two values that have to be told apart are closer than
-// that, those that may be among the J best once more in 64: some tokens in a
-// hundred, some ten values each.  (All of them in 64 bits: 4 million exponentials
-// at GB300's FP64 rate would take 0.3 ms.)
+// that, the few that matter once more in 64: for some tokens in a hundred.  (All
+// of them in 64 bits: 4 million exponentials at GB300's FP64 rate would take 0.3 ms.)
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -53,8 +52,8 @@ struct Choose {
 
 // Floats as unsigned numbers of the same order; -0 is taken for 0.
 __device__ __forceinline__ uint32_t rank_of(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    return u >> 31 ? ~u : u | 0x80000000u;
+    const int u = __float_as_int(v + 0.0f);
+    return static_cast<uint32_t>(u ^ (u >> 31 | INT_MIN));
 }
 __device__ __forceinline__ float of_rank(uint32_t r) { return __uint_as_float(r >> 31 ? r & 0x7fffffffu : ~r); }
 __device__ __forceinline__ unsigned long long rank_of(double v) {
@@ -79,9 +78,15 @@ __device__ __forceinline__ F warp_sum(F v) {
     for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(ALL, v, k);
     return v;
 }
+// The larger, or a NaN if either is one.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float warp_max_f(float v) {
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, k));
+    for (int k = 16; k > 0; k >>= 1) v = max_or_nan(v, __shfl_xor_sync(ALL, v, k));
     return v;
 }
 // logistic(l), small ones included
@@ -158,31 +163,54 @@ __device__ __forceinline__ void keep_two(R r, R &first, R &second) {
     second = r > first ? first : r > second ? r : second;
     first = r > first ? r : first;
 }
-// Which groups compete: lane g holds the rank of group g's sum (0: none of its experts may be chosen).
-template <typename R>
-__device__ __forceinline__ bool stays(const Choose &c, R total, int lane) {
-    int before = 0;
-    for (int g = 0; g < c.groups; ++g) {
-        const R o = __shfl_sync(ALL, total, g);
-        before += o > total || (o == total && g < lane) ? 1 : 0;
+// Which groups compete, a bit each: lane g holds the rank of group g's sum (0: none of its experts may be chosen).
+__device__ __forceinline__ unsigned kept_groups(const Choose &c, uint32_t total, int lane) {
+    unsigned keep = 0;
+    for (int k = 0; k < c.kept; ++k) {
+        const uint32_t high = warp_max(total);
+        if (high == 0) break;
+        const unsigned one = __ballot_sync(ALL, total == high);
+        keep |= one & (0u - one);  // the lowest
+        if ((keep >> lane & 1) != 0) total = 0;
     }
-    return lane < c.groups && before < c.kept && total != 0;
+    return keep;
 }
 __device__ __forceinline__ unsigned group_of(const Choose &c, int e) { return e * c.per >> 20; }
 
 // A warp's room: ranks and numbers of experts whose values are told apart in 64 bits.
 struct Held {
     unsigned long long *rank;
-    int *expert;
+    unsigned short *expert;
 };
 
-// The choice in 64 bits, for a token whose values are too close for 32, among the
-// n experts of `held`; their groups too, if `grouped` (then held has all experts
-// in order).  Returns this lane's picks (pick j at lane j % 32, in mine[j / 32]).
+// Puts the experts of this lane for which which(i) holds into `held`, all lanes' in
+// the order of their numbers.  How many there are; none are put there if more than `room`.
+template <int NV, typename I, typename F>
+__device__ __forceinline__ int bring_together(I *expert, int room, int e0, int lane, F &&which) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine += which(i) ? 1 : 0;
+    int n = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(ALL, n, k);
+        if (lane >= k) n += o;
+    }
+    int at = n - mine;
+    n = __shfl_sync(ALL, n, 31);
+    __syncwarp();
+    if (n <= room) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (which(i)) expert[at++] = static_cast<I>(e0 + i);
+    }
+    __syncwarp();
+    return n;
+}
+
+// The values of the n experts of `held` in 64 bits.
 template <typename T>
-__device__ __noinline__ void choose_in_64(const Choose &c, const T *row, const Held &held, int n, bool grouped, int lane,
-                                          int (&mine)[2]) {
-    mine[0] = mine[1] = -1;
+__device__ __noinline__ void values_in_64(const Choose &c, const T *row, const Held &held, int n, int lane) {
     double m = -INFINITY, z = 0.0;
     if (c.scoring == EXPERTS_SOFTMAX) {
         for (int e = lane; e < c.E; e += 32) m = fmax(m, static_cast<double>(to_f(row[e])));
@@ -195,52 +223,44 @@ __device__ __noinline__ void choose_in_64(const Choose &c, const T *row, const H
         const int e = held.expert[k];
         const double l = static_cast<double>(to_f(row[e]));
         double v = c.scoring == EXPERTS_SOFTMAX ? exp(l - m) / z : sigmoid(l);
-        bool in = l > -INFINITY;
-        if (c.bias != nullptr) {
-            v += static_cast<double>(c.bias[e]);
-            in = in && v > -INFINITY;
-        }
-        held.rank[k] = in ? rank_of(v) : 0ull;
+        if (c.bias != nullptr) v += static_cast<double>(c.bias[e]);
+        held.rank[k] = rank_of(v);
     }
     __syncwarp();
-    if (grouped) {
-        unsigned long long total = 0;  // lane g: of group g
-        for (int g = 0; g < c.groups; ++g) {
-            unsigned long long first = 0, second = 0, any;
-            for (int i = lane; i < c.size; i += 32) keep_two(held.rank[g * c.size + i], first, second);
-            const double sum = best_two<unsigned long long, double>(first, second, c.top > 1, &any);
-            if (lane == g && any != 0) total = rank_of(sum);
-        }
-        const unsigned keep = __ballot_sync(ALL, stays(c, total, lane));
-        for (int e = lane; e < n; e += 32)
-            if ((keep >> group_of(c, e) & 1) == 0) held.rank[e] = 0;
-        __syncwarp();
-    }
-    if (c.bias == nullptr)
-        for (int k = lane; k < n; k += 32)
-            if (held.rank[k] != 0) held.rank[k] = rank_of(static_cast<double>(to_f(row[held.expert[k]])));
-    __syncwarp();
+}
+// The J best of those, one after the other: this lane's picks (pick j at lane
+// j % 32, in mine[j / 32]).
+__device__ __noinline__ void pick_in_64(const Choose &c, const Held &held, int n, int lane, int (&mine)[2]) {
+    mine[0] = mine[1] = -1;
     for (int j = 0; j < c.J; ++j) {
         unsigned long long best = 0;
-        int at = -1, who = INT_MAX;
+        int at = -1;
         for (int k = lane; k < n; k += 32)
-            if (held.rank[k] > best || (held.rank[k] == best && best != 0 && held.expert[k] < who)) {
+            if (held.rank[k] > best) {  // the first of equal ones: they are in order
                 best = held.rank[k];
                 at = k;
-                who = held.expert[k];
             }
         const unsigned long long high = warp_max(best);
         if (high == 0) break;
-        const int pick = __reduce_min_sync(ALL, best == high ? who : INT_MAX);
-        if (best == high && who == pick) held.rank[at] = 0;
-        if ((j & 31) == lane) mine[j >> 5] = pick;
+        const int pick = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
+        if ((j & 31) == lane) mine[j >> 5] = held.expert[pick];
+        __syncwarp();
+        if (at == pick) held.rank[at] = 0;
         __syncwarp();
     }
 }
+// The sum in 64 bits of group g's best, of those of `held`.
+__device__ __noinline__ double group_in_64(const Choose &c, const Held &held, int n, unsigned g, int lane) {
+    unsigned long long first = 0, second = 0, any;
+    for (int k = lane; k < n; k += 32)
+        if (group_of(c, held.expert[k]) == g) keep_two(held.rank[k], first, second);
+    return best_two<unsigned long long, double>(first, second, c.top > 1, &any);
+}
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_constant__ Choose c) {
+__global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 8 : 1) choose_kernel(const __grid_constant__ Choose c) {
     extern __shared__ unsigned long long room[];
+    __shared__ int picks[CHOOSE_WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * CHOOSE_WARPS + warp;
     tc::grid_trigger();
@@ -252,14 +272,10 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
     float l[NV];
     load_row<T, NV>(row, lane, c.E, c.wide, -INFINITY, l);
     float m = -INFINITY;
-    bool wrong = false;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        wrong = wrong || l[i] != l[i];
-        m = fmaxf(m, l[i]);
-    }
+    for (int i = 0; i < NV; ++i) m = max_or_nan(m, l[i]);
     m = warp_max_f(m);
-    wrong = __any_sync(ALL, wrong) || (softmax && m == INFINITY);
+    const bool wrong = m != m || (softmax && m == INFINITY);
     const bool summed = c.groups > 1 && c.top > 1;  // groups by sums of scores
     float z = 1.0f;
     if (softmax && (c.bias != nullptr || !c.renormalize || summed) && m > -INFINITY) {
@@ -280,22 +296,25 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
     uint32_t key[NV];
     float bias[NV];
     if (c.bias != nullptr) load_row<float, NV>(c.bias, lane, c.E, c.wide_bias, -INFINITY, bias);
-    auto score = [&](int i) { return softmax ? expf(l[i] - m) * most : sigmoid_about(l[i]); };
+    auto score_of = [&](float x) { return softmax ? expf(x - m) * most : sigmoid_about(x); };
+    auto value_of = [&](float x, float b) { return __fadd_rn(score_of(x), b); };  // the same bits wherever it is worked out
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         key[i] = 0;
         if (l[i] > -INFINITY && !wrong) {
-            const float v = c.bias != nullptr ? score(i) + bias[i] : l[i];
+            const float v = c.bias != nullptr ? value_of(l[i], bias[i]) : l[i];
             if (v > -INFINITY) {
                 key[i] = rank_of(v);
                 if (c.bias != nullptr) size = fmaxf(size, fabsf(v));
             }
         }
     }
-    bool doubt = false, doubt_groups = false;
+    Held held;
+    held.rank = room + static_cast<size_t>(warp) * c.E;
+    held.expert = reinterpret_cast<unsigned short *>(room + static_cast<size_t>(CHOOSE_WARPS) * c.E) + warp * c.E;
     if (c.groups > 1) {
-        uint32_t total = 0;  // lane g: of group g
-        auto rank = [&](int i) { return summed && c.bias == nullptr && key[i] != 0 ? rank_of(score(i)) : key[i]; };
+        uint32_t total = 0, least = 0;  // lane g: the rank of group g's sum, and of the least value in it
+        auto rank = [&](int i) { return summed && c.bias == nullptr && key[i] != 0 ? rank_of(score_of(l[i])) : key[i]; };
         if (c.lanes > 0) {  // a group is `lanes` lanes, a power of two
             uint32_t first = 0, second = 0;
 #pragma unroll
@@ -307,8 +326,8 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
             }
             float sum = of_rank(first);
             if (c.top > 1 && second != 0) sum += of_rank(second);
-            const uint32_t mine = first != 0 ? rank_of(sum) : 0;
-            total = __shfl_sync(ALL, mine, lane * c.lanes & 31);
+            total = __shfl_sync(ALL, first != 0 ? rank_of(sum) : 0, lane * c.lanes & 31);
+            least = __shfl_sync(ALL, c.top > 1 ? second : first, lane * c.lanes & 31);
             if (lane >= c.groups) total = 0;
         } else {
             for (int g = 0; g < c.groups; ++g) {
@@ -317,99 +336,151 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_kernel(const __grid_
                 for (int i = 0; i < NV; ++i)
                     if (group_of(c, e0 + i) == static_cast<unsigned>(g)) keep_two(rank(i), first, second);
                 const float sum = best_two<uint32_t, float>(first, second, c.top > 1, &any);
-                if (lane == g && any != 0) total = rank_of(sum);
+                const uint32_t low = c.top > 1 && __popc(__ballot_sync(ALL, first != 0)) + __popc(__ballot_sync(ALL, second != 0)) < 2
+                                         ? 0
+                                         : rank_of(c.top > 1 ? sum - of_rank(any) : sum);
+                if (lane == g && any != 0) {
+                    total = rank_of(sum);
+                    least = low;
+                }
             }
         }
-        const bool stay = stays(c, total, lane);
-        const unsigned keep = __ballot_sync(ALL, stay);
+        unsigned keep = kept_groups(c, total, lane);
+        const bool stay = (keep >> lane & 1) != 0;
         if (summed || c.bias != nullptr) {
+            // in doubt: the groups whose sums are within `width` of the border's other side
+            if (c.bias != nullptr) size = warp_max_f(size);
+            const float width = 2.0f * slack + 0x1p-21f * size;  // 4 scores; 4 sums with biases, 2 of two values
             const uint32_t low = __reduce_min_sync(ALL, stay ? total : 0xffffffffu);
             const uint32_t out = warp_max(lane < c.groups && !stay ? total : 0u);
-            if (c.bias != nullptr) size = warp_max_f(size);
-            if (out != 0) {
-                const float a = of_rank(low), b = of_rank(out);
-                doubt_groups = !(a - b >= 2.0f * slack + 0x1p-21f * size);  // 4 scores; 4 sums with biases, 2 of two values
+            if (out != 0 && !(of_rank(low) - of_rank(out) >= width)) {
+                const float v = of_rank(total);
+                const unsigned near = __ballot_sync(ALL, lane < c.groups && total != 0 && (stay ? !(v - of_rank(out) >= width) : !(of_rank(low) - v >= width)));
+                const int n = bring_together<NV>(held.expert, c.E, e0, lane, [&](int i) {
+                    const unsigned g = group_of(c, e0 + i) & 31;
+                    // the group's best, and what may be among them: 2 scores, 2 sums with the bias, and what `least` lost
+                    const uint32_t bound = __shfl_sync(ALL, least, g);
+                    return key[i] != 0 && (near >> g & 1) != 0 && (bound == 0 || !(of_rank(rank(i)) < of_rank(bound) - width));
+                });
+                values_in_64(c, row, held, n, lane);
+                unsigned long long exact = 0;  // lane g
+                for (unsigned left = near; left != 0; left &= left - 1) {
+                    const int g = __ffs(left) - 1;
+                    const double sum = group_in_64(c, held, n, g, lane);
+                    if (lane == g) exact = rank_of(sum);
+                }
+                const int places = __popc(keep & near);
+                int before = 0;
+                for (unsigned left = near; left != 0; left &= left - 1) {
+                    const int g = __ffs(left) - 1;
+                    const unsigned long long o = __shfl_sync(ALL, exact, g);
+                    before += o > exact || (o == exact && g < lane) ? 1 : 0;
+                }
+                keep = (keep & ~near) | __ballot_sync(ALL, (near >> lane & 1) != 0 && before < places);
             }
         }
+        if (c.lanes > 0) {
+            const bool in = (keep >> (group_of(c, e0) & 31) & 1) != 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if ((keep >> (group_of(c, e0 + i) & 31) & 1) == 0) key[i] = 0;
+            for (int i = 0; i < NV; ++i) key[i] = in ? key[i] : 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((keep >> (group_of(c, e0 + i) & 31) & 1) == 0) key[i] = 0;
+        }
     }
-    int mine[2] = {-1, -1};
-    uint32_t best = 0, second = 0, taken = 0;  // this lane's best two that are left, and which are not
-    int at = INT_MAX, at_second = INT_MAX;
-    auto look = [&] {
-        best = second = 0;
-        at = at_second = INT_MAX;
+    uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint32_t k = taken >> i & 1 ? 0u : key[i];
-            if (k > best) {
-                second = best;
-                at_second = at;
-                best = k;
-                at = e0 + i;
-            } else if (k > second) {
-                second = k;
-                at_second = e0 + i;
+    for (int i = 0; i < NV; ++i) best = key[i] > best ? key[i] : best;
+    int mine[2] = {-1, -1}, *pick = picks[warp];
+    float floor = 0.0f;  // the least pick's value
+    bool doubt = false;
+    int n = 33;
+    if (c.J < 32) {
+        // of as many lanes' best as there are picks and one more, the least: a bound
+        uint32_t left = best, bound = 0;
+        for (int got = 0; got <= c.J;) {
+            bound = warp_max(left);
+            if (bound == 0) break;
+            const unsigned there = __ballot_sync(ALL, left == bound);
+            if (left == bound) left = 0;
+            got += __popc(there);
+        }
+        n = bring_together<NV>(pick, 32, e0, lane, [&](int i) { return key[i] != 0 && key[i] >= bound; });
+    }
+    if (n <= 32) {
+        int e = lane < n ? pick[lane] : -1;
+        // its value again, as its lane has it
+        float le = e >= 0 ? to_f(row[e]) : 0.0f, be = e >= 0 && c.bias != nullptr ? c.bias[e] : 0.0f;
+        float v = c.bias != nullptr ? value_of(le, be) : le;
+        const uint32_t k = e >= 0 ? rank_of(v) : 0;
+        int place = 0;
+#pragma unroll 4
+        for (int o = 0; o < n; ++o) {
+            const uint32_t other = __shfl_sync(ALL, k, o);
+            place += other > k || (other == k && o < lane) ? 1 : 0;
+        }
+        __syncwarp();
+        if (e >= 0) pick[place] = lane;
+        __syncwarp();
+        const int from = lane < n ? pick[lane] : 0;
+        e = __shfl_sync(ALL, e, from);
+        if (lane < c.J && lane < n) mine[0] = e;
+        if (c.bias != nullptr) {
+            // neighbours among the picks and the first that is none: 2 scores, 2 sums with the bias; values of equal
+            // logits and biases are equal in 64 bits too
+            v = __shfl_sync(ALL, v, from);
+            floor = __shfl_sync(ALL, v, min(c.J, n) - 1 & 31);
+            const float next = __shfl_down_sync(ALL, v, 1);
+            const bool close = lane < c.J && lane + 1 < n && !(v - next >= slack + 0x1p-22f * fabsf(v));
+            if (__any_sync(ALL, close)) {
+                le = __shfl_sync(ALL, le, from);
+                be = __shfl_sync(ALL, be, from);
+                const float ln = __shfl_down_sync(ALL, le, 1), bn = __shfl_down_sync(ALL, be, 1);
+                doubt = __any_sync(ALL, close && !(le == ln && be == bn));
             }
         }
-    };
-    look();
-    float last = 0.0f, floor = 0.0f;
-    int last_who = -1;
-    const int rounds = c.bias != nullptr && !doubt_groups ? c.J + 1 : doubt_groups ? 0 : c.J;  // one more: the best that is left out
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t high = warp_max(best);
-        if (high == 0) break;
-        const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
-        if (c.bias != nullptr) {
-            const float v = of_rank(high);
-            // 2 scores, 2 sums with the bias; values of equal logits and biases are equal in 64 bits too
-            if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)))
-                doubt = doubt || !(to_f(row[who]) == to_f(row[last_who]) && c.bias[who] == c.bias[last_who]);
-            last = v;
-            last_who = who;
-            if (j < c.J) floor = v;
-        }
-        if (j < c.J && (j & 31) == lane) mine[j >> 5] = who;
-        if (who == at) {
-            taken |= 1u << (who - e0);
-            if (second != 0) {
-                best = second;
-                at = at_second;
-                second = 0;
-            } else {
+    } else {  // many picks or many equal values: one after the other
+        uint32_t taken = 0;
+        int at = INT_MAX;
+        auto look = [&] {
+            best = 0;
+            at = INT_MAX;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((taken >> i & 1) == 0 && key[i] > best) {
+                    best = key[i];
+                    at = e0 + i;
+                }
+        };
+        look();
+        float last = 0.0f;
+        int last_who = -1;
+        const int rounds = c.bias != nullptr ? c.J + 1 : c.J;  // one more: the best that is left out
+        for (int j = 0; j < rounds; ++j) {
+            const uint32_t high = warp_max(best);
+            if (high == 0) break;
+            const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
+            if (c.bias != nullptr) {
+                const float v = of_rank(high);
+                if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)))
+                    doubt = doubt || !(to_f(row[who]) == to_f(row[last_who]) && c.bias[who] == c.bias[last_who]);
+                last = v;
+                last_who = who;
+                if (j < c.J) floor = v;
+            }
+            if (j < c.J && (j & 31) == lane) mine[j >> 5] = who;
+            if (who == at) {
+                taken |= 1u << (who - e0);
                 look();
             }
         }
     }
-    if (doubt || doubt_groups) {
-        Held held;
-        held.rank = room + static_cast<size_t>(warp) * c.E;
-        held.expert = reinterpret_cast<int *>(room + static_cast<size_t>(CHOOSE_WARPS) * c.E) + warp * c.E;
-        int n = c.E;
-        if (doubt_groups) {
-            for (int e = lane; e < c.E; e += 32) held.expert[e] = e;
-        } else {  // those that may be among the J best
-            const float low = floor - slack - 0x1p-22f * fabsf(floor);
-            int before = 0, mine_n = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) mine_n += key[i] != 0 && of_rank(key[i]) >= low ? 1 : 0;
-            n = mine_n;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const int o = __shfl_up_sync(ALL, n, k);
-                if (lane >= k) n += o;
-            }
-            before = n - mine_n;
-            n = __shfl_sync(ALL, n, 31);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (key[i] != 0 && of_rank(key[i]) >= low) held.expert[before++] = e0 + i;
-        }
-        __syncwarp();
-        choose_in_64(c, row, held, n, doubt_groups, lane, mine);
+    if (doubt) {  // those that may be among the J best, in 64 bits
+        const float low = floor - slack - 0x1p-22f * fabsf(floor);
+        const int some = bring_together<NV>(held.expert, c.E, e0, lane, [&](int i) { return key[i] != 0 && !(of_rank(key[i]) < low); });
+        values_in_64(c, row, held, some, lane);
+        pick_in_64(c, held, some, lane, mine);
     }
 
     // weights of the picks
@@ -610,7 +681,7 @@ extern "C" int expert_choose(int type, int T, int E, int J, const void *logits, 
     c.renormalize = renormalize != 0, c.scale = scale;
     if (groups == 1) c.top = 1;
     const bool in_64 = bias != nullptr || (groups > 1 && group_top > 1);
-    const size_t smem = in_64 ? (sizeof(unsigned long long) + sizeof(int)) * CHOOSE_WARPS * static_cast<size_t>(E) : 0;
+    const size_t smem = in_64 ? (sizeof(unsigned long long) + sizeof(unsigned short)) * CHOOSE_WARPS * static_cast<size_t>(E) : 0;
     sg_nvtx::Range r("experts: choose");
     return with_experts(E, [&](auto n) {
         constexpr int NV = decltype(n)::value;

@@ -68,7 +68,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[MOST_WARPS]
         if constexpr (SEVERAL)
             asm volatile("bar.sync %0, %1;\n" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
         else
-            __syncthreads();
+            asm volatile("bar.sync 0;\n" ::: "memory");  // reached from either of a kernel's two loops
         t = 0.0f;
         for (int w = lane & 7; w < warps; w += 8) t += part[turn][first + w][N == 1 ? 0 : lane / SHARE];
         t = across(t, 4);
@@ -101,12 +101,11 @@ struct Ahead {
     __device__ __forceinline__ void ask(int m, int i, bool in, const T *src) {
         if constexpr (ASYNC) {
             const uint32_t to = at + other + (m * PPT + i) * APART;
-            if constexpr (P::BYTES == 16) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(src), "r"(in ? 16 : 0) : "memory");
-            } else {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(P::BYTES < 4 ? 4 : P::BYTES),
-                             "r"(in ? P::BYTES : 0)
-                             : "memory");
+            if (in) {
+                if constexpr (P::BYTES == 16)
+                    tc::cp_async16(to, src);
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(to), "l"(src), "n"(P::BYTES < 4 ? 4 : P::BYTES) : "memory");
             }
         } else {
             next[m * PPT + i] = load_if<T, V>(in, src);
@@ -222,11 +221,20 @@ __device__ __forceinline__ Spread spread_of(const Forward &c, const float (&q)[2
     return {rest, 1.0f / sqrtf(fmaxf(var, 0.0f) + c.eps)};
 }
 
-// PPT packs a thread.  FAST: all threads have as many, and there are a weight and a
-// bias (the gradient: a weight and dx), so nothing is asked in a row.  A block takes every
-// blocks-th row (of each of its threadIdx.y) and asks for its next row before it
-// sums up this one.  Weight and bias come from L1 for each row.
-template <typename T, int V, int PPT, int THREADS, bool FAST>
+// The loop over the rows is there twice: for warps whose share is whole, with a
+// weight and a bias (the gradient: a weight and dx), so that nothing is asked in a
+// row, and for the others.
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
+// PPT packs a thread.  A block takes every blocks-th row (of each of its
+// threadIdx.y) and asks for its next row before it sums up this one.  Weight and
+// bias come from L1 for each row.
+template <typename T, int V, int PPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const __grid_constant__ Forward c) {
     using R = Row<T, V>;
     using Num = typename R::Num;
@@ -237,50 +245,58 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const 
     const T *wp = static_cast<const T *>(c.weight), *bp = static_cast<const T *>(c.bias);
     Ahead<T, V, PPT, 1, THREADS> ahead(room);
     const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
-    auto mine = [&](int i) { return FAST || p0 + 32 * i < c.packs; };
-    auto ask = [&](long long row) {
-        if (row < c.M) {
-            const T *x = static_cast<const T *>(c.x) + row * c.ldx + p0 * V;
-#pragma unroll
-            for (int i = 0; i < PPT; ++i) ahead.ask(0, i, mine(i), mine(i) ? x + 32 * i * V : static_cast<const T *>(c.x));
-        }
-        ahead.asked();
-    };
     tc::grid_trigger();
     tc::grid_wait();
-    ask(r);
-    int turn = 0;
-    for (; r < c.M; r += step) {
-        ahead.turn();
-        Num f[PPT][R::L::N], sum = all<Num>(0.0f), square = sum;
+    auto rows = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        auto mine = [&](int i) { return WHOLE || p0 + 32 * i < c.packs; };
+        auto ask = [&](long long row) {
+            if (row < c.M) {
+                const T *x = static_cast<const T *>(c.x) + row * c.ldx + p0 * V;
 #pragma unroll
-        for (int i = 0; i < PPT; ++i) R::add_up(ahead.get(0, i), f[i], sum);
-        ask(r + step);
-        float s[1] = {sum_of(sum)};
-        row_sum<false>(s, part, turn);
-        const float mean = s[0] * c.inverse;
-        const Num minus_mean = all<Num>(-mean);
-        sum = all<Num>(0.0f);
+                for (int i = 0; i < PPT; ++i) ahead.ask(0, i, mine(i), x + 32 * i * V);
+            }
+            ahead.asked();
+        };
+        ask(r);
+        int turn = 0;
+        for (; r < c.M; r += step) {
+            ahead.turn();
+            Num f[PPT][R::L::N], sum = all<Num>(0.0f), square = sum;
 #pragma unroll
-        for (int i = 0; i < PPT; ++i)
-            if (mine(i)) R::spread(f[i], minus_mean, sum, square);
-        float q[2] = {sum_of(sum), sum_of(square)};
-        row_sum<false>(q, part, turn);
-        const Spread sp = spread_of(c, q);
-        if (c.stats != nullptr && threadIdx.x == 0) {
-            c.stats[2 * r] = mean + sp.rest;
-            c.stats[2 * r + 1] = sp.rstd;
+            for (int i = 0; i < PPT; ++i)
+                if (mine(i)) R::add_up(ahead.get(0, i), f[i], sum);
+            ask(r + step);
+            float s[1] = {sum_of(sum)};
+            row_sum<false>(s, part, turn);
+            const float mean = s[0] * c.inverse;
+            const Num minus_mean = all<Num>(-mean);
+            sum = all<Num>(0.0f);
+#pragma unroll
+            for (int i = 0; i < PPT; ++i)
+                if (mine(i)) R::spread(f[i], minus_mean, sum, square);
+            float q[2] = {sum_of(sum), sum_of(square)};
+            row_sum<false>(q, part, turn);
+            const Spread sp = spread_of(c, q);
+            if (c.stats != nullptr && threadIdx.x == 0) {
+                c.stats[2 * r] = mean + sp.rest;
+                c.stats[2 * r + 1] = sp.rstd;
+            }
+            const Num rstd = all<Num>(sp.rstd), minus_rest = all<Num>(-sp.rest * sp.rstd);
+            T *y = static_cast<T *>(c.y) + r * c.ldy;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i) {
+                const int p = p0 + 32 * i;
+                if (mine(i))
+                    R::finish(f[i], load_or_ones<T, V>(WHOLE || wp != nullptr, wp + p * V), load_if<T, V>(WHOLE || bp != nullptr, bp + p * V),
+                              rstd, minus_rest, y + p * V);
+            }
         }
-        const Num rstd = all<Num>(sp.rstd), minus_rest = all<Num>(-sp.rest * sp.rstd);
-        T *y = static_cast<T *>(c.y) + r * c.ldy;
-#pragma unroll
-        for (int i = 0; i < PPT; ++i) {
-            const int p = p0 + 32 * i;
-            if (mine(i))
-                R::finish(f[i], load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V), load_if<T, V>(FAST || bp != nullptr, bp + p * V),
-                          rstd, minus_rest, y + p * V);
-        }
-    }
+    };
+    if ((threadIdx.x & ~31) * PPT + 32 * PPT <= c.packs && wp != nullptr && bp != nullptr)
+        rows(Yes());
+    else
+        rows(No());
 }
 
 // Rows that no block's registers hold: read three times, the later ones from L2.
@@ -359,8 +375,9 @@ __device__ __forceinline__ RowMeans row_means(const float (&q)[3], float inverse
 // A grid of `blocks` blocks, one an SM, takes the rows in turn, one each of their
 // threadIdx.y at a time; a thread keeps the sums of its columns in registers, and
 // the block's are joined in shared memory at the end.  Each row's packs are read
-// from their slots twice, before and after its means are known.
-template <typename T, int V, int PPT, int THREADS, bool FAST>
+// from their slots twice, before and after its means are known.  Weights in packs of
+// 4 bytes and less stay in registers, wider ones come from L1.
+template <typename T, int V, int PPT, int THREADS>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Backward c) {
     using R = Row<T, V>;
     using Num = typename R::Num;
@@ -377,51 +394,66 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     Ahead<T, V, PPT, 2, THREADS> ahead(room);
     const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
+    constexpr bool HOLD = Pack<T, V>::BYTES <= 4;
     float next_mean = 0.0f, next_rstd = 0.0f;
-    auto mine = [&](int i) { return FAST || p0 + 32 * i < c.packs; };
-    auto ask = [&](long long row) {
-        if (row < c.M) {
-            const T *xr = static_cast<const T *>(c.x) + row * c.ldx + p0 * V, *gr = static_cast<const T *>(c.dy) + row * c.lddy + p0 * V;
-#pragma unroll
-            for (int i = 0; i < PPT; ++i) {
-                ahead.ask(0, i, mine(i), mine(i) ? xr + 32 * i * V : static_cast<const T *>(c.x));
-                ahead.ask(1, i, mine(i), mine(i) ? gr + 32 * i * V : static_cast<const T *>(c.dy));
-            }
-            next_mean = c.stats[2 * row];
-            next_rstd = c.stats[2 * row + 1];
-        }
-        ahead.asked();
-    };
     tc::grid_trigger();
     tc::grid_wait();
-    ask(r);
-    int turn = 0;
-    for (; r < c.M; r += step) {
-        ahead.turn();
-        const float rstd = next_rstd;
-        const Num minus_mean = all<Num>(-next_mean);
-        ask(r + step);
-        Num sg = all<Num>(0.0f), sgd = sg, sd = sg;
+    auto rows = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        auto mine = [&](int i) { return WHOLE || p0 + 32 * i < c.packs; };
+        auto ask = [&](long long row) {
+            if (row < c.M) {
+                const T *xr = static_cast<const T *>(c.x) + row * c.ldx + p0 * V, *gr = static_cast<const T *>(c.dy) + row * c.lddy + p0 * V;
 #pragma unroll
-        for (int i = 0; i < PPT; ++i) {
-            const int p = p0 + 32 * i;
-            if (mine(i)) R::means(ahead.get(0, i), ahead.get(1, i), load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V), minus_mean, sg, sgd, sd);
-        }
-        float q[3] = {sum_of(sg), sum_of(sgd), sum_of(sd)};
-        row_sum<true>(q, part, turn);
-        const RowMeans m = row_means(q, c.inverse, rstd);
-        const Num n_rstd = all<Num>(rstd), minus_rest = all<Num>(-m.rest * rstd), a = all<Num>(m.a), b = all<Num>(m.b);
-        T *dx = static_cast<T *>(c.dx) + r * c.lddx;
-#pragma unroll
-        for (int i = 0; i < PPT; ++i) {
-            const int p = p0 + 32 * i;
-            if (mine(i)) {
-                const Pack<T, V> o = R::gradient(ahead.get(0, i), ahead.get(1, i), load_or_ones<T, V>(FAST || wp != nullptr, wp + p * V),
-                                                 minus_mean, n_rstd, minus_rest, a, b, dw[i], db[i]);
-                if (FAST || c.dx != nullptr) store<T, V>(dx + p * V, o);
+                for (int i = 0; i < PPT; ++i) {
+                    ahead.ask(0, i, mine(i), xr + 32 * i * V);
+                    ahead.ask(1, i, mine(i), gr + 32 * i * V);
+                }
+                next_mean = c.stats[2 * row];
+                next_rstd = c.stats[2 * row + 1];
             }
+            ahead.asked();
+        };
+        ask(r);
+        Pack<T, V> held[HOLD ? PPT : 1];
+        auto fetch_weight = [&](int i) { return load_or_ones<T, V>(WHOLE || (mine(i) && wp != nullptr), wp + (p0 + 32 * i) * V); };
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int i = 0; i < PPT; ++i) held[i] = fetch_weight(i);
         }
-    }
+        auto weight = [&](int i) {
+            if constexpr (HOLD)
+                return held[i];
+            else
+                return fetch_weight(i);
+        };
+        int turn = 0;
+        for (; r < c.M; r += step) {
+            ahead.turn();
+            const float rstd = next_rstd;
+            const Num minus_mean = all<Num>(-next_mean);
+            ask(r + step);
+            Num sg = all<Num>(0.0f), sgd = sg, sd = sg;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i)
+                if (mine(i)) R::means(ahead.get(0, i), ahead.get(1, i), weight(i), minus_mean, sg, sgd, sd);
+            float q[3] = {sum_of(sg), sum_of(sgd), sum_of(sd)};
+            row_sum<true>(q, part, turn);
+            const RowMeans m = row_means(q, c.inverse, rstd);
+            const Num n_rstd = all<Num>(rstd), minus_rest = all<Num>(-m.rest * rstd), a = all<Num>(m.a), b = all<Num>(m.b);
+            T *dx = static_cast<T *>(c.dx) + r * c.lddx;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i)
+                if (mine(i)) {
+                    const Pack<T, V> o = R::gradient(ahead.get(0, i), ahead.get(1, i), weight(i), minus_mean, n_rstd, minus_rest, a, b, dw[i], db[i]);
+                    if (WHOLE || c.dx != nullptr) store<T, V>(dx + (p0 + 32 * i) * V, o);
+                }
+        }
+    };
+    if ((threadIdx.x & ~31) * PPT + 32 * PPT <= c.packs && wp != nullptr && c.dx != nullptr)
+        rows(Yes());
+    else
+        rows(No());
     if (c.sums == nullptr) return;
     // the rows' sums, in their order: V values of a thread lie together, so no two threads share any
     float *joined = reinterpret_cast<float *>(room);
@@ -431,7 +463,7 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < PPT; ++i) {
             const int p = p0 + 32 * i;
-            if (mine(i))
+            if (p < c.packs)
 #pragma unroll
                 for (int k = 0; k < LN; ++k)
 #pragma unroll
@@ -600,17 +632,10 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
         };
         // 32 values of a row a thread (one by one: 16), or a quarter of that of a short one
         constexpr int LARGE = V > 1 ? 32 / V : 16, SMALL = LARGE / 4;
-        if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128, false>, SMALL, 128);
-        auto pick = [&](auto t) {
-            constexpr int THREADS = decltype(t)::value;
-            if constexpr (BYTES == 16)
-                if (c.packs % (32 * LARGE) == 0 && weight != nullptr && bias != nullptr)
-                    return run(forward_kernel<El, V, LARGE, THREADS, true>, LARGE, THREADS);
-            return run(forward_kernel<El, V, LARGE, THREADS, false>, LARGE, THREADS);
-        };
-        if (c.packs <= LARGE * 128) return pick(lt::Int<128>{});
-        if (c.packs <= LARGE * 256) return pick(lt::Int<256>{});
-        if (c.packs <= LARGE * MOST_THREADS) return pick(lt::Int<MOST_THREADS>{});
+        if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128>, SMALL, 128);
+        if (c.packs <= LARGE * 128) return run(forward_kernel<El, V, LARGE, 128>, LARGE, 128);
+        if (c.packs <= LARGE * 256) return run(forward_kernel<El, V, LARGE, 256>, LARGE, 256);
+        if (c.packs <= LARGE * MOST_THREADS) return run(forward_kernel<El, V, LARGE, MOST_THREADS>, LARGE, MOST_THREADS);
         return launched(tc::launch(forward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
     });
 }
@@ -683,11 +708,8 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
         // 16 values of a row a thread (one by one: 8), or 32 of a wide one
         constexpr int SMALL = V > 1 ? 16 / V : 8, LARGE = 2 * SMALL;
         constexpr int MANY = BACKWARD_THREADS, FEW = sizeof(El) == 4 ? 384 : MOST_THREADS;
-        if constexpr (BYTES == 16)
-            if (c.packs % (32 * SMALL) == 0 && c.packs <= SMALL * MANY && weight != nullptr && dx != nullptr)
-                return run(backward_kernel<El, V, SMALL, MANY, true>, SMALL, MANY);
-        if (c.packs <= SMALL * MANY) return run(backward_kernel<El, V, SMALL, MANY, false>, SMALL, MANY);
-        if (c.packs <= LARGE * FEW) return run(backward_kernel<El, V, LARGE, FEW, false>, LARGE, FEW);
+        if (c.packs <= SMALL * MANY) return run(backward_kernel<El, V, SMALL, MANY>, SMALL, MANY);
+        if (c.packs <= LARGE * FEW) return run(backward_kernel<El, V, LARGE, FEW>, LARGE, FEW);
         int s = launched(tc::launch(backward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
         if (s == SGEMM_OK && columns) {
             c.blocks = c.blocks < WIDE_BLOCKS ? c.blocks : WIDE_BLOCKS;

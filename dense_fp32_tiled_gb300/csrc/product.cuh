@@ -66,7 +66,7 @@ constexpr int KBLK = 2;
 constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles up to 224 tokens
 // The 16-bit types' LOG_SUM, whose results are FP32, adds in registers too, after
 // LOG_SUM_KBLK tiles of K.
-constexpr int LOG_SUM_KBLK = 4;
+constexpr int LOG_SUM_KBLK = 8;
 constexpr int LOG_SUM_REGS = 128;
 
 enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
@@ -111,6 +111,7 @@ struct Product {
     int nt, nf;               // tiles in tokens (DENSE, K_BY_EXPERT) and in features
     int splits;               // CTAs of a cluster that share the K of a tile (CG = 1)
     int stages, stage_bytes, q_bytes;
+    int p_bytes;              // the loss's epilogues: of P's tile that are copied (see few_rows)
     int epi_offset, epi_bytes;  // the epilogue's buffers in dynamic shared memory, per warp
     int p_mn, q_mn;
     const void *bias, *residual;
@@ -655,6 +656,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     float *partial = reinterpret_cast<float *>(sgen + static_cast<size_t>(p.stages) * p.stage_bytes);
     int *tables = reinterpret_cast<int *>(partial + (S > 1 ? p.bt * PROWS : 0));
     const Tables tb{tables, tables + p.E + 2};
+    // P's tile in a stage; Q's follows it
+    const uint32_t p_bytes = EPI == LOG_SUM || EPI == SOFTMAX_GRADIENT ? p.p_bytes : P_BYTES;
     const uint32_t epi = tc::smem_u32(smem_raw) + p.epi_offset + (warp < EPI_WARPS ? warp : 0) * p.epi_bytes;
 
     if (warp == 0) {  // a barrier or three per lane: one thread would take as long as a copy from L2
@@ -754,7 +757,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         const uint32_t full0 = CG == 2 ? tc::peer_addr(tc::smem_u32(&full_bar[0]), 0) : tc::smem_u32(&full_bar[0]);
         const uint32_t empty0 = tc::smem_u32(&empty_bar[0]);
         const uint32_t tail0 = CG == 2 ? tc::peer_addr(tc::smem_u32(&tail_bar[0]), rank) : tc::smem_u32(&tail_bar[0]);
-        const uint32_t bytes = P_BYTES + p.q_bytes;
+        const uint32_t bytes = p_bytes + p.q_bytes;
         const bool p_mn = p.p_mn != 0, q_mn = p.q_mn != 0;
         const int z_planes = p.mode == ROWS_BY_EXPERT ? p.E : 1;
         uint32_t ph = 1;
@@ -786,9 +789,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         }
                         if (q_mn) {
                             for (int i = 0; i < q_rows; i += 64)
-                                tc::tma_load_3d<CG>(st + P_BYTES + i * (MN_BOX_BYTES / 64), &maps.q, tq + i, k, zq, bar);
+                                tc::tma_load_3d<CG>(st + p_bytes + i * (MN_BOX_BYTES / 64), &maps.q, tq + i, k, zq, bar);
                         } else {
-                            tc::tma_load_3d<CG>(st + P_BYTES, &maps.q, k, tq, zq, bar);
+                            tc::tma_load_3d<CG>(st + p_bytes, &maps.q, k, tq, zq, bar);
                         }
                     }
                     __syncwarp();
@@ -852,7 +855,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t idesc = tc::instr_desc_f16(BF16, p.p_mn != 0, p.q_mn != 0, PROWS * CG, p.bt);
             const uint32_t p_step = (p.p_mn ? 2048u : 32u) >> 4, q_step = (p.q_mn ? 2048u : 32u) >> 4;  // per 16 K
             const uint64_t ad0 = tc::smem_desc(sbase, p.p_mn ? MN_BOX_BYTES : 16);
-            const uint64_t bd0 = tc::smem_desc(sbase + P_BYTES, p.q_mn ? MN_BOX_BYTES : 16);
+            const uint64_t bd0 = tc::smem_desc(sbase + p_bytes, p.q_mn ? MN_BOX_BYTES : 16);
             const uint32_t full0 = tc::smem_u32(&full_bar[0]), empty0 = tc::smem_u32(&empty_bar[0]);
             uint32_t ph = 0, g = 0;
             int s = 0;
@@ -1354,6 +1357,15 @@ inline Plan choose(const Product &p, const Device &d, int type, const Tune &only
     return best;
 }
 
+// Rows of P's tile that are copied.  A copy takes as long for a row outside the
+// operand as for one inside (one token of 32768 x 4096 in bf16: 64 us), so of
+// few tokens only theirs are copied; the tensor core then takes what lies behind them
+// in the stage for the tile's other rows, which come out on lanes that nothing reads.
+inline int few_rows(const Product &p, int epi, const Plan &pl, const Operand &P) {
+    if ((epi != LOG_SUM && epi != SOFTMAX_GRADIENT) || P.mn || pl.cg != 1 || p.F >= PROWS) return PROWS;
+    return (p.F + 7) / 8 * 8;
+}
+
 template <int CG, typename T, int EPI>
 cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
@@ -1398,7 +1410,10 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.bt = pl.bt;
     p.splits = pl.splits;
     p.q_bytes = q_bytes_of(p.bt / pl.cg, Q.mn);
-    p.stage_bytes = P_BYTES + p.q_bytes;
+    const int p_rows = few_rows(p, EPI, pl, P);
+    p.p_bytes = p_rows * 128;
+    p.stage_bytes = p.p_bytes + p.q_bytes;
+    if (p.stage_bytes < P_BYTES) p.stage_bytes = P_BYTES;
     const int per_unit = PROWS * pl.cg;
     p.nf = (p.F + per_unit - 1) / per_unit;
     p.nt = (p.T + p.bt - 1) / p.bt;
@@ -1425,7 +1440,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     Maps maps;
     memset(&maps, 0, sizeof maps);
     const bool f16 = type == LINEAR_F16;
-    if (p.K > 0 && (!encode(maps.p, P, f16, P.mn ? BK : PROWS) || !encode(maps.q, Q, f16, Q.mn ? BK : p.bt / pl.cg)))
+    if (p.K > 0 && (!encode(maps.p, P, f16, P.mn ? BK : p_rows) || !encode(maps.q, Q, f16, Q.mn ? BK : p.bt / pl.cg)))
         return SGEMM_ERR_DEVICE;
     const int units = static_cast<int>(tiles < pl.units ? tiles : pl.units);
     const int grid = units * (pl.cg == 2 ? 2 : p.splits);
