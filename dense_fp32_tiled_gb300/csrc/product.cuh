@@ -80,7 +80,7 @@ enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
 //                     value at its target
 //   SOFTMAX_GRADIENT  out = a exp(product - lse) - g [target] (FP32: in pieces)
 //   SCALED_SUM        out = alpha (product + acc), or acc += product
-// The last three have no experts, and no splits but for a SCALED_SUM without acc.
+// The last three have no splits and no experts.
 enum Epilogue { LAYER = 0, LOG_SUM = 1, SOFTMAX_GRADIENT = 2, SCALED_SUM = 3 };
 struct Token {  // of SOFTMAX_GRADIENT
     float lse;  // 16-bit types: times log2(e)
@@ -968,9 +968,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const uint32_t set = g & 1;
             bool freed = false;  // the accumulators are reported read
             const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
-            const bool shared = EPI == SCALED_SUM && S > 1;  // its K by a cluster: handed over as the layer's
-            if (EPI != LAYER && !shared) {
-              if constexpr (EPI != LAYER) {
+            if constexpr (EPI != LAYER) {
                 const int n = f - lane < p.F ? min(cols, n_tile - col0) : 0;
                 if (!BLOCKS && any) {
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
@@ -1002,7 +1000,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     ++g;
                 }
                 continue;
-              }
             }
             if (S > 1 && !w.none) {
                 // hand this CTA's part over: wait until the last one is read, store, tell all
@@ -1030,7 +1027,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         for (int i = 0; i < 16; ++i) partial[(col0 + c + i) * PROWS + fl] = v[i];
                     }
                 asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
-            } else if constexpr (EPI != LAYER) {  // done above
             } else if constexpr (F32) {
 #pragma unroll
                 for (int c = 0; c < F32_COLS; c += 16)
@@ -1155,7 +1151,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const T *bias_e = p.bias == nullptr ? nullptr
                                                     : static_cast<const T *>(p.bias) +
                                                           (p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0);
-                const float alpha = EPI == SCALED_SUM ? *p.loss.alpha : 1.0f;
                 constexpr int U = 2;
                 const int items = n_tile * (PROWS / 4), step = S * EPI_THREADS;
                 for (int i0 = static_cast<int>(rank) * EPI_THREADS + threadIdx.x; i0 < items; i0 += U * step) {
@@ -1188,10 +1183,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             v[0] += part[u][s].x, v[1] += part[u][s].y, v[2] += part[u][s].z, v[3] += part[u][s].w;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) v[k] += b[u][k];
-                        if constexpr (EPI == SCALED_SUM) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v[k] *= alpha;
-                        }
                         if (p.z != nullptr) {
                             T *z = static_cast<T *>(p.z) + row * p.ldz + fi;
 #pragma unroll
@@ -1403,9 +1394,8 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.p_mn = P.mn;
     p.q_mn = Q.mn;
     p.timeout_flag = d.timeout_flag;
-    const bool whole_k = EPI != LAYER && !(EPI == SCALED_SUM && p.loss.first && p.loss.last);  // no splits
     Tune only = tune();
-    if (whole_k) only.splits = 1;
+    if (EPI != LAYER) only.splits = 1;
     if (EPI == LOG_SUM && only.bt < LOG_SUM_COLS) only.bt = 0;  // no narrower ones
     Plan pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     if (pl.cost > 1e299) {
@@ -1414,7 +1404,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
             fprintf(stderr, "LINEAR_TUNE leaves no plan for a product of %d x %d x %d and is not applied to it\n", p.T, p.F, p.K);
         });
         only = Tune();
-        if (whole_k) only.splits = 1;
+        if (EPI != LAYER) only.splits = 1;
         pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     }
     p.bt = pl.bt;
