@@ -126,8 +126,9 @@ std::mutex g_mutex;
 Ready g_ready[64];
 
 template <int EPI>
-bool opt_in_16() {
-    return opt_in<1, __nv_bfloat16, EPI>() && opt_in<2, __nv_bfloat16, EPI>() && opt_in<1, __half, EPI>() && opt_in<2, __half, EPI>();
+bool opt_in_all() {
+    return opt_in<1, __nv_bfloat16, EPI>() && opt_in<2, __nv_bfloat16, EPI>() && opt_in<1, __half, EPI>() && opt_in<2, __half, EPI>() &&
+           opt_in<1, float, EPI>() && opt_in<2, float, EPI>();
 }
 int ready(Device *d) {
     const int st = set_up(d);
@@ -141,10 +142,7 @@ int ready(Device *d) {
     Ready &r = g_ready[dev];
     if (r.state == 0 || r.ctx != d->ctx) {
         r.ctx = d->ctx;
-        r.state = opt_in_16<LOG_SUM>() && opt_in_16<SOFTMAX_GRADIENT>() && opt_in_16<SCALED_SUM>() && opt_in<1, float, LOG_SUM>() &&
-                          opt_in<2, float, LOG_SUM>() && opt_in<1, float, SOFTMAX_GRADIENT>() && opt_in<2, float, SOFTMAX_GRADIENT>()
-                      ? 1
-                      : -1;
+        r.state = opt_in_all<LOG_SUM>() && opt_in_all<SOFTMAX_GRADIENT>() && opt_in_all<SCALED_SUM>() ? 1 : -1;
         (void)cudaGetLastError();
     }
     return r.state > 0 ? SGEMM_OK : SGEMM_ERR_DEVICE;
@@ -259,8 +257,28 @@ int forward(const Head &h, float *loss, float *lse, void *workspace, size_t work
 }
 
 // ---- gradient ------------------------------------------------------------------------
+constexpr int SMS = 152, MOST_CHUNKS = 64;
+
+// dx (M rows of K) from the sums of its chunks, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) chunks_kernel(const float *__restrict__ acc, int chunks, int M, int K, const float *alpha,
+                                                     T *__restrict__ dx, long long lddx) {
+    tc::grid_trigger();
+    tc::grid_wait();
+    const long long all = static_cast<long long>(M) * K;
+    const float scale = alpha != nullptr ? *alpha : 1.0f;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<long long>(gridDim.x) * 256) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int c = 0; c < chunks; ++c) s += acc[c * all + i];
+        const long long row = i / K;
+        dx[row * lddx + (i - row * K)] = from_f<T>(s * scale);
+    }
+}
+
 struct BackwardBytes {
-    int piece;  // columns of the vocabulary at a time
+    int piece;   // columns of the vocabulary at a time
+    int chunks;  // of them, most sums of dx side by side
     size_t dz, tokens, acc, total;
 };
 BackwardBytes backward_bytes(const Head &h, bool want_dx, bool want_dw) {
@@ -273,7 +291,10 @@ BackwardBytes backward_bytes(const Head &h, bool want_dx, bool want_dw) {
     b.piece = static_cast<int>(piece < h.N ? piece : h.N);
     b.dz = up256(b.piece * up8(h.M) * 2 * (h.type == LINEAR_F32 ? 3 : 1));
     b.tokens = up256(static_cast<long long>(sizeof(Token)) * h.M) + 256;
-    b.acc = want_dx && b.piece < h.N && h.type != LINEAR_F32 ? up256(4LL * h.M * h.K) : 0;
+    // where dx has fewer tiles than there are SMs, the vocabulary is shared out
+    const long long tiles = ((h.M + 127LL) / 128) * ((h.K + 127LL) / 128);
+    b.chunks = tiles > SMS / 2 ? 1 : static_cast<int>(SMS / tiles < MOST_CHUNKS ? SMS / tiles : MOST_CHUNKS);
+    b.acc = want_dx && (b.piece < h.N || b.chunks > 1) ? up256(4LL * b.chunks * h.M * h.K) : 0;
     b.total = b.dz + b.tokens + b.acc + operand_bytes(h.type, x_matrix(h)) + operand_bytes(h.type, w_matrix(h));
     return b;
 }
@@ -351,6 +372,7 @@ int backward(const Head &h, const float *dloss, const float *dlse, const float *
     p.loss.alpha = f32 ? nullptr : alpha;
     p.loss.acc = reinterpret_cast<float *>(ws + need.dz + need.tokens);
     const long long ldz = up8(h.M);
+    int chunks = -need.chunks;
     for (int begin = 0; begin < h.N; begin += need.piece) {
         const int n = h.N - begin < need.piece ? h.N - begin : need.piece;
         Operand Z;  // n rows of M
@@ -385,11 +407,11 @@ int backward(const Head &h, const float *dloss, const float *dlse, const float *
             g.order = two ? ORDER_FIRST : ORDER_ALONE;
             g.loss.first = begin == 0;
             g.loss.last = begin + n == h.N;
-            if (f32 && begin > 0) {
-                g.residual = dx;
-                g.ldr = lddx;
-            }
-            st = f32 ? run_layer(h.type, g, P, Q, d, stream) : run_product<SCALED_SUM>(h.type, g, P, Q, d, stream);
+            const bool whole = need.piece == h.N;
+            if (f32 && whole && need.chunks == 1)
+                st = run_layer(h.type, g, P, Q, d, stream);
+            else
+                st = run_product<SCALED_SUM>(h.type, g, P, Q, d, stream, nullptr, &chunks);
             if (st != SGEMM_OK) return st;
         }
         if (dw != nullptr) {
@@ -405,9 +427,24 @@ int backward(const Head &h, const float *dloss, const float *dlse, const float *
             g.ldo = lddw;
             g.order = two ? ORDER_BESIDE : ORDER_ALONE;
             g.loss.first = g.loss.last = 1;
+            g.loss.acc = nullptr;
             const Operand &P = h.w_order ? Xt : Zk, &Q = h.w_order ? Zk : Xt;
             st = f32 ? run_layer(h.type, g, P, Q, d, stream) : run_product<SCALED_SUM>(h.type, g, P, Q, d, stream);
             if (st != SGEMM_OK) return st;
+        }
+    }
+    if (dx != nullptr && chunks > 1) {
+        sg_nvtx::Range r("cross entropy: sum of chunks");
+        const long long blocks = (static_cast<long long>(h.M) * h.K + 255) / 256;
+        auto sum = [&](auto el) {
+            using El = decltype(el);
+            return tc::launch(chunks_kernel<El>, static_cast<unsigned>(blocks < SMS * 16 ? blocks : SMS * 16), dim3(256), 0, stream,
+                              static_cast<const float *>(p.loss.acc), chunks, h.M, h.K, p.loss.alpha, static_cast<El *>(dx), lddx);
+        };
+        const cudaError_t err = f32 ? sum(float()) : h.type == LINEAR_BF16 ? sum(__nv_bfloat16()) : sum(__half());
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SGEMM_ERR_LAUNCH;
         }
     }
     return SGEMM_OK;

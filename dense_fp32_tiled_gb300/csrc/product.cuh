@@ -101,6 +101,7 @@ struct Loss {
     float *acc;           // T x F
     const float *alpha;
     int first, last;      // acc holds nothing yet; out is wanted
+    int chunks;           // of K, each with a T x F of its own in acc (1: none)
 };
 
 struct Product {
@@ -187,7 +188,8 @@ __device__ __forceinline__ void raster(int idx, int nt, int nf, int &tt, int &ft
 // issue loops derive from it stays in uniform registers.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-template <int CG>
+// CHUNKS: tile idx of p.chunks * nt x nf, chunk e of K.
+template <int CG, bool CHUNKS = false>
 __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &tb, int rank) {
     Tile w;
     int tt, ft, ktiles = (p.K + BK - 1) / BK;
@@ -196,6 +198,10 @@ __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &
     w.kbase = 0;
     w.k_rows = p.K;
     if (p.mode == DENSE) {
+        if (CHUNKS && p.loss.chunks > 1) {
+            w.e = idx / (p.nt * p.nf);
+            idx -= w.e * (p.nt * p.nf);
+        }
         raster(idx, p.nt, p.nf, tt, ft);
         w.t0 = tt * p.bt;
         w.t_end = p.T;
@@ -241,6 +247,9 @@ __device__ __forceinline__ Tile locate(int idx, const Product &p, const Tables &
     if (CG == 1 && p.splits > 1) {
         w.k0 = static_cast<int>(static_cast<long long>(ktiles) * rank / p.splits);
         w.k1 = static_cast<int>(static_cast<long long>(ktiles) * (rank + 1) / p.splits);
+    } else if (CHUNKS && p.loss.chunks > 1) {
+        w.k0 = static_cast<int>(static_cast<long long>(ktiles) * w.e / p.loss.chunks);
+        w.k1 = static_cast<int>(static_cast<long long>(ktiles) * (w.e + 1) / p.loss.chunks);
     } else {
         w.k0 = 0;
         w.k1 = ktiles;
@@ -536,10 +545,12 @@ __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f
         }
     } else {
         const float alpha = p.loss.alpha != nullptr ? *p.loss.alpha : 1.0f;
-        for (int c = 0; c < n; c += 16) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+            if (c >= n) break;
             float v[16], before[16];
             const long long row = static_cast<long long>(w.t0) + col0 + c;
-            float *acc = p.loss.acc + row * p.F + f;
+            float *acc = p.loss.acc + (static_cast<long long>(w.e) * p.T + row) * p.F + f;
             if (!p.loss.first && f_ok) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -561,24 +572,34 @@ __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f
     }
 }
 
-// SOFTMAX_GRADIENT of the 16-bit types: fragments through shared memory as in the
-// layer's epilogue, four tokens a thread (8 o + lane / 4), so that rows of 32
-// tokens leave in 16-byte stores.
-template <typename T>
-__device__ __forceinline__ void gradient_tile(const Product &p, const Tile &w, int f, bool f_ok, int col0, int n, bool any,
-                                              uint32_t t_set, uint32_t buf, int lane) {
-    if (n <= 0) return;
-    Token mine = {0.0f, 0.0f, 0.0f, -1};
-    if (f_ok) mine = p.loss.tokens[f];
-    int t = mine.target < 0 ? -1 : mine.target - p.loss.begin - (w.t0 + col0);
-    if (t < 0 || t >= n) t = -1;
-    Token k[4];
+// SOFTMAX_GRADIENT of the 16-bit types, and their SCALED_SUM without acc where rows
+// allow 16-byte accesses (narrower ones take longer through shared memory than straight
+// from each lane: 960 x 40493 in bf16 80 us for 53): fragments through shared
+// memory as in the layer's epilogue, four features a thread (8 o + lane / 4), so
+// that rows of 32 leave in 16-byte stores.  release() is called when all accumulators
+// have been read.  (Reading them one step ahead, as the layer's epilogue does, took
+// longer here: 4346 x 43840 x 219 in bf16 143 us for 126.)
+template <typename T, int EPI, typename Release>
+__device__ __forceinline__ void staged_tile(const Product &p, const Tile &w, int f, bool f_ok, int col0, int n, bool any,
+                                            uint32_t t_set, uint32_t buf, int lane, Release &&release) {
+    if (n <= 0) {
+        if (any) release();
+        return;
+    }
+    const float alpha = EPI == SCALED_SUM ? *p.loss.alpha : 1.0f;
+    Token mine = {0.0f, 0.0f, 0.0f, -1}, k[4];
+    int t = -1;
+    if constexpr (EPI == SOFTMAX_GRADIENT) {
+        if (f_ok) mine = p.loss.tokens[f];
+        t = mine.target < 0 ? -1 : mine.target - p.loss.begin - (w.t0 + col0);
+        if (t < 0 || t >= n) t = -1;
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-        k[o].lse = __shfl_sync(0xffffffffu, mine.lse, 8 * o + (lane >> 2));
-        k[o].a = __shfl_sync(0xffffffffu, mine.a, 8 * o + (lane >> 2));
-        k[o].g = __shfl_sync(0xffffffffu, mine.g, 8 * o + (lane >> 2));
-        k[o].target = __shfl_sync(0xffffffffu, t, 8 * o + (lane >> 2));
+        for (int o = 0; o < 4; ++o) {
+            k[o].lse = __shfl_sync(0xffffffffu, mine.lse, 8 * o + (lane >> 2));
+            k[o].a = __shfl_sync(0xffffffffu, mine.a, 8 * o + (lane >> 2));
+            k[o].g = __shfl_sync(0xffffffffu, mine.g, 8 * o + (lane >> 2));
+            k[o].target = __shfl_sync(0xffffffffu, t, 8 * o + (lane >> 2));
+        }
     }
     const long long row0 = static_cast<long long>(w.t0) + col0;
     for (int c = 0; c < n; c += EPI_T) {
@@ -588,6 +609,7 @@ __device__ __forceinline__ void gradient_tile(const Product &p, const Tile &w, i
             tc::tmem_ld_frag(t_set + c + 16, v[1]);
             tc::tmem_ld_wait(v[0]);
             tc::tmem_ld_wait(v[1]);
+            if (c + EPI_T >= n) release();
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -598,17 +620,23 @@ __device__ __forceinline__ void gradient_tile(const Product &p, const Tile &w, i
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const Token &q = k[2 * (i >> 3) + (i >> 1 & 1)];
-                v[h][i] = q.a * lt::fast_exp2(fmaf(v[h][i], lt::kLog2E, -q.lse));
-            }
-        if (__any_sync(0xffffffffu, t >= c && t < c + EPI_T)) {  // a target among these
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                if constexpr (EPI == SCALED_SUM) {
+                    v[h][i] *= alpha;
+                } else {
                     const Token &q = k[2 * (i >> 3) + (i >> 1 & 1)];
-                    if (q.target == c + 16 * h + 8 * (i >> 2 & 1) + 2 * (lane & 3) + (i & 1)) v[h][i] -= q.g;
+                    v[h][i] = q.a * lt::fast_exp2(fmaf(v[h][i], lt::kLog2E, -q.lse));
                 }
+            }
+        if constexpr (EPI == SOFTMAX_GRADIENT) {
+            if (__any_sync(0xffffffffu, t >= c && t < c + EPI_T)) {  // a target among these
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const Token &q = k[2 * (i >> 3) + (i >> 1 & 1)];
+                        if (q.target == c + 16 * h + 8 * (i >> 2 & 1) + 2 * (lane & 3) + (i & 1)) v[h][i] -= q.g;
+                    }
+            }
         }
         __syncwarp();  // the buffer's last contents have been read
         stage_fragments<T>(v, buf, lane);
@@ -741,6 +769,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         tc::fence_after();
         tmem = uniform(static_cast<int>(tmem_slot));
     }
+    if (EPI == SCALED_SUM) tiles *= p.loss.chunks;
     if (p.mode == ROWS_BY_EXPERT)
         tiles = tb.first[p.E + 1];
     else if (p.mode == K_BY_EXPERT)
@@ -763,7 +792,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         uint32_t ph = 1;
         int s = 0, issued = 0;  // stage; how many of the ring are in use, at most
         for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
-            const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+            const Tile w = locate<CG, EPI == SCALED_SUM>(idx, p, tb, static_cast<int>(rank));
             const int f0 = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS;
             const int tq = w.t0 + static_cast<int>(CG == 2 ? rank : 0) * q_rows;
             const int z_p = p.mode == ROWS_BY_EXPERT ? w.e : 0;
@@ -830,7 +859,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             uint32_t phases = 0;  // of tail_bar, a bit per stage
             int s = 0;
             for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
-                const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+                const Tile w = locate<CG, EPI == SCALED_SUM>(idx, p, tb, static_cast<int>(rank));
                 const int left = w.k_rows % BK;  // both operands are MN-major: a box row is one K
                 const bool tail = left != 0 && w.k0 <= w.k_rows / BK && w.k_rows / BK < w.k1;
                 s = (s + (F32 ? PIECES : 1) * (w.k1 - w.k0 - (tail ? 1 : 0))) % stages;
@@ -860,7 +889,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             uint32_t ph = 0, g = 0;
             int s = 0;
             for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
-                const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+                const Tile w = locate<CG, EPI == SCALED_SUM>(idx, p, tb, static_cast<int>(rank));
                 const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
                 for (int kb = w.k0; kb < w.k1; kb += BLOCKS ? BLOCK : w.k1 - w.k0, ++g) {
                     const int ke = BLOCKS ? min(kb + BLOCK, w.k1) : w.k1;
@@ -929,7 +958,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         const uint32_t acc_empty0 = tc::peer_addr(tc::smem_u32(&acc_empty[0]), lead);
         uint32_t g = 0, handed = 0;
         for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
-            const Tile w = locate<CG>(idx, p, tb, static_cast<int>(rank));
+            const Tile w = locate<CG, EPI == SCALED_SUM>(idx, p, tb, static_cast<int>(rank));
             const int fl = 32 * q + lane;           // feature within the CTA's 128
             const int f = w.ft * (PROWS * CG) + static_cast<int>(CG == 2 ? rank : 0) * PROWS + fl;
             T *out = static_cast<T *>(p.out) + (p.mode == K_BY_EXPERT ? w.e * p.out_expert : 0);
@@ -975,9 +1004,18 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     __syncwarp();
                     tc::fence_after();
                 }
-                if constexpr (EPI == SOFTMAX_GRADIENT && !F32) {
-                    gradient_tile<T>(p, w, f, f_ok, col0, n, any, t_set, epi, lane);
-                } else {
+                bool done = false;
+                if constexpr (!F32 && EPI != LOG_SUM) {
+                    if (EPI == SOFTMAX_GRADIENT || (p.loss.first && p.loss.last && ((p.widths >> OUT_SHIFT) & 255) == 16)) {
+                        staged_tile<T, EPI>(p, w, f, f_ok, col0, n, any, t_set, epi, lane, [&] {
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                        });
+                        done = true;
+                    }
+                }
+                if (!done) {
                     auto read = [&](int c, float (&v)[16]) {
                         if constexpr (BLOCKS) {
 #pragma unroll
@@ -994,9 +1032,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     loss_tile<T, EPI, COLS>(p, w, f, f_ok, col0, n, read);
                 }
                 if (!BLOCKS && any) {
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                    if (!done) {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                    }
                     ++g;
                 }
                 continue;
@@ -1305,7 +1345,7 @@ inline int q_bytes_of(int rows, bool mn) { return mn ? (rows + 63) / 64 * MN_BOX
 // between filling the pipeline and draining the last accumulator about 6000
 // clocks pass.  Measured on 4096^3 in bf16 (us): pairs 224 wide 73, 256 wide 82,
 // 128 wide 95; single CTAs 256 wide 93, 128 wide 126.
-inline Plan choose(const Product &p, const Device &d, int type, const Tune &only, int least = 0) {
+inline Plan choose(const Product &p, const Device &d, int type, const Tune &only, int least = 0, int chunks = 1) {
     const bool f32 = type == LINEAR_F32;
     Plan best;
     const int bts[] = {256, 224, 192, 160, 128, 96, 64, 32, 16};
@@ -1327,6 +1367,8 @@ inline Plan choose(const Product &p, const Device &d, int type, const Tune &only
                     ktiles = (p.K / (p.E > 0 ? p.E : 1) + BK - 1) / BK + 0.5;
                 }
             }
+            nt *= chunks;
+            ktiles /= chunks;
             const double tiles = nt * ((p.F + PROWS * cg - 1) / (PROWS * cg));
             double per = 370.0;
             const double copy = (P_BYTES + q_bytes_of(bt / cg, p.q_mn != 0)) / 62.0;
@@ -1389,7 +1431,7 @@ cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cu
 // Enqueue one product: P and Q as 16-bit operands (FP32: three planes each).
 template <int EPI>
 int run_product(int type, Product p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream,
-                int *token_tiles = nullptr) {
+                int *token_tiles = nullptr, int *chunks = nullptr) {
     if (p.T == 0 || p.F == 0 || (p.mode == K_BY_EXPERT && p.E == 0)) return SGEMM_OK;
     p.p_mn = P.mn;
     p.q_mn = Q.mn;
@@ -1407,6 +1449,27 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
         if (EPI != LAYER) only.splits = 1;
         pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
     }
+    p.loss.chunks = 1;
+    if (EPI == SCALED_SUM && chunks != nullptr) {
+        const int ktiles = (p.K + BK - 1) / BK;
+        if (*chunks >= 0) {  // as many as the piece before had
+            p.loss.chunks = *chunks;
+            pl = choose(p, d, type, only, 0, *chunks);
+        } else {
+            // of few tiles and a long K, shares of it side by side; their sums are 4 us of launch and
+            // what they write and read
+            for (int c = 2; c <= -*chunks && 4 * c <= ktiles; c += (c + 3) / 4) {
+                Plan with = choose(p, d, type, only, 0, c);
+                with.cost += 8000.0 + static_cast<double>(c) * p.T * p.F * 8 / (d.sms * 20.0);
+                if (with.cost < 0.9 * pl.cost) {
+                    pl = with;
+                    p.loss.chunks = c;
+                }
+            }
+            *chunks = p.loss.chunks;
+        }
+        if (*chunks > 1) p.loss.last = 0;
+    }
     p.bt = pl.bt;
     p.splits = pl.splits;
     p.q_bytes = q_bytes_of(p.bt / pl.cg, Q.mn);
@@ -1421,6 +1484,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     long long tiles = static_cast<long long>(p.nt) * p.nf;
     if (p.mode == ROWS_BY_EXPERT) tiles = (static_cast<long long>(p.nt) + p.E + 1) * p.nf;  // at most
     if (p.mode == K_BY_EXPERT) tiles *= p.E;
+    tiles *= p.loss.chunks;
     if (tiles > INT_MAX / 2) return SGEMM_ERR_INVALID_DIM;
     const int tables = p.mode == DENSE ? 0 : 2 * (p.E + 2) * 4;
     const int part = p.splits > 1 ? p.bt * PROWS * 4 : 0;
@@ -1447,8 +1511,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     sg_nvtx::Range r("linear: product");
     cudaError_t err = cudaErrorInvalidValue;
     if (type == LINEAR_F32) {
-        if constexpr (EPI != SCALED_SUM)
-            err = pl.cg == 2 ? launch<2, float, EPI>(maps, p, grid, smem, stream) : launch<1, float, EPI>(maps, p, grid, smem, stream);
+        err = pl.cg == 2 ? launch<2, float, EPI>(maps, p, grid, smem, stream) : launch<1, float, EPI>(maps, p, grid, smem, stream);
     } else if (type == LINEAR_BF16) {
         err = pl.cg == 2 ? launch<2, __nv_bfloat16, EPI>(maps, p, grid, smem, stream)
                          : launch<1, __nv_bfloat16, EPI>(maps, p, grid, smem, stream);

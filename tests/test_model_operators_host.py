@@ -115,9 +115,12 @@ def test_workspace_sizes(lib):
     assert size(BF16, 4, 32, 16, A + 2, 16, B, 32, 0) == 256 + 256 + 256       # a copy of x
     size = lib.linear_cross_entropy_backward_workspace_size
     assert size(BF16, 4, 32, 16, A, 16, B, 32, 0, 0, 0) == 0 and size(BF16, 4, 32, 0, A, 16, B, 32, 0, 1, 1) == 0
-    # at most 2**28 values of dz, whatever the vocabulary, and FP32 sums of dx where it takes several pieces
+    # at most 2**28 values of dz, whatever the vocabulary, and FP32 sums of dx where it takes several pieces (and
+    # several at once where it has few tiles)
     assert size(BF16, 8192, 10 ** 6, 64, A, 64, B, 64, 1, 0, 1) < 2 * 2 ** 28 + 2 ** 20
-    assert size(BF16, 8192, 10 ** 6, 64, A, 64, B, 64, 1, 1, 1) - size(BF16, 8192, 10 ** 6, 64, A, 64, B, 64, 1, 0, 1) == 8192 * 64 * 4
+    assert size(BF16, 8192, 10 ** 6, 512, A, 512, B, 512, 1, 1, 1) - size(BF16, 8192, 10 ** 6, 512, A, 512, B, 512, 1, 0, 1) == 8192 * 512 * 4
+    assert size(BF16, 8192, 10 ** 6, 64, A, 64, B, 64, 1, 1, 1) - size(BF16, 8192, 10 ** 6, 64, A, 64, B, 64, 1, 0, 1) == 2 * 8192 * 64 * 4
+    assert size(BF16, 1, 1000, 64, A, 64, B, 64, 1, 1, 1) - size(BF16, 1, 1000, 64, A, 64, B, 64, 1, 0, 1) == 64 * 64 * 4
 
 
 def test_wrappers_refuse_other_tensors(lib):
