@@ -91,8 +91,8 @@ __device__ __forceinline__ float warp_max_f(float v) {
 }
 // logistic(l), small ones included
 __device__ __forceinline__ float sigmoid(float l) {
-    const float e = expf(-fabsf(l));
-    return l < 0.0f ? e / (1.0f + e) : 1.0f / (1.0f + e);
+    const float e = expf(-fabsf(l)), s = lt::fast_reciprocal(1.0f + e);
+    return l < 0.0f ? e * s : s;
 }
 __device__ __forceinline__ double sigmoid(double l) {
     const double e = exp(-fabs(l));
@@ -258,7 +258,7 @@ __device__ __noinline__ double group_in_64(const Choose &c, const Held &held, in
 }
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 8 : 1) choose_kernel(const __grid_constant__ Choose c) {
+__global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS : 1) choose_kernel(const __grid_constant__ Choose c) {
     extern __shared__ unsigned long long room[];
     __shared__ int picks[CHOOSE_WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 8 : 1) choose_ker
     // 0.33 at most reach the score; the sum adds 1, the reciprocal 2: 5 a score.  Softmax, of the largest
     // score 1 / z: 4 of its own exponential (expf), less than 1 of the rounding of l - m (x exp(-x) < 0.4),
     // and those of z: 36 of up to 31 sums in a lane and 5 across, 11 of the exponentials (4, and the
-    // rounding of l - m at a mean of up to log 1024); 2 of quotient and product.
-    const float most = softmax ? 1.0f / z : 1.0f;
+    // rounding of l - m at a mean of up to log 1024); 3 of reciprocal and product.
+    const float most = softmax ? lt::fast_reciprocal(z) : 1.0f;
     const float slack = softmax ? most * 0x1p-17f : 0x1p-20f;
     float size = 1.0f;  // of what groups' sums add up
     uint32_t key[NV];
@@ -501,17 +501,18 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 8 : 1) choose_ker
         for (int s = 0; s < 2; ++s) {
             if (s >= slots) break;
             w[s] = softmax || lj[s] < 0.0f ? expf(lj[s] - ref) : 1.0f;
-            if (!softmax) w[s] /= 1.0f + expf(-fabsf(lj[s]));
+            if (!softmax) w[s] *= lt::fast_reciprocal(1.0f + expf(-fabsf(lj[s])));
             if (mine[s] < 0) w[s] = 0.0f;
             sum += w[s];
         }
         sum = warp_sum(sum);
     }
+    const float share = lt::fast_reciprocal(sum);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if (s >= slots) break;
         if (c.renormalize)
-            w[s] /= sum;
+            w[s] *= share;
         else
             w[s] = softmax ? expf(lj[s] - m) * most : sigmoid(lj[s]);
         w[s] = wrong ? __int_as_float(0x7fffffff) : mine[s] < 0 ? 0.0f : w[s] * c.scale;
@@ -584,15 +585,16 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_backward_kernel(cons
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         p[s] = softmax || l[s] < 0.0f ? expf(l[s] - ref) : 1.0f;
-        if (!softmax) p[s] /= 1.0f + expf(-fabsf(l[s]));
+        if (!softmax) p[s] *= lt::fast_reciprocal(1.0f + expf(-fabsf(l[s])));
         if (e[s] < 0) p[s] = 0.0f;
         sum += p[s];
     }
     const float whole = all ? z : warp_sum(sum);
+    const float share = any ? lt::fast_reciprocal(whole) : 1.0f;
     float mean = 0.0f;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        p[s] /= any ? whole : 1.0f;
+        p[s] *= share;
         mean += p[s] * g[s];
     }
     mean = softmax || c.renormalize ? warp_sum(mean) : 0.0f;
@@ -621,7 +623,6 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32) choose_backward_kernel(cons
     }
     T *out = static_cast<T *>(c.dlogits) + t * c.ldd;
     if (all) {
-        const float share = 1.0f / z;
 #pragma unroll
         for (int i = 0; i < NV; ++i) d[i] = any ? x[i] * share * (d[i] - mean) : 0.0f;
     }
