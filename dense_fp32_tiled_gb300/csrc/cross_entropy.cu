@@ -259,21 +259,20 @@ int forward(const Head &h, float *loss, float *lse, void *workspace, size_t work
 // ---- gradient ------------------------------------------------------------------------
 constexpr int SMS = 152, MOST_CHUNKS = 64;
 
-// dx (M rows of K) from the sums of its chunks, in their order.
+// dx (M rows of K) from the sums of its chunks, in their order: a block takes 256 of a row.
 template <typename T>
-__global__ void __launch_bounds__(256) chunks_kernel(const float *__restrict__ acc, int chunks, int M, int K, const float *alpha,
-                                                     T *__restrict__ dx, long long lddx) {
+__global__ void __launch_bounds__(256) chunks_kernel(const float *__restrict__ acc, int chunks, int M, int K, int strips,
+                                                     const float *alpha, T *__restrict__ dx, long long lddx) {
     tc::grid_trigger();
     tc::grid_wait();
+    const int row = blockIdx.x / strips, k = (blockIdx.x - row * strips) * 256 + threadIdx.x;
+    if (k >= K) return;
     const long long all = static_cast<long long>(M) * K;
-    const float scale = alpha != nullptr ? *alpha : 1.0f;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<long long>(gridDim.x) * 256) {
-        float s = 0.0f;
+    const float *from = acc + static_cast<long long>(row) * K + k;
+    float s = 0.0f;
 #pragma unroll 8
-        for (int c = 0; c < chunks; ++c) s += acc[c * all + i];
-        const long long row = i / K;
-        dx[row * lddx + (i - row * K)] = from_f<T>(s * scale);
-    }
+    for (int c = 0; c < chunks; ++c) s += from[c * all];
+    dx[row * lddx + k] = from_f<T>(alpha != nullptr ? s * *alpha : s);
 }
 
 struct BackwardBytes {
@@ -435,11 +434,11 @@ int backward(const Head &h, const float *dloss, const float *dlse, const float *
     }
     if (dx != nullptr && chunks > 1) {
         sg_nvtx::Range r("cross entropy: sum of chunks");
-        const long long blocks = (static_cast<long long>(h.M) * h.K + 255) / 256;
+        const int strips = (h.K + 255) / 256;  // chunks are for few tiles: M * strips fits
         auto sum = [&](auto el) {
             using El = decltype(el);
-            return tc::launch(chunks_kernel<El>, static_cast<unsigned>(blocks < SMS * 16 ? blocks : SMS * 16), dim3(256), 0, stream,
-                              static_cast<const float *>(p.loss.acc), chunks, h.M, h.K, p.loss.alpha, static_cast<El *>(dx), lddx);
+            return tc::launch(chunks_kernel<El>, static_cast<unsigned>(h.M) * strips, dim3(256), 0, stream,
+                              static_cast<const float *>(p.loss.acc), chunks, h.M, h.K, strips, p.loss.alpha, static_cast<El *>(dx), lddx);
         };
         const cudaError_t err = f32 ? sum(float()) : h.type == LINEAR_BF16 ? sum(__nv_bfloat16()) : sum(__half());
         if (err != cudaSuccess) {

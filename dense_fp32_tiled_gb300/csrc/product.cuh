@@ -545,9 +545,7 @@ __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f
         }
     } else {
         const float alpha = p.loss.alpha != nullptr ? *p.loss.alpha : 1.0f;
-#pragma unroll
-        for (int c = 0; c < COLS; c += 16) {
-            if (c >= n) break;
+        auto step = [&](int c) {
             float v[16], before[16];
             const long long row = static_cast<long long>(w.t0) + col0 + c;
             float *acc = p.loss.acc + (static_cast<long long>(w.e) * p.T + row) * p.F + f;
@@ -557,7 +555,7 @@ __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f
                     if (c + i < n) before[i] = acc[static_cast<long long>(i) * p.F];
             }
             read(c, v);
-            if (!f_ok) continue;
+            if (!f_ok) return;
             T *o = static_cast<T *>(p.out) + row * p.ldo + f;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -568,6 +566,13 @@ __device__ __forceinline__ void loss_tile(const Product &p, const Tile &w, int f
                     else
                         acc[static_cast<long long>(i) * p.F] = s;
                 }
+        };
+        if constexpr (std::is_same<T, float>::value) {  // from registers, whose numbers are constants
+#pragma unroll
+            for (int c = 0; c < COLS; c += 16)
+                if (c < n) step(c);
+        } else {
+            for (int c = 0; c < n; c += 16) step(c);
         }
     }
 }
@@ -1456,7 +1461,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
             p.loss.chunks = *chunks;
             pl = choose(p, d, type, only, 0, *chunks);
         } else {
-            // of few tiles and a long K, shares of it side by side; their sums are 4 us of launch and
+            // of few tiles and a long K, shares of it side by side; joining them takes 4 us and
             // what they write and read
             for (int c = 2; c <= -*chunks && 4 * c <= ktiles; c += (c + 3) / 4) {
                 Plan with = choose(p, d, type, only, 0, c);
