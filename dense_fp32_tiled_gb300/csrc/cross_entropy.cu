@@ -21,6 +21,7 @@
 #include <mutex>
 
 #include "cross_entropy.h"
+#include "linear_few.cuh"
 #include "linear_prep.cuh"
 #include "nvtx_range.cuh"
 #include "product.cuh"
@@ -67,6 +68,42 @@ join_kernel(const float2 *__restrict__ parts, int n, int M, int N, int tokens, c
     const long long t = target_of(l, i);
     lse[i] = s;
     loss[i] = t >= 0 && t < N ? s - l.hit[i] : 0.0f;
+}
+
+// ---- few tokens in FP32 ---------------------------------------------------------------
+// The product kernel wants the weight in three bf16 pieces, which for few tokens costs
+// more than all else (4 x 56678 x 1024: 86 of 154 us); linear's form for few tokens reads
+// it once as it is.  It leaves the logits of those few tokens in the workspace,
+// and a block here makes a part of STRIP of a token's.
+constexpr int STRIP_THREADS = 256, STRIP = 8 * STRIP_THREADS;
+__global__ void __launch_bounds__(STRIP_THREADS) strips_kernel(const float *__restrict__ z, int M, int N, int strips, const Loss l) {
+    __shared__ float2 part[STRIP_THREADS / 32];
+    const int i = blockIdx.x / strips, strip = blockIdx.x - i * strips;
+    const int j0 = strip * STRIP;
+    const float *row = z + static_cast<long long>(i) * N;
+    tc::grid_trigger();
+    tc::grid_wait();
+    const long long t = target_of(l, i);
+    float v[8];
+    float2 a = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * STRIP_THREADS + threadIdx.x;
+        v[k] = j < N ? row[j] : -INFINITY;
+        a.x = fmaxf(a.x, v[k]);
+        if (j < N && j == t) l.hit[i] = v[k];
+    }
+    const float ref = a.x == -INFINITY ? 0.0f : a.x;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a.y += expf(v[k] - ref);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1)
+        a = join(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, k), __shfl_xor_sync(0xffffffffu, a.y, k)));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < STRIP_THREADS / 32; ++w) a = join(a, part[w]);
+    l.parts[static_cast<long long>(strip) * M + i] = a;
 }
 
 // ---- what the gradient's epilogue needs of each token -------------------------------
@@ -182,8 +219,16 @@ Matrix w_matrix(const Head &h) {
 Span w_span(const void *p, const Head &h, long long ld) { return span(p, w_outer(h), w_inner(h), ld, lt::type_bytes(h.type)); }
 
 // ---- forward -------------------------------------------------------------------------
+linear_few::Few few(const Head &h) {
+    linear_few::Few p;
+    memset(&p, 0, sizeof p);
+    p.T = h.M, p.F = h.N, p.K = h.K, p.x = h.x, p.w = h.w, p.ldx = h.ldx, p.ldw = h.ldw, p.ldo = h.N, p.order = h.w_order;
+    return p;
+}
+bool few_tokens(const Head &h) { return h.type == LINEAR_F32 && h.K > 0 && linear_few::takes(h.type, few(h)); }
+
 struct ForwardBytes {
-    size_t parts, hit, total;
+    size_t parts, hit, z, total;
 };
 ForwardBytes forward_bytes(const Head &h) {
     ForwardBytes b{};
@@ -191,8 +236,9 @@ ForwardBytes forward_bytes(const Head &h) {
     const long long tiles = (static_cast<long long>(h.N) + LOG_SUM_COLS - 1) / LOG_SUM_COLS;
     b.parts = up256(2 * tiles * h.M * static_cast<long long>(sizeof(float2)));
     b.hit = up256(4LL * h.M);
-    b.total = b.parts + b.hit;
-    if (h.K > 0) b.total += operand_bytes(h.type, x_matrix(h)) + operand_bytes(h.type, w_matrix(h));
+    if (few_tokens(h)) b.z = up256(4LL * h.M * h.N);
+    b.total = b.parts + b.hit + b.z;
+    if (h.K > 0 && b.z == 0) b.total += operand_bytes(h.type, x_matrix(h)) + operand_bytes(h.type, w_matrix(h));
     return b;
 }
 
@@ -228,7 +274,21 @@ int forward(const Head &h, float *loss, float *lse, void *workspace, size_t work
     p.loss.targets = h.targets;
     p.loss.target_bytes = h.target_bytes;
     int parts = 0;
-    if (h.N > 0) {
+    auto failed = [] {
+        (void)cudaGetLastError();
+        return SGEMM_ERR_LAUNCH;
+    };
+    if (need.z > 0) {
+        linear_few::Few f = few(h);
+        f.out = ws + need.parts + need.hit;
+        f.sms = d.sms;
+        if (linear_few::run(h.type, f, stream) != cudaSuccess) return failed();
+        parts = (h.N + STRIP - 1) / STRIP;
+        sg_nvtx::Range r("cross entropy: strips");
+        if (tc::launch(strips_kernel, static_cast<unsigned>(parts) * h.M, dim3(STRIP_THREADS), 0, stream, static_cast<const float *>(f.out),
+                       h.M, h.N, parts, p.loss) != cudaSuccess)
+            return failed();
+    } else if (h.N > 0) {
         Operand P, Q;
         if (h.K > 0) {
             Copies copies(ws + need.parts + need.hit);
@@ -251,9 +311,7 @@ int forward(const Head &h, float *loss, float *lse, void *workspace, size_t work
     const cudaError_t err = tc::launch(join_kernel, static_cast<unsigned>((static_cast<long long>(h.M) + tokens - 1) / tokens),
                                        dim3(JOIN_THREADS), 0, stream, static_cast<const float2 *>(p.loss.parts), parts, h.M, h.N, tokens,
                                        p.loss, loss, lse);
-    if (err == cudaSuccess) return SGEMM_OK;
-    (void)cudaGetLastError();
-    return SGEMM_ERR_LAUNCH;
+    return err == cudaSuccess ? SGEMM_OK : failed();
 }
 
 // ---- gradient ------------------------------------------------------------------------
