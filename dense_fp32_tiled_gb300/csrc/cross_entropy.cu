@@ -233,7 +233,7 @@ struct ForwardBytes {
 ForwardBytes forward_bytes(const Head &h) {
     ForwardBytes b{};
     if (check_sizes(h) != SGEMM_OK || h.M == 0 || h.N == 0) return b;
-    const long long tiles = (static_cast<long long>(h.N) + LOG_SUM_COLS - 1) / LOG_SUM_COLS;
+    const long long columns = log_sum_columns(h.N, h.M), tiles = (h.N + columns - 1) / columns;
     b.parts = up256(2 * tiles * h.M * static_cast<long long>(sizeof(float2)));
     b.hit = up256(4LL * h.M);
     if (few_tokens(h)) b.z = up256(4LL * h.M * h.N);

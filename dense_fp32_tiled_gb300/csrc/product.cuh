@@ -1307,8 +1307,9 @@ inline bool encode(CUtensorMap &map, const Operand &o, bool f16, int box_outer) 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Narrowest tile of LOG_SUM: the room for its parts is known without a plan.
-constexpr int LOG_SUM_COLS = 64;
+// Narrowest tile of LOG_SUM, T x F: the room for its parts is known without a plan.
+// Only products of few tiles want one narrower than 128.
+inline int log_sum_columns(long long T, long long F) { return T * F > 1 << 22 ? 128 : 64; }
 struct Plan {
     int cg = 2, bt = 256, splits = 1, units = 1;
     double cost = 1e300;
@@ -1443,8 +1444,9 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.timeout_flag = d.timeout_flag;
     Tune only = tune();
     if (EPI != LAYER) only.splits = 1;
-    if (EPI == LOG_SUM && only.bt < LOG_SUM_COLS) only.bt = 0;  // no narrower ones
-    Plan pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
+    const int least = EPI == LOG_SUM ? log_sum_columns(p.T, p.F) : 0;
+    if (only.bt < least) only.bt = 0;  // no narrower ones
+    Plan pl = choose(p, d, type, only, least);
     if (pl.cost > 1e299) {
         static std::once_flag told;
         std::call_once(told, [&] {
@@ -1452,7 +1454,7 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
         });
         only = Tune();
         if (EPI != LAYER) only.splits = 1;
-        pl = choose(p, d, type, only, EPI == LOG_SUM ? LOG_SUM_COLS : 0);
+        pl = choose(p, d, type, only, least);
     }
     p.loss.chunks = 1;
     if (EPI == SCALED_SUM && chunks != nullptr) {
