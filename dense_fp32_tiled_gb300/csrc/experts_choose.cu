@@ -6,7 +6,7 @@
 // lanes in a row).  The J + 1 lanes with the largest best value give a bound that
 // all picks reach; the some ten experts that do are brought together, one a
 // lane, and each counts those before it: its place.  (Picking one after the
-// other took 36 us for 16384 tokens of 256 experts in 8 groups; this NN.)  Values are compared as
+// other took 36 us for 16384 tokens of 256 experts in 8 groups; this 24.)  Values are compared as
 // whole numbers of the same order as the floats (0: not to be chosen), so a
 // maximum over a warp is one instruction.  Bound by instructions.
 //
@@ -94,10 +94,6 @@ __device__ __forceinline__ float sigmoid(float l) {
     const float e = expf(-fabsf(l)), s = lt::fast_reciprocal(1.0f + e);
     return l < 0.0f ? e * s : s;
 }
-__device__ __forceinline__ double sigmoid(double l) {
-    const double e = exp(-fabs(l));
-    return l < 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);
-}
 // The same for a comparison: see `slack`.
 __device__ __forceinline__ float sigmoid_about(float l) { return lt::fast_reciprocal(1.0f + lt::fast_exp2(-lt::kLog2E * l)); }
 
@@ -163,80 +159,123 @@ __device__ __forceinline__ void keep_two(R r, R &first, R &second) {
     second = r > first ? first : r > second ? r : second;
     first = r > first ? r : first;
 }
-// Which groups compete, a bit each: lane g holds the rank of group g's sum (0: none of its experts may be chosen).
-__device__ __forceinline__ unsigned kept_groups(const Choose &c, uint32_t total, int lane) {
-    unsigned keep = 0;
-    for (int k = 0; k < c.kept; ++k) {
-        const uint32_t high = warp_max(total);
-        if (high == 0) break;
-        const unsigned one = __ballot_sync(ALL, total == high);
-        keep |= one & (0u - one);  // the lowest
-        if ((keep >> lane & 1) != 0) total = 0;
-    }
-    return keep;
-}
 __device__ __forceinline__ unsigned group_of(const Choose &c, int e) { return e * c.per >> 20; }
 
-// A warp's room: ranks and numbers of experts whose values are told apart in 64 bits.
+// A token's scores for comparing: m its largest logit, most = 1 / sum of exp(l - m).
+struct Scores {
+    bool softmax;
+    float m, most;
+    __device__ __forceinline__ float of(float l) const { return softmax ? expf(l - m) * most : sigmoid_about(l); }
+    __device__ __forceinline__ float with(float l, float bias) const { return __fadd_rn(of(l), bias); }  // the same bits everywhere
+};
+
+// ---- in 64 bits: for few tokens, so in little code (an SM fetches it anew) -----------
+// A warp's room: the experts whose values are told apart, in order, and their ranks.
 struct Held {
     unsigned long long *rank;
     unsigned short *expert;
 };
-
-// Puts the experts of this lane for which which(i) holds into `held`, all lanes' in
-// the order of their numbers.  How many there are; none are put there if more than `room`.
-template <int NV, typename I, typename F>
-__device__ __forceinline__ int bring_together(I *expert, int room, int e0, int lane, F &&which) {
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) mine += which(i) ? 1 : 0;
-    int n = mine;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const int o = __shfl_up_sync(ALL, n, k);
-        if (lane >= k) n += o;
+// Brings together the experts of the groups in `mask` whose values in 32 bits are not
+// below `least` (lane g's: of group g) and works out their values.  How many there are.
+// (All in one pass of the exponential and the quotient, which take a warp 2 us.)
+template <typename T>
+__device__ __noinline__ int values_in_64(const Choose &c, const T *row, const Held &held, const Scores &s, unsigned mask, float least,
+                                         int lane) {
+    int n = 0;
+#pragma unroll 1
+    for (int first = 0; first < c.E; first += 32) {
+        const int e = first + lane;
+        const unsigned g = e < c.E ? group_of(c, e) : 0;
+        const float bound = __shfl_sync(ALL, least, g);
+        bool in = false;
+        if (e < c.E && (mask >> g & 1) != 0) {
+            const float l = to_f(row[e]), b = c.bias != nullptr ? c.bias[e] : 0.0f;
+            in = l > -INFINITY && b > -INFINITY && !(s.with(l, b) < bound);
+        }
+        const unsigned all = __ballot_sync(ALL, in);
+        if (in) held.expert[n + __popc(all & ((1u << lane) - 1))] = static_cast<unsigned short>(e);
+        n += __popc(all);
     }
-    int at = n - mine;
-    n = __shfl_sync(ALL, n, 31);
+    double z = 1.0;  // without a bias the scores' proportions are enough
+    if (s.softmax && c.bias != nullptr) {
+        z = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < c.E; e += 32) z += exp(static_cast<double>(to_f(row[e])) - static_cast<double>(s.m));
+        z = warp_sum(z);
+    }
     __syncwarp();
-    if (n <= room) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (which(i)) expert[at++] = static_cast<I>(e0 + i);
+#pragma unroll 1
+    for (int k = lane; k < n; k += 32) {
+        const int e = held.expert[k];
+        // exp(l - m) / z, or 1 / (1 + exp(-l)) in the form that keeps small ones
+        const double l = static_cast<double>(to_f(row[e])), x = exp(s.softmax ? l - static_cast<double>(s.m) : -fabs(l));
+        const double v = (s.softmax || l < 0.0 ? x : 1.0) / (s.softmax ? z : 1.0 + x);
+        held.rank[k] = rank_of(c.bias != nullptr ? v + static_cast<double>(c.bias[e]) : v);
     }
     __syncwarp();
     return n;
 }
-
-// The values of the n experts of `held` in 64 bits.
+// The groups that compete, of which `keep` do by sums in 32 bits: those whose sums are
+// within `width` of the border's other side (low: the least that stays, out: the
+// largest that does not) by their sums in 64.
 template <typename T>
-__device__ __noinline__ void values_in_64(const Choose &c, const T *row, const Held &held, int n, int lane) {
-    double m = -INFINITY, z = 0.0;
-    if (c.scoring == EXPERTS_SOFTMAX) {
-        for (int e = lane; e < c.E; e += 32) m = fmax(m, static_cast<double>(to_f(row[e])));
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) m = fmax(m, __shfl_xor_sync(ALL, m, k));
-        for (int e = lane; e < c.E; e += 32) z += exp(static_cast<double>(to_f(row[e])) - m);
-        z = warp_sum(z);
+__device__ __noinline__ unsigned groups_in_64(const Choose &c, const T *row, const Held &held, const Scores &s, unsigned keep,
+                                              uint32_t total, uint32_t least, float low, float out, float width, int lane) {
+    const float v = of_rank(total);
+    const bool stays = (keep >> lane & 1) != 0;
+    const unsigned near = __ballot_sync(ALL, lane < c.groups && total != 0 && !((stays ? v - out : low - v) >= width));
+    // a group's best are among those not further below its last one in 32 bits: 2 scores, 2 sums with the
+    // bias, and what `least` lost
+    const int n = values_in_64(c, row, held, s, near, least != 0 ? of_rank(least) - width : -INFINITY, lane);
+    unsigned long long exact = 0;  // lane g
+    int before = 0;
+#pragma unroll 1
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        unsigned long long first = 0, second = 0, any;
+        for (int k = lane; k < n; k += 32)
+            if (group_of(c, held.expert[k]) == static_cast<unsigned>(g)) keep_two(held.rank[k], first, second);
+        const double sum = best_two<unsigned long long, double>(first, second, c.top > 1, &any);
+        if (lane == g) exact = rank_of(sum);
     }
-    for (int k = lane; k < n; k += 32) {
-        const int e = held.expert[k];
-        const double l = static_cast<double>(to_f(row[e]));
-        double v = c.scoring == EXPERTS_SOFTMAX ? exp(l - m) / z : sigmoid(l);
-        if (c.bias != nullptr) v += static_cast<double>(c.bias[e]);
-        held.rank[k] = rank_of(v);
+#pragma unroll 1
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const unsigned long long o = __shfl_sync(ALL, exact, g);
+        before += o > exact || (o == exact && g < lane) ? 1 : 0;
     }
-    __syncwarp();
+    return (keep & ~near) | __ballot_sync(ALL, (near >> lane & 1) != 0 && before < __popc(keep & near));
 }
-// The J best of those, one after the other: this lane's picks (pick j at lane
-// j % 32, in mine[j / 32]).
-__device__ __noinline__ void pick_in_64(const Choose &c, const Held &held, int n, int lane, int (&mine)[2]) {
+// The J best of the groups in `mask`, of those not below `least`: this lane's picks
+// (pick j at lane j % 32, in mine[j / 32]).
+template <typename T>
+__device__ __noinline__ void picks_in_64(const Choose &c, const T *row, const Held &held, const Scores &s, unsigned mask, float least,
+                                         int lane, int *mine) {
+    const int n = values_in_64(c, row, held, s, mask, least, lane);
     mine[0] = mine[1] = -1;
+    if (n <= 32) {  // each counts those before it
+        const unsigned long long k = lane < n ? held.rank[lane] : 0;
+        const int e = lane < n ? held.expert[lane] : -1;
+        int place = 0;
+#pragma unroll 1
+        for (int o = 0; o < n; ++o) {
+            const unsigned long long other = __shfl_sync(ALL, k, o);
+            place += other > k || (other == k && o < lane) ? 1 : 0;
+        }
+        __syncwarp();
+        if (e >= 0) held.expert[place] = static_cast<unsigned short>(e);
+        __syncwarp();
+        if (lane < n && lane < c.J) mine[0] = held.expert[lane];
+        __syncwarp();
+        return;
+    }
+#pragma unroll 1
     for (int j = 0; j < c.J; ++j) {
         unsigned long long best = 0;
-        int at = -1;
+        int at = INT_MAX;
+#pragma unroll 1
         for (int k = lane; k < n; k += 32)
-            if (held.rank[k] > best) {  // the first of equal ones: they are in order
+            if (held.rank[k] > best) {
                 best = held.rank[k];
                 at = k;
             }
@@ -249,13 +288,6 @@ __device__ __noinline__ void pick_in_64(const Choose &c, const Held &held, int n
         __syncwarp();
     }
 }
-// The sum in 64 bits of group g's best, of those of `held`.
-__device__ __noinline__ double group_in_64(const Choose &c, const Held &held, int n, unsigned g, int lane) {
-    unsigned long long first = 0, second = 0, any;
-    for (int k = lane; k < n; k += 32)
-        if (group_of(c, held.expert[k]) == g) keep_two(held.rank[k], first, second);
-    return best_two<unsigned long long, double>(first, second, c.top > 1, &any);
-}
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS : 1) choose_kernel(const __grid_constant__ Choose c) {
@@ -267,7 +299,9 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
     tc::grid_wait();
     if (t >= c.T) return;
     const T *row = static_cast<const T *>(c.logits) + t * c.ld;
-    const bool softmax = c.scoring == EXPERTS_SOFTMAX;
+    Held held;
+    held.rank = room + static_cast<size_t>(warp) * c.E;
+    held.expert = reinterpret_cast<unsigned short *>(room + static_cast<size_t>(CHOOSE_WARPS) * c.E) + warp * c.E;
     const int e0 = lane * NV;
     float l[NV];
     load_row<T, NV>(row, lane, c.E, c.wide, -INFINITY, l);
@@ -275,14 +309,20 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
 #pragma unroll
     for (int i = 0; i < NV; ++i) m = max_or_nan(m, l[i]);
     m = warp_max_f(m);
-    const bool wrong = m != m || (softmax && m == INFINITY);
+    Scores s{c.scoring == EXPERTS_SOFTMAX, m, 1.0f};
+    if (m != m || (s.softmax && m == INFINITY)) {
+        for (int j = lane; j < c.J; j += 32) {
+            c.chosen[static_cast<long long>(t) * c.J + j] = -1;
+            c.weights[static_cast<long long>(t) * c.J + j] = __int_as_float(0x7fffffff);
+        }
+        return;
+    }
     const bool summed = c.groups > 1 && c.top > 1;  // groups by sums of scores
-    float z = 1.0f;
-    if (softmax && (c.bias != nullptr || !c.renormalize || summed) && m > -INFINITY) {
-        z = 0.0f;
+    if (s.softmax && (c.bias != nullptr || !c.renormalize || summed) && m > -INFINITY) {
+        float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) z += expf(l[i] - m);
-        z = warp_sum(z);
+        s.most = lt::fast_reciprocal(warp_sum(z));
     }
     // How far the difference of two scores may be off, in units of 2^-24.  Sigmoid: the exponential is
     // within 4 of its value and the rounding of its argument moves it by 1.44 |l|, of which a quarter and
@@ -290,35 +330,29 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
     // score 1 / z: 4 of its own exponential (expf), less than 1 of the rounding of l - m (x exp(-x) < 0.4),
     // and those of z: 36 of up to 31 sums in a lane and 5 across, 11 of the exponentials (4, and the
     // rounding of l - m at a mean of up to log 1024); 3 of reciprocal and product.
-    const float most = softmax ? lt::fast_reciprocal(z) : 1.0f;
-    const float slack = softmax ? most * 0x1p-17f : 0x1p-20f;
-    float size = 1.0f;  // of what groups' sums add up
+    const float slack = s.softmax ? s.most * 0x1p-17f : 0x1p-20f;
     uint32_t key[NV];
-    float bias[NV];
-    if (c.bias != nullptr) load_row<float, NV>(c.bias, lane, c.E, c.wide_bias, -INFINITY, bias);
-    auto score_of = [&](float x) { return softmax ? expf(x - m) * most : sigmoid_about(x); };
-    auto value_of = [&](float x, float b) { return __fadd_rn(score_of(x), b); };  // the same bits wherever it is worked out
+    if (c.bias != nullptr) {
+        float bias[NV];
+        load_row<float, NV>(c.bias, lane, c.E, c.wide_bias, -INFINITY, bias);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        key[i] = 0;
-        if (l[i] > -INFINITY && !wrong) {
-            const float v = c.bias != nullptr ? value_of(l[i], bias[i]) : l[i];
-            if (v > -INFINITY) {
-                key[i] = rank_of(v);
-                if (c.bias != nullptr) size = fmaxf(size, fabsf(v));
-            }
+        for (int i = 0; i < NV; ++i) {
+            const float v = s.with(l[i], bias[i]);
+            key[i] = l[i] > -INFINITY && v > -INFINITY ? rank_of(v) : 0;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = l[i] > -INFINITY ? rank_of(l[i]) : 0;
     }
-    Held held;
-    held.rank = room + static_cast<size_t>(warp) * c.E;
-    held.expert = reinterpret_cast<unsigned short *>(room + static_cast<size_t>(CHOOSE_WARPS) * c.E) + warp * c.E;
+    unsigned keep = 1;  // a bit a group
     if (c.groups > 1) {
         uint32_t total = 0, least = 0;  // lane g: the rank of group g's sum, and of the least value in it
-        auto rank = [&](int i) { return summed && c.bias == nullptr && key[i] != 0 ? rank_of(score_of(l[i])) : key[i]; };
+        const bool scores = summed && c.bias == nullptr;
+        auto value_rank = [&](int i) { return scores && key[i] != 0 ? rank_of(s.of(l[i])) : key[i]; };
         if (c.lanes > 0) {  // a group is `lanes` lanes, a power of two
             uint32_t first = 0, second = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) keep_two(rank(i), first, second);
+            for (int i = 0; i < NV; ++i) keep_two(value_rank(i), first, second);
             for (int k = 1; k < c.lanes; k <<= 1) {
                 const uint32_t o1 = __shfl_xor_sync(ALL, first, k), o2 = __shfl_xor_sync(ALL, second, k);
                 keep_two(o1, first, second);
@@ -334,49 +368,33 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
                 uint32_t first = 0, second = 0, any;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    if (group_of(c, e0 + i) == static_cast<unsigned>(g)) keep_two(rank(i), first, second);
+                    if (group_of(c, e0 + i) == static_cast<unsigned>(g)) keep_two(value_rank(i), first, second);
                 const float sum = best_two<uint32_t, float>(first, second, c.top > 1, &any);
-                const uint32_t low = c.top > 1 && __popc(__ballot_sync(ALL, first != 0)) + __popc(__ballot_sync(ALL, second != 0)) < 2
-                                         ? 0
-                                         : rank_of(c.top > 1 ? sum - of_rank(any) : sum);
+                const int values = __popc(__ballot_sync(ALL, first != 0)) + __popc(__ballot_sync(ALL, second != 0));
                 if (lane == g && any != 0) {
                     total = rank_of(sum);
-                    least = low;
+                    least = c.top == 1 ? total : values < 2 ? 0 : rank_of(sum - of_rank(any));
                 }
             }
         }
-        unsigned keep = kept_groups(c, total, lane);
-        const bool stay = (keep >> lane & 1) != 0;
+        // group g's place: those before it (lanes without a group hold 0)
+        int before = 0;
+        for (int g = 0; g < c.groups; g += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                before += __shfl_sync(ALL, total, g + u & 31) > total - (g + u < lane ? 1u : 0u) ? 1 : 0;
+        const bool stays = total != 0 && before < c.kept;
+        keep = __ballot_sync(ALL, stays);
         if (summed || c.bias != nullptr) {
-            // in doubt: the groups whose sums are within `width` of the border's other side
-            if (c.bias != nullptr) size = warp_max_f(size);
-            const float width = 2.0f * slack + 0x1p-21f * size;  // 4 scores; 4 sums with biases, 2 of two values
-            const uint32_t low = __reduce_min_sync(ALL, stay ? total : 0xffffffffu);
-            const uint32_t out = warp_max(lane < c.groups && !stay ? total : 0u);
-            if (out != 0 && !(of_rank(low) - of_rank(out) >= width)) {
-                const float v = of_rank(total);
-                const unsigned near = __ballot_sync(ALL, lane < c.groups && total != 0 && (stay ? !(v - of_rank(out) >= width) : !(of_rank(low) - v >= width)));
-                const int n = bring_together<NV>(held.expert, c.E, e0, lane, [&](int i) {
-                    const unsigned g = group_of(c, e0 + i) & 31;
-                    // the group's best, and what may be among them: 2 scores, 2 sums with the bias, and what `least` lost
-                    const uint32_t bound = __shfl_sync(ALL, least, g);
-                    return key[i] != 0 && (near >> g & 1) != 0 && (bound == 0 || !(of_rank(rank(i)) < of_rank(bound) - width));
-                });
-                values_in_64(c, row, held, n, lane);
-                unsigned long long exact = 0;  // lane g
-                for (unsigned left = near; left != 0; left &= left - 1) {
-                    const int g = __ffs(left) - 1;
-                    const double sum = group_in_64(c, held, n, g, lane);
-                    if (lane == g) exact = rank_of(sum);
-                }
-                const int places = __popc(keep & near);
-                int before = 0;
-                for (unsigned left = near; left != 0; left &= left - 1) {
-                    const int g = __ffs(left) - 1;
-                    const unsigned long long o = __shfl_sync(ALL, exact, g);
-                    before += o > exact || (o == exact && g < lane) ? 1 : 0;
-                }
-                keep = (keep & ~near) | __ballot_sync(ALL, (near >> lane & 1) != 0 && before < places);
+            const uint32_t low = __reduce_min_sync(ALL, stays ? total : 0xffffffffu), out = warp_max(stays ? 0u : total);
+            if (out != 0) {
+                const float a = of_rank(least), v = of_rank(total);  // of what the sums add up: the size
+                float size = total == 0 ? 0.0f : least == 0 ? fabsf(v) : fmaxf(fabsf(a), fabsf(v - a));
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) size = fmaxf(size, __shfl_xor_sync(ALL, size, k));
+                const float width = 2.0f * slack + 0x1p-21f * size;  // 4 scores; 4 sums with biases, 2 of two values
+                if (!(of_rank(low) - of_rank(out) >= width))
+                    keep = groups_in_64(c, row, held, s, keep, total, least, of_rank(low), of_rank(out), width, lane);
             }
         }
         if (c.lanes > 0) {
@@ -395,31 +413,42 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
     int mine[2] = {-1, -1}, *pick = picks[warp];
     float floor = 0.0f;  // the least pick's value
     bool doubt = false;
-    int n = 33;
+    int n = 33, count = 0, at_list = 0;
+    uint32_t mask = 0;  // of this lane's experts, those brought together
     if (c.J < 32) {
         // of as many lanes' best as there are picks and one more, the least: a bound
-        uint32_t left = best, bound = 0;
-        for (int got = 0; got <= c.J;) {
+        uint32_t left = best, bound;
+        int need = c.J;
+        do {
             bound = warp_max(left);
-            if (bound == 0) break;
-            const unsigned there = __ballot_sync(ALL, left == bound);
-            if (left == bound) left = 0;
-            got += __popc(there);
+            need -= __popc(__ballot_sync(ALL, left == bound));
+            left = left == bound ? 0 : left;
+        } while (need >= 0 && bound != 0);
+        bound = bound > 1 ? bound : 1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) mask |= key[i] >= bound ? 1u << i : 0u;
+        count = __popc(mask);
+        n = count;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int o = __shfl_up_sync(ALL, n, k);
+            if (lane >= k) n += o;
         }
-        n = bring_together<NV>(pick, 32, e0, lane, [&](int i) { return key[i] != 0 && key[i] >= bound; });
+        at_list = n - count;
+        n = __shfl_sync(ALL, n, 31);
     }
     if (n <= 32) {
+        for (; mask != 0; mask &= mask - 1) pick[at_list++] = e0 + __ffs(mask) - 1;
+        __syncwarp();
         int e = lane < n ? pick[lane] : -1;
         // its value again, as its lane has it
         float le = e >= 0 ? to_f(row[e]) : 0.0f, be = e >= 0 && c.bias != nullptr ? c.bias[e] : 0.0f;
-        float v = c.bias != nullptr ? value_of(le, be) : le;
+        float v = c.bias != nullptr ? s.with(le, be) : le;
         const uint32_t k = e >= 0 ? rank_of(v) : 0;
         int place = 0;
-#pragma unroll 4
-        for (int o = 0; o < n; ++o) {
-            const uint32_t other = __shfl_sync(ALL, k, o);
-            place += other > k || (other == k && o < lane) ? 1 : 0;
-        }
+        for (int o = 0; o < n; o += 4)  // lanes without an expert hold 0
+#pragma unroll
+            for (int u = 0; u < 4; ++u) place += __shfl_sync(ALL, k, o + u & 31) > k - (o + u < lane ? 1u : 0u) ? 1 : 0;
         __syncwarp();
         if (e >= 0) pick[place] = lane;
         __syncwarp();
@@ -476,50 +505,46 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
             }
         }
     }
-    if (doubt) {  // those that may be among the J best, in 64 bits
-        const float low = floor - slack - 0x1p-22f * fabsf(floor);
-        const int some = bring_together<NV>(held.expert, c.E, e0, lane, [&](int i) { return key[i] != 0 && !(of_rank(key[i]) < low); });
-        values_in_64(c, row, held, some, lane);
-        pick_in_64(c, held, some, lane, mine);
-    }
+    if (doubt)  // those that may be among the J best, in 64 bits
+        picks_in_64(c, row, held, s, keep, floor - slack - 0x1p-22f * fabsf(floor), lane, mine);
 
     // weights of the picks
     float lj[2], w[2];
     float high = -INFINITY;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        lj[s] = mine[s] >= 0 ? to_f(row[mine[s]]) : -INFINITY;
-        high = fmaxf(high, lj[s]);
+    for (int u = 0; u < 2; ++u) {
+        lj[u] = mine[u] >= 0 ? to_f(row[mine[u]]) : -INFINITY;
+        high = fmaxf(high, lj[u]);
     }
     float sum = 0.0f;
     const int slots = c.J > 32 ? 2 : 1;
     if (c.renormalize) {
         // relative to the largest pick, so that no pick's score is lost below the smallest number
         high = warp_max_f(high);
-        const float ref = softmax ? high : fminf(high, 0.0f);
-        #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (s >= slots) break;
-            w[s] = softmax || lj[s] < 0.0f ? expf(lj[s] - ref) : 1.0f;
-            if (!softmax) w[s] *= lt::fast_reciprocal(1.0f + expf(-fabsf(lj[s])));
-            if (mine[s] < 0) w[s] = 0.0f;
-            sum += w[s];
+        const float ref = s.softmax ? high : fminf(high, 0.0f);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (u >= slots) break;
+            w[u] = s.softmax || lj[u] < 0.0f ? expf(lj[u] - ref) : 1.0f;
+            if (!s.softmax) w[u] *= lt::fast_reciprocal(1.0f + expf(-fabsf(lj[u])));
+            if (mine[u] < 0) w[u] = 0.0f;
+            sum += w[u];
         }
         sum = warp_sum(sum);
     }
     const float share = lt::fast_reciprocal(sum);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        if (s >= slots) break;
+    for (int u = 0; u < 2; ++u) {
+        if (u >= slots) break;
         if (c.renormalize)
-            w[s] *= share;
+            w[u] *= share;
         else
-            w[s] = softmax ? expf(lj[s] - m) * most : sigmoid(lj[s]);
-        w[s] = wrong ? __int_as_float(0x7fffffff) : mine[s] < 0 ? 0.0f : w[s] * c.scale;
-        const int j = s * 32 + lane;
+            w[u] = s.softmax ? expf(lj[u] - m) * s.most : sigmoid(lj[u]);
+        w[u] = mine[u] < 0 ? 0.0f : w[u] * c.scale;
+        const int j = u * 32 + lane;
         if (j < c.J) {
-            c.chosen[static_cast<long long>(t) * c.J + j] = mine[s];
-            c.weights[static_cast<long long>(t) * c.J + j] = w[s];
+            c.chosen[static_cast<long long>(t) * c.J + j] = mine[u];
+            c.weights[static_cast<long long>(t) * c.J + j] = w[u];
         }
     }
 }
