@@ -64,10 +64,12 @@ join_kernel(const float2 *__restrict__ parts, int n, int M, int N, int tokens, c
     }
     if (threadIdx.x >= tokens || i >= M) return;
     a = part[threadIdx.x];
-    const float s = a.x + logf(a.y);
+    const float s = logf(a.y);
     const long long t = target_of(l, i);
-    lse[i] = s;
-    loss[i] = t >= 0 && t < N ? s - l.hit[i] : 0.0f;
+    lse[i] = a.x + s;
+    // not lse - hit: the rounding of lse is of the logits' size, and where the target is
+    // near the largest logit the difference to that is exact and the loss small
+    loss[i] = t >= 0 && t < N ? (a.x - l.hit[i]) + s : 0.0f;
 }
 
 // ---- few tokens in FP32 ---------------------------------------------------------------

@@ -15,7 +15,7 @@
 // group's best two) the order is that of the scores in 64 bits.  A warp computes
 // them in 32, by the hardware's exponential and reciprocal, with a known bound on
 // the error, and where two values that have to be told apart are closer than
-// that, the few that matter once more in 64: for some tokens in a hundred.  (All
+// that, the few that matter once more in 64: for about a token in a thousand.  (All
 // of them in 64 bits: 4 million exponentials at GB300's FP64 rate would take 0.3 ms.)
 #include <cuda_runtime.h>
 
