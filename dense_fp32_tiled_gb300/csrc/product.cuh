@@ -63,6 +63,11 @@ constexpr int SMEM_MAX = 227 * 1024;
 constexpr int PIECES = 3;
 constexpr int PRODUCTS = 6;
 constexpr int KBLK = 2;
+// Logits under an exponential: an error of theirs is one of the same size in its share, and
+// those of likely targets are large sums of one sign, cut off always the same way.  After
+// every K tile (4096 x 32768 x 2048 1689 us for 1651): gradients of 2533 x 23936 x 128 are
+// 7e-7 off instead of 3.5e-6, a matrix product of FP32 FMAs before the exponential 1.2e-6.
+constexpr int LOGITS_KBLK = 1;
 constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles up to 224 tokens
 // The 16-bit types' LOG_SUM, whose results are FP32, adds in registers too, after
 // LOG_SUM_KBLK tiles of K.
@@ -673,7 +678,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr bool BF16 = !std::is_same<T, __half>::value;  // FP32's pieces are bf16
     constexpr bool BLOCKS = F32 || EPI == LOG_SUM;          // K in blocks, added up in registers
-    constexpr int BLOCK = F32 ? KBLK : LOG_SUM_KBLK, COLS = F32 ? F32_COLS : LOG_SUM_REGS;
+    constexpr int BLOCK = !F32 ? LOG_SUM_KBLK : EPI == LOG_SUM || EPI == SOFTMAX_GRADIENT ? LOGITS_KBLK : KBLK;
+    constexpr int COLS = F32 ? F32_COLS : LOG_SUM_REGS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES], acc_full[2], acc_empty[2];
     __shared__ __align__(8) uint64_t tail_bar[MAX_STAGES], part_ready, part_read;

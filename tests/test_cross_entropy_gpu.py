@@ -265,3 +265,48 @@ def test_refusals():
                         (lambda: sg.linear_cross_entropy_backward(f, x, w, t, f, dlse=f.double()), TypeError)]:
         with pytest.raises(error):
             call()
+
+
+# Logits known exactly: 1000 of the target and 992 of the 63 others.  The loss is
+# log(1 + 63 e**-8) = 0.0209, whose terms are off by 2**-21 of them and whose sum by at
+# most 64 + 16 roundings of about 1: 5e-6.  lse is near 1000, a rounding of it 3e-5.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_loss_below_the_rounding_of_lse(dtype, tokens):
+    w = torch.eye(64, device="cuda", dtype=dtype)
+    targets = torch.arange(tokens, device="cuda") % 64
+    x = torch.full((tokens, 64), 992.0, device="cuda", dtype=dtype)
+    x[torch.arange(tokens, device="cuda"), targets] = 1000.0
+    loss, lse = sg.linear_cross_entropy(x, w, targets)
+    want = torch.logsumexp(x.double(), 1) - 1000
+    assert float((loss.double() - want).abs().max()) <= 80 * U + 0.0212 * 2.0 ** -21
+    assert float((lse.double() - want - 1000).abs().max()) <= 2.0 ** -15 + 80 * U
+
+
+# Half of the tokens' logits are sums of one sign (the target's weight is in x), where
+# additions that are cut off instead of rounded tell most.  dx = dz w^T with p = exp(z - lse):
+# a relative 2**-24 (|z| + |lse|) of p for the exponent's rounding, and of z itself the
+# products' 2**-22 |z| (three pieces of each operand hold 24 bits; 64 K's worth of largest
+# products is cut off four times by at most 2**-23 of the sum), |z| and |lse| at most 40.
+@pytest.mark.parametrize("M,N,K", [(90, 74, 1088), (533, 2397, 128), (37, 64, 227)])
+def test_gradient_of_large_logits(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    w = torch.randn((N, K), generator=g, device="cuda") * (2 / K ** 0.5)
+    targets = torch.randint(0, N, (M,), generator=g, device="cuda")
+    x = torch.randn((M, K), generator=g, device="cuda")
+    x[::2] += 3 * w[targets[::2]]
+    dloss = torch.full((M,), 1.0 / M, device="cuda")
+    z = x.double() @ w.double().t()
+    assert float(z.abs().max()) < 40
+    lse = torch.logsumexp(z, 1).float()
+    dx, dw = sg.linear_cross_entropy_backward(dloss, x, w.t(), targets, lse)
+    p = torch.exp(z - lse.double()[:, None])
+    dz = p.clone()
+    dz[torch.arange(M), targets] -= 1
+    dz /= M
+    pb = p / M * (2.0 ** -24 * (2 * 40 + 8) + 2.0 ** -22 * z.abs() + 2.0 ** -22)
+    pb[torch.arange(M), targets] += 2.0 ** -23 / M
+    S = pb @ w.double().abs()
+    A = dz.abs() @ w.double().abs()
+    err = (dx.double() - dz @ w.double()).norm()
+    assert float(err) <= float((S + L.product_bound(N, A, torch.float32)).norm())
