@@ -14,7 +14,9 @@ float16): ``linear(x, w, bias, residual, activation)`` and
 ``linear_backward``; ``expert_linear`` and ``expert_linear_backward``, the same
 over rows sorted by expert; ``expert_sort``, ``expert_gather`` and
 ``expert_combine`` with their gradients, the tokens' way to their experts and
-back.
+back.  Around those layers, with their gradients: ``expert_choose``, a router's
+choice of experts; ``layer_norm``; ``linear_cross_entropy``, the loss of a product
+with a vocabulary without its logits in memory.
 """
 from ._binding import (SGEMM_OK, WAIT_SELFTESTS, SgemmError, bank_pattern_probe, bank_stride_probe, copy_timeouts, declared_functions, host_workspace_size,
                        load_library, sgemm, sgemm_f32, sgemm_f32_3xtf32, sgemm_f32_host, sgemm_host,

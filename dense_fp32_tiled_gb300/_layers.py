@@ -1,7 +1,7 @@
 """Layer operators on torch tensors: argument marshalling for include/linear.h,
-include/experts.h, include/norm.h and
-include/cross_entropy.h.  As in ``_binding``, every arithmetic step runs in the
-CUDA library; PyTorch supplies device memory, strides and the current stream.
+include/experts.h, include/norm.h and include/cross_entropy.h.  As in
+``_binding``, every arithmetic step runs in the CUDA library; PyTorch supplies
+device memory, strides and the current stream.
 
 Every function runs on ``stream`` (a torch.cuda.Stream) or the current one, is
 asynchronous, and allocates what it returns on that stream.  Tensors of one
