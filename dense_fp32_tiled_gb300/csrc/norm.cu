@@ -28,7 +28,7 @@ namespace {
 using namespace rows;
 
 constexpr int MOST_THREADS = 512;       // of a row held in registers
-constexpr int BACKWARD_THREADS = 768;   // of the gradient's block, if they hold 16 values each
+constexpr int MANY_THREADS = 768;       // of a block of several rows, if they hold 16 values each
 constexpr int MOST_WARPS = 24;
 
 // The sums of N values over the threads of a row (blockDim.x of them), the same
@@ -232,19 +232,28 @@ struct No {
 };
 
 // PPT packs a thread.  A block takes every blocks-th row (of each of its
-// threadIdx.y) and asks for its next row before it sums up this one.  Weight and
-// bias come from L1 for each row.
-template <typename T, int V, int PPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const __grid_constant__ Forward c) {
+// threadIdx.y) and asks for its next row before it sums up this one.
+// SEVERAL: one block an SM, of as many rows as it has threads for, with weight and bias
+// in shared memory.  They could come from L1 for each row, in blocks of a row, of which
+// an SM has several; but narrow asynchronous copies go through L1 and drive them out, and
+// blocks' rooms are less of an SM's the wider the rows (us; there, here: 16384 x 4096
+// bf16 46.4, 43.4; 8192 x 5120 f32 88, 60; 8188 x 4098 f32 128, 57; 60000 x 1001 bf16
+// 141, 76).  Rows of a warp and rows of which a block has one are there all the same
+// (60000 x 128 f32 18.4 us, here 20.5).
+template <typename T, int V, int PPT, int THREADS, bool SEVERAL>
+__global__ void __launch_bounds__(THREADS, SEVERAL ? 1 : 1024 / THREADS) forward_kernel(const __grid_constant__ Forward c) {
     using R = Row<T, V>;
     using Num = typename R::Num;
+    using P = Pack<T, V>;
+    using A = Ahead<T, V, PPT, 1, THREADS>;
     __shared__ __align__(16) float part[2][MOST_WARPS][4];
     extern __shared__ __align__(16) uint8_t room[];
     const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
     long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const T *wp = static_cast<const T *>(c.weight), *bp = static_cast<const T *>(c.bias);
-    Ahead<T, V, PPT, 1, THREADS> ahead(room);
+    A ahead(room);
     const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
+    P *const ws = reinterpret_cast<P *>(room + 2 * A::ROOM), *const bs = ws + c.packs;
     tc::grid_trigger();
     tc::grid_wait();
     auto rows = [&](auto whole) {
@@ -259,6 +268,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const 
             ahead.asked();
         };
         ask(r);
+        if constexpr (SEVERAL) {
+            for (int p = threadIdx.y * blockDim.x + threadIdx.x; p < c.packs; p += blockDim.x * blockDim.y) {
+                ws[p] = load_or_ones<T, V>(wp != nullptr, wp + static_cast<long long>(p) * V);
+                bs[p] = load_if<T, V>(bp != nullptr, bp + static_cast<long long>(p) * V);
+            }
+            asm volatile("bar.sync 0;\n" ::: "memory");
+        }
         int turn = 0;
         for (; r < c.M; r += step) {
             ahead.turn();
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const 
                 if (mine(i)) R::add_up(ahead.get(0, i), f[i], sum);
             ask(r + step);
             float s[1] = {sum_of(sum)};
-            row_sum<false>(s, part, turn);
+            row_sum<SEVERAL>(s, part, turn);
             const float mean = s[0] * c.inverse;
             const Num minus_mean = all<Num>(-mean);
             sum = all<Num>(0.0f);
@@ -276,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const 
             for (int i = 0; i < PPT; ++i)
                 if (mine(i)) R::spread(f[i], minus_mean, sum, square);
             float q[2] = {sum_of(sum), sum_of(square)};
-            row_sum<false>(q, part, turn);
+            row_sum<SEVERAL>(q, part, turn);
             const Spread sp = spread_of(c, q);
             if (c.stats != nullptr && threadIdx.x == 0) {
                 c.stats[2 * r] = mean + sp.rest;
@@ -287,13 +303,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) forward_kernel(const 
 #pragma unroll
             for (int i = 0; i < PPT; ++i) {
                 const int p = p0 + 32 * i;
-                if (mine(i))
+                if (!mine(i)) continue;
+                if constexpr (SEVERAL)
+                    R::finish(f[i], ws[p], bs[p], rstd, minus_rest, y + p * V);
+                else
                     R::finish(f[i], load_or_ones<T, V>(WHOLE || wp != nullptr, wp + p * V), load_if<T, V>(WHOLE || bp != nullptr, bp + p * V),
                               rstd, minus_rest, y + p * V);
             }
         }
     };
-    if ((threadIdx.x & ~31) * PPT + 32 * PPT <= c.packs && wp != nullptr && bp != nullptr)
+    if ((threadIdx.x & ~31) * PPT + 32 * PPT <= c.packs && (SEVERAL || (wp != nullptr && bp != nullptr)))
         rows(Yes());
     else
         rows(No());
@@ -570,10 +589,16 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ su
 // ---- host ----------------------------------------------------------------------------
 constexpr int SMS = 152;
 constexpr int WIDE_BLOCKS = 32;            // row groups of columns_kernel
-constexpr size_t ROOM = 200 * 1024;        // of shared memory, for rows on their way and the joined sums
+constexpr size_t ROOM = 200 * 1024;        // of shared memory, for rows on their way, weights and joined sums
+constexpr size_t SHARED = 171 * 1024;      // of an SM's shared memory, what allow_room's division gives several blocks
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
+// Rows that a block of MANY_THREADS has threads for (and named barriers, where a row is not a warp's).
+int rows_at_once(int packs, int ppt) {
+    const int threads = round32((packs + ppt - 1) / ppt), rows = MANY_THREADS / threads;
+    return rows > 15 && threads > 32 ? 15 : rows;
+}
 // Blocks of the gradient, at most: one an SM (the workspace holds the sums of each).
 int backward_blocks(int M) { return M < SMS ? M : SMS; }
 // The kernel may have `bytes` of shared memory, and (several: more blocks than SMs) an
@@ -625,17 +650,36 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
         auto run = [&](auto kernel, int ppt, int block) {
             const int threads = round32((c.packs + ppt - 1) / ppt), rows = threads == 32 ? 4 : 1;
             const long long groups = (static_cast<long long>(M) + rows - 1) / rows;
-            const long long most = static_cast<long long>(SMS) * (threads * rows <= 1024 ? 1024 / (threads * rows) : 1);
             const size_t room = BYTES >= 4 ? static_cast<size_t>(2) * ppt * block * BYTES : 0;
+            // all blocks at once: each has its rows from the start
+            long long most = threads * rows <= 1024 ? 1024 / (threads * rows) : 1;
+            const long long rooms = static_cast<long long>(SHARED / (room + 2048));
+            if (most > rooms) most = rooms;
+            most *= SMS;
             if (!allow_room(kernel, room, groups > SMS)) return static_cast<int>(SGEMM_ERR_DEVICE);
             return launched(tc::launch(kernel, static_cast<unsigned>(groups < most ? groups : most), dim3(threads, rows), room, stream, c));
         };
-        // 32 values of a row a thread (one by one: 16), or a quarter of that of a short one
+        // Of rows longer than a warp's, 16 values (one by one: 8) or 32 (16) a thread, what has
+        // more rows at once.  Two blocks an SM where that is one and the packs are 16 bytes
+        // (3000 x 14336 bf16 39 us for 46), or where weight and bias have no room (FP32).
         constexpr int LARGE = V > 1 ? 32 / V : 16, SMALL = LARGE / 4;
-        if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128>, SMALL, 128);
-        if (c.packs <= LARGE * 128) return run(forward_kernel<El, V, LARGE, 128>, LARGE, 128);
-        if (c.packs <= LARGE * 256) return run(forward_kernel<El, V, LARGE, 256>, LARGE, 256);
-        if (c.packs <= LARGE * MOST_THREADS) return run(forward_kernel<El, V, LARGE, MOST_THREADS>, LARGE, MOST_THREADS);
+        if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128, false>, SMALL, 128);
+        const int few = rows_at_once(c.packs, LARGE / 2), many = rows_at_once(c.packs, LARGE);
+        const size_t slots = BYTES >= 4 ? static_cast<size_t>(2) * MANY_THREADS * BYTES : 0, weights = static_cast<size_t>(2) * c.packs * BYTES;
+        const bool many_fit = weights + LARGE * slots <= ROOM, few_fit = weights + LARGE / 2 * slots <= ROOM;
+        if constexpr (BYTES == 16 || (sizeof(El) == 4 && V > 1))
+            if (c.packs <= LARGE * MOST_THREADS && (BYTES == 16 ? many <= 1 : !many_fit && (few == 0 || !few_fit)))
+                return run(forward_kernel<El, V, LARGE, MOST_THREADS, false>, LARGE, MOST_THREADS);
+        auto several = [&](auto kernel, int ppt, int rows) {
+            if (rows > (M + SMS - 1) / SMS) rows = (M + SMS - 1) / SMS;
+            const long long groups = (static_cast<long long>(M) + rows - 1) / rows;
+            const size_t room = weights + ppt * slots;
+            if (!allow_room(kernel, room, false)) return static_cast<int>(SGEMM_ERR_DEVICE);
+            return launched(tc::launch(kernel, static_cast<unsigned>(groups < SMS ? groups : SMS),
+                                       dim3(round32((c.packs + ppt - 1) / ppt), rows), room, stream, c));
+        };
+        if (many > few && many_fit) return several(forward_kernel<El, V, LARGE, MANY_THREADS, true>, LARGE, many);
+        if (few > 0 && few_fit) return several(forward_kernel<El, V, LARGE / 2, MANY_THREADS, true>, LARGE / 2, few);
         return launched(tc::launch(forward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
     });
 }
@@ -707,7 +751,7 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
         };
         // 16 values of a row a thread (one by one: 8), or 32 of a wide one
         constexpr int SMALL = V > 1 ? 16 / V : 8, LARGE = 2 * SMALL;
-        constexpr int MANY = BACKWARD_THREADS, FEW = sizeof(El) == 4 ? 384 : MOST_THREADS;
+        constexpr int MANY = MANY_THREADS, FEW = sizeof(El) == 4 ? 384 : MOST_THREADS;
         if (c.packs <= SMALL * MANY) return run(backward_kernel<El, V, SMALL, MANY>, SMALL, MANY);
         if (c.packs <= LARGE * FEW) return run(backward_kernel<El, V, LARGE, FEW>, LARGE, FEW);
         int s = launched(tc::launch(backward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));

@@ -183,3 +183,18 @@ def test_empty_and_refused():
                         (lambda: sg.layer_norm_backward(x.half(), x, w, stats), TypeError)]:
         with pytest.raises(error):
             call()
+
+
+# Where the blocks' forms change: rows of a warp, several rows a block (their number by the
+# rows there are, not a multiple of them), one, two blocks an SM, rows read more than once.
+@pytest.mark.parametrize("dtype", L.TYPES)
+@pytest.mark.parametrize("M,N", [(1, 129), (153, 257), (2000, 1001), (1999, 1000), (700, 4097), (611, 4098), (305, 6145), (304, 6148), (153, 8193),
+                                 (160, 12288), (155, 12289), (154, 12290), (153, 12296), (5, 14336), (3, 16384), (4, 16386), (3, 24576), (2, 24577)])
+@pytest.mark.parametrize("weights", ["both", "weight", "bias", "none"])
+def test_forward_forms(dtype, M, N, weights):
+    dt = L.TYPES[dtype]
+    g = L.rng(M * 7 + N)
+    x = L.strided(g, M, N, dt, 0, 0, scale=2.0)
+    weight = L.randn(g, (N,), dt) if weights in ("both", "weight") else None
+    bias = L.randn(g, (N,), dt) if weights in ("both", "bias") else None
+    check_forward(x, weight, bias, 1e-5)
