@@ -16,6 +16,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "linear_types.cuh"
 #include "norm.h"
@@ -394,9 +395,11 @@ __device__ __forceinline__ RowMeans row_means(const float (&q)[3], float inverse
 // A grid of `blocks` blocks, one an SM, takes the rows in turn, one each of their
 // threadIdx.y at a time; a thread keeps the sums of its columns in registers, and
 // the block's are joined in shared memory at the end.  Each row's packs are read
-// from their slots twice, before and after its means are known.  Weights in packs of
-// 4 bytes and less stay in registers, wider ones come from L1.
-template <typename T, int V, int PPT, int THREADS>
+// from their slots twice, before and after its means are known.  Weights are in shared
+// memory (16384 x 4096 bf16 69 us, from L1 for each row 77; 16380 x 4097 154, held in
+// registers 174; 60000 x 128 38, from L1 34); FP32 ones by 4 bytes stay in registers, and
+// those of wide FP32 rows, which leave no room there, come from L1.
+template <typename T, int V, int PPT, int THREADS, bool SHARED_WEIGHT>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Backward c) {
     using R = Row<T, V>;
     using Num = typename R::Num;
@@ -413,7 +416,8 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
     long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     Ahead<T, V, PPT, 2, THREADS> ahead(room);
     const int p0 = (threadIdx.x & ~31) * PPT + (threadIdx.x & 31);
-    constexpr bool HOLD = Pack<T, V>::BYTES <= 4;
+    constexpr bool HOLD = std::is_same<T, float>::value && V == 1;
+    Pack<T, V> *const ws = reinterpret_cast<Pack<T, V> *>(room + 2 * decltype(ahead)::ROOM);
     float next_mean = 0.0f, next_rstd = 0.0f;
     tc::grid_trigger();
     tc::grid_wait();
@@ -435,6 +439,11 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
         };
         ask(r);
         Pack<T, V> held[HOLD ? PPT : 1];
+        if constexpr (SHARED_WEIGHT) {
+            for (int p = threadIdx.y * blockDim.x + threadIdx.x; p < c.packs; p += blockDim.x * blockDim.y)
+                ws[p] = load_or_ones<T, V>(wp != nullptr, wp + static_cast<long long>(p) * V);
+            asm volatile("bar.sync 0;\n" ::: "memory");
+        }
         auto fetch_weight = [&](int i) { return load_or_ones<T, V>(WHOLE || (mine(i) && wp != nullptr), wp + (p0 + 32 * i) * V); };
         if constexpr (HOLD) {
 #pragma unroll
@@ -443,6 +452,8 @@ __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant
         auto weight = [&](int i) {
             if constexpr (HOLD)
                 return held[i];
+            else if constexpr (SHARED_WEIGHT)
+                return ws[p0 + 32 * i];
             else
                 return fetch_weight(i);
         };
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float *__restrict__ su
 // ---- host ----------------------------------------------------------------------------
 constexpr int SMS = 152;
 constexpr int WIDE_BLOCKS = 32;            // row groups of columns_kernel
-constexpr size_t ROOM = 200 * 1024;        // of shared memory, for rows on their way, weights and joined sums
+constexpr size_t ROOM = 226 * 1024;        // of shared memory, for rows on their way, weights and joined sums
 constexpr size_t SHARED = 171 * 1024;      // of an SM's shared memory, what allow_room's division gives several blocks
 
 int round32(int v) { return (v + 31) / 32 * 32; }
@@ -661,12 +672,14 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
         };
         // Of rows longer than a warp's, 16 values (one by one: 8) or 32 (16) a thread, what has
         // more rows at once.  Two blocks an SM where that is one and the packs are 16 bytes
-        // (3000 x 14336 bf16 39 us for 46), or where weight and bias have no room (FP32).
+        // (3000 x 14336 bf16 39 us for 46), or where weight and bias have no room (FP32).  FP32
+        // by 8 bytes: 16 values (8188 x 4098 57 us, 32 values 70).
         constexpr int LARGE = V > 1 ? 32 / V : 16, SMALL = LARGE / 4;
         if (c.packs <= SMALL * 32) return run(forward_kernel<El, V, SMALL, 128, false>, SMALL, 128);
         const int few = rows_at_once(c.packs, LARGE / 2), many = rows_at_once(c.packs, LARGE);
         const size_t slots = BYTES >= 4 ? static_cast<size_t>(2) * MANY_THREADS * BYTES : 0, weights = static_cast<size_t>(2) * c.packs * BYTES;
-        const bool many_fit = weights + LARGE * slots <= ROOM, few_fit = weights + LARGE / 2 * slots <= ROOM;
+        constexpr bool MANY = sizeof(El) == 2 || V != 2;
+        const bool many_fit = MANY && weights + LARGE * slots <= ROOM, few_fit = weights + LARGE / 2 * slots <= ROOM;
         if constexpr (BYTES == 16 || (sizeof(El) == 4 && V > 1))
             if (c.packs <= LARGE * MOST_THREADS && (BYTES == 16 ? many <= 1 : !many_fit && (few == 0 || !few_fit)))
                 return run(forward_kernel<El, V, LARGE, MOST_THREADS, false>, LARGE, MOST_THREADS);
@@ -678,7 +691,8 @@ extern "C" int layer_norm_forward(int type, int M, int N, const void *x, int64_t
             return launched(tc::launch(kernel, static_cast<unsigned>(groups < SMS ? groups : SMS),
                                        dim3(round32((c.packs + ppt - 1) / ppt), rows), room, stream, c));
         };
-        if (many > few && many_fit) return several(forward_kernel<El, V, LARGE, MANY_THREADS, true>, LARGE, many);
+        if constexpr (MANY)
+            if (many > few && many_fit) return several(forward_kernel<El, V, LARGE, MANY_THREADS, true>, LARGE, many);
         if (few > 0 && few_fit) return several(forward_kernel<El, V, LARGE / 2, MANY_THREADS, true>, LARGE / 2, few);
         return launched(tc::launch(forward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
     });
@@ -738,22 +752,32 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
         using El = decltype(el);
         constexpr int V = decltype(v)::value;
         constexpr int BYTES = V * static_cast<int>(sizeof(El));
-        auto run = [&](auto kernel, int ppt, int block) {
+        auto run = [&](auto kernel, int ppt, int block, size_t room) {
             const int threads = round32((c.packs + ppt - 1) / ppt);
             int rows = block / threads;
             if (rows > 15 && threads > 32) rows = 15;  // named barriers
             const int groups = static_cast<int>((static_cast<long long>(M) + rows - 1) / rows);
             if (groups < c.blocks) c.blocks = groups;
-            const size_t slots = BYTES >= 4 ? static_cast<size_t>(4) * ppt * block * BYTES : 0, sums = sizeof(float) * 2 * static_cast<size_t>(N);
-            const size_t room = slots > sums ? slots : sums;
             if (!allow_room(kernel, room, false)) return static_cast<int>(SGEMM_ERR_DEVICE);
             return launched(tc::launch(kernel, static_cast<unsigned>(c.blocks), dim3(threads, rows), room, stream, c));
         };
-        // 16 values of a row a thread (one by one: 8), or 32 of a wide one
+        // 16 values of a row a thread (one by one: 8), or 32 of a wide one in 16 bits
         constexpr int SMALL = V > 1 ? 16 / V : 8, LARGE = 2 * SMALL;
-        constexpr int MANY = MANY_THREADS, FEW = sizeof(El) == 4 ? 384 : MOST_THREADS;
-        if (c.packs <= SMALL * MANY) return run(backward_kernel<El, V, SMALL, MANY>, SMALL, MANY);
-        if (c.packs <= LARGE * FEW) return run(backward_kernel<El, V, LARGE, FEW>, LARGE, FEW);
+        auto room_of = [&](int ppt, int block, bool weight) {
+            const size_t slots = BYTES >= 4 ? static_cast<size_t>(4) * ppt * block * BYTES : 0, sums = sizeof(float) * 2 * static_cast<size_t>(N);
+            const size_t rows = slots + (weight ? static_cast<size_t>(c.packs) * BYTES : 0);
+            return rows > sums ? rows : sums;
+        };
+        constexpr bool SHARED_WEIGHT = BYTES != 4 || sizeof(El) == 2;
+        if (c.packs <= SMALL * MANY_THREADS) {
+            const size_t room = room_of(SMALL, MANY_THREADS, SHARED_WEIGHT);
+            if constexpr (SHARED_WEIGHT && sizeof(El) == 4)
+                if (room > ROOM) return run(backward_kernel<El, V, SMALL, MANY_THREADS, false>, SMALL, MANY_THREADS, room_of(SMALL, MANY_THREADS, false));
+            return run(backward_kernel<El, V, SMALL, MANY_THREADS, SHARED_WEIGHT>, SMALL, MANY_THREADS, room);
+        }
+        if constexpr (sizeof(El) == 2)
+            if (c.packs <= LARGE * MOST_THREADS)
+                return run(backward_kernel<El, V, LARGE, MOST_THREADS, SHARED_WEIGHT>, LARGE, MOST_THREADS, room_of(LARGE, MOST_THREADS, SHARED_WEIGHT));
         int s = launched(tc::launch(backward_wide_kernel<El, V>, static_cast<unsigned>(M), dim3(MOST_THREADS), 0, stream, c));
         if (s == SGEMM_OK && columns) {
             c.blocks = c.blocks < WIDE_BLOCKS ? c.blocks : WIDE_BLOCKS;

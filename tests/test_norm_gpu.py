@@ -198,3 +198,16 @@ def test_forward_forms(dtype, M, N, weights):
     weight = L.randn(g, (N,), dt) if weights in ("both", "weight") else None
     bias = L.randn(g, (N,), dt) if weights in ("both", "bias") else None
     check_forward(x, weight, bias, 1e-5)
+
+
+# The gradient's: several rows a block, one, weights in shared memory, in registers, from L1
+# (wide rows in FP32), rows read more than once.
+@pytest.mark.parametrize("dtype", L.TYPES)
+@pytest.mark.parametrize("M,N", [(1, 129), (153, 257), (2000, 1001), (700, 4097), (611, 4098), (609, 4100), (155, 6145), (160, 7600), (155, 8200),
+                                 (154, 8194), (153, 8193), (160, 12288), (155, 12290), (153, 12296), (5, 16384), (4, 16386)])
+@pytest.mark.parametrize("weight", [True, False])
+def test_backward_forms(dtype, M, N, weight):
+    dt = L.TYPES[dtype]
+    g = L.rng(M * 5 + N)
+    x, dy = L.strided(g, M, N, dt, 0, 0, scale=2.0), L.strided(g, M, N, dt, 0)
+    check_backward(x, dy, L.randn(g, (N,), dt) if weight else None)
