@@ -211,3 +211,12 @@ def test_backward_forms(dtype, M, N, weight):
     g = L.rng(M * 5 + N)
     x, dy = L.strided(g, M, N, dt, 0, 0, scale=2.0), L.strided(g, M, N, dt, 0)
     check_backward(x, dy, L.randn(g, (N,), dt) if weight else None)
+
+
+# Of rows read in pieces: more rows than the column sums' blocks, and fewer.
+@pytest.mark.parametrize("dtype", L.TYPES)
+@pytest.mark.parametrize("M,N", [(300, 12289), (1100, 12290), (257, 16388), (33, 24579), (700, 9001), (155, 11999)])
+def test_backward_wide(dtype, M, N):
+    dt = L.TYPES[dtype]
+    g = L.rng(M + 3 * N)
+    check_backward(L.strided(g, M, N, dt, 0, 0, scale=2.0), L.strided(g, M, N, dt, 0), L.randn(g, (N,), dt))
