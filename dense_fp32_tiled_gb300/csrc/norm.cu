@@ -84,8 +84,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[MOST_WARPS]
 // The packs of a thread's next row, on their way while it works on this one: in
 // slots of shared memory that only this thread reads, so no barrier is needed
 // (2-byte packs, which no asynchronous copy moves: in registers).  COUNT matrices
-// of PPT packs each; two rows' room.  (Two rows ahead took longer, for the L1 that
-// their room takes from the weights: 16384 x 4096 bf16 62 us for 47, its gradient 88 for 84.)
+// of PPT packs each; two rows' room.  (Two rows ahead took longer while weights came from
+// the L1 that their room takes: 16384 x 4096 bf16 62 us for 47.)
 template <typename T, int V, int PPT, int COUNT, int THREADS>
 struct Ahead {
     using P = Pack<T, V>;
