@@ -6,7 +6,7 @@
 // lanes in a row).  The J + 1 lanes with the largest best value give a bound that
 // all picks reach; the some ten experts that do are brought together, one a
 // lane, and each counts those before it: its place.  (Picking one after the
-// other took 36 us for 16384 tokens of 256 experts in 8 groups; this 22.)  Values are compared as
+// other took 36 us for 16384 tokens of 256 experts in 8 groups; this 23.)  Values are compared as
 // whole numbers of the same order as the floats (0: not to be chosen), so a
 // maximum over a warp is one instruction.  Bound by instructions.
 //
