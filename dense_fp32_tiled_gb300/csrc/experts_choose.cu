@@ -289,6 +289,22 @@ __device__ __noinline__ void picks_in_64(const Choose &c, const T *row, const He
     }
 }
 
+// The last pick (logit l, bias b, value v) and the first expert that is left out are equal, which their
+// numbers decide.  Whether an expert with another logit or bias lies so near (`width`) that it may come
+// before both.  For few tokens: in little code.
+template <typename T>
+__device__ __noinline__ bool others_near(const Choose &c, const T *row, const Scores &s, unsigned mask, float l, float b, float v,
+                                         float width, int lane) {
+    bool near = false;
+#pragma unroll 1
+    for (int e = lane; e < c.E; e += 32) {
+        const float le = to_f(row[e]), be = c.bias[e];
+        if ((mask >> group_of(c, e) & 1) != 0 && le > -INFINITY && be > -INFINITY && !(le == l && be == b))
+            near = near || !(fabsf(v - s.with(le, be)) >= width);
+    }
+    return __any_sync(ALL, near);
+}
+
 template <typename T, int NV>
 __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS : 1) choose_kernel(const __grid_constant__ Choose c) {
     extern __shared__ unsigned long long room[];
@@ -466,7 +482,11 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
                 le = __shfl_sync(ALL, le, from);
                 be = __shfl_sync(ALL, be, from);
                 const float ln = __shfl_down_sync(ALL, le, 1), bn = __shfl_down_sync(ALL, be, 1);
-                doubt = __any_sync(ALL, close && !(le == ln && be == bn));
+                const unsigned equal = __ballot_sync(ALL, close && le == ln && be == bn);
+                doubt = __ballot_sync(ALL, close) != equal;
+                if (!doubt && c.J < n && (equal >> (c.J - 1) & 1) != 0)  // what is behind both may come before them
+                    doubt = others_near(c, row, s, keep, __shfl_sync(ALL, le, c.J - 1), __shfl_sync(ALL, be, c.J - 1), floor,
+                                        slack + 0x1p-22f * fabsf(floor), lane);
             }
         }
     } else {  // many picks or many equal values: one after the other
@@ -492,8 +512,11 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
             const int who = __reduce_min_sync(ALL, best == high ? at : INT_MAX);
             if (c.bias != nullptr) {
                 const float v = of_rank(high);
-                if (j > 0 && !(last - v >= slack + 0x1p-22f * fabsf(last)))
-                    doubt = doubt || !(to_f(row[who]) == to_f(row[last_who]) && c.bias[who] == c.bias[last_who]);
+                if (j > 0 && !doubt && !(last - v >= slack + 0x1p-22f * fabsf(last))) {
+                    const float l_last = to_f(row[last_who]), b_last = c.bias[last_who];
+                    doubt = !(to_f(row[who]) == l_last && c.bias[who] == b_last);
+                    if (!doubt && j == c.J) doubt = others_near(c, row, s, keep, l_last, b_last, last, slack + 0x1p-22f * fabsf(last), lane);
+                }
                 last = v;
                 last_who = who;
                 if (j < c.J) floor = v;
