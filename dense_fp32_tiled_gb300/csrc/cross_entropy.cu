@@ -432,8 +432,9 @@ int backward(const Head &h, const float *dloss, const float *dlse, const float *
     p.loss.acc = reinterpret_cast<float *>(ws + need.dz + need.tokens);
     const long long ldz = up8(h.M);
     int chunks = -need.chunks;
-    for (int begin = 0; begin < h.N; begin += need.piece) {
-        const int n = h.N - begin < need.piece ? h.N - begin : need.piece;
+    // 64 bits: pieces are whole tiles, so past the last one of the largest N lies more than an int holds
+    for (long long next = 0; next < h.N; next += need.piece) {
+        const int begin = static_cast<int>(next), n = h.N - begin < need.piece ? h.N - begin : need.piece;
         Operand Z;  // n rows of M
         Z.base = ws;
         Z.inner = h.M;
