@@ -143,9 +143,10 @@ tokens_kernel(int M, int N, const Loss l, const float *__restrict__ dloss, const
         scale = m > 0.0f && m < INFINITY ? m : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0) *alpha = scale / up;
     }
-    for (int i = blockIdx.x * TOKEN_THREADS + threadIdx.x; i < M; i += gridDim.x * TOKEN_THREADS) {
+    // 64 bits: a step past the last of the most tokens is more than an int holds
+    for (long long i = blockIdx.x * TOKEN_THREADS + threadIdx.x; i < M; i += static_cast<int>(gridDim.x) * TOKEN_THREADS) {
         Token k;
-        gradients_of(l, dloss, dlse, i, N, k.a, k.g, k.target);
+        gradients_of(l, dloss, dlse, static_cast<int>(i), N, k.a, k.g, k.target);
         k.lse = lse[i];
         if (fractions) {
             k.lse *= lt::kLog2E;

@@ -1,5 +1,5 @@
 """linear_cross_entropy and its gradient at the largest vocabulary that a call takes,
-where the end of the last piece is past 2**31 (needs a GB300 and about 40 GB of free
+where the end of the last piece is past 2**31, and of most tokens (needs a GB300 and about 40 GB of free
 device memory).
 
 One input of one token makes the logits the weights themselves, w of 33 values: the sum
@@ -62,3 +62,31 @@ def test_the_last_piece_of_the_largest_vocabulary():
             assert ((dw[0, r].double() - ref).abs() <= bound).all(), (r.start, r.stop)
     assert float(dw[0, target]) < -0.9
     assert sg.linear_timeouts() == 0
+
+
+def test_the_last_of_the_most_tokens():
+    # (about 110 GB of device memory)  One column and a gradient of the log sum alone: dz is 1, dx the weight.
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dense_fp32_tiled_gb300 import build
+    build.build()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 140 << 30:
+        pytest.skip("needs 140 GiB free on the device")
+    M = 2147480000  # a step of the blocks that look after the tokens is 152 * 1024
+    x = torch.ones((M, 1), dtype=torch.bfloat16, device="cuda")
+    w = torch.full((1, 1), 1.5, dtype=torch.bfloat16, device="cuda")
+    targets = torch.zeros(M, dtype=torch.int32, device="cuda")
+    lse, dlse = torch.full((M,), 1.5, device="cuda"), torch.ones(M, device="cuda")
+    dlse[-1] = 0.5
+    dx, dw = sg.linear_cross_entropy_backward(None, x, w, targets, lse, dlse=dlse, need_dw=False)
+    assert dw is None and dx.shape == (M, 1)
+    for a in range(0, M, 1 << 28):
+        part = dx[a:a + (1 << 28), 0]
+        if a + (1 << 28) >= M:
+            assert float(part[-1]) == 0.75
+            part = part[:-1]
+        assert (part == 1.5).all()
+    assert sg.linear_timeouts() == 0
+    del x, targets, lse, dlse, dx, part
+    torch.cuda.empty_cache()
