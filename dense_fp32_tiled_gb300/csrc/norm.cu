@@ -219,7 +219,7 @@ struct Spread {
 };
 __device__ __forceinline__ Spread spread_of(const Forward &c, const float (&q)[2]) {
     const float rest = q[0] * c.inverse, var = fmaf(-rest, rest, q[1] * c.inverse);
-    return {rest, 1.0f / sqrtf(fmaxf(var, 0.0f) + c.eps)};
+    return {rest, 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + c.eps)};  // a NaN stays one
 }
 
 // The loop over the rows is there twice: for warps whose share is whole, with a
