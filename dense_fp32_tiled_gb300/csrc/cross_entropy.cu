@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(STRIP_THREADS) strips_kernel(const float *__re
 }
 
 // ---- what the gradient's epilogue needs of each token -------------------------------
-// 16-bit types: a and g as fractions of the largest of them (times `up`), and
+// 16-bit types: a and g as fractions of the largest finite one of them (times `up`), and
 // alpha, which the products take that back with.  Each block finds the largest by itself.
 constexpr int TOKEN_THREADS = 1024;
 constexpr int TOKEN_BLOCKS = 152;
@@ -133,14 +133,16 @@ tokens_kernel(int M, int N, const Loss l, const float *__restrict__ dloss, const
             float a, g;
             int t;
             gradients_of(l, dloss, dlse, i, N, a, g, t);
-            m = fmaxf(m, fmaxf(fabsf(a), fabsf(g)));
+            a = fabsf(a), g = fabsf(g);
+            if (a < INFINITY) m = fmaxf(m, a);  // an infinity or a NaN is its token's alone
+            if (g < INFINITY) m = fmaxf(m, g);
         }
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
         __syncthreads();
         for (int k = 0; k < TOKEN_THREADS / 32; ++k) m = fmaxf(m, most[k]);
-        scale = m > 0.0f && m < INFINITY ? m : 1.0f;
+        scale = m > 0.0f ? m : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0) *alpha = scale / up;
     }
     // 64 bits: a step past the last of the most tokens is more than an int holds

@@ -18,7 +18,7 @@
  * token and 32 to 128 columns (FP32 up to 64 tokens: the logits, in the workspace); the gradient makes the logits again, some of the
  * vocabulary at a time, and keeps at most CROSS_ENTROPY_PIECE of dz.
  * The 16-bit types round dz to themselves before the two products, as fractions
- * of the largest |dloss| and |dloss + dlse| (float16: times 2^14), so that with equal losses the
+ * of the largest finite |dloss| and |dloss + dlse| (float16: times 2^14), so that with equal losses the
  * targets' -1 is exact and small gradients do not vanish.
  * Sums have a fixed order: a call gives the same bits every time.
  *
