@@ -145,8 +145,8 @@ tokens_kernel(int M, int N, const Loss l, const float *__restrict__ dloss, const
         scale = m > 0.0f ? m : 1.0f;
         if (blockIdx.x == 0 && threadIdx.x == 0) *alpha = scale / up;
     }
-    // 64 bits: a step past the last of the most tokens is more than an int holds
-    for (long long i = blockIdx.x * TOKEN_THREADS + threadIdx.x; i < M; i += static_cast<int>(gridDim.x) * TOKEN_THREADS) {
+    // unsigned: a step past the last of the most tokens is more than an int holds.  (64 bits took 1 us longer.)
+    for (unsigned i = blockIdx.x * TOKEN_THREADS + threadIdx.x; i < static_cast<unsigned>(M); i += gridDim.x * TOKEN_THREADS) {
         Token k;
         gradients_of(l, dloss, dlse, static_cast<int>(i), N, k.a, k.g, k.target);
         k.lse = lse[i];
