@@ -184,7 +184,9 @@ int ready(Device *d) {
     Ready &r = g_ready[dev];
     if (r.state == 0 || r.ctx != d->ctx) {
         r.ctx = d->ctx;
-        r.state = opt_in_all<LOG_SUM>() && opt_in_all<SOFTMAX_GRADIENT>() && opt_in_all<SCALED_SUM>() ? 1 : -1;
+        const bool many = opt_in<1, __nv_bfloat16, SOFTMAX_GRADIENT, true>() && opt_in<2, __nv_bfloat16, SOFTMAX_GRADIENT, true>() &&
+                          opt_in<1, __half, SOFTMAX_GRADIENT, true>() && opt_in<2, __half, SOFTMAX_GRADIENT, true>();
+        r.state = opt_in_all<LOG_SUM>() && opt_in_all<SOFTMAX_GRADIENT>() && many && opt_in_all<SCALED_SUM>() ? 1 : -1;
         (void)cudaGetLastError();
     }
     return r.state > 0 ? SGEMM_OK : SGEMM_ERR_DEVICE;

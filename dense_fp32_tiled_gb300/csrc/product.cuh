@@ -69,10 +69,16 @@ constexpr int KBLK = 2;
 // 7e-7 off instead of 3.5e-6, a matrix product of FP32 FMAs before the exponential 1.2e-6.
 constexpr int LOGITS_KBLK = 1;
 constexpr int F32_COLS = 112;  // accumulator columns per epilogue thread: tiles up to 224 tokens
-// The 16-bit types' LOG_SUM, whose results are FP32, adds in registers too, after
-// LOG_SUM_KBLK tiles of K.
-constexpr int LOG_SUM_KBLK = 8;
-constexpr int LOG_SUM_REGS = 128;
+// The 16-bit types' logits are added up in registers too, after each `block` of K tiles: of
+// LOGITS_BLOCK at most, and of FEW_BLOCK where one tile holds all tokens of a LOG_SUM, which
+// then waits for the vocabulary's bytes (one token of 32768 x 4096 in bf16: blocks of 8 tiles
+// 47.0 us, 4 47.4, 2 48.2, 1 49.3, and its log sum 4.3, 2.0, 0.9 and 0.9 x 1e-7 off).  With 8 tiles
+// 8192 x 65536 x 2048 takes about as long as with none (1204 us, gradient 4081 for 4058), with
+// 4 it takes 1311 and 4175.  A target's logit is a sum of one sign, so that what is cut off adds up:
+// of tokens that the model is sure of (p = 0.98, 512 x 4096 x 8192 in bf16) dx is 2.3e-3 off and of the
+// median one 3.1e-3, in one block 3.3e-3 and 3.3e-2 (from FP32 sums 1.7e-3 and 2.9e-3).
+constexpr int LOGITS_BLOCK = 8, FEW_BLOCK = 2;
+constexpr int LOGITS_REGS = 128;
 
 enum Mode { DENSE = 0, ROWS_BY_EXPERT = 1, K_BY_EXPERT = 2 };
 
@@ -118,6 +124,7 @@ struct Product {
     int splits;               // CTAs of a cluster that share the K of a tile (CG = 1)
     int stages, stage_bytes, q_bytes;
     int p_bytes;              // the loss's epilogues: of P's tile that are copied (see few_rows)
+    int block;                // of the 16-bit types' logits: K tiles that are added up in tensor memory
     int epi_offset, epi_bytes;  // the epilogue's buffers in dynamic shared memory, per warp
     int p_mn, q_mn;
     const void *bias, *residual;
@@ -672,14 +679,18 @@ __device__ __forceinline__ void staged_tile(const Product &p, const Tile &w, int
 // rows in both operands (a NaN times 0 would be one) and then reports the stage
 // full, while the copies go on.  Before that, the same warp adds up the bias
 // gradient, where the product is the first of a backward pass.
-template <int CG, typename T, int EPI = LAYER>
+//
+// MANY: a SOFTMAX_GRADIENT of the 16-bit types with more than one block of K: their sum goes back
+// into tensor memory, from where it is read as the only one's is.  (A kernel of its own: the only
+// block's needs 101 registers, this one 166.)
+template <int CG, typename T, int EPI = LAYER, bool MANY = false>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
     constexpr bool F32 = std::is_same<T, float>::value;
     constexpr bool BF16 = !std::is_same<T, __half>::value;  // FP32's pieces are bf16
     constexpr bool BLOCKS = F32 || EPI == LOG_SUM;          // K in blocks, added up in registers
-    constexpr int BLOCK = !F32 ? LOG_SUM_KBLK : EPI == LOG_SUM || EPI == SOFTMAX_GRADIENT ? LOGITS_KBLK : KBLK;
-    constexpr int COLS = F32 ? F32_COLS : LOG_SUM_REGS;
+    constexpr int COLS = F32 ? F32_COLS : LOGITS_REGS;
+    const int block = !F32 ? p.block : EPI == LOG_SUM || EPI == SOFTMAX_GRADIENT ? LOGITS_KBLK : KBLK;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES], acc_full[2], acc_empty[2];
     __shared__ __align__(8) uint64_t tail_bar[MAX_STAGES], part_ready, part_read;
@@ -902,8 +913,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             for (int idx = unit; idx < tiles; idx = next_tile(idx, unit, units, snake)) {
                 const Tile w = locate<CG, EPI == SCALED_SUM>(idx, p, tb, static_cast<int>(rank));
                 const int tail_kt = p.mode == K_BY_EXPERT && w.k_rows % BK != 0 ? w.k_rows / BK : -1;
-                for (int kb = w.k0; kb < w.k1; kb += BLOCKS ? BLOCK : w.k1 - w.k0, ++g) {
-                    const int ke = BLOCKS ? min(kb + BLOCK, w.k1) : w.k1;
+                for (int kb = w.k0; kb < w.k1; kb += BLOCKS || MANY ? block : w.k1 - w.k0, ++g) {
+                    const int ke = BLOCKS || MANY ? min(kb + block, w.k1) : w.k1;
                     const uint32_t set = g & 1;
                     waiter.wait(tc::smem_u32(&acc_empty[set]), ((g >> 1) & 1) ^ 1);
                     tc::fence_after();
@@ -979,13 +990,45 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             if (p.bias != nullptr && f_ok && !w.none)
                 bias = to_f(static_cast<const T *>(p.bias)[(p.mode == ROWS_BY_EXPERT ? static_cast<long long>(w.e) * p.F : 0) + f]);
             const bool any = w.k1 > w.k0;
-            float total[BLOCKS ? COLS : 1];
+            float total[BLOCKS || MANY ? COLS : 1];
+            if constexpr (MANY) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) total[c] = 0.0f;
+                for (int kb = w.k0; kb < w.k1; kb += block) {
+                    const uint32_t set = g & 1;
+                    waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
+                    __syncwarp();
+                    tc::fence_after();
+                    const uint32_t t_set = tmem + set * (TMEM_COLS / 2) + t_off;
+                    const bool last = kb + block >= w.k1;
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 16)
+                        if (c < cols) {
+                            float v[16];
+                            tc::tmem_ld16(t_set + c, v);
+                            tc::tmem_ld_wait(v);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) total[c + i] += v[i];
+                            if (last) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = total[c + i];
+                                tc::tmem_st16(t_set + c, v);
+                            }
+                        }
+                    if (last) break;  // its set is reported read where the sum is
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_relaxed(acc_empty0 + 8u * set);
+                    ++g;
+                }
+                tc::tmem_st_wait();
+            }
             if constexpr (BLOCKS) {
                 if (p.residual != nullptr && !w.none && S == 1 && f - lane < p.F)
                     prefetch_residual<T>(p, static_cast<long long>(w.t0) + col0, min(cols, n_tile - col0), f - lane, lane);
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) total[c] = 0.0f;
-                for (int kb = w.k0; kb < w.k1; kb += BLOCK, ++g) {
+                for (int kb = w.k0; kb < w.k1; kb += block, ++g) {
                     const uint32_t set = g & 1;
                     waiter.wait(tc::smem_u32(&acc_full[set]), (g / 2) & 1);
                     __syncwarp();
@@ -1420,7 +1463,7 @@ inline int few_rows(const Product &p, int epi, const Plan &pl, const Operand &P)
     return (p.F + 7) / 8 * 8;
 }
 
-template <int CG, typename T, int EPI>
+template <int CG, typename T, int EPI, bool MANY>
 cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -1437,7 +1480,7 @@ cudaError_t launch(const Maps &maps, const Product &p, int grid, size_t smem, cu
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, product_kernel<CG, T, EPI>, maps, p);
+    return cudaLaunchKernelEx(&cfg, product_kernel<CG, T, EPI, MANY>, maps, p);
 }
 
 // Enqueue one product: P and Q as 16-bit operands (FP32: three planes each).
@@ -1488,6 +1531,10 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     p.q_bytes = q_bytes_of(p.bt / pl.cg, Q.mn);
     const int p_rows = few_rows(p, EPI, pl, P);
     p.p_bytes = p_rows * 128;
+    // blocks of K as long as one another
+    const int ktiles = (p.K + BK - 1) / BK, most = EPI == LOG_SUM && p.F <= PROWS ? FEW_BLOCK : LOGITS_BLOCK;
+    const int blocks = (ktiles + most - 1) / most;
+    p.block = blocks > 0 ? (ktiles + blocks - 1) / blocks : 1;
     p.stage_bytes = p.p_bytes + p.q_bytes;
     if (p.stage_bytes < P_BYTES) p.stage_bytes = P_BYTES;
     const int per_unit = PROWS * pl.cg;
@@ -1522,15 +1569,19 @@ int run_product(int type, Product p, const Operand &P, const Operand &Q, const D
     const int units = static_cast<int>(tiles < pl.units ? tiles : pl.units);
     const int grid = units * (pl.cg == 2 ? 2 : p.splits);
     sg_nvtx::Range r("linear: product");
-    cudaError_t err = cudaErrorInvalidValue;
-    if (type == LINEAR_F32) {
-        err = pl.cg == 2 ? launch<2, float, EPI>(maps, p, grid, smem, stream) : launch<1, float, EPI>(maps, p, grid, smem, stream);
-    } else if (type == LINEAR_BF16) {
-        err = pl.cg == 2 ? launch<2, __nv_bfloat16, EPI>(maps, p, grid, smem, stream)
-                         : launch<1, __nv_bfloat16, EPI>(maps, p, grid, smem, stream);
-    } else {
-        err = pl.cg == 2 ? launch<2, __half, EPI>(maps, p, grid, smem, stream) : launch<1, __half, EPI>(maps, p, grid, smem, stream);
-    }
+    auto start = [&](auto el, auto many) {
+        using El = decltype(el);
+        constexpr bool MANY = decltype(many)::value;
+        return pl.cg == 2 ? launch<2, El, EPI, MANY>(maps, p, grid, smem, stream) : launch<1, El, EPI, MANY>(maps, p, grid, smem, stream);
+    };
+    auto half = [&](auto el) {
+        if constexpr (EPI == SOFTMAX_GRADIENT)
+            if (blocks > 1) return start(el, std::true_type());
+        return start(el, std::false_type());
+    };
+    const cudaError_t err = type == LINEAR_F32    ? start(float(), std::false_type())
+                            : type == LINEAR_BF16 ? half(__nv_bfloat16())
+                                                  : half(__half());
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return SGEMM_ERR_LAUNCH;
@@ -1629,9 +1680,9 @@ int set_up(Device *out);
 // A product with the layer's epilogue.
 int run_layer(int type, const Product &p, const Operand &P, const Operand &Q, const Device &d, cudaStream_t stream);
 // Allows this kernel all the shared memory that a product may use.
-template <int CG, typename T, int EPI>
+template <int CG, typename T, int EPI, bool MANY = false>
 bool opt_in() {
-    return cudaFuncSetAttribute(product_kernel<CG, T, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) ==
+    return cudaFuncSetAttribute(product_kernel<CG, T, EPI, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX - 1024) ==
            cudaSuccess;
 }
 

@@ -239,6 +239,16 @@ __device__ __forceinline__ void tmem_ld_wait(float (&v)[16]) {
                  :
                  : "memory");
 }
+// The same back into tensor memory; what this warp reads after tmem_st_wait is what it stored.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};\n" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // 32 lanes x 16 columns as the fragments of 8 x 8 matrices: thread i gets, of
 // lanes 8 o + i / 4, columns 8 j + 2 (i % 4) and the next, in v[8 (o / 2) +
 // 4 j + 2 (o % 2)] and the next (o < 4, j < 2).

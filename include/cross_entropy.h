@@ -14,7 +14,8 @@
  * x is M x K (tokens), w is K x N (the vocabulary) in either order, as in
  * linear.h; both and the gradients have one type, losses, log sums and their
  * gradients are FP32.  Products are those of linear.h: exact, added in FP32
- * (FP32: six products of bf16 pieces).  The forward pass keeps two numbers per
+ * (FP32: six products of bf16 pieces); logits by blocks of K (at most 512 in 16 bits, 64
+ * in FP32), whose sums are added with round-to-nearest.  The forward pass keeps two numbers per
  * token and 32 to 128 columns (FP32 up to 64 tokens: the logits, in the workspace); the gradient makes the logits again, some of the
  * vocabulary at a time, and keeps at most CROSS_ENTROPY_PIECE of dz.
  * The 16-bit types round dz to themselves before the two products, as fractions
