@@ -397,8 +397,8 @@ __device__ __forceinline__ RowMeans row_means(const float (&q)[3], float inverse
 // the block's are joined in shared memory at the end.  Each row's packs are read
 // from their slots twice, before and after its means are known.  Weights are in shared
 // memory (16384 x 4096 bf16 69 us, from L1 for each row 77; 16380 x 4097 154, held in
-// registers 174; 60000 x 128 38, from L1 34); FP32 ones by 4 bytes stay in registers, and
-// those of wide FP32 rows, which leave no room there, come from L1.
+// registers 174); FP32 ones by 4 bytes stay in registers, and those of wide FP32 rows, which
+// leave no room there, and of 16-bit rows of a pack a lane come from L1.
 template <typename T, int V, int PPT, int THREADS, bool SHARED_WEIGHT>
 __global__ void __launch_bounds__(THREADS) backward_kernel(const __grid_constant__ Backward c) {
     using R = Row<T, V>;
@@ -785,8 +785,11 @@ extern "C" int layer_norm_backward(int type, int M, int N, const void *dy, int64
         constexpr bool SHARED_WEIGHT = BYTES != 4 || sizeof(El) == 2;
         if (c.packs <= SMALL * MANY_THREADS) {
             const size_t room = room_of(SMALL, MANY_THREADS, SHARED_WEIGHT);
-            if constexpr (SHARED_WEIGHT && sizeof(El) == 4)
-                if (room > ROOM) return run(backward_kernel<El, V, SMALL, MANY_THREADS, false>, SMALL, MANY_THREADS, room_of(SMALL, MANY_THREADS, false));
+            // (a lane's one pack of weights comes sooner from L1: 400000 x 128 bf16 122 us for 150, 60000 x 256 29.6
+            // for 33.5; not so where it has more, or in FP32: 60000 x 512 bf16 48.7 for 45.4, 60000 x 128 f32 24.8 for 22.8)
+            if constexpr (SHARED_WEIGHT && (sizeof(El) == 4 || BYTES == 16))
+                if (room > ROOM || (sizeof(El) == 2 && c.packs <= 32))
+                    return run(backward_kernel<El, V, SMALL, MANY_THREADS, false>, SMALL, MANY_THREADS, room_of(SMALL, MANY_THREADS, false));
             return run(backward_kernel<El, V, SMALL, MANY_THREADS, SHARED_WEIGHT>, SMALL, MANY_THREADS, room);
         }
         if constexpr (sizeof(El) == 2 || V == 1) {
