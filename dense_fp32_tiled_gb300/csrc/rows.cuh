@@ -100,20 +100,6 @@ __device__ __forceinline__ void store(T *p, const Pack<T, V> &v) {
     *reinterpret_cast<typename Pack<T, V>::Raw *>(p) = v.raw;
 }
 
-// The same values, of which the compiler keeps nothing that it made of them
-// before: converting them again costs an instruction, keeping them a register each.
-template <typename T, int V>
-__device__ __forceinline__ void forget(Pack<T, V> &v) {
-    if constexpr (Pack<T, V>::BYTES == 16)
-        asm volatile("" : "+r"(v.raw.x), "+r"(v.raw.y), "+r"(v.raw.z), "+r"(v.raw.w));
-    else if constexpr (Pack<T, V>::BYTES == 8)
-        asm volatile("" : "+r"(v.raw.x), "+r"(v.raw.y));
-    else if constexpr (Pack<T, V>::BYTES == 4)
-        asm volatile("" : "+r"(v.raw));
-    else
-        asm volatile("" : "+h"(v.raw));
-}
-
 // ---- two values at a time ------------------------------------------------------------
 // FP32 arithmetic on pairs: one instruction for two, each rounded as by itself.  A pack of V values is V / 2 pairs, or one float.
 using Pair = float2;
