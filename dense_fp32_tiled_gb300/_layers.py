@@ -12,6 +12,7 @@ status of the library raises SgemmError.
 from __future__ import annotations
 
 import ctypes
+import operator
 from contextlib import nullcontext
 
 from ._binding import SGEMM_OK, SgemmError, load_library
@@ -512,7 +513,8 @@ def expert_choose(logits, choices, bias=None, scoring="softmax", groups=1, kept_
     kind, how = _type_of(logits, "logits"), _scoring(scoring)
     if logits.dim() != 2:
         raise ValueError(f"logits must be 2-D, got {tuple(logits.shape)}")
-    (T, E), J, dtype, dev = logits.shape, int(choices), logits.dtype, logits.get_device()
+    (T, E), dtype, dev = logits.shape, logits.dtype, logits.get_device()
+    J, groups, kept_groups, group_top = (operator.index(n) for n in (choices, groups, kept_groups, group_top))
     _fits(T, E, J, groups, kept_groups, group_top)
     lp, ldl = _rows(logits, T, E, dtype, dev, "logits")
     bp = _vector(bias, (E,), torch.float32, dev, "bias")
