@@ -289,18 +289,28 @@ __device__ __noinline__ void picks_in_64(const Choose &c, const T *row, const He
     }
 }
 
-// The last pick (logit l, bias b, value v) and the first expert that is left out are equal, which their
+// The last pick (logit lp, bias bp, value v) and the first expert that is left out are equal, which their
 // numbers decide.  Whether an expert with another logit or bias lies so near (`width`) that it may come
-// before both.  For few tokens: in little code.
-template <typename T>
-__device__ __noinline__ bool others_near(const Choose &c, const T *row, const Scores &s, unsigned mask, float l, float b, float v,
+// before both.  The scores are worked out again: kept, they cost every token registers (16384 x 256 in 8 groups
+// 24.2 us for 23.3, without groups and of logits in half numbers, where many tokens come here, 18 for 22).  A lane's own
+// experts in wide accesses; where those are many, one after the other, for the kernel's registers.
+template <typename T, int NV>
+__device__ __noinline__ bool others_near(const Choose &c, const T *row, const Scores &s, unsigned mask, float lp, float bp, float v,
                                          float width, int lane) {
     bool near = false;
+    auto look = [&](int e, float l, float b) {
+        const bool in = (mask >> (group_of(c, e) & 31) & 1) != 0 && l > -INFINITY && b > -INFINITY;
+        near |= in && !(fabsf(v - s.with(l, b)) >= width) && !(l == lp && b == bp);
+    };
+    if constexpr (NV <= 8) {
+        float l[NV], b[NV];
+        load_row<T, NV>(row, lane, c.E, c.wide, -INFINITY, l);
+        load_row<float, NV>(c.bias, lane, c.E, c.wide_bias, -INFINITY, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) look(lane * NV + i, l[i], b[i]);
+    } else {
 #pragma unroll 1
-    for (int e = lane; e < c.E; e += 32) {
-        const float le = to_f(row[e]), be = c.bias[e];
-        if ((mask >> group_of(c, e) & 1) != 0 && le > -INFINITY && be > -INFINITY && !(le == l && be == b))
-            near = near || !(fabsf(v - s.with(le, be)) >= width);
+        for (int e = lane; e < c.E; e += 32) look(e, to_f(row[e]), c.bias[e]);
     }
     return __any_sync(ALL, near);
 }
@@ -485,7 +495,7 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
                 const unsigned equal = __ballot_sync(ALL, close && le == ln && be == bn);
                 doubt = __ballot_sync(ALL, close) != equal;
                 if (!doubt && c.J < n && (equal >> (c.J - 1) & 1) != 0)  // what is behind both may come before them
-                    doubt = others_near(c, row, s, keep, __shfl_sync(ALL, le, c.J - 1), __shfl_sync(ALL, be, c.J - 1), floor,
+                    doubt = others_near<T, NV>(c, row, s, keep, __shfl_sync(ALL, le, c.J - 1), __shfl_sync(ALL, be, c.J - 1), floor,
                                         slack + 0x1p-22f * fabsf(floor), lane);
             }
         }
@@ -515,7 +525,7 @@ __global__ void __launch_bounds__(CHOOSE_WARPS * 32, NV <= 8 ? 32 / CHOOSE_WARPS
                 if (j > 0 && !doubt && !(last - v >= slack + 0x1p-22f * fabsf(last))) {
                     const float l_last = to_f(row[last_who]), b_last = c.bias[last_who];
                     doubt = !(to_f(row[who]) == l_last && c.bias[who] == b_last);
-                    if (!doubt && j == c.J) doubt = others_near(c, row, s, keep, l_last, b_last, last, slack + 0x1p-22f * fabsf(last), lane);
+                    if (!doubt && j == c.J) doubt = others_near<T, NV>(c, row, s, keep, l_last, b_last, last, slack + 0x1p-22f * fabsf(last), lane);
                 }
                 last = v;
                 last_who = who;
