@@ -382,7 +382,9 @@ def linear_cross_entropy(x, w, targets, stream=None):
 def linear_cross_entropy_backward(dloss, x, w, targets, lse, dlse=None, need_dx=True, need_dw=True, stream=None):
     """(dx, dw) of linear_cross_entropy for the gradients of its losses and (dlse,
     None for none) of its log sums, float32 (M,); lse is what it returned.  dw
-    has the memory order of w; what is not needed is None."""
+    has the memory order of w; what is not needed is None.  In the 16-bit types
+    the logits' gradients are rounded to them, as fractions of the largest, before
+    the two products."""
     if stream is None and _fast is not None:
         r = _fast.cross_entropy_backward(dloss, x, w, targets, lse, dlse, need_dx, need_dw)
         if r is not NotImplemented:
@@ -503,7 +505,8 @@ def expert_choose(logits, choices, bias=None, scoring="softmax", groups=1, kept_
     (1 or 2) best have the largest sum.  chosen is int32 (T, choices); weights,
     float32, are scale times the chosen scores, divided by their sum if
     ``renormalize``.  Experts with a logit of -inf are never chosen; places left
-    over are -1 (which expert_sort drops), their weights 0.
+    over are -1 (which expert_sort drops), their weights 0.  A token with a NaN
+    among its logits chooses none, and its weights are NaN.
     """
     if stream is None and _fast is not None:
         r = _fast.choose(logits, choices, bias, scoring, groups, kept_groups, group_top, renormalize, scale)
